@@ -435,6 +435,163 @@ size_t phs_hybrid_stack_fused_workspace_bytes(int32_t batch, int32_t num_q_heads
                                               int32_t num_kv_heads, int32_t head_dim,
                                               int32_t max_seq_len, int32_t num_full_layers);
 
+/* ------------------------------------------------------------------------
+ * Page operations on the device: free and fork requests and compact a pool,
+ * with the block tables, lengths and reference counts the decode kernels
+ * read kept in device memory (no host round trip; recordable into a CUDA
+ * graph).  page_refcount (int32 [num_pages]) is the truth for these calls:
+ * a page is free when its count is 0.  A host phs_page_allocator that keeps
+ * books on the same pool takes the new counts with
+ * phs_page_load_refcounts, and after a compaction a radix tree takes the
+ * new page ids with phs_radix_remap.
+ * block_table is int32 [num_rows][max_pages_per_seq], seq_lens int32
+ * [num_rows]; row r holds pages block_table[r][0 .. ceil(seq_lens[r] / 16)).
+ * pools: host array of num_layers descriptors that share the block table
+ * (same num_pages, Hkv and head_dim).
+ *
+ * phs_pages_free: for each i < n, takes one reference off every page of row
+ * rows[i] (a page that reaches 0 is free) and sets seq_lens[rows[i]] = 0;
+ * the row's table entries stay as they are.  A row listed again is skipped
+ * (PHS_EINVAL).
+ *
+ * phs_pages_fork: for each i < n, row dst_rows[i] becomes a continuation of
+ * row src_rows[i]: same length, whole pages shared (one more reference
+ * each), and a last page that is only partly filled copied, in every layer,
+ * into a fresh page with count 1, so that the next append writes into a
+ * page of its own.  Fresh pages are the lowest-numbered free ones, given to
+ * the entries in their order.  dst_rows[i] must be a free row (seq_lens 0)
+ * that no src_rows[j] and no earlier dst_rows[j] names, else PHS_EINVAL; an
+ * entry without a page left is PHS_ENOSPACE; either entry is skipped, the
+ * others are done.  workspace: phs_pages_fork_workspace_bytes, 256-byte
+ * aligned.
+ *
+ * phs_pages_compact: with L pages live, moves the live pages with ids >= L
+ * into the free ids below L, in every layer: the highest live page to the
+ * lowest free id, and so on.  block_table_out, page_refcount_out: the
+ * tables and counts by the new ids (may be the inputs themselves); entries
+ * behind a row's length are copied as they are.  page_map (int32
+ * [num_pages]): new id of each live page, -1 for the others.  num_live
+ * (int32 [1]): L.  Only page contents below L are changed.  workspace:
+ * phs_pages_compact_workspace_bytes, 256-byte aligned.
+ *
+ * Device-checked: rows, lengths and page ids out of range, and references
+ * to pages that are not live, record PHS_ERANGE and are skipped (a bad
+ * table entry stays as it is).  Calls that use the same tables or counts
+ * run in stream order; two captured graphs that may run at once need a
+ * workspace each.
+ * ---------------------------------------------------------------------- */
+int phs_pages_free(const int32_t *block_table, int32_t num_rows, int32_t max_pages_per_seq,
+                   int32_t *seq_lens, int32_t *page_refcount, int64_t num_pages,
+                   const int32_t *rows, int32_t n, int32_t *dev_status, void *stream);
+size_t phs_pages_fork_workspace_bytes(int32_t num_rows, int32_t n);
+int phs_pages_fork(const phs_paged_pool *pools, int32_t num_layers, int32_t *block_table,
+                   int32_t num_rows, int32_t max_pages_per_seq, int32_t *seq_lens,
+                   int32_t *page_refcount, const int32_t *src_rows, const int32_t *dst_rows,
+                   int32_t n, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                   void *stream);
+size_t phs_pages_compact_workspace_bytes(int64_t num_pages);
+int phs_pages_compact(const phs_paged_pool *pools, int32_t num_layers,
+                      const int32_t *block_table, int32_t num_rows, int32_t max_pages_per_seq,
+                      const int32_t *seq_lens, const int32_t *page_refcount,
+                      int32_t *block_table_out, int32_t *page_refcount_out, int32_t *page_map,
+                      int32_t *num_live, void *workspace, size_t workspace_bytes,
+                      int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Differential attention, one new token per request over the paged pool:
+ *     out_i = (softmax(s q_{2i} K1^T) - lambda softmax(s q_{2i+1} K2^T)) V
+ *     lambda = exp(lambda_q1 . lambda_k1) - exp(lambda_q2 . lambda_k2)
+ *              + lambda_init
+ * for heads i < num_heads, over tokens [0, seq_lens[b]).  The pool has
+ * 2 Hv KV heads of width D: heads 2j and 2j + 1 of K are the keys K1 and K2
+ * of value head j, and the same two heads of V hold the first and the last
+ * D of its 2D value columns (so a [..][Hv][2D] value is a [..][2 Hv][D]
+ * one, and append, copies and page operations take the pool as any other).
+ * Head i reads value head i / (num_heads / Hv); num_heads / Hv <= 16.
+ *   q    bf16 [batch][2 num_heads][D]: rows 2i and 2i + 1 are head i's
+ *        queries of the two maps
+ *   out  [batch][num_heads][2D], bf16 or fp32
+ * With norm_weight (fp32 [2D]) each head's output is then normalised:
+ *     out_i <- (1 - lambda_init) norm_weight out_i
+ *              / sqrt(mean(out_i^2) + norm_eps).
+ * The lambda vectors are fp32 [D] (lambda_per_head 0) or [num_heads][D]
+ * (1), device memory.  Sums, softmax statistics and the norm are fp32.
+ * Splits, workspace, k_new / v_new / page_refcount (bf16
+ * [batch][2 Hv][D]) and errors as for phs_attn_decode_full_paged; a request
+ * of length 0 gets a zero row.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    const float *lambda_q1;   /* device */
+    const float *lambda_k1;
+    const float *lambda_q2;
+    const float *lambda_k2;
+    const float *norm_weight; /* device fp32 [2D], or NULL: no norm */
+    float lambda_init;
+    float norm_eps;
+    int32_t lambda_per_head;
+} phs_diff_weights;
+
+size_t phs_diff_workspace_bytes(int32_t batch, int32_t num_heads, int32_t num_value_heads,
+                                int32_t head_dim, int32_t max_seq_len,
+                                int32_t tokens_per_split);
+int phs_attn_decode_diff_paged(const void *q, int32_t num_heads, const phs_paged_pool *pool,
+                               const int32_t *block_table, int32_t max_pages_per_seq,
+                               const int32_t *seq_lens, int32_t max_seq_len, int32_t batch,
+                               const phs_diff_weights *weights, float softmax_scale,
+                               int32_t tokens_per_split, void *out, int32_t out_dtype,
+                               void *workspace, size_t workspace_bytes, const void *k_new,
+                               const void *v_new, const int32_t *page_refcount,
+                               int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head.  A request's cache is one
+ * D x D state per KV head:
+ *     S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T
+ *     o_t = scale q_t^T S_t          (query head i: h = i / (Hq / Hkv))
+ * log_decay: device fp32 [Hkv], <= 0 (minus infinity: no memory).
+ * State pool: fp32 [num_states][Hkv][D (k)][D (v)], updated in place.
+ * state_ids (device int32 [batch], NULL: request b has state b): a negative
+ * id marks an inactive request; an id outside the pool (PHS_ERANGE) or one
+ * that an earlier request of the call has (PHS_EINVAL) is recorded.  Such a
+ * request updates nothing and its output rows are zero.
+ *
+ * phs_linear_attn_decode: one token per request.  q, out [batch][Hq][D],
+ * k_new, v_new bf16 [batch][Hkv][D]; out bf16 or fp32.
+ *
+ * phs_linear_attn_prompt: whole prompts, packed: request b has tokens
+ * [cu_seqlens[b], cu_seqlens[b + 1]) (device int32 [batch + 1], not
+ * decreasing) of q [total_tokens][Hq][D] and k, v [total_tokens][Hkv][D].
+ * It starts from its state where resume[b] != 0 (device int32 [batch]), else
+ * (or where resume is NULL) from a zero state, and leaves the state after
+ * its last token in the pool, ready for the next part of the prompt or for
+ * phs_linear_attn_decode.  max_seq_len (host) bounds the requests' lengths.
+ * out bf16 [total_tokens][Hq][D]; rows of no request are left as they were.
+ * A request with a bad token range (outside the tokens, or beginning before
+ * an earlier one's end) or a length above max_seq_len records PHS_ERANGE and
+ * is left out whole.  workspace:
+ * phs_linear_prompt_workspace_bytes, 256-byte aligned.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    float *s;             /* device, fp32 [num_states][Hkv][D][D] */
+    int64_t num_states;
+    int32_t num_kv_heads;
+    int32_t head_dim;     /* D: 64 or 128 */
+} phs_state_pool;
+
+int phs_linear_attn_decode(const void *q, int32_t num_q_heads, const phs_state_pool *pool,
+                           const void *k_new, const void *v_new, const float *log_decay,
+                           const int32_t *state_ids, int32_t batch, float scale, void *out,
+                           int32_t out_dtype, int32_t *dev_status, void *stream);
+size_t phs_linear_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads,
+                                         int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t total_tokens, int32_t max_seq_len);
+int phs_linear_attn_prompt(const void *q, int32_t num_q_heads, const void *k, const void *v,
+                           const int32_t *cu_seqlens, int32_t total_tokens, int32_t max_seq_len,
+                           const phs_state_pool *pool, const int32_t *state_ids,
+                           const int32_t *resume, const float *log_decay, int32_t batch,
+                           float scale, void *out, void *workspace, size_t workspace_bytes,
+                           int32_t *dev_status, void *stream);
+
 /* KV tokens held by a hybrid stack (host arrays in, host results out):
  * Full layers hold seq_lens[b] tokens per request, SWA layers
  * min(seq_lens[b], window).  Source: MiMo page, section 1 (the 10/60 stack
@@ -486,6 +643,11 @@ int phs_page_refcounts(phs_page_allocator *a, int32_t *out);
  * shared page loses one reference, and the fresh id is returned -- the
  * caller copies the contents with phs_copy_pages and updates its table. */
 int phs_page_cow(phs_page_allocator *a, int32_t page, int32_t *out_page);
+
+/* Takes counts (host int32 [num_pages], none negative, else PHS_EINVAL and no
+ * change) as the allocator's own: the counts that phs_pages_free, _fork or
+ * _compact left on the device, brought to the host. */
+int phs_page_load_refcounts(phs_page_allocator *a, const int32_t *counts);
 
 /* Device copy of whole pages (K and V, all heads): dst_pages[i] <- src_pages[i]
  * (device int32 arrays).  Out-of-range ids record PHS_ERANGE. */
@@ -545,6 +707,11 @@ int phs_radix_insert(phs_radix_tree *t, const int32_t *tokens, int64_t n, const 
  * is evictable; their SWA segment pages are released too. */
 int phs_radix_evict(phs_radix_tree *t, int64_t pages, int64_t *out_freed);
 int64_t phs_radix_cached_pages(phs_radix_tree *t);
+/* Renames the tree's Full pages by page_map (host int32 [num_pages], the map
+ * phs_pages_compact wrote): page p becomes page_map[p].  PHS_ERANGE, and no
+ * change, if a cached page has no new id.  References are not touched: the
+ * moved counts come with phs_page_load_refcounts. */
+int phs_radix_remap(phs_radix_tree *t, const int32_t *page_map, int64_t num_pages);
 /* Window-safe length as a plain function: the largest L <= match_len, L a
  * multiple of align, with swa_valid[t] != 0 (host uint8) for every t in
  * [max(0, L - window), L); 0 if none. */

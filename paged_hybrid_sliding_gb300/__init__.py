@@ -29,6 +29,10 @@ __all__ = [
     "attn_decode_hybrid_stack_fused", "hybrid_stack_fused_workspace_bytes",
     "hybrid_kv_tokens", "copy_d2d", "read_checksum", "copy_pages", "PageAllocator", "RadixTree",
     "window_safe_len", "swa_ring_save", "swa_ring_seed", "lib", "PAGE", "QBLOCK",
+    "pages_free", "pages_fork", "pages_compact", "pages_fork_workspace_bytes",
+    "pages_compact_workspace_bytes",
+    "DiffWeights", "attn_decode_diff_paged", "diff_workspace_bytes",
+    "StatePool", "linear_attn_decode", "linear_attn_prompt", "linear_prompt_workspace_bytes",
 ]
 
 PAGE = 16
@@ -616,6 +620,14 @@ class PageAllocator:
         _check(lib().phs_page_refcounts(self._h, out.ctypes.data), "page_refcounts")
         return out
 
+    def load_refcounts(self, counts):
+        """Take counts (host int32 [num_pages]) as the allocator's own: what
+        pages_free / pages_fork / pages_compact left on the device."""
+        c = _i32(counts)
+        if c.shape != (self.num_pages,):
+            raise ValueError("counts must be [num_pages]")
+        _check(lib().phs_page_load_refcounts(self._h, c.ctypes.data), "page_load_refcounts")
+
     def cow(self, page: int) -> int:
         out = ctypes.c_int32()
         _check(lib().phs_page_cow(self._h, int(page), ctypes.byref(out)), "page_cow")
@@ -688,6 +700,12 @@ class RadixTree:
         _check(lib().phs_radix_evict(self._h, int(pages), ctypes.byref(freed)), "radix_evict")
         return freed.value
 
+    def remap(self, page_map):
+        """Rename the tree's Full pages by the map pages_compact wrote (host
+        int32 [num_pages])."""
+        m = _i32(page_map)
+        _check(lib().phs_radix_remap(self._h, m.ctypes.data, m.shape[0]), "radix_remap")
+
     def cached_pages(self) -> int:
         return int(lib().phs_radix_cached_pages(self._h))
 
@@ -741,3 +759,291 @@ def window_safe_len(swa_valid, match_len: int, window: int, align: int = 1) -> i
     r = int(lib().phs_window_safe_len(v.ctypes.data, int(match_len), int(window), int(align)))
     _check(min(r, 0), "window_safe_len")
     return r
+
+
+# ---------------------------------------------------------- page operations --
+def _same_device(first, *others):
+    """The tensors of one call live on the device that the call runs on."""
+    if first.device.index != torch.cuda.current_device() \
+            or any(t is not None and t.device != first.device for t in others):
+        raise ValueError("all tensors must be on the current CUDA device")
+
+
+def _tables(block_table, seq_lens, page_refcount):
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    _need(page_refcount, torch.int32, "page_refcount", 1)
+    if seq_lens.shape[0] != block_table.shape[0]:
+        raise ValueError("seq_lens needs one entry per row of block_table")
+
+
+def _pools_of(pools, page_refcount):
+    if not pools:
+        raise ValueError("pools must name at least one pool")
+    if any(p.k.shape[0] != page_refcount.shape[0] for p in pools):
+        raise ValueError("page_refcount needs one entry per page")
+    return _pool_array(_lib.PagedPoolC, pools)
+
+
+def pages_free(block_table, seq_lens, page_refcount, rows, status=None, stream=None):
+    """Free the listed rows of the block table: one reference less on each
+    of their pages, their lengths zero."""
+    _tables(block_table, seq_lens, page_refcount)
+    _need(rows, torch.int32, "rows", 1)
+    _opt(status, torch.int32, "status")
+    _same_device(block_table, seq_lens, page_refcount, rows, status)
+    _check(lib().phs_pages_free(_ptr(block_table), block_table.shape[0], block_table.shape[1],
+                                _ptr(seq_lens), _ptr(page_refcount), page_refcount.shape[0],
+                                _ptr(rows), rows.shape[0], _ptr(status), _stream(stream)),
+           "pages_free")
+
+
+def pages_fork_workspace_bytes(num_rows, n) -> int:
+    return int(lib().phs_pages_fork_workspace_bytes(num_rows, n))
+
+
+def pages_fork(pools, block_table, seq_lens, page_refcount, src_rows, dst_rows, workspace=None,
+               status=None, stream=None):
+    """Continue row src_rows[i] in the free row dst_rows[i]: whole pages
+    shared, a partly filled last page copied into the lowest free page, in
+    every pool of `pools` (list of PagedPool sharing the block table)."""
+    _tables(block_table, seq_lens, page_refcount)
+    _need(src_rows, torch.int32, "src_rows", 1)
+    _need(dst_rows, torch.int32, "dst_rows", 1)
+    if src_rows.shape != dst_rows.shape:
+        raise ValueError("src_rows and dst_rows go together")
+    _opt(status, torch.int32, "status")
+    arr = _pools_of(pools, page_refcount)
+    rows, n = block_table.shape[0], src_rows.shape[0]
+    ws = _workspace(workspace, pages_fork_workspace_bytes(rows, n), block_table.device)
+    _same_device(block_table, seq_lens, page_refcount, src_rows, dst_rows, ws, status,
+                 *[t for p in pools for t in (p.k, p.v)])
+    _check(lib().phs_pages_fork(arr, len(pools), _ptr(block_table), rows, block_table.shape[1],
+                                _ptr(seq_lens), _ptr(page_refcount), _ptr(src_rows),
+                                _ptr(dst_rows), n, _ptr(ws), ws.numel(), _ptr(status),
+                                _stream(stream)), "pages_fork")
+
+
+def pages_compact_workspace_bytes(num_pages) -> int:
+    return int(lib().phs_pages_compact_workspace_bytes(num_pages))
+
+
+def pages_compact(pools, block_table, seq_lens, page_refcount, block_table_out=None,
+                  page_refcount_out=None, page_map=None, num_live=None, workspace=None,
+                  status=None, stream=None):
+    """Move the live pages to the lowest page ids in every pool of `pools`;
+    returns (page_map [num_pages]: new id or -1, num_live [1]).  The tables
+    and counts are rewritten in place unless *_out are given."""
+    _tables(block_table, seq_lens, page_refcount)
+    arr = _pools_of(pools, page_refcount)
+    bt = block_table if block_table_out is None else block_table_out
+    rc = page_refcount if page_refcount_out is None else page_refcount_out
+    if page_map is None:
+        page_map = torch.empty_like(page_refcount)
+    if num_live is None:
+        num_live = torch.empty(1, dtype=torch.int32, device=block_table.device)
+    for t, like, name in ((bt, block_table, "block_table_out"),
+                          (rc, page_refcount, "page_refcount_out"),
+                          (page_map, page_refcount, "page_map")):
+        _need(t, torch.int32, name, like.dim())
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must be {tuple(like.shape)}")
+    _need(num_live, torch.int32, "num_live", 1)
+    if num_live.shape[0] != 1:
+        raise ValueError("num_live must be [1]")
+    _opt(status, torch.int32, "status")
+    ws = _workspace(workspace, pages_compact_workspace_bytes(page_refcount.shape[0]),
+                    block_table.device)
+    _same_device(block_table, seq_lens, page_refcount, bt, rc, page_map, num_live, ws, status,
+                 *[t for p in pools for t in (p.k, p.v)])
+    _check(lib().phs_pages_compact(arr, len(pools), _ptr(block_table), block_table.shape[0],
+                                   block_table.shape[1], _ptr(seq_lens), _ptr(page_refcount),
+                                   _ptr(bt), _ptr(rc), _ptr(page_map), _ptr(num_live), _ptr(ws),
+                                   ws.numel(), _ptr(status), _stream(stream)), "pages_compact")
+    return page_map, num_live
+
+
+# --------------------------------------------------- differential attention --
+@dataclass
+class DiffWeights:
+    """Learned weights of a differential attention layer: lambda vectors
+    fp32 [D] (or [H, D], one per head) and, for the norm of each head's
+    output, fp32 [2D] (None: no norm)."""
+    lambda_q1: torch.Tensor
+    lambda_k1: torch.Tensor
+    lambda_q2: torch.Tensor
+    lambda_k2: torch.Tensor
+    lambda_init: float
+    norm_weight: torch.Tensor | None = None
+    norm_eps: float = 1e-5
+
+    def c(self, num_heads, head_dim):
+        vecs = (self.lambda_q1, self.lambda_k1, self.lambda_q2, self.lambda_k2)
+        per_head = self.lambda_q1.dim() == 2
+        want = (num_heads, head_dim) if per_head else (head_dim,)
+        for t in vecs:
+            _need(t, torch.float32, "lambda vectors")
+            if tuple(t.shape) != want:
+                raise ValueError(f"lambda vectors must be [{head_dim}] or "
+                                 f"[{num_heads}, {head_dim}], all alike")
+        _opt(self.norm_weight, torch.float32, "norm_weight", 1)
+        if self.norm_weight is not None and self.norm_weight.shape[0] != 2 * head_dim:
+            raise ValueError(f"norm_weight must be [{2 * head_dim}]")
+        return _lib.DiffWeightsC(*(t.data_ptr() for t in vecs),
+                                 0 if self.norm_weight is None else self.norm_weight.data_ptr(),
+                                 float(self.lambda_init), float(self.norm_eps), int(per_head))
+
+
+def diff_workspace_bytes(batch, num_heads, num_value_heads, head_dim, max_seq_len,
+                         tokens_per_split=0) -> int:
+    """Workspace bytes for attn_decode_diff_paged; 0 if unsupported."""
+    return int(lib().phs_diff_workspace_bytes(batch, num_heads, num_value_heads, head_dim,
+                                              max_seq_len, tokens_per_split))
+
+
+def attn_decode_diff_paged(q, pool: PagedPool, block_table, seq_lens, max_seq_len: int,
+                           weights: DiffWeights, softmax_scale=None, tokens_per_split=0, out=None,
+                           out_dtype=torch.bfloat16, workspace=None, k_new=None, v_new=None,
+                           page_refcount=None, status=None, stream=None):
+    """Differential attention decode: q [B, 2H, D] (rows 2i, 2i + 1: head i's
+    queries of the two maps), pool of 2 Hv heads of width D; returns out
+    [B, H, 2D].  k_new / v_new ([B, 2 Hv, D] bf16): append token
+    seq_lens[b] - 1 in the same call."""
+    _need(q, torch.bfloat16, "q", 3)
+    pc = pool.c()
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    _opt(status, torch.int32, "status")
+    B, H2, D = q.shape
+    heads = pool.k.shape[1]
+    if H2 % 2 != 0 or heads % 2 != 0:
+        raise ValueError("q and the pool need an even number of heads (two maps)")
+    if D != pool.k.shape[3]:
+        raise ValueError("q and the pool differ in head_dim")
+    if block_table.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("block_table and seq_lens need one row per request")
+    H = H2 // 2
+    if out is None:
+        out = torch.empty((B, H, 2 * D), dtype=out_dtype, device=q.device)
+    _need(out, out.dtype, "out", 3)
+    if tuple(out.shape) != (B, H, 2 * D):
+        raise ValueError("out must be [batch, H, 2 head_dim]")
+    _append_args(k_new, v_new, page_refcount, B, heads, D)
+    if page_refcount is not None and page_refcount.shape[0] != pool.k.shape[0]:
+        raise ValueError("page_refcount needs one entry per page")
+    wc = weights.c(H, D)
+    scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
+    ws = _workspace(workspace, diff_workspace_bytes(B, H, heads // 2, D, max_seq_len,
+                                                    tokens_per_split), q.device)
+    _same_device(q, pool.k, pool.v, block_table, seq_lens, out, ws, k_new, v_new, page_refcount,
+                 status, weights.lambda_q1, weights.lambda_k1, weights.lambda_q2,
+                 weights.lambda_k2, weights.norm_weight)
+    _check(lib().phs_attn_decode_diff_paged(
+        _ptr(q), H, ctypes.byref(pc), _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+        int(max_seq_len), B, ctypes.byref(wc), scale, int(tokens_per_split), _ptr(out),
+        _out_code(out.dtype), _ptr(ws), ws.numel(), _ptr(k_new), _ptr(v_new),
+        _ptr(page_refcount), _ptr(status), _stream(stream)), "attn_decode_diff_paged")
+    return out
+
+
+# --------------------------------------------------------- linear attention --
+@dataclass
+class StatePool:
+    """States of linear attention: s fp32 [num_states, Hkv, D (k), D (v)]."""
+    s: torch.Tensor
+
+    def c(self):
+        _need(self.s, torch.float32, "state.s", 4)
+        n, h, d, d2 = self.s.shape
+        if d != d2:
+            raise ValueError("state.s must be [num_states, Hkv, D, D]")
+        return _lib.StatePoolC(self.s.data_ptr(), n, h, d)
+
+    @staticmethod
+    def zeros(num_states, num_kv_heads, head_dim, device="cuda"):
+        return StatePool(torch.zeros((num_states, num_kv_heads, head_dim, head_dim),
+                                     dtype=torch.float32, device=device))
+
+
+def _linear_args(q, k, v, pool, log_decay, state_ids, batch, status):
+    pc = pool.c()
+    _need(q, torch.bfloat16, "q", 3)
+    Hkv, D = pool.s.shape[1], pool.s.shape[2]
+    for t, name in ((k, "k"), (v, "v")):
+        _need(t, torch.bfloat16, name, 3)
+        if tuple(t.shape) != (q.shape[0], Hkv, D):
+            raise ValueError(f"{name} must be [tokens, Hkv, head_dim]")
+    if q.shape[2] != D:
+        raise ValueError("q and the state pool differ in head_dim")
+    _need(log_decay, torch.float32, "log_decay", 1)
+    if log_decay.shape[0] != Hkv:
+        raise ValueError("log_decay must be [Hkv]")
+    _opt(state_ids, torch.int32, "state_ids", 1)
+    if state_ids is not None and state_ids.shape[0] != batch:
+        raise ValueError("state_ids must be [batch]")
+    _opt(status, torch.int32, "status")
+    return pc
+
+
+def _linear_out(out, q, dtype):
+    if out is None:
+        return torch.empty(q.shape, dtype=dtype, device=q.device)
+    _need(out, out.dtype, "out", 3)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    return out
+
+
+def linear_attn_decode(q, k_new, v_new, pool: StatePool, log_decay, state_ids=None, scale=None,
+                       out=None, out_dtype=torch.bfloat16, status=None, stream=None):
+    """One token of linear attention per request: q [B, Hq, D], k_new, v_new
+    [B, Hkv, D] bf16; updates the states and returns out [B, Hq, D]."""
+    B = q.shape[0]
+    pc = _linear_args(q, k_new, v_new, pool, log_decay, state_ids, B, status)
+    out = _linear_out(out, q, out_dtype)
+    _same_device(q, k_new, v_new, pool.s, log_decay, state_ids, out, status)
+    scale = 1.0 / math.sqrt(q.shape[2]) if scale is None else float(scale)
+    _check(lib().phs_linear_attn_decode(_ptr(q), q.shape[1], ctypes.byref(pc), _ptr(k_new),
+                                        _ptr(v_new), _ptr(log_decay), _ptr(state_ids), B, scale,
+                                        _ptr(out), _out_code(out.dtype), _ptr(status),
+                                        _stream(stream)), "linear_attn_decode")
+    return out
+
+
+def linear_prompt_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, total_tokens,
+                                  max_seq_len) -> int:
+    """Workspace bytes for linear_attn_prompt; 0 if unsupported."""
+    return int(lib().phs_linear_prompt_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim,
+                                                       total_tokens, max_seq_len))
+
+
+def linear_attn_prompt(q, k, v, cu_seqlens, max_seq_len: int, pool: StatePool, log_decay,
+                       state_ids=None, resume=None, scale=None, out=None, workspace=None,
+                       status=None, stream=None):
+    """Linear attention over packed prompts: request b has tokens
+    [cu_seqlens[b], cu_seqlens[b + 1]) of q [T, Hq, D] and k, v [T, Hkv, D]
+    bf16, starts from its state where resume[b] != 0 (else from zero) and
+    leaves its last state in the pool.  Returns out bf16 [T, Hq, D]; rows of
+    no request are left as they were (unset in an output made here)."""
+    _need(cu_seqlens, torch.int32, "cu_seqlens", 1)
+    B = cu_seqlens.shape[0] - 1
+    if B < 0:
+        raise ValueError("cu_seqlens must be [batch + 1]")
+    pc = _linear_args(q, k, v, pool, log_decay, state_ids, B, status)
+    _opt(resume, torch.int32, "resume", 1)
+    if resume is not None and resume.shape[0] != B:
+        raise ValueError("resume must be [batch]")
+    out = _linear_out(out, q, torch.bfloat16)
+    if out.dtype != torch.bfloat16:
+        raise ValueError("out must be bfloat16")
+    T, Hq, D = q.shape
+    ws = _workspace(workspace, linear_prompt_workspace_bytes(B, Hq, pool.s.shape[1], D, T,
+                                                             max_seq_len), q.device)
+    _same_device(q, k, v, cu_seqlens, pool.s, log_decay, state_ids, resume, out, ws, status)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    _check(lib().phs_linear_attn_prompt(_ptr(q), Hq, _ptr(k), _ptr(v), _ptr(cu_seqlens), T,
+                                        int(max_seq_len), ctypes.byref(pc), _ptr(state_ids),
+                                        _ptr(resume), _ptr(log_decay), B, scale, _ptr(out),
+                                        _ptr(ws), ws.numel(), _ptr(status), _stream(stream)),
+           "linear_attn_prompt")
+    return out

@@ -39,6 +39,16 @@ class LayerC(ctypes.Structure):
                 ("paged", PagedPoolC), ("ring", RingPoolC)]
 
 
+class DiffWeightsC(ctypes.Structure):
+    _fields_ = [("lambda_q1", c_vp), ("lambda_k1", c_vp), ("lambda_q2", c_vp),
+                ("lambda_k2", c_vp), ("norm_weight", c_vp), ("lambda_init", c_f32),
+                ("norm_eps", c_f32), ("lambda_per_head", c_i32)]
+
+
+class StatePoolC(ctypes.Structure):
+    _fields_ = [("s", c_vp), ("num_states", c_i64), ("num_kv_heads", c_i32), ("head_dim", c_i32)]
+
+
 _P = ctypes.POINTER
 _SIGS = {
     "phs_version": (c_i32, []),
@@ -84,6 +94,27 @@ _SIGS = {
     "phs_copy_d2d": (ctypes.c_int, [c_vp, c_vp, c_size, c_vp]),
     "phs_read_checksum": (ctypes.c_int, [c_vp, c_size, c_vp, c_vp]),
     "phs_copy_pages": (ctypes.c_int, [_P(PagedPoolC), c_vp, c_vp, c_i32, c_vp, c_vp]),
+    "phs_pages_free": (ctypes.c_int, [c_vp, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp,
+                                      c_vp]),
+    "phs_pages_fork_workspace_bytes": (c_size, [c_i32, c_i32]),
+    "phs_pages_fork": (ctypes.c_int, [_P(PagedPoolC), c_i32, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp,
+                                      c_vp, c_i32, c_vp, c_size, c_vp, c_vp]),
+    "phs_pages_compact_workspace_bytes": (c_size, [c_i64]),
+    "phs_pages_compact": (ctypes.c_int, [_P(PagedPoolC), c_i32, c_vp, c_i32, c_i32, c_vp, c_vp,
+                                         c_vp, c_vp, c_vp, c_vp, c_vp, c_size, c_vp, c_vp]),
+    "phs_diff_workspace_bytes": (c_size, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32]),
+    "phs_attn_decode_diff_paged": (ctypes.c_int, [c_vp, c_i32, _P(PagedPoolC), c_vp, c_i32, c_vp,
+                                                  c_i32, c_i32, _P(DiffWeightsC), c_f32, c_i32,
+                                                  c_vp, c_i32, c_vp, c_size, c_vp, c_vp, c_vp,
+                                                  c_vp, c_vp]),
+    "phs_linear_attn_decode": (ctypes.c_int, [c_vp, c_i32, _P(StatePoolC), c_vp, c_vp, c_vp, c_vp,
+                                              c_i32, c_f32, c_vp, c_i32, c_vp, c_vp]),
+    "phs_linear_prompt_workspace_bytes": (c_size, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32]),
+    "phs_linear_attn_prompt": (ctypes.c_int, [c_vp, c_i32, c_vp, c_vp, c_vp, c_i32, c_i32,
+                                              _P(StatePoolC), c_vp, c_vp, c_vp, c_i32, c_f32, c_vp,
+                                              c_vp, c_size, c_vp, c_vp]),
+    "phs_page_load_refcounts": (ctypes.c_int, [c_vp, c_vp]),
+    "phs_radix_remap": (ctypes.c_int, [c_vp, c_vp, c_i64]),
     "phs_page_allocator_create": (c_vp, [c_i64]),
     "phs_page_allocator_destroy": (None, [c_vp]),
     "phs_page_alloc": (ctypes.c_int, [c_vp, c_i32, c_vp]),

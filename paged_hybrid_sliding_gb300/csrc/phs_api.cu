@@ -11,6 +11,7 @@
 #include <utility>
 
 #include "phs_internal.h"
+#include "phs_ops.h"
 
 namespace phs {
 
@@ -1402,3 +1403,326 @@ extern "C" int phs_attn_decode_full_paged_noalloc(
   if (c.pl.max_splits == 1) return PHS_OK;  // every request finished in its only split
   return launch_merge(c.pl.D, c.m, batch, s);
 }
+
+// ------------------------------------------------------ page operations --
+namespace {
+
+int check_tables(const void* block_table, const void* seq_lens, int32_t num_rows,
+                 int32_t max_pages) {
+  if (!block_table || !seq_lens) return PHS_EINVAL;
+  if (num_rows <= 0 || max_pages <= 0) return PHS_EINVAL;
+  // lengths in tokens are int32
+  return max_pages > INT32_MAX / kPage ? PHS_EUNSUPPORTED : PHS_OK;
+}
+
+// The pools of a page operation, in launches of up to kPagesMaxLayers.
+int check_pools(const phs_paged_pool* pools, int32_t num_layers) {
+  if (!pools || num_layers <= 0) return PHS_EINVAL;
+  for (int32_t l = 0; l < num_layers; ++l) {
+    const int st = check_paged(pools + l);
+    if (st) return st;
+    if (pools[l].num_pages != pools[0].num_pages ||
+        pools[l].num_kv_heads != pools[0].num_kv_heads ||
+        pools[l].head_dim != pools[0].head_dim)
+      return PHS_ESHAPE;
+  }
+  return PHS_OK;
+}
+
+int copy_in_pools(const phs_paged_pool* pools, int32_t num_layers, const int32_t* src,
+                  const int32_t* dst, const int32_t* n_dev, int64_t n, cudaStream_t s) {
+  DevInfo di;
+  int st = dev_info(di);
+  for (int32_t l0 = 0; !st && l0 < num_layers; l0 += kPagesMaxLayers) {
+    PagePools p;
+    std::memset(&p, 0, sizeof(p));
+    p.num_layers = std::min(num_layers - l0, kPagesMaxLayers);
+    p.page_vecs = pools[0].num_kv_heads * kPage * pools[0].head_dim * 2 / 16;
+    for (int l = 0; l < p.num_layers; ++l) {
+      p.k[l] = reinterpret_cast<uint4*>(pools[l0 + l].k);
+      p.v[l] = reinterpret_cast<uint4*>(pools[l0 + l].v);
+    }
+    st = launch_pages_copy(p, src, dst, n_dev, n, di.sms, s);
+  }
+  return st;
+}
+
+// Consecutive 256-byte-aligned int32 arrays of a workspace.
+struct Carve {
+  char* at;
+  size_t used = 0;
+  int32_t* take(int64_t n) {
+    int32_t* p = reinterpret_cast<int32_t*>(at + used);
+    used += align256(static_cast<size_t>(n) * sizeof(int32_t));
+    return p;
+  }
+};
+
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (!workspace || bytes < need) return PHS_EWORKSPACE;
+  return (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ? PHS_EALIGN : PHS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int phs_pages_free(const int32_t* block_table, int32_t num_rows, int32_t max_pages_per_seq,
+                   int32_t* seq_lens, int32_t* page_refcount, int64_t num_pages,
+                   const int32_t* rows, int32_t n, int32_t* dev_status, void* stream) {
+  const int st = check_tables(block_table, seq_lens, num_rows, max_pages_per_seq);
+  if (st) return st;
+  if (!page_refcount || num_pages <= 0 || num_pages > INT32_MAX || n < 0 || (n > 0 && !rows))
+    return PHS_EINVAL;
+  if (n == 0) return PHS_OK;
+  const PageFreeArgs a{block_table, seq_lens, page_refcount,     rows, dev_status,
+                       num_pages,   num_rows, max_pages_per_seq, n};
+  return launch_pages_free(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t phs_pages_fork_workspace_bytes(int32_t num_rows, int32_t n) {
+  if (num_rows <= 0 || n < 0) return 0;
+  return 2 * align256(static_cast<size_t>(num_rows) * 4) + 4 * align256(static_cast<size_t>(n) * 4);
+}
+
+int phs_pages_fork(const phs_paged_pool* pools, int32_t num_layers, int32_t* block_table,
+                   int32_t num_rows, int32_t max_pages_per_seq, int32_t* seq_lens,
+                   int32_t* page_refcount, const int32_t* src_rows, const int32_t* dst_rows,
+                   int32_t n, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                   void* stream) {
+  int st = check_pools(pools, num_layers);
+  if (st) return st;
+  if ((st = check_tables(block_table, seq_lens, num_rows, max_pages_per_seq))) return st;
+  if (!page_refcount || n < 0 || (n > 0 && (!src_rows || !dst_rows))) return PHS_EINVAL;
+  if (n == 0) return PHS_OK;
+  if ((st = check_workspace(workspace, workspace_bytes,
+                            phs_pages_fork_workspace_bytes(num_rows, n))))
+    return st;
+  PageForkArgs a;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.refcount = page_refcount;
+  a.src_rows = src_rows;
+  a.dst_rows = dst_rows;
+  a.status = dev_status;
+  a.num_pages = pools[0].num_pages;
+  a.num_rows = num_rows;
+  a.max_pages = max_pages_per_seq;
+  a.n = n;
+  Carve ws{reinterpret_cast<char*>(workspace)};
+  a.first_dst = ws.take(num_rows);
+  a.is_src = ws.take(num_rows);
+  a.rank = ws.take(n);
+  a.fresh = ws.take(n);
+  a.copy_src = ws.take(n);
+  a.copy_dst = ws.take(n);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = launch_pages_fork_plan(a, s))) return st;
+  if ((st = launch_pages_fork_share(a, s))) return st;
+  return copy_in_pools(pools, num_layers, a.copy_src, a.copy_dst, nullptr, n, s);
+}
+
+size_t phs_pages_compact_workspace_bytes(int64_t num_pages) {
+  if (num_pages <= 0 || num_pages > INT32_MAX) return 0;
+  return 3 * align256(static_cast<size_t>(num_pages) * 4) + 256;
+}
+
+int phs_pages_compact(const phs_paged_pool* pools, int32_t num_layers,
+                      const int32_t* block_table, int32_t num_rows, int32_t max_pages_per_seq,
+                      const int32_t* seq_lens, const int32_t* page_refcount,
+                      int32_t* block_table_out, int32_t* page_refcount_out, int32_t* page_map,
+                      int32_t* num_live, void* workspace, size_t workspace_bytes,
+                      int32_t* dev_status, void* stream) {
+  int st = check_pools(pools, num_layers);
+  if (st) return st;
+  if ((st = check_tables(block_table, seq_lens, num_rows, max_pages_per_seq))) return st;
+  if (!page_refcount || !block_table_out || !page_refcount_out || !page_map || !num_live)
+    return PHS_EINVAL;
+  if ((st = check_workspace(workspace, workspace_bytes,
+                            phs_pages_compact_workspace_bytes(pools[0].num_pages))))
+    return st;
+  PageCompactArgs a;
+  a.block_table = block_table;
+  a.block_table_out = block_table_out;
+  a.seq_lens = seq_lens;
+  a.refcount = page_refcount;
+  a.refcount_out = page_refcount_out;
+  a.page_map = page_map;
+  a.num_live = num_live;
+  a.status = dev_status;
+  a.num_pages = pools[0].num_pages;
+  a.num_rows = num_rows;
+  a.max_pages = max_pages_per_seq;
+  Carve ws{reinterpret_cast<char*>(workspace)};
+  a.move = ws.take(a.num_pages);
+  a.movers = ws.take(a.num_pages);
+  a.holes = ws.take(a.num_pages);
+  a.meta = ws.take(2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = launch_pages_compact_plan(a, s))) return st;
+  if ((st = launch_pages_compact_tables(a, s))) return st;
+  return copy_in_pools(pools, num_layers, a.movers, a.holes, a.meta + 1, 0, s);
+}
+
+// ------------------------------------------------ differential attention --
+size_t phs_diff_workspace_bytes(int32_t batch, int32_t num_heads, int32_t num_value_heads,
+                                int32_t head_dim, int32_t max_seq_len,
+                                int32_t tokens_per_split) {
+  DecodePlan pl;
+  if (make_plan(pl, batch, num_heads, num_value_heads, head_dim, max_seq_len, tokens_per_split,
+                false))
+    return 0;
+  return 256;
+}
+
+int phs_attn_decode_diff_paged(const void* q, int32_t num_heads, const phs_paged_pool* pool,
+                               const int32_t* block_table, int32_t max_pages_per_seq,
+                               const int32_t* seq_lens, int32_t max_seq_len, int32_t batch,
+                               const phs_diff_weights* weights, float softmax_scale,
+                               int32_t tokens_per_split, void* out, int32_t out_dtype,
+                               void* workspace, size_t workspace_bytes, const void* k_new,
+                               const void* v_new, const int32_t* page_refcount,
+                               int32_t* dev_status, void* stream) {
+  int st = check_paged(pool);
+  if (st) return st;
+  if (!q || !block_table || !seq_lens || !out || !weights) return PHS_EINVAL;
+  if (!weights->lambda_q1 || !weights->lambda_k1 || !weights->lambda_q2 || !weights->lambda_k2)
+    return PHS_EINVAL;
+  if (!std::isfinite(weights->lambda_init) || !(weights->norm_eps >= 0.f) ||
+      !std::isfinite(weights->norm_eps))
+    return PHS_EINVAL;
+  if ((k_new == nullptr) != (v_new == nullptr)) return PHS_EINVAL;
+  if (k_new && (!aligned16(k_new) || !aligned16(v_new))) return PHS_EALIGN;
+  if (max_pages_per_seq <= 0 || !(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
+    return PHS_EINVAL;
+  if (out_dtype != PHS_OUT_BF16 && out_dtype != PHS_OUT_F32) return PHS_EINVAL;
+  if (pool->num_kv_heads % 2 != 0) return PHS_ESHAPE;
+  const int Hv = pool->num_kv_heads / 2, D = pool->head_dim;
+  DecodePlan pl;
+  if ((st = make_plan(pl, batch, num_heads, Hv, D, max_seq_len, tokens_per_split, false)))
+    return st;
+  if ((st = check_workspace(workspace, workspace_bytes,
+                            phs_diff_workspace_bytes(batch, num_heads, Hv, D, max_seq_len,
+                                                     tokens_per_split))))
+    return st;
+  if (!aligned16(q) || !aligned16(out)) return PHS_EALIGN;
+  if (k_new) {
+    if ((st = phs_kv_append_paged(pool, k_new, v_new, block_table, max_pages_per_seq, seq_lens,
+                                  batch, page_refcount, dev_status, stream)))
+      return st;
+  }
+  DiffArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.k = reinterpret_cast<const __nv_bfloat16*>(pool->k);
+  a.v = reinterpret_cast<const __nv_bfloat16*>(pool->v);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.status = dev_status;
+  a.num_pages = pool->num_pages;
+  a.H = num_heads;
+  a.Hv = Hv;
+  a.G = num_heads / Hv;
+  a.max_pages = max_pages_per_seq;
+  a.n_clamp = static_cast<int>(std::min<long long>(max_seq_len, 1LL * max_pages_per_seq * kPage));
+  a.out_f32 = out_dtype == PHS_OUT_F32;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.lambda_q1 = weights->lambda_q1;
+  a.lambda_k1 = weights->lambda_k1;
+  a.lambda_q2 = weights->lambda_q2;
+  a.lambda_k2 = weights->lambda_k2;
+  a.norm_weight = weights->norm_weight;
+  a.lambda_init = weights->lambda_init;
+  a.norm_eps = weights->norm_eps;
+  a.lambda_per_head = weights->lambda_per_head != 0;
+  return launch_diff_decode(D, a, batch, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------ linear attention --
+namespace {
+
+int linear_args(LinearArgs& a, const void* q, int32_t num_q_heads, const void* k, const void* v,
+                const phs_state_pool* pool, const int32_t* state_ids, const float* log_decay,
+                int32_t batch, int32_t tokens, float scale, void* out, int32_t out_dtype,
+                int32_t* dev_status) {
+  if (!pool || !pool->s || pool->num_states <= 0 || pool->num_kv_heads <= 0) return PHS_EINVAL;
+  if (!log_decay || batch < 0 || tokens < 0 || !std::isfinite(scale)) return PHS_EINVAL;
+  if (tokens > 0 && (!q || !k || !v || !out)) return PHS_EINVAL;
+  if (out_dtype != PHS_OUT_BF16 && out_dtype != PHS_OUT_F32) return PHS_EINVAL;
+  const int st = check_dims(num_q_heads, pool->num_kv_heads, pool->head_dim);
+  if (st) return st;
+  if (pool->num_kv_heads > 65535) return PHS_EUNSUPPORTED;  // grid y
+  if (!state_ids && batch > pool->num_states) return PHS_ESHAPE;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(pool->s))
+    return PHS_EALIGN;
+  std::memset(&a, 0, sizeof(a));
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  a.v = reinterpret_cast<const __nv_bfloat16*>(v);
+  a.state = pool->s;
+  a.log_decay = log_decay;
+  a.state_ids = state_ids;
+  a.out = out;
+  a.status = dev_status;
+  a.num_states = pool->num_states;
+  a.Hq = num_q_heads;
+  a.Hkv = pool->num_kv_heads;
+  a.G = num_q_heads / pool->num_kv_heads;
+  a.B = batch;
+  a.out_f32 = out_dtype == PHS_OUT_F32;
+  a.scale = scale;
+  return PHS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int phs_linear_attn_decode(const void* q, int32_t num_q_heads, const phs_state_pool* pool,
+                           const void* k_new, const void* v_new, const float* log_decay,
+                           const int32_t* state_ids, int32_t batch, float scale, void* out,
+                           int32_t out_dtype, int32_t* dev_status, void* stream) {
+  LinearArgs a;
+  const int st = linear_args(a, q, num_q_heads, k_new, v_new, pool, state_ids, log_decay, batch,
+                             batch, scale, out, out_dtype, dev_status);
+  if (st || batch == 0) return st;
+  return launch_linear_decode(pool->head_dim, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t phs_linear_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads,
+                                         int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t total_tokens, int32_t max_seq_len) {
+  if (batch < 0 || total_tokens < 0 || max_seq_len < 0 ||
+      check_dims(num_q_heads, num_kv_heads, head_dim))
+    return 0;
+  return 256;
+}
+
+int phs_linear_attn_prompt(const void* q, int32_t num_q_heads, const void* k, const void* v,
+                           const int32_t* cu_seqlens, int32_t total_tokens, int32_t max_seq_len,
+                           const phs_state_pool* pool, const int32_t* state_ids,
+                           const int32_t* resume, const float* log_decay, int32_t batch,
+                           float scale, void* out, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_status, void* stream) {
+  LinearArgs a;
+  int st = linear_args(a, q, num_q_heads, k, v, pool, state_ids, log_decay, batch,
+                       total_tokens, scale, out, PHS_OUT_BF16, dev_status);
+  if (st) return st;
+  if (!cu_seqlens || max_seq_len < 0) return PHS_EINVAL;
+  if (batch == 0) return PHS_OK;
+  if ((st = check_workspace(workspace, workspace_bytes,
+                            phs_linear_prompt_workspace_bytes(batch, num_q_heads,
+                                                              pool->num_kv_heads, pool->head_dim,
+                                                              total_tokens, max_seq_len))))
+    return st;
+  a.cu_seqlens = cu_seqlens;
+  a.resume = resume;
+  a.total_tokens = total_tokens;
+  a.max_seq = max_seq_len;
+  return launch_linear_prompt(pool->head_dim, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

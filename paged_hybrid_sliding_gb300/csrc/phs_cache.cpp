@@ -125,6 +125,18 @@ int phs_page_refcounts(phs_page_allocator* a, int32_t* out) {
   return PHS_OK;
 }
 
+int phs_page_load_refcounts(phs_page_allocator* a, const int32_t* counts) {
+  if (!a || !counts) return PHS_EINVAL;
+  std::lock_guard<std::mutex> lock(a->mu);
+  const size_t n = a->rc.size();
+  if (std::any_of(counts, counts + n, [](int32_t c) { return c < 0; })) return PHS_EINVAL;
+  a->rc.assign(counts, counts + n);
+  a->free_list.clear();
+  for (size_t p = n; p-- > 0;)  // the lowest free page is handed out first
+    if (counts[p] == 0) a->free_list.push_back(static_cast<int32_t>(p));
+  return PHS_OK;
+}
+
 int phs_page_cow(phs_page_allocator* a, int32_t page, int32_t* out_page) {
   if (!a || !out_page) return PHS_EINVAL;
   std::lock_guard<std::mutex> lock(a->mu);
@@ -470,6 +482,28 @@ int phs_radix_evict(phs_radix_tree* t, int64_t pages, int64_t* out_freed) {
         std::vector<int32_t>(victim->tokens.begin(), victim->tokens.begin() + t->P));
   }
   *out_freed = freed;
+  return PHS_OK;
+}
+
+int phs_radix_remap(phs_radix_tree* t, const int32_t* page_map, int64_t num_pages) {
+  if (!t || !page_map || num_pages <= 0) return PHS_EINVAL;
+  std::lock_guard<std::mutex> lock(t->mu);
+  {
+    std::lock_guard<std::mutex> alock(t->alloc->mu);
+    if (static_cast<size_t>(num_pages) != t->alloc->rc.size()) return PHS_ESHAPE;
+  }
+  std::vector<Node*> nodes, stack{&t->root};
+  while (!stack.empty()) {
+    Node* n = stack.back();
+    stack.pop_back();
+    nodes.push_back(n);
+    for (auto& kv : n->children) stack.push_back(kv.second.get());
+    for (int32_t p : n->pages)
+      if (p < 0 || p >= num_pages || page_map[p] < 0 || page_map[p] >= num_pages)
+        return PHS_ERANGE;
+  }
+  for (Node* n : nodes)
+    for (int32_t& p : n->pages) p = page_map[p];
   return PHS_OK;
 }
 

@@ -1,0 +1,126 @@
+// phs_ops.h -- argument blocks and launchers of the page operations
+// (phs_pages.cu), differential attention (phs_diff.cu) and linear attention
+// (phs_linear.cu), shared with the C-ABI front end (phs_api.cu).
+#pragma once
+
+#include "phs_internal.h"
+
+namespace phs {
+
+// ------------------------------------------------------ page operations --
+constexpr int kPagesMaxLayers = 64;  // pools per launch
+
+struct PagePools {
+  uint4* k[kPagesMaxLayers];
+  uint4* v[kPagesMaxLayers];
+  int num_layers;
+  int page_vecs;  // 16-byte vectors of one page of K (and of V), a multiple of 128
+};
+
+struct PageFreeArgs {
+  const int32_t* block_table;
+  int32_t* seq_lens;
+  int32_t* refcount;
+  const int32_t* rows;
+  int32_t* status;
+  int64_t num_pages;
+  int num_rows, max_pages, n;
+};
+
+struct PageForkArgs {
+  int32_t* block_table;
+  int32_t* seq_lens;
+  int32_t* refcount;
+  const int32_t* src_rows;
+  const int32_t* dst_rows;
+  int32_t* status;
+  int64_t num_pages;
+  int num_rows, max_pages, n;
+  // workspace
+  int32_t* first_dst;  // [num_rows] first entry that names the row as its destination
+  int32_t* is_src;     // [num_rows]
+  int32_t* rank;       // [n] rank among the entries that need a fresh page, -1 none, -2 refused
+  int32_t* fresh;      // [n] the lowest free pages, ascending
+  int32_t* copy_src;   // [n] page to copy, or -1
+  int32_t* copy_dst;   // [n]
+};
+
+struct PageCompactArgs {
+  const int32_t* block_table;
+  int32_t* block_table_out;
+  const int32_t* seq_lens;
+  const int32_t* refcount;
+  int32_t* refcount_out;
+  int32_t* page_map;
+  int32_t* num_live;
+  int32_t* status;
+  int64_t num_pages;
+  int num_rows, max_pages;
+  // workspace
+  int32_t* move;    // [num_pages] -1 free, -2 stays, m >= 0: the m-th highest moving page
+  int32_t* movers;  // [num_pages] page that is m-th from the top
+  int32_t* holes;   // [num_pages] m-th lowest hole
+  int32_t* meta;    // [2] live pages, moves
+};
+
+int launch_pages_free(const PageFreeArgs& a, cudaStream_t stream);
+int launch_pages_fork_plan(const PageForkArgs& a, cudaStream_t stream);
+int launch_pages_fork_share(const PageForkArgs& a, cudaStream_t stream);
+int launch_pages_compact_plan(const PageCompactArgs& a, cudaStream_t stream);
+int launch_pages_compact_tables(const PageCompactArgs& a, cudaStream_t stream);
+// pages src[i] -> dst[i] (i < *n_dev, or i < n where n_dev is null; negative
+// src: none) of every pool
+int launch_pages_copy(const PagePools& p, const int32_t* src, const int32_t* dst,
+                      const int32_t* n_dev, int64_t n, int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------ differential attention --
+struct DiffArgs {
+  const __nv_bfloat16* q;  // [B][2H][D]
+  const __nv_bfloat16* k;  // [num_pages][2Hv][16][D]
+  const __nv_bfloat16* v;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  void* out;               // [B][H][2D]
+  int32_t* status;
+  int64_t num_pages;
+  int H, Hv, G;
+  int max_pages;
+  int n_clamp;
+  int out_f32;
+  float scale_log2;
+  // weights
+  const float* lambda_q1;  // [D], or [H][D] where lambda_per_head
+  const float* lambda_k1;
+  const float* lambda_q2;
+  const float* lambda_k2;
+  const float* norm_weight;  // [2D] or null
+  float lambda_init, norm_eps;
+  int lambda_per_head;
+};
+
+int launch_diff_decode(int D, const DiffArgs& a, int B, cudaStream_t stream);
+
+// ------------------------------------------------------ linear attention --
+struct LinearArgs {
+  const __nv_bfloat16* q;  // [tokens][Hq][D]
+  const __nv_bfloat16* k;  // [tokens][Hkv][D]
+  const __nv_bfloat16* v;
+  float* state;            // [num_states][Hkv][D][D]
+  const float* log_decay;  // [Hkv]
+  const int32_t* state_ids;  // null: identity
+  void* out;               // [tokens][Hq][D]
+  int32_t* status;
+  int64_t num_states;
+  int Hq, Hkv, G, B;
+  int out_f32;
+  float scale;
+  // prompt
+  const int32_t* cu_seqlens;  // [B + 1]
+  const int32_t* resume;      // [B] or null: from a zero state
+  int total_tokens, max_seq;
+};
+
+int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream);
+int launch_linear_prompt(int D, const LinearArgs& a, cudaStream_t stream);
+
+}  // namespace phs
