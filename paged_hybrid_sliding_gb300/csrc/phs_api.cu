@@ -87,12 +87,12 @@ EncodeTiledFn encode_fn() {
 
 // bf16 pool viewed as a 2-D tensor of `rows` rows of D elements; boxes of
 // 16 rows x 64 columns (128 bytes) with the 128-byte swizzle.
-int map_bf16_rows(CUtensorMap* m, const void* base, int64_t rows, int D) {
+int map_bf16_rows(CUtensorMap* m, const void* base, int64_t rows, int D, uint32_t box_rows = 16) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return PHS_ECUDA;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * 2};
-  cuuint32_t box[2] = {64, 16};
+  cuuint32_t box[2] = {64, box_rows};
   cuuint32_t es[2] = {1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
                    box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -104,12 +104,12 @@ int map_bf16_rows(CUtensorMap* m, const void* base, int64_t rows, int D) {
 // halves} (strides 256 B, 128 B): one box of {64, 16, 2} fetches a whole
 // 16-row page block as [half][16 rows][128 B] with the 128-byte swizzle --
 // one 4 KB copy instead of two 2 KB ones (the copy engine's cost is per box).
-int map_bf16_pages3d(CUtensorMap* m, const void* base, int64_t rows) {
+int map_bf16_pages3d(CUtensorMap* m, const void* base, int64_t rows, uint32_t box_rows = 16) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return PHS_ECUDA;
   cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), 2};
   cuuint64_t strides[2] = {256, 128};
-  cuuint32_t box[3] = {64, 16, 2};
+  cuuint32_t box[3] = {64, box_rows, 2};
   cuuint32_t es[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
                    box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -120,8 +120,10 @@ int map_bf16_pages3d(CUtensorMap* m, const void* base, int64_t rows) {
 // Map for the per-page K/V copies of the decode kernels: one 3-D box per
 // 16-row block when D = 128, two 2-D boxes of 64 columns otherwise (D = 64:
 // one box).  Both land as [column half][16 rows][128 B] in shared memory.
-int map_bf16_kv(CUtensorMap* m, const void* base, int64_t rows, int D) {
-  return D == 128 ? map_bf16_pages3d(m, base, rows) : map_bf16_rows(m, base, rows, D);
+// (box_rows 32: two neighbouring heads of a page at once).
+int map_bf16_kv(CUtensorMap* m, const void* base, int64_t rows, int D, uint32_t box_rows = 16) {
+  return D == 128 ? map_bf16_pages3d(m, base, rows, box_rows)
+                  : map_bf16_rows(m, base, rows, D, box_rows);
 }
 
 // int8 codes, rows of D bytes; boxes of 32 rows x D with the 128-byte
@@ -1565,6 +1567,25 @@ int phs_pages_compact(const phs_paged_pool* pools, int32_t num_layers,
 }
 
 // ------------------------------------------------ differential attention --
+}  // extern "C"
+
+namespace {
+
+static_assert(kDiffMaxSplit == kMaxSplitTokens, "the split kernel's chunk lists");
+
+// Partials of a split: one 2D-wide row and one (max, sum) for each map of
+// each head.  A call that needs none (one split) still takes a workspace.
+size_t diff_rows(const DecodePlan& pl, int B) {
+  return static_cast<size_t>(B) * pl.Hkv * pl.max_splits * pl.G * 2;
+}
+size_t diff_o_bytes(const DecodePlan& pl, int B) {
+  return align256(diff_rows(pl, B) * 2 * pl.D * sizeof(float));
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t phs_diff_workspace_bytes(int32_t batch, int32_t num_heads, int32_t num_value_heads,
                                 int32_t head_dim, int32_t max_seq_len,
                                 int32_t tokens_per_split) {
@@ -1572,7 +1593,7 @@ size_t phs_diff_workspace_bytes(int32_t batch, int32_t num_heads, int32_t num_va
   if (make_plan(pl, batch, num_heads, num_value_heads, head_dim, max_seq_len, tokens_per_split,
                 false))
     return 0;
-  return 256;
+  return diff_o_bytes(pl, batch) + align256(diff_rows(pl, batch) * 2 * sizeof(float));
 }
 
 int phs_attn_decode_diff_paged(const void* q, int32_t num_heads, const phs_paged_pool* pool,
@@ -1606,19 +1627,21 @@ int phs_attn_decode_diff_paged(const void* q, int32_t num_heads, const phs_paged
                                                      tokens_per_split))))
     return st;
   if (!aligned16(q) || !aligned16(out)) return PHS_EALIGN;
-  if (k_new) {
-    if ((st = phs_kv_append_paged(pool, k_new, v_new, block_table, max_pages_per_seq, seq_lens,
-                                  batch, page_refcount, dev_status, stream)))
-      return st;
-  }
   DiffArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
-  a.k = reinterpret_cast<const __nv_bfloat16*>(pool->k);
-  a.v = reinterpret_cast<const __nv_bfloat16*>(pool->v);
+  a.k = reinterpret_cast<__nv_bfloat16*>(pool->k);
+  a.v = reinterpret_cast<__nv_bfloat16*>(pool->v);
+  a.k_new = reinterpret_cast<const __nv_bfloat16*>(k_new);
+  a.v_new = reinterpret_cast<const __nv_bfloat16*>(v_new);
   a.block_table = block_table;
   a.seq_lens = seq_lens;
+  a.page_refcount = page_refcount;
   a.out = out;
+  a.ws_o = reinterpret_cast<float*>(workspace);
+  a.ws_ml = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + diff_o_bytes(pl, batch));
+  a.T = pl.T;
+  a.max_splits = pl.max_splits;
   a.status = dev_status;
   a.num_pages = pool->num_pages;
   a.H = num_heads;
@@ -1636,7 +1659,11 @@ int phs_attn_decode_diff_paged(const void* q, int32_t num_heads, const phs_paged
   a.lambda_init = weights->lambda_init;
   a.norm_eps = weights->norm_eps;
   a.lambda_per_head = weights->lambda_per_head != 0;
-  return launch_diff_decode(D, a, batch, reinterpret_cast<cudaStream_t>(stream));
+  CUtensorMap tk, tv;
+  const int64_t rows = pool->num_pages * pool->num_kv_heads * kPage;
+  if ((st = map_bf16_kv(&tk, pool->k, rows, D, 2 * kPage))) return st;
+  if ((st = map_bf16_kv(&tv, pool->v, rows, D, 2 * kPage))) return st;
+  return launch_diff_decode(D, tk, tv, a, batch, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

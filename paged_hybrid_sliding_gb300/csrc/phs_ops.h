@@ -74,20 +74,29 @@ int launch_pages_copy(const PagePools& p, const int32_t* src, const int32_t* dst
                       const int32_t* n_dev, int64_t n, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------ differential attention --
+constexpr int kDiffMaxSplit = 4096;  // tokens
+
 struct DiffArgs {
   const __nv_bfloat16* q;  // [B][2H][D]
-  const __nv_bfloat16* k;  // [num_pages][2Hv][16][D]
-  const __nv_bfloat16* v;
+  __nv_bfloat16* k;        // [num_pages][2Hv][16][D]
+  __nv_bfloat16* v;
+  const __nv_bfloat16* k_new;  // [B][2Hv][D], or null: no append
+  const __nv_bfloat16* v_new;
   const int32_t* block_table;
   const int32_t* seq_lens;
+  const int32_t* page_refcount;  // or null
   void* out;               // [B][H][2D]
+  float* ws_o;             // [B][Hv][max_splits][G][map][2D]
+  float* ws_ml;            // [B][Hv][max_splits][G][map][max, sum]
   int32_t* status;
   int64_t num_pages;
   int H, Hv, G;
   int max_pages;
-  int n_clamp;
+  int n_clamp;             // lengths above this are an error and clamped
+  int T;                   // tokens per split (multiple of 32)
+  int max_splits;
   int out_f32;
-  float scale_log2;
+  float scale_log2;        // softmax_scale * log2(e)
   // weights
   const float* lambda_q1;  // [D], or [H][D] where lambda_per_head
   const float* lambda_k1;
@@ -98,7 +107,8 @@ struct DiffArgs {
   int lambda_per_head;
 };
 
-int launch_diff_decode(int D, const DiffArgs& a, int B, cudaStream_t stream);
+int launch_diff_decode(int D, const CUtensorMap& tk, const CUtensorMap& tv, const DiffArgs& a,
+                       int B, cudaStream_t stream);
 
 // ------------------------------------------------------ linear attention --
 struct LinearArgs {
