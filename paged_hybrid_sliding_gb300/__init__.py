@@ -49,7 +49,7 @@ class PhsError(RuntimeError):
 
 
 def lib():
-    return _lib.load()
+    return _lib._lib or _lib.load()
 
 
 def _check(code: int, what: str):
@@ -58,10 +58,13 @@ def _check(code: int, what: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, dtype, name, dims=None):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() \
+            and (dims is None or t.dim() == dims):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -80,8 +83,9 @@ def _opt(t, dtype, name, dims=None):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle: making a Stream object for it costs a small call 3 us
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None \
+        else stream.cuda_stream
 
 
 def _out_code(dtype):
@@ -764,9 +768,14 @@ def window_safe_len(swa_valid, match_len: int, window: int, align: int = 1) -> i
 # ---------------------------------------------------------- page operations --
 def _same_device(first, *others):
     """The tensors of one call live on the device that the call runs on."""
-    if first.device.index != torch.cuda.current_device() \
-            or any(t is not None and t.device != first.device for t in others):
-        raise ValueError("all tensors must be on the current CUDA device")
+    device = torch.cuda.current_device()
+    if first.get_device() == device:
+        for t in others:
+            if t is not None and t.get_device() != device:
+                break
+        else:
+            return
+    raise ValueError("all tensors must be on the current CUDA device")
 
 
 def _tables(block_table, seq_lens, page_refcount):
@@ -883,7 +892,7 @@ class DiffWeights:
         want = (num_heads, head_dim) if per_head else (head_dim,)
         for t in vecs:
             _need(t, torch.float32, "lambda vectors")
-            if tuple(t.shape) != want:
+            if t.shape != want:
                 raise ValueError(f"lambda vectors must be [{head_dim}] or "
                                  f"[{num_heads}, {head_dim}], all alike")
         _opt(self.norm_weight, torch.float32, "norm_weight", 1)
@@ -926,7 +935,7 @@ def attn_decode_diff_paged(q, pool: PagedPool, block_table, seq_lens, max_seq_le
     if out is None:
         out = torch.empty((B, H, 2 * D), dtype=out_dtype, device=q.device)
     _need(out, out.dtype, "out", 3)
-    if tuple(out.shape) != (B, H, 2 * D):
+    if out.shape != (B, H, 2 * D):
         raise ValueError("out must be [batch, H, 2 head_dim]")
     _append_args(k_new, v_new, page_refcount, B, heads, D)
     if page_refcount is not None and page_refcount.shape[0] != pool.k.shape[0]:
@@ -971,7 +980,7 @@ def _linear_args(q, k, v, pool, log_decay, state_ids, batch, status):
     Hkv, D = pool.s.shape[1], pool.s.shape[2]
     for t, name in ((k, "k"), (v, "v")):
         _need(t, torch.bfloat16, name, 3)
-        if tuple(t.shape) != (q.shape[0], Hkv, D):
+        if t.shape != (q.shape[0], Hkv, D):
             raise ValueError(f"{name} must be [tokens, Hkv, head_dim]")
     if q.shape[2] != D:
         raise ValueError("q and the state pool differ in head_dim")

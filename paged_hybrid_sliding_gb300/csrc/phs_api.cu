@@ -1417,7 +1417,6 @@ int check_tables(const void* block_table, const void* seq_lens, int32_t num_rows
   return max_pages > INT32_MAX / kPage ? PHS_EUNSUPPORTED : PHS_OK;
 }
 
-// The pools of a page operation, in launches of up to kPagesMaxLayers.
 int check_pools(const phs_paged_pool* pools, int32_t num_layers) {
   if (!pools || num_layers <= 0) return PHS_EINVAL;
   for (int32_t l = 0; l < num_layers; ++l) {
@@ -1431,22 +1430,17 @@ int check_pools(const phs_paged_pool* pools, int32_t num_layers) {
   return PHS_OK;
 }
 
-int copy_in_pools(const phs_paged_pool* pools, int32_t num_layers, const int32_t* src,
-                  const int32_t* dst, const int32_t* n_dev, int64_t n, cudaStream_t s) {
-  DevInfo di;
-  int st = dev_info(di);
-  for (int32_t l0 = 0; !st && l0 < num_layers; l0 += kPagesMaxLayers) {
-    PagePools p;
-    std::memset(&p, 0, sizeof(p));
-    p.num_layers = std::min(num_layers - l0, kPagesMaxLayers);
-    p.page_vecs = pools[0].num_kv_heads * kPage * pools[0].head_dim * 2 / 16;
-    for (int l = 0; l < p.num_layers; ++l) {
-      p.k[l] = reinterpret_cast<uint4*>(pools[l0 + l].k);
-      p.v[l] = reinterpret_cast<uint4*>(pools[l0 + l].v);
-    }
-    st = launch_pages_copy(p, src, dst, n_dev, n, di.sms, s);
+// The pools of a page operation from layer l0 on, as many as a launch takes.
+PagePools pools_from(const phs_paged_pool* pools, int32_t num_layers, int32_t l0) {
+  PagePools p;
+  std::memset(&p, 0, sizeof(p));
+  p.num_layers = std::min(num_layers - l0, kPagesMaxLayers);
+  p.page_vecs = pools[0].num_kv_heads * kPage * pools[0].head_dim * 2 / 16;
+  for (int l = 0; l < p.num_layers; ++l) {
+    p.k[l] = reinterpret_cast<uint4*>(pools[l0 + l].k);
+    p.v[l] = reinterpret_cast<uint4*>(pools[l0 + l].v);
   }
-  return st;
+  return p;
 }
 
 // Consecutive 256-byte-aligned int32 arrays of a workspace.
@@ -1519,14 +1513,19 @@ int phs_pages_fork(const phs_paged_pool* pools, int32_t num_layers, int32_t* blo
   a.copy_src = ws.take(n);
   a.copy_dst = ws.take(n);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((st = launch_pages_fork_plan(a, s))) return st;
-  if ((st = launch_pages_fork_share(a, s))) return st;
-  return copy_in_pools(pools, num_layers, a.copy_src, a.copy_dst, nullptr, n, s);
+  DevInfo di;
+  if ((st = dev_info(di))) return st;
+  st = launch_pages_fork(a, pools_from(pools, num_layers, 0), di.sms, s);
+  for (int32_t l = kPagesMaxLayers; !st && l < num_layers; l += kPagesMaxLayers)
+    st = launch_pages_copy(pools_from(pools, num_layers, l), a.copy_src, a.copy_dst, nullptr, n,
+                           di.sms, s);
+  return st;
 }
 
 size_t phs_pages_compact_workspace_bytes(int64_t num_pages) {
   if (num_pages <= 0 || num_pages > INT32_MAX) return 0;
-  return 3 * align256(static_cast<size_t>(num_pages) * 4) + 256;
+  return 3 * align256(static_cast<size_t>(num_pages) * 4) + 256 +
+         align256(static_cast<size_t>((num_pages + kPagesTile - 1) / kPagesTile) * 4);
 }
 
 int phs_pages_compact(const phs_paged_pool* pools, int32_t num_layers,
@@ -1560,10 +1559,15 @@ int phs_pages_compact(const phs_paged_pool* pools, int32_t num_layers,
   a.movers = ws.take(a.num_pages);
   a.holes = ws.take(a.num_pages);
   a.meta = ws.take(2);
+  a.tile_live = ws.take((a.num_pages + kPagesTile - 1) / kPagesTile);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((st = launch_pages_compact_plan(a, s))) return st;
-  if ((st = launch_pages_compact_tables(a, s))) return st;
-  return copy_in_pools(pools, num_layers, a.movers, a.holes, a.meta + 1, 0, s);
+  DevInfo di;
+  if ((st = dev_info(di))) return st;
+  st = launch_pages_compact(a, pools_from(pools, num_layers, 0), di.sms, s);
+  for (int32_t l = kPagesMaxLayers; !st && l < num_layers; l += kPagesMaxLayers)
+    st = launch_pages_copy(pools_from(pools, num_layers, l), a.movers, a.holes, a.meta + 1,
+                           a.num_pages / 2, di.sms, s);
+  return st;
 }
 
 // ------------------------------------------------ differential attention --
@@ -1719,13 +1723,51 @@ int phs_linear_attn_decode(const void* q, int32_t num_q_heads, const phs_state_p
   return launch_linear_decode(pool->head_dim, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+}  // extern "C"
+
+namespace {
+
+// Segments of the longest prompt: as many as fill the SMs once where the
+// (request, KV head) pairs alone do not, each of at least 8 chunks.
+#ifndef PHS_LINEAR_SEG_CHUNKS
+#define PHS_LINEAR_SEG_CHUNKS 8
+#endif
+int linear_segments(int B, int Hkv, int max_seq, int sms) {
+  const long long pairs = std::max(1LL, 1LL * B * Hkv);
+  const long long chunks = (max_seq + kLinearChunk - 1LL) / kLinearChunk;
+  return static_cast<int>(
+      std::max(1LL, std::min(sms / pairs, chunks / PHS_LINEAR_SEG_CHUNKS)));
+}
+
+// [tokens][heads * D] bf16; boxes of 128 tokens x 64 columns
+int map_bf16_tokens(CUtensorMap* m, const void* base, int64_t tokens, int64_t cols) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return PHS_ECUDA;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  cuuint32_t box[2] = {64, kLinearChunk};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PHS_OK : PHS_ECUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t phs_linear_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads,
                                          int32_t num_kv_heads, int32_t head_dim,
                                          int32_t total_tokens, int32_t max_seq_len) {
   if (batch < 0 || total_tokens < 0 || max_seq_len < 0 ||
       check_dims(num_q_heads, num_kv_heads, head_dim))
     return 0;
-  return 256;
+  DevInfo di;
+  if (dev_info(di)) return 0;
+  const int nseg = linear_segments(batch, num_kv_heads, max_seq_len, di.sms);
+  const size_t state = static_cast<size_t>(head_dim) * head_dim * sizeof(float);
+  return nseg > 1 ? static_cast<size_t>(batch) * num_kv_heads * nseg * state : 256;
 }
 
 int phs_linear_attn_prompt(const void* q, int32_t num_q_heads, const void* k, const void* v,
@@ -1749,7 +1791,22 @@ int phs_linear_attn_prompt(const void* q, int32_t num_q_heads, const void* k, co
   a.resume = resume;
   a.total_tokens = total_tokens;
   a.max_seq = max_seq_len;
-  return launch_linear_prompt(pool->head_dim, a, reinterpret_cast<cudaStream_t>(stream));
+  DevInfo di;
+  if ((st = dev_info(di))) return st;
+  a.nseg = linear_segments(batch, a.Hkv, max_seq_len, di.sms);
+  a.ws = reinterpret_cast<float*>(workspace);
+  CUtensorMap tq, tk, tv;
+  std::memset(&tq, 0, sizeof(tq));
+  if (total_tokens > 0) {
+    const int D = pool->head_dim;
+    if ((st = map_bf16_tokens(&tq, q, total_tokens, int64_t{a.Hq} * D))) return st;
+    if ((st = map_bf16_tokens(&tk, k, total_tokens, int64_t{a.Hkv} * D))) return st;
+    if ((st = map_bf16_tokens(&tv, v, total_tokens, int64_t{a.Hkv} * D))) return st;
+  } else {
+    tk = tv = tq;  // no chunk, no copy
+  }
+  return launch_linear_prompt(pool->head_dim, tq, tk, tv, a,
+                              reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

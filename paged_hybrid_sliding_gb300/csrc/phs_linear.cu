@@ -7,6 +7,7 @@
 #include "phs_common.cuh"
 #include "phs_merge.cuh"
 #include "phs_ops.h"
+#include "phs_tc.cuh"
 
 namespace phs {
 
@@ -122,58 +123,600 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
   return D == 128 ? launch_linear_decode_t<128>(a, stream) : launch_linear_decode_t<64>(a, stream);
 }
 
-// The recurrence token by token: one CTA per (16 columns of v, KV head,
-// request).  Eight threads share a column, each with D/8 rows of the state
-// in registers.
+// ------------------------------------------------------------- prompts --
+// Prompts go in chunks of C = 128 tokens.  With S the state before a chunk,
+// rows i, j of the chunk, v rows of it real and pw[n] = exp(g n):
+//   O = diag(scale pw[i + 1]) Q S + (scale pw[i - j] Q K^T, j <= i) V
+//   S <- pw[v] S + sum_j pw[v - 1 - j] k_j v_j^T
+// Four matrix products a chunk (and query head), on the tensor cores:
+//   QK = Q K^T     128 x 128 x D   A = Q, B = K                (shared memory)
+//   QS = Q S       128 x D x D     A = Q, B = S                (shared memory)
+//   PV = P V       128 x D x 128   A = P in tensor memory, B = V
+//   KV = K'^T V    D x D x 128     A = K'^T in tensor memory, B = V
+// The tokens' decay makes P and K' values of 24 bits, and the state is an
+// fp32 one.  They enter as sums of bf16 terms: P and S as two (16 bits of
+// each value; one term would put its 2^-9 beside the output's own rounding),
+// K' as three (24 bits: the state is kept in fp32 and must stay one), and V
+// and Q are exact.  KV is accumulated from its smallest term up, chunk by
+// chunk from zero, and added to the state in fp32 registers: the tensor
+// cores' own sums drop the bits below the running sum's last one, which
+// over a long memory would pull the state down.
+//
+// One CTA per (segment, KV head, request) walks its chunks in order:
+//   warps 0-3  rows of the chunk: scores -> P, the inter-chunk part scaled,
+//              the output rows
+//   warps 4-7  rows of the state (one per thread, in registers): state ->
+//              two terms in shared memory, K tile -> K'^T terms
+//   warp 8     TMA: K and V two chunks deep, Q one
+//   (warps 10 and 11 fill the third warpgroup)
+//   warp 9     issues the products: QS, KV, PV, then QK of the next chunk,
+//              so that the state's and P's way through the registers runs
+//              beside them
+// Where there are fewer (request, KV head) pairs than SMs, prompts are cut
+// into segments: a first launch sums up each segment's own state (K and V
+// alone), the second starts each segment from the joined states before it.
+constexpr int kLinC = kLinearChunk;
+constexpr int kLinThreads = 384;
+// registers a thread: 168 at launch; the third warpgroup (copies, products)
+// gives up what the other two take, 72 + 200 + 232 = 3 x 168
+constexpr int kLinRegsRows = 200, kLinRegsState = 232, kLinRegsIssue = 72;
+constexpr uint32_t kTmU = 0, kTmSc = 128, kTmOut = 256, kTmKp = 384;  // tensor-memory columns
+
 template <int D>
-__global__ void __launch_bounds__(128) phs_linear_prompt_kernel(const LinearArgs a) {
-  constexpr int R = D / 8;
-  const int b = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * 16;
-  const int col = threadIdx.x / 8, part = threadIdx.x % 8;
+struct LinLayout {
+  static constexpr int kTile = kLinC * D * 2;  // [D / 64 halves][128 rows][128 bytes]
+  static constexpr int kQ = 0;
+  static constexpr int kK = kTile;             // 2 stages
+  static constexpr int kV = kK + 2 * kTile;
+  static constexpr int kS = kV + 2 * kTile;    // 2 terms [D / 64][D rows][128 bytes]
+  static constexpr int kSTerm = D * D * 2;
+  static constexpr int kPw = kS + 2 * kSTerm;  // float [kLinC + 4]: exp(g n)
+  static constexpr int kPs = kPw + (kLinC + 4) * 4;  // the same times scale
+  static constexpr int kBar = kPs + (kLinC + 4) * 4;
+  static constexpr int kMisc = kBar + 20 * 8;  // tensor-memory base, abort flag
+  static constexpr int kAlloc = kMisc + 16 + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory of the prompt kernel");
+};
+
+// Bounded wait that also gives up when another role has.
+__device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 63u) {
+      if (*abort) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+    }
+  }
+}
+
+// The same by a whole warp, one answer for all its lanes.
+__device__ __forceinline__ bool lin_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, lin_wait(bar, parity, abort));
+}
+
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// bf16 pair of two values; the values keep what it leaves of them
+__device__ __forceinline__ uint32_t take_term(float& x0, float& x1) {
+  const uint32_t w = pack_bf16(x0, x1);
+  x0 -= __uint_as_float(w << 16);
+  x1 -= __uint_as_float(w & 0xffff0000u);
+  return w;
+}
+
+__device__ __forceinline__ float lds_bf16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+
+// STATES: the first launch (sums of each segment but the last, no outputs)
+template <int D, bool STATES>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    phs_linear_prompt_kernel(const __grid_constant__ CUtensorMap tq,
+                             const __grid_constant__ CUtensorMap tk,
+                             const __grid_constant__ CUtensorMap tv,
+                             const __grid_constant__ LinearArgs a) {
+  using L = LinLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x, h = blockIdx.y, seg = blockIdx.z;
+
+  // ---- this CTA's chunks
   const int64_t id = request_state(a, b);
   int t0, t1;
   if (!request_tokens(a, b, t0, t1)) return;
-  if (id < 0) {
-    for (int t = t0; t < t1; ++t)
-      for (int g = part; g < a.G; g += 8)
-        store_out(a.out, (static_cast<size_t>(t) * a.Hq + h * a.G + g) * D + c0 + col, 0.f,
-                  a.out_f32);
+  const int all = (t1 - t0 + kLinC - 1) / kLinC;             // chunks of the request
+  const int per = max(1, (all + a.nseg - 1) / a.nseg);       // of a segment
+  const int segs = max(1, (all + per - 1) / per);
+  if (seg >= segs || (STATES && seg + 1 >= segs)) return;
+  t0 += seg * per * kLinC;
+  t1 = min(t1, t0 + per * kLinC);
+  if (id < 0) {  // no state: zero rows
+    if (!STATES)
+      for (int64_t e = tid; e < static_cast<int64_t>(t1 - t0) * a.G * D; e += kLinThreads) {
+        const int64_t t = t0 + e / (a.G * D);
+        reinterpret_cast<__nv_bfloat16*>(a.out)[(t * a.Hq + h * a.G) * D + e % (a.G * D)] =
+            __float2bfloat16_rn(0.f);
+      }
     return;
   }
-  float* S = a.state + (id * a.Hkv + h) * D * D;
-  const float decay = expm1f(a.log_decay[h]);
-  const bool resume = a.resume && a.resume[b] != 0;
-  float s[R];
+  const int nch = (t1 - t0 + kLinC - 1) / kLinC;
+  const float g0 = a.log_decay[h], g = g0 < -1e4f ? -1e4f : g0;  // exp(g n) is 0 there anyway
+
+  const uint32_t kv_full = sb + L::kBar, kv_empty = kv_full + 16, q_full = kv_empty + 16,
+                 q_empty = q_full + 8, sc_full = q_empty + 8, qs_done = sc_full + 8,
+                 pv_ready = qs_done + 8, o_done = pv_ready + 8, o_free = o_done + 8,
+                 kp_full = o_free + 8, kp_empty = kp_full + 16, s_ready = kp_empty + 16,
+                 u_done = s_ready + 8, u_free = u_done + 8, drain = u_free + 8;
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  float* pw = reinterpret_cast<float*>(smem + L::kPw);
+  float* ps = reinterpret_cast<float*>(smem + L::kPs);
+  if (warp == 9) {
+    tmem_alloc(sb + L::kMisc, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(kv_full + 8 * i, 1);
+      mbar_init(kv_empty + 8 * i, 129);  // the products, and the 128 state rows
+      mbar_init(kp_full + 8 * i, 128);
+      mbar_init(kp_empty + 8 * i, 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(sc_full, 1);
+    mbar_init(qs_done, 1);
+    mbar_init(pv_ready, 128);
+    mbar_init(o_done, 1);
+    mbar_init(o_free, 128);
+    mbar_init(s_ready, 128);
+    mbar_init(u_done, 1);
+    mbar_init(u_free, 128);
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  for (int n = tid; n <= kLinC; n += kLinThreads) {
+    const float p = expf(g * n);
+    pw[n] = p;
+    ps[n] = p * a.scale;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
+  const uint32_t my_lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+
+  if (warp >= 8) regs_dec<kLinRegsIssue>();
+  if (warp == 8) {
+    // ---------------------------------------------------------------- TMA
+    if (lane == 0 && nch > 0) {
+      const uint64_t pol = policy_evict_first();
+      auto load = [&](const CUtensorMap* map, uint32_t dst, int head, int t, uint32_t bar) {
+        for (int hf = 0; hf < D / 64; ++hf)
+          tma_load_2d(dst + hf * (kLinC * 128), map, head * D + 64 * hf, t, bar, pol);
+      };
+      bool ok = true;
+      int nq = 0, kv_issued = 0;
+      for (int n = 0; ok && n < nch; ++n) {
+        const int st = n & 1, t = t0 + n * kLinC;
+        if (n >= 2) ok = lin_wait(kv_empty + 8 * st, ((n >> 1) - 1) & 1, abort);
+        if (!ok) break;
+        mbar_arrive_expect_tx(kv_full + 8 * st, 2 * L::kTile);
+        load(&tk, sb + L::kK + st * L::kTile, h, t, kv_full + 8 * st);
+        load(&tv, sb + L::kV + st * L::kTile, h, t, kv_full + 8 * st);
+        kv_issued = n + 1;
+        if (STATES) continue;
+        for (int gq = 0; ok && gq < a.G; ++gq, ++nq) {
+          if (nq >= 1) ok = lin_wait(q_empty, (nq - 1) & 1, abort);
+          if (!ok) break;
+          mbar_arrive_expect_tx(q_full, L::kTile);
+          load(&tq, sb + L::kQ, h * a.G + gq, t, q_full);
+        }
+      }
+      if (!ok) {
+        set_status(a.status, PHS_ETIMEOUT);
+        *abort = 1;
+      }
+      // copies still in flight land before the CTA ends
+      for (int n = max(0, kv_issued - 2); n < kv_issued; ++n)
+        (void)mbar_wait(kv_full + 8 * (n & 1), (n >> 1) & 1);
+      if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
+    }
+  } else if (warp == 9) {
+    // ----------------------------------------------------------- products
+    if (lane == 0 && nch > 0) {
+      constexpr uint32_t kIdQK = idesc_bf16_f32(128, kLinC, false, false);
+      constexpr uint32_t kIdD = idesc_bf16_f32(128, D, false, true);
+      bool ok = true;
+      int nq = 0;  // (chunk, query head) pairs whose QK has been issued
+      auto issue_qk = [&](int n) {
+        const int st = n & 1;
+        ok = ok && lin_wait(kv_full + 8 * st, (n >> 1) & 1, abort) &&
+             lin_wait(q_full, nq & 1, abort) &&
+             (nq == 0 || lin_wait(o_done, (nq - 1) & 1, abort));  // P of the last pair is read
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t kst = sb + L::kK + st * L::kTile;
 #pragma unroll
-  for (int r = 0; r < R; ++r) s[r] = resume ? S[(part + 8 * r) * D + c0 + col] : 0.f;
-  for (int t = t0; t < t1; ++t) {
-    const __nv_bfloat16* k = a.k + (static_cast<size_t>(t) * a.Hkv + h) * D;
-    const float v = __bfloat162float(a.v[(static_cast<size_t>(t) * a.Hkv + h) * D + c0 + col]);
+        for (int ks = 0; ks < D / 16; ++ks)
+          umma_bf16(tmem + kTmSc,
+                    sdesc_sw128(sb + L::kQ + (ks >> 2) * (kLinC * 128) + (ks & 3) * 32, 16, 1024),
+                    sdesc_sw128(kst + (ks >> 2) * (kLinC * 128) + (ks & 3) * 32, 16, 1024), kIdQK,
+                    ks > 0);
+        umma_commit(sc_full);
+        ++nq;
+      };
+      int m = 0;  // K' terms
+      auto issue_kv = [&](int n) {
+        const uint32_t vst = sb + L::kV + (n & 1) * L::kTile;
+        if (n >= 1) ok = ok && lin_wait(u_free, (n - 1) & 1, abort);
+        if (STATES) ok = ok && lin_wait(kv_full + 8 * (n & 1), (n >> 1) & 1, abort);
+        for (int t = 0; ok && t < 3; ++t, ++m) {
+          ok = lin_wait(kp_full + 8 * (m & 1), (m >> 1) & 1, abort);
+          if (!ok) return;
+          tc_fence_after();
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      s[r] = fmaf(__bfloat162float(k[part + 8 * r]), v, decayed(s[r], decay));
-    for (int g = 0; g < a.G; ++g) {
-      const size_t row = (static_cast<size_t>(t) * a.Hq + h * a.G + g) * D;
-      float x = 0.f;
+          for (int ks = 0; ks < kLinC / 16; ++ks)
+            umma_bf16_ts(tmem + kTmU, tmem + kTmKp + 64 * (m & 1) + 8 * ks,
+                         sdesc_sw128(vst + ks * 2048, kLinC * 128, 1024), kIdD, t > 0 || ks > 0);
+          umma_commit(kp_empty + 8 * (m & 1));
+        }
+        if (ok) umma_commit(u_done);
+      };
+      if (!STATES) issue_qk(0);
+      int pair = 0;
+      for (int n = 0; ok && n < nch; ++n) {
+        const uint32_t vst = sb + L::kV + (n & 1) * L::kTile;
+        if (STATES) {
+          issue_kv(n);
+          if (ok) umma_commit(kv_empty + 8 * (n & 1));
+          continue;
+        }
+        for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
+          if (gq == 0) ok = lin_wait(s_ready, n & 1, abort);
+          if (pair >= 1) ok = ok && lin_wait(o_free, (pair - 1) & 1, abort);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-      for (int r = 0; r < R; ++r) x = fmaf(__bfloat162float(a.q[row + part + 8 * r]), s[r], x);
-      x += __shfl_xor_sync(0xffffffffu, x, 1);
-      x += __shfl_xor_sync(0xffffffffu, x, 2);
-      x += __shfl_xor_sync(0xffffffffu, x, 4);
-      if (part == 0) store_out(a.out, row + c0 + col, x * a.scale, a.out_f32);
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              umma_bf16(
+                  tmem + kTmOut,
+                  sdesc_sw128(sb + L::kQ + (ks >> 2) * (kLinC * 128) + (ks & 3) * 32, 16, 1024),
+                  sdesc_sw128(sb + L::kS + t * L::kSTerm + ks * 2048, D * 128, 1024), kIdD,
+                  t > 0 || ks > 0);
+          umma_commit(qs_done);
+          umma_commit(q_empty);
+          if (gq == a.G - 1) issue_kv(n);
+          ok = ok && lin_wait(pv_ready, pair & 1, abort);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int ks = 0; ks < kLinC / 16; ++ks)
+              umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 64 * t + 8 * ks,
+                           sdesc_sw128(vst + ks * 2048, kLinC * 128, 1024), kIdD, 1u);
+          umma_commit(o_done);
+          if (gq == a.G - 1) umma_commit(kv_empty + 8 * (n & 1));
+          if (gq + 1 < a.G)
+            issue_qk(n);
+          else if (n + 1 < nch)
+            issue_qk(n + 1);
+        }
+      }
+      if (!ok) {
+        set_status(a.status, PHS_ETIMEOUT);
+        *abort = 1;
+      }
+      umma_commit(drain);  // every product is complete before tensor memory is released
+      (void)mbar_wait(drain, 0);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------- rows of the chunk
+    regs_inc<kLinRegsRows>();
+    const int i = tid;  // row
+    bool ok = !STATES;
+    int pair = 0;
+    for (int n = 0; ok && n < nch; ++n)
+      for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
+        ok = lin_wait_warp(sc_full, pair & 1, abort);
+        if (!ok) break;
+        tc_fence_after();
+        // P: term 0 in columns 0..63 of the scores' place, term 1 in 64..127.
+        // A half is written once the scores under it have been read.
+        uint32_t lo[2][32];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t s0[32], s1[32], hi[32];
+          tmem_ld32(my_lanes + kTmSc + 64 * hf, s0);
+          tmem_ld32(my_lanes + kTmSc + 64 * hf + 32, s1);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float x[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int j = 64 * hf + 2 * c + e, k = (2 * c + e) & 31;
+              const float s = __uint_as_float(c < 16 ? s0[k] : s1[k]);
+              x[e] = j <= i ? s * ps[max(i - j, 0)] : 0.f;
+            }
+            hi[c] = take_term(x[0], x[1]);
+            lo[hf][c] = pack_bf16(x[0], x[1]);
+          }
+          tmem_st32(my_lanes + kTmSc + 32 * hf, hi);
+        }
+        tmem_st32(my_lanes + kTmSc + 64, lo[0]);
+        tmem_st32(my_lanes + kTmSc + 96, lo[1]);
+        // the part before the chunk, scaled in place
+        ok = lin_wait_warp(qs_done, pair & 1, abort);
+        if (!ok) break;
+        tc_fence_after();
+        const float f = ps[i + 1];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(my_lanes + kTmOut + 32 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          tmem_st32(my_lanes + kTmOut + 32 * c, o);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(pv_ready);
+        // output row
+        ok = lin_wait_warp(o_done, pair & 1, abort);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t y[D / 2];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(my_lanes + kTmOut + 32 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            y[16 * c + e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+        }
+        tc_fence_before();
+        mbar_arrive(o_free);
+        const int t = t0 + n * kLinC + i;
+        if (t < t1) {
+          uint4* to = reinterpret_cast<uint4*>(
+              reinterpret_cast<__nv_bfloat16*>(a.out) +
+              (static_cast<size_t>(t) * a.Hq + h * a.G + gq) * D);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            to[c] = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
+        }
+      }
+    if (!STATES && !ok) {
+      set_status(a.status, PHS_ETIMEOUT);
+      *abort = 1;
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------- rows of the state
+    regs_inc<kLinRegsState>();
+    const int r = tid - 128;  // row (a k index); D = 64: the upper half has none
+    const bool mine = r < D;
+    const size_t row = static_cast<size_t>(r) * D;
+    float* pool = a.state + (id * a.Hkv + h) * D * D + row;
+    float* ws = a.ws + (static_cast<size_t>(b) * a.Hkv + h) * a.nseg * D * D + row;
+    const bool resume = a.resume != nullptr && a.resume[b] != 0;
+    float S[D];
+#pragma unroll
+    for (int c = 0; c < D; ++c) S[c] = 0.f;
+    auto load_row = [&](const float* from, float keep_m1) {  // S <- exp() S + from
+#pragma unroll
+      for (int c = 0; c < D; c += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(from + c);
+        S[c] = decayed(S[c], keep_m1) + x.x;
+        S[c + 1] = decayed(S[c + 1], keep_m1) + x.y;
+        S[c + 2] = decayed(S[c + 2], keep_m1) + x.z;
+        S[c + 3] = decayed(S[c + 3], keep_m1) + x.w;
+      }
+    };
+    auto store_row = [&](float* to) {
+#pragma unroll
+      for (int c = 0; c < D; c += 4)
+        *reinterpret_cast<float4*>(to + c) = make_float4(S[c], S[c + 1], S[c + 2], S[c + 3]);
+    };
+    if (mine) {
+      if (seg == 0) {
+        // with several segments the pool's state is overwritten by the last
+        // one's CTA: the first launch keeps a copy for the second
+        if (resume) load_row(!STATES && segs > 1 ? ws + (a.nseg - 1) * D * D : pool, 0.f);
+        if (STATES && resume) store_row(ws + (a.nseg - 1) * D * D);
+      } else if (!STATES) {
+        const float keep = expm1f(g * (per * kLinC));
+        for (int s = 0; s < seg; ++s) load_row(ws + s * D * D, keep);
+      }
+    }
+    if (!mine) {  // D = 64: rows 64..127 of K'^T are zero
+      uint32_t z[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) z[c] = 0u;
+      for (int c = 0; c < 8; ++c) tmem_st16(my_lanes + kTmKp + 16 * c, z);
+      tmem_st_wait();
+    }
+    // byte offsets of column r in rows 0..7 of a K tile
+    uint32_t off[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      off[e] = (r >> 6) * (kLinC * 128) + e * 128 + ((((r >> 3) ^ e) & 7) << 4) + (r & 7) * 2;
+    bool ok = true;
+    int m = 0;
+    auto add_chunk = [&](int n) {  // S <- state after chunk n
+      if (!ok) return;
+      ok = lin_wait_warp(u_done, n & 1, abort);
+      if (!ok) return;
+      tc_fence_after();
+      const float keep = expm1f(g * min(kLinC, t1 - t0 - n * kLinC));
+      if (mine) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t u[32];
+          tmem_ld32(my_lanes + kTmU + 32 * c, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            S[32 * c + e] = decayed(S[32 * c + e], keep) + __uint_as_float(u[e]);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(u_free);
+    };
+    for (int n = 0; ok && n < nch; ++n) {
+      if (n > 0) add_chunk(n - 1);
+      if (!ok) break;
+      if (!STATES) {
+        if (mine) {
+          uint8_t* rowp = smem + L::kS + r * 128;
+#pragma unroll
+          for (int u = 0; u < D / 8; ++u) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float x0 = S[8 * u + 2 * e], x1 = S[8 * u + 2 * e + 1];
+              hi[e] = take_term(x0, x1);
+              lo[e] = pack_bf16(x0, x1);
+            }
+            uint8_t* at = rowp + (u >> 3) * (D * 128) + (((u ^ r) & 7) << 4);
+            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(at + L::kSTerm) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(s_ready);
+      }
+      // K'^T: terms lo2, lo, then hi
+      const int st = n & 1, v = min(kLinC, t1 - t0 - n * kLinC);
+      ok = lin_wait_warp(kv_full + 8 * st, (n >> 1) & 1, abort);
+      if (!ok) break;
+      if (v < kLinC) {  // V rows behind the last token: no 0 * NaN
+        uint8_t* tile = smem + L::kV + st * L::kTile;
+        for (int u = r; u < D / 64 * (kLinC - v) * 8; u += 128) {
+          const int hf = u / ((kLinC - v) * 8), w = u % ((kLinC - v) * 8);
+          *reinterpret_cast<uint4*>(tile + hf * (kLinC * 128) + v * 128 + w * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      const uint32_t kst = sb + L::kK + st * L::kTile;
+      // k'_t of this row
+      auto kp = [&](int t, int e) {  // t a multiple of 8
+        const float k = lds_bf16(kst + t * 128 + off[e]);
+        return t + e < v ? k * pw[v - 1 - t - e] : 0.f;
+      };
+      auto wait_empty = [&](int mm) {
+        if (mm >= 2) ok = ok && lin_wait_warp(kp_empty + 8 * (mm & 1), ((mm >> 1) - 1) & 1, abort);
+      };
+      wait_empty(m);
+      wait_empty(m + 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (mine) {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w2[16], w1[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int t = 32 * q + ((2 * c) & ~7), e = (2 * c) & 7;
+            float x0 = kp(t, e), x1 = kp(t, e + 1);
+            (void)take_term(x0, x1);
+            w1[c] = take_term(x0, x1);
+            w2[c] = pack_bf16(x0, x1);
+          }
+          tmem_st16(my_lanes + kTmKp + 64 * (m & 1) + 16 * q, w2);
+          tmem_st16(my_lanes + kTmKp + 64 * ((m + 1) & 1) + 16 * q, w1);
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      mbar_arrive(kp_full + 8 * (m & 1));
+      mbar_arrive(kp_full + 8 * ((m + 1) & 1));
+      m += 2;
+      wait_empty(m);
+      if (!ok) break;
+      tc_fence_after();
+      if (mine) {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w0[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int t = 32 * q + ((2 * c) & ~7), e = (2 * c) & 7;
+            w0[c] = pack_bf16(kp(t, e), kp(t, e + 1));
+          }
+          tmem_st16(my_lanes + kTmKp + 64 * (m & 1) + 16 * q, w0);
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      mbar_arrive(kp_full + 8 * (m & 1));
+      mbar_arrive(kv_empty + 8 * st);
+      ++m;
+    }
+    if (nch > 0) add_chunk(nch - 1);
+    if (!ok) {
+      set_status(a.status, PHS_ETIMEOUT);
+      *abort = 1;
+    } else if (mine && (STATES || seg + 1 == segs)) {
+      store_row(STATES ? ws + seg * D * D : pool);
     }
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r) S[(part + 8 * r) * D + c0 + col] = s[r];
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
-int launch_linear_prompt(int D, const LinearArgs& a, cudaStream_t stream) {
-  const dim3 grid(a.B, a.Hkv, D / 16);
-  if (D == 128)
-    phs_linear_prompt_kernel<128><<<grid, 128, 0, stream>>>(a);
-  else
-    phs_linear_prompt_kernel<64><<<grid, 128, 0, stream>>>(a);
+template <int D>
+static int launch_linear_prompt_t(const CUtensorMap& tq, const CUtensorMap& tk,
+                                  const CUtensorMap& tv, const LinearArgs& a, cudaStream_t stream) {
+  using L = LinLayout<D>;
+  auto states = phs_linear_prompt_kernel<D, true>;
+  auto rows = phs_linear_prompt_kernel<D, false>;
+  if (ensure_dynamic_smem(reinterpret_cast<const void*>(rows), L::kAlloc) != PHS_OK ||
+      ensure_dynamic_smem(reinterpret_cast<const void*>(states), L::kAlloc) != PHS_OK)
+    return PHS_ECUDA;
+  if (a.nseg > 1)
+    states<<<dim3(a.B, a.Hkv, a.nseg - 1), kLinThreads, L::kAlloc, stream>>>(tq, tk, tv, a);
+  rows<<<dim3(a.B, a.Hkv, a.nseg), kLinThreads, L::kAlloc, stream>>>(tq, tk, tv, a);
   return cudaGetLastError() == cudaSuccess ? PHS_OK : PHS_ECUDA;
+}
+
+int launch_linear_prompt(int D, const CUtensorMap& tq, const CUtensorMap& tk,
+                         const CUtensorMap& tv, const LinearArgs& a, cudaStream_t stream) {
+  return D == 128 ? launch_linear_prompt_t<128>(tq, tk, tv, a, stream)
+                  : launch_linear_prompt_t<64>(tq, tk, tv, a, stream);
 }
 
 }  // namespace phs

@@ -43,6 +43,7 @@ struct PageForkArgs {
   int32_t* fresh;      // [n] the lowest free pages, ascending
   int32_t* copy_src;   // [n] page to copy, or -1
   int32_t* copy_dst;   // [n]
+  int share_ctas;
 };
 
 struct PageCompactArgs {
@@ -61,13 +62,15 @@ struct PageCompactArgs {
   int32_t* movers;  // [num_pages] page that is m-th from the top
   int32_t* holes;   // [num_pages] m-th lowest hole
   int32_t* meta;    // [2] live pages, moves
+  int32_t* tile_live;  // live pages of each tile of ids
+  int table_ctas;
 };
 
+constexpr int kPagesTile = 8192;  // ids of a tile
+
 int launch_pages_free(const PageFreeArgs& a, cudaStream_t stream);
-int launch_pages_fork_plan(const PageForkArgs& a, cudaStream_t stream);
-int launch_pages_fork_share(const PageForkArgs& a, cudaStream_t stream);
-int launch_pages_compact_plan(const PageCompactArgs& a, cudaStream_t stream);
-int launch_pages_compact_tables(const PageCompactArgs& a, cudaStream_t stream);
+int launch_pages_fork(PageForkArgs a, const PagePools& p, int num_sms, cudaStream_t stream);
+int launch_pages_compact(PageCompactArgs a, const PagePools& p, int num_sms, cudaStream_t stream);
 // pages src[i] -> dst[i] (i < *n_dev, or i < n where n_dev is null; negative
 // src: none) of every pool
 int launch_pages_copy(const PagePools& p, const int32_t* src, const int32_t* dst,
@@ -128,9 +131,14 @@ struct LinearArgs {
   const int32_t* cu_seqlens;  // [B + 1]
   const int32_t* resume;      // [B] or null: from a zero state
   int total_tokens, max_seq;
+  int nseg;                   // segments of the longest prompt
+  float* ws;                  // [B][Hkv][nseg][D][D]: segment sums, then the first state
 };
 
+constexpr int kLinearChunk = 128;  // tokens
+
 int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream);
-int launch_linear_prompt(int D, const LinearArgs& a, cudaStream_t stream);
+int launch_linear_prompt(int D, const CUtensorMap& tq, const CUtensorMap& tk,
+                         const CUtensorMap& tv, const LinearArgs& a, cudaStream_t stream);
 
 }  // namespace phs
