@@ -1795,17 +1795,18 @@ int phs_linear_attn_prompt(const void* q, int32_t num_q_heads, const void* k, co
   if ((st = dev_info(di))) return st;
   a.nseg = linear_segments(batch, a.Hkv, max_seq_len, di.sms);
   a.ws = reinterpret_cast<float*>(workspace);
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   std::memset(&tq, 0, sizeof(tq));
   if (total_tokens > 0) {
     const int D = pool->head_dim;
     if ((st = map_bf16_tokens(&tq, q, total_tokens, int64_t{a.Hq} * D))) return st;
     if ((st = map_bf16_tokens(&tk, k, total_tokens, int64_t{a.Hkv} * D))) return st;
     if ((st = map_bf16_tokens(&tv, v, total_tokens, int64_t{a.Hkv} * D))) return st;
+    if ((st = map_bf16_tokens(&to, out, total_tokens, int64_t{a.Hq} * D))) return st;
   } else {
-    tk = tv = tq;  // no chunk, no copy
+    tk = tv = to = tq;  // no chunk, no copy
   }
-  return launch_linear_prompt(pool->head_dim, tq, tk, tv, a,
+  return launch_linear_prompt(pool->head_dim, tq, tk, tv, to, a,
                               reinterpret_cast<cudaStream_t>(stream));
 }
 

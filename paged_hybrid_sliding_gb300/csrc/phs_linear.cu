@@ -147,35 +147,39 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 //              the output rows
 //   warps 4-7  rows of the state (one per thread, in registers): state ->
 //              two terms in shared memory, K tile -> K'^T terms
-//   warp 8     TMA: K and V two chunks deep, Q one
-//   (warps 10 and 11 fill the third warpgroup)
+//   warp 8     TMA loads: a ring of three K and V tiles, one Q tile
 //   warp 9     issues the products: QS, KV, PV, then QK of the next chunk,
 //              so that the state's and P's way through the registers runs
 //              beside them
+//   warp 10    TMA stores of the output tile (warp 11 fills the warpgroup)
+// What a chunk moves through shared memory bounds the kernel next to HBM: at
+// D = 128 the products read 352 KB, copies and registers move 300 KB, about
+// 5,200 cycles of 128 bytes; its share of HBM (128 KB) takes 5,300.
 // Where there are fewer (request, KV head) pairs than SMs, prompts are cut
 // into segments: a first launch sums up each segment's own state (K and V
 // alone), the second starts each segment from the joined states before it.
 constexpr int kLinC = kLinearChunk;
 constexpr int kLinThreads = 384;
 // registers a thread: 168 at launch; the third warpgroup (copies, products)
-// gives up what the other two take, 72 + 200 + 232 = 3 x 168
-constexpr int kLinRegsRows = 200, kLinRegsState = 232, kLinRegsIssue = 72;
+// gives up what the other two take, 88 + 184 + 232 = 3 x 168
+constexpr int kLinRegsRows = 184, kLinRegsState = 232, kLinRegsIssue = 88;
 constexpr uint32_t kTmU = 0, kTmSc = 128, kTmOut = 256, kTmKp = 384;  // tensor-memory columns
 
 template <int D>
 struct LinLayout {
   static constexpr int kTile = kLinC * D * 2;  // [D / 64 halves][128 rows][128 bytes]
+  static constexpr int kHalf = kLinC * 128;
+  static constexpr int kSlots = 3;             // K(0) V(0) K(1) V(1) ... in turn
   static constexpr int kQ = 0;
-  static constexpr int kK = kTile;             // 2 stages
-  static constexpr int kV = kK + 2 * kTile;
-  static constexpr int kS = kV + 2 * kTile;    // 2 terms [D / 64][D rows][128 bytes]
+  static constexpr int kKV = kTile;
+  static constexpr int kOut = kKV + kSlots * kTile;
+  static constexpr int kS = kOut + kTile;      // 2 terms [D / 64][D rows][128 bytes]
   static constexpr int kSTerm = D * D * 2;
-  static constexpr int kPw = kS + 2 * kSTerm;  // float [kLinC + 4]: exp(g n)
-  static constexpr int kPs = kPw + (kLinC + 4) * 4;  // the same times scale
-  static constexpr int kBar = kPs + (kLinC + 4) * 4;
-  static constexpr int kMisc = kBar + 20 * 8;  // tensor-memory base, abort flag
+  static constexpr int kBar = kS + 2 * kSTerm;
+  static constexpr int kMisc = kBar + 24 * 8;  // tensor-memory base, abort flag
   static constexpr int kAlloc = kMisc + 16 + 1024;
-  static_assert(kAlloc <= 227 * 1024, "shared memory of the prompt kernel");
+  static constexpr int kTables = (2 * (kLinC + 4) + 32) * 4;  // static
+  static_assert(kAlloc + kTables <= 227 * 1024, "shared memory of the prompt kernel");
 };
 
 // Bounded wait that also gives up when another role has.
@@ -214,6 +218,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// The value, in a register of its own from here: sums of it with constants
+// are then formed where they are used and not all kept across a loop.
+__device__ __forceinline__ uint64_t here(uint64_t x) {
+  asm volatile("" : "+l"(x));
+  return x;
+}
+
 // bf16 pair of two values; the values keep what it leaves of them
 __device__ __forceinline__ uint32_t take_term(float& x0, float& x1) {
   const uint32_t w = pack_bf16(x0, x1);
@@ -222,10 +233,28 @@ __device__ __forceinline__ uint32_t take_term(float& x0, float& x1) {
   return w;
 }
 
-__device__ __forceinline__ float lds_bf16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z,
+                                       uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z),
+               "r"(w)
+               : "memory");
+}
+
+// Tensor-memory store in the layout that ldmatrix.trans delivers: 16 lanes,
+// 4 N columns; thread 4 r + c holds column 4 i + c of lanes r (word 2 i) and
+// r + 8 (word 2 i + 1).  Here N = 4.
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
 }
 
 // STATES: the first launch (sums of each segment but the last, no outputs)
@@ -234,9 +263,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     phs_linear_prompt_kernel(const __grid_constant__ CUtensorMap tq,
                              const __grid_constant__ CUtensorMap tk,
                              const __grid_constant__ CUtensorMap tv,
+                             const __grid_constant__ CUtensorMap to,
                              const __grid_constant__ LinearArgs a) {
   using L = LinLayout<D>;
   extern __shared__ uint8_t smem_raw[];
+  // pw[n] = exp(g n), ps[n] = scale pw[n], col[n] = pw[31 - n]
+  __shared__ float pw[kLinC + 4], ps[kLinC + 4], col[32];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -265,25 +297,33 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int nch = (t1 - t0 + kLinC - 1) / kLinC;
   const float g0 = a.log_decay[h], g = g0 < -1e4f ? -1e4f : g0;  // exp(g n) is 0 there anyway
 
-  const uint32_t kv_full = sb + L::kBar, kv_empty = kv_full + 16, q_full = kv_empty + 16,
+  // barriers: tile loaded / used, Q, scores, the inter-chunk part, P and that
+  // part ready, output complete / read, K' terms written / used, state terms
+  // written, V's rows behind the last token zero, chunk sum complete / read,
+  // output tile written / stored
+  const uint32_t kv_full = sb + L::kBar, kv_empty = kv_full + 24, q_full = kv_empty + 24,
                  q_empty = q_full + 8, sc_full = q_empty + 8, qs_done = sc_full + 8,
                  pv_ready = qs_done + 8, o_done = pv_ready + 8, o_free = o_done + 8,
                  kp_full = o_free + 8, kp_empty = kp_full + 16, s_ready = kp_empty + 16,
-                 u_done = s_ready + 8, u_free = u_done + 8, drain = u_free + 8;
+                 u_done = s_ready + 8, u_free = u_done + 8, y_full = u_free + 8,
+                 y_free = y_full + 8, v_ready = y_free + 8, drain = v_ready + 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
-  float* pw = reinterpret_cast<float*>(smem + L::kPw);
-  float* ps = reinterpret_cast<float*>(smem + L::kPs);
   if (warp == 9) {
     tmem_alloc(sb + L::kMisc, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(kv_full + 8 * i, 1);
       mbar_init(kv_empty + 8 * i, 129);  // the products, and the 128 state rows
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(kp_full + 8 * i, 128);
       mbar_init(kp_empty + 8 * i, 1);
     }
+    mbar_init(v_ready, 128);
+    mbar_init(y_full, 128);
+    mbar_init(y_free, 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(sc_full, 1);
@@ -302,6 +342,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const float p = expf(g * n);
     pw[n] = p;
     ps[n] = p * a.scale;
+    if (n < 32) col[31 - n] = p;
   }
   tc_fence_before();
   __syncthreads();
@@ -319,30 +360,36 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           tma_load_2d(dst + hf * (kLinC * 128), map, head * D + 64 * hf, t, bar, pol);
       };
       bool ok = true;
-      int nq = 0, kv_issued = 0;
+      int nq = 0, tiles = 0;  // Q tiles, K and V tiles issued
+      auto load_kv = [&](const CUtensorMap* map, int t) {
+        const int slot = tiles % L::kSlots, turn = tiles / L::kSlots;
+        if (turn > 0) ok = ok && lin_wait(kv_empty + 8 * slot, (turn - 1) & 1, abort);
+        if (!ok) return;
+        mbar_arrive_expect_tx(kv_full + 8 * slot, L::kTile);
+        load(map, sb + L::kKV + slot * L::kTile, h, t, kv_full + 8 * slot);
+        ++tiles;
+      };
+      auto load_q = [&](int gq, int t) {
+        if (nq >= 1) ok = ok && lin_wait(q_empty, (nq - 1) & 1, abort);
+        if (!ok) return;
+        mbar_arrive_expect_tx(q_full, L::kTile);
+        load(&tq, sb + L::kQ, h * a.G + gq, t, q_full);
+        ++nq;
+      };
       for (int n = 0; ok && n < nch; ++n) {
-        const int st = n & 1, t = t0 + n * kLinC;
-        if (n >= 2) ok = lin_wait(kv_empty + 8 * st, ((n >> 1) - 1) & 1, abort);
-        if (!ok) break;
-        mbar_arrive_expect_tx(kv_full + 8 * st, 2 * L::kTile);
-        load(&tk, sb + L::kK + st * L::kTile, h, t, kv_full + 8 * st);
-        load(&tv, sb + L::kV + st * L::kTile, h, t, kv_full + 8 * st);
-        kv_issued = n + 1;
-        if (STATES) continue;
-        for (int gq = 0; ok && gq < a.G; ++gq, ++nq) {
-          if (nq >= 1) ok = lin_wait(q_empty, (nq - 1) & 1, abort);
-          if (!ok) break;
-          mbar_arrive_expect_tx(q_full, L::kTile);
-          load(&tq, sb + L::kQ, h * a.G + gq, t, q_full);
-        }
+        const int t = t0 + n * kLinC;
+        load_kv(&tk, t);
+        if (!STATES && ok) load_q(0, t);
+        if (ok) load_kv(&tv, t);
+        for (int gq = 1; !STATES && ok && gq < a.G; ++gq) load_q(gq, t);
       }
       if (!ok) {
         set_status(a.status, PHS_ETIMEOUT);
         *abort = 1;
       }
       // copies still in flight land before the CTA ends
-      for (int n = max(0, kv_issued - 2); n < kv_issued; ++n)
-        (void)mbar_wait(kv_full + 8 * (n & 1), (n >> 1) & 1);
+      for (int i = max(0, tiles - L::kSlots); i < tiles; ++i)
+        (void)mbar_wait(kv_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1);
       if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
     }
   } else if (warp == 9) {
@@ -352,47 +399,58 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       constexpr uint32_t kIdD = idesc_bf16_f32(128, D, false, true);
       bool ok = true;
       int nq = 0;  // (chunk, query head) pairs whose QK has been issued
-      auto issue_qk = [&](int n) {
-        const int st = n & 1;
-        ok = ok && lin_wait(kv_full + 8 * st, (n >> 1) & 1, abort) &&
-             lin_wait(q_full, nq & 1, abort) &&
+      // descriptors; a later part of a tile is `bytes >> 4` further on
+      const uint64_t dq = sdesc_sw128(sb + L::kQ, 16, 1024);
+      const uint64_t ds = sdesc_sw128(sb + L::kS, D * 128, 1024);
+      // tile i of the ring: its place, once it has been loaded
+      auto tile = [&](int i) { return sb + L::kKV + (i % L::kSlots) * L::kTile; };
+      auto wait_tile = [&](int i) {
+        ok = ok && lin_wait(kv_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1, abort);
+      };
+      auto free_tile = [&](int i) {
+        if (ok) umma_commit(kv_empty + 8 * (i % L::kSlots));
+      };
+      auto issue_qk = [&](int n, bool last) {
+        wait_tile(2 * n);
+        ok = ok && lin_wait(q_full, nq & 1, abort) &&
              (nq == 0 || lin_wait(o_done, (nq - 1) & 1, abort));  // P of the last pair is read
         if (!ok) return;
         tc_fence_after();
-        const uint32_t kst = sb + L::kK + st * L::kTile;
+        const uint64_t q = here(dq), k = here(sdesc_sw128(tile(2 * n), 16, 1024));
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          umma_bf16(tmem + kTmSc,
-                    sdesc_sw128(sb + L::kQ + (ks >> 2) * (kLinC * 128) + (ks & 3) * 32, 16, 1024),
-                    sdesc_sw128(kst + (ks >> 2) * (kLinC * 128) + (ks & 3) * 32, 16, 1024), kIdQK,
-                    ks > 0);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t at = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
+          umma_bf16(tmem + kTmSc, q + at, k + at, kIdQK, ks > 0);
+        }
         umma_commit(sc_full);
+        if (last) free_tile(2 * n);
         ++nq;
       };
       int m = 0;  // K' terms
       auto issue_kv = [&](int n) {
-        const uint32_t vst = sb + L::kV + (n & 1) * L::kTile;
+        wait_tile(2 * n + 1);
         if (n >= 1) ok = ok && lin_wait(u_free, (n - 1) & 1, abort);
-        if (STATES) ok = ok && lin_wait(kv_full + 8 * (n & 1), (n >> 1) & 1, abort);
+        const uint64_t dv = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
         for (int t = 0; ok && t < 3; ++t, ++m) {
           ok = lin_wait(kp_full + 8 * (m & 1), (m >> 1) & 1, abort);
           if (!ok) return;
           tc_fence_after();
+          const uint64_t v = here(dv);
 #pragma unroll
           for (int ks = 0; ks < kLinC / 16; ++ks)
-            umma_bf16_ts(tmem + kTmU, tmem + kTmKp + 64 * (m & 1) + 8 * ks,
-                         sdesc_sw128(vst + ks * 2048, kLinC * 128, 1024), kIdD, t > 0 || ks > 0);
+            umma_bf16_ts(tmem + kTmU, tmem + kTmKp + 64 * (m & 1) + 8 * ks, v + (ks * 2048 >> 4),
+                         kIdD, t > 0 || ks > 0);
           umma_commit(kp_empty + 8 * (m & 1));
         }
         if (ok) umma_commit(u_done);
       };
-      if (!STATES) issue_qk(0);
+      if (!STATES) issue_qk(0, a.G == 1);
       int pair = 0;
       for (int n = 0; ok && n < nch; ++n) {
-        const uint32_t vst = sb + L::kV + (n & 1) * L::kTile;
         if (STATES) {
           issue_kv(n);
-          if (ok) umma_commit(kv_empty + 8 * (n & 1));
+          free_tile(2 * n);
+          free_tile(2 * n + 1);
           continue;
         }
         for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
@@ -400,33 +458,36 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (pair >= 1) ok = ok && lin_wait(o_free, (pair - 1) & 1, abort);
           if (!ok) break;
           tc_fence_after();
+          const uint64_t q = here(dq), s = here(ds);
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-              umma_bf16(
-                  tmem + kTmOut,
-                  sdesc_sw128(sb + L::kQ + (ks >> 2) * (kLinC * 128) + (ks & 3) * 32, 16, 1024),
-                  sdesc_sw128(sb + L::kS + t * L::kSTerm + ks * 2048, D * 128, 1024), kIdD,
-                  t > 0 || ks > 0);
+              umma_bf16(tmem + kTmOut, q + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4),
+                        s + ((t * L::kSTerm + ks * 2048) >> 4), kIdD, t > 0 || ks > 0);
           umma_commit(qs_done);
           umma_commit(q_empty);
           if (gq == a.G - 1) issue_kv(n);
+          if (gq == 0) {
+            wait_tile(2 * n + 1);
+            ok = ok && lin_wait(v_ready, n & 1, abort);
+          }
           ok = ok && lin_wait(pv_ready, pair & 1, abort);
           if (!ok) break;
           tc_fence_after();
+          const uint64_t dv = here(sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024));
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int ks = 0; ks < kLinC / 16; ++ks)
-              umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 64 * t + 8 * ks,
-                           sdesc_sw128(vst + ks * 2048, kLinC * 128, 1024), kIdD, 1u);
+              umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 64 * t + 8 * ks, dv + (ks * 2048 >> 4),
+                           kIdD, 1u);
           umma_commit(o_done);
-          if (gq == a.G - 1) umma_commit(kv_empty + 8 * (n & 1));
+          if (gq == a.G - 1) free_tile(2 * n + 1);
           if (gq + 1 < a.G)
-            issue_qk(n);
+            issue_qk(n, gq + 2 == a.G);
           else if (n + 1 < nch)
-            issue_qk(n + 1);
+            issue_qk(n + 1, a.G == 1);
         }
       }
       if (!ok) {
@@ -435,6 +496,27 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
       umma_commit(drain);  // every product is complete before tensor memory is released
       (void)mbar_wait(drain, 0);
+    }
+  } else if (warp == 10) {
+    // --------------------------------------------- whole output tiles out
+    if (!STATES && lane == 0) {
+      const int whole = (t1 - t0) / kLinC * a.G;
+      bool ok = true;
+      for (int p = 0; ok && p < whole; ++p) {
+        ok = lin_wait(y_full, p & 1, abort);
+        if (!ok) break;
+        for (int hf = 0; hf < D / 64; ++hf)
+          tma_store_2d(&to, sb + L::kOut + hf * L::kHalf, (h * a.G + p % a.G) * D + 64 * hf,
+                       t0 + p / a.G * kLinC);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        mbar_arrive(y_free);
+      }
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      if (!ok) {
+        set_status(a.status, PHS_ETIMEOUT);
+        *abort = 1;
+      }
     }
   } else if (warp < 4) {
     // ------------------------------------------------- rows of the chunk
@@ -447,27 +529,45 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         ok = lin_wait_warp(sc_full, pair & 1, abort);
         if (!ok) break;
         tc_fence_after();
-        // P: term 0 in columns 0..63 of the scores' place, term 1 in 64..127.
+        // P: term 0 in columns 0..63 of the scores' place, term 1 in 64..127;
+        // columns 32 c .. of a row i are before the diagonal block (c < warp),
+        // where exp(g (i - j)) = exp(g (i - 32 c - 31)) exp(g (32 c + 31 - j)),
+        // on it, or behind it, where P is zero.
         // A half is written once the scores under it have been read.
         uint32_t lo[2][32];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          uint32_t s0[32], s1[32], hi[32];
-          tmem_ld32(my_lanes + kTmSc + 64 * hf, s0);
-          tmem_ld32(my_lanes + kTmSc + 64 * hf + 32, s1);
-          tmem_ld_wait();
+          uint32_t hi[32];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float x[2];
+          for (int q = 0; q < 2; ++q) {
+            const int c = 2 * hf + q;
+            if (c > warp) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = 64 * hf + 2 * c + e, k = (2 * c + e) & 31;
-              const float s = __uint_as_float(c < 16 ? s0[k] : s1[k]);
-              x[e] = j <= i ? s * ps[max(i - j, 0)] : 0.f;
+              for (int e = 0; e < 16; ++e) hi[16 * q + e] = lo[hf][16 * q + e] = 0u;
+              continue;
             }
-            hi[c] = take_term(x[0], x[1]);
-            lo[hf][c] = pack_bf16(x[0], x[1]);
+            uint32_t sc[32];
+            tmem_ld32(my_lanes + kTmSc + 32 * c, sc);
+            tmem_ld_wait();
+            const float rf = ps[max(i - 32 * c - 31, 0)];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float s0 = __uint_as_float(sc[2 * e]), s1 = __uint_as_float(sc[2 * e + 1]);
+              float x0, x1;
+              if (c < warp) {
+                x0 = s0 * (rf * col[2 * e]);
+                x1 = s1 * (rf * col[2 * e + 1]);
+              } else {
+                const int n0 = lane - 2 * e;  // i - j
+                const float f0 = ps[max(n0, 0)], f1 = ps[max(n0 - 1, 0)];
+                x0 = n0 >= 0 ? s0 * f0 : 0.f;
+                x1 = n0 >= 1 ? s1 * f1 : 0.f;
+              }
+              hi[16 * q + e] = take_term(x0, x1);
+              lo[hf][16 * q + e] = pack_bf16(x0, x1);
+            }
           }
+          // (the scores of columns 32.. of the second half's place are read by then)
           tmem_st32(my_lanes + kTmSc + 32 * hf, hi);
         }
         tmem_st32(my_lanes + kTmSc + 64, lo[0]);
@@ -506,13 +606,23 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         tc_fence_before();
         mbar_arrive(o_free);
         const int t = t0 + n * kLinC + i;
-        if (t < t1) {
-          uint4* to = reinterpret_cast<uint4*>(
+        if (t0 + (n + 1) * kLinC <= t1) {  // a whole chunk: through shared memory and TMA
+          if (pair >= 1) ok = lin_wait_warp(y_free, (pair - 1) & 1, abort);
+          if (!ok) break;
+          const uint32_t row = sb + L::kOut + i * 128;
+#pragma unroll
+          for (int u = 0; u < D / 8; ++u)
+            sts128(row + (u >> 3) * L::kHalf + (((u ^ i) & 7) << 4), y[4 * u], y[4 * u + 1],
+                   y[4 * u + 2], y[4 * u + 3]);
+          fence_proxy_async_smem();
+          mbar_arrive(y_full);
+        } else if (t < t1) {  // the rows behind the last are another request's
+          uint4* to_row = reinterpret_cast<uint4*>(
               reinterpret_cast<__nv_bfloat16*>(a.out) +
               (static_cast<size_t>(t) * a.Hq + h * a.G + gq) * D);
 #pragma unroll
           for (int c = 0; c < D / 8; ++c)
-            to[c] = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
+            to_row[c] = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
         }
       }
     if (!STATES && !ok) {
@@ -564,96 +674,126 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       for (int c = 0; c < 8; ++c) tmem_st16(my_lanes + kTmKp + 16 * c, z);
       tmem_st_wait();
     }
-    // byte offsets of column r in rows 0..7 of a K tile
-    uint32_t off[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      off[e] = (r >> 6) * (kLinC * 128) + e * 128 + ((((r >> 3) ^ e) & 7) << 4) + (r & 7) * 2;
     bool ok = true;
     int m = 0;
-    auto add_chunk = [&](int n) {  // S <- state after chunk n
-      if (!ok) return;
-      ok = lin_wait_warp(u_done, n & 1, abort);
-      if (!ok) return;
-      tc_fence_after();
-      const float keep = expm1f(g * min(kLinC, t1 - t0 - n * kLinC));
+    // S <- state after chunk n (n >= 0), and where `terms` its two terms to
+    // shared memory for the next chunk's QS (the last one has read its own
+    // by then: the chunk's sum was issued after it)
+    auto next_state = [&](int n, bool terms) {
+      float keep = 0.f;
+      if (n >= 0) {
+        ok = ok && lin_wait_warp(u_done, n & 1, abort);
+        if (!ok) return;
+        tc_fence_after();
+        keep = expm1f(g * min(kLinC, t1 - t0 - n * kLinC));
+      }
       if (mine) {
+        const uint32_t my_row = sb + L::kS + r * 128;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t u[32];
-          tmem_ld32(my_lanes + kTmU + 32 * c, u);
-          tmem_ld_wait();
+          if (n >= 0) {
+            uint32_t u[32];
+            tmem_ld32(my_lanes + kTmU + 32 * c, u);
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            S[32 * c + e] = decayed(S[32 * c + e], keep) + __uint_as_float(u[e]);
-        }
-      }
-      tc_fence_before();
-      mbar_arrive(u_free);
-    };
-    for (int n = 0; ok && n < nch; ++n) {
-      if (n > 0) add_chunk(n - 1);
-      if (!ok) break;
-      if (!STATES) {
-        if (mine) {
-          uint8_t* rowp = smem + L::kS + r * 128;
-#pragma unroll
-          for (int u = 0; u < D / 8; ++u) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x0 = S[8 * u + 2 * e], x1 = S[8 * u + 2 * e + 1];
-              hi[e] = take_term(x0, x1);
-              lo[e] = pack_bf16(x0, x1);
-            }
-            uint8_t* at = rowp + (u >> 3) * (D * 128) + (((u ^ r) & 7) << 4);
-            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(at + L::kSTerm) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int e = 0; e < 32; ++e)
+              S[32 * c + e] = decayed(S[32 * c + e], keep) + __uint_as_float(u[e]);
           }
-          fence_proxy_async_smem();
+          if (terms) {
+#pragma unroll
+            for (int u = 4 * c; u < 4 * c + 4; ++u) {
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float x0 = S[8 * u + 2 * e], x1 = S[8 * u + 2 * e + 1];
+                hi[e] = take_term(x0, x1);
+                lo[e] = pack_bf16(x0, x1);
+              }
+              const uint32_t at = my_row + (u >> 3) * (D * 128) + (((u ^ r) & 7) << 4);
+              sts128(at, hi[0], hi[1], hi[2], hi[3]);
+              sts128(at + L::kSTerm, lo[0], lo[1], lo[2], lo[3]);
+            }
+          }
         }
-        mbar_arrive(s_ready);
+        if (terms) fence_proxy_async_smem();
       }
-      // K'^T: terms lo2, lo, then hi
-      const int st = n & 1, v = min(kLinC, t1 - t0 - n * kLinC);
-      ok = lin_wait_warp(kv_full + 8 * st, (n >> 1) & 1, abort);
+      if (n >= 0) {
+        tc_fence_before();
+        mbar_arrive(u_free);
+      }
+      if (terms) mbar_arrive(s_ready);
+    };
+    // K'^T of this warp's 32 columns of K: ldmatrix.trans gives thread 4 x + y
+    // tokens 2 y, 2 y + 1 (of 8) of column x of each of 4 groups of 8 columns
+    const int w = warp - 4, kx = lane >> 3;  // matrix kx: columns 32 w + 8 kx ..
+    const uint32_t kcol = (w >> 1) * L::kHalf + (lane & 7) * 128 +
+                          ((((4 * (w & 1) + kx) ^ lane) & 7) << 4);
+    for (int n = 0; ok && n < nch; ++n) {
+      next_state(n - 1, !STATES);
       if (!ok) break;
-      if (v < kLinC) {  // V rows behind the last token: no 0 * NaN
-        uint8_t* tile = smem + L::kV + st * L::kTile;
+      const int v = min(kLinC, t1 - t0 - n * kLinC);
+      const int ki = 2 * n, vi = 2 * n + 1;  // tiles of the ring
+      const uint32_t kt = sb + L::kKV + (ki % L::kSlots) * L::kTile;
+      ok = lin_wait_warp(kv_full + 8 * (ki % L::kSlots), (ki / L::kSlots) & 1, abort);
+      if (!ok) break;
+      if (v < kLinC) {
+        // rows behind the last token: no 0 * NaN.  K: the columns this warp
+        // reads itself (QK may read either; those scores are masked); V: all.
+        ok = lin_wait_warp(kv_full + 8 * (vi % L::kSlots), (vi / L::kSlots) & 1, abort);
+        if (!ok) break;
+        const uint32_t vt = sb + L::kKV + (vi % L::kSlots) * L::kTile;
+        for (int t = v + (lane >> 2); mine && t < kLinC; t += 8)
+          sts128(kt + (w >> 1) * L::kHalf + t * 128 +
+                     ((((4 * (w & 1) + (lane & 3)) ^ t) & 7) << 4),
+                 0, 0, 0, 0);
         for (int u = r; u < D / 64 * (kLinC - v) * 8; u += 128) {
-          const int hf = u / ((kLinC - v) * 8), w = u % ((kLinC - v) * 8);
-          *reinterpret_cast<uint4*>(tile + hf * (kLinC * 128) + v * 128 + w * 16) =
-              make_uint4(0, 0, 0, 0);
+          const int hf = u / ((kLinC - v) * 8), x = u % ((kLinC - v) * 8);
+          sts128(vt + hf * L::kHalf + v * 128 + x * 16, 0, 0, 0, 0);
         }
         fence_proxy_async_smem();
+        __syncwarp();
       }
-      const uint32_t kst = sb + L::kK + st * L::kTile;
-      // k'_t of this row
-      auto kp = [&](int t, int e) {  // t a multiple of 8
-        const float k = lds_bf16(kst + t * 128 + off[e]);
-        return t + e < v ? k * pw[v - 1 - t - e] : 0.f;
-      };
+      if (!STATES) mbar_arrive(v_ready);
       auto wait_empty = [&](int mm) {
         if (mm >= 2) ok = ok && lin_wait_warp(kp_empty + 8 * (mm & 1), ((mm >> 1) - 1) & 1, abort);
       };
+      // weights of this thread's two tokens of group q (0 behind the last)
+      auto weights = [&](int q, float& w0, float& w1) {
+        const int e = v - 1 - 8 * q - 2 * (lane & 3);
+        const float f0 = pw[max(e, 0)], f1 = pw[max(e - 1, 0)];
+        w0 = e >= 0 ? f0 : 0.f;
+        w1 = e >= 1 ? f1 : 0.f;
+      };
+      // terms lo2 and lo
       wait_empty(m);
       wait_empty(m + 1);
       if (!ok) break;
       tc_fence_after();
       if (mine) {
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t w2[16], w1[16];
+        for (int b4 = 0; b4 < 4; ++b4) {  // 32 tokens
+          uint32_t w2[2][8], w1[2][8];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int t = 32 * q + ((2 * c) & ~7), e = (2 * c) & 7;
-            float x0 = kp(t, e), x1 = kp(t, e + 1);
-            (void)take_term(x0, x1);
-            w1[c] = take_term(x0, x1);
-            w2[c] = pack_bf16(x0, x1);
+          for (int q = 0; q < 4; ++q) {
+            uint32_t k[4];
+            ldsm_x4_t(kt + kcol + (4 * b4 + q) * 1024, k[0], k[1], k[2], k[3]);
+            float f0, f1;
+            weights(4 * b4 + q, f0, f1);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              float x0 = __uint_as_float(k[x] << 16) * f0;
+              float x1 = __uint_as_float(k[x] & 0xffff0000u) * f1;
+              (void)take_term(x0, x1);
+              w1[x >> 1][2 * q + (x & 1)] = take_term(x0, x1);
+              w2[x >> 1][2 * q + (x & 1)] = pack_bf16(x0, x1);
+            }
           }
-          tmem_st16(my_lanes + kTmKp + 64 * (m & 1) + 16 * q, w2);
-          tmem_st16(my_lanes + kTmKp + 64 * ((m + 1) & 1) + 16 * q, w1);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t at = my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp + 16 * b4;
+            tmem_st_16x128(at + 64 * (m & 1), w2[x]);
+            tmem_st_16x128(at + 64 * ((m + 1) & 1), w1[x]);
+          }
         }
         tmem_st_wait();
       }
@@ -661,28 +801,40 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       mbar_arrive(kp_full + 8 * (m & 1));
       mbar_arrive(kp_full + 8 * ((m + 1) & 1));
       m += 2;
+      // term hi
       wait_empty(m);
       if (!ok) break;
       tc_fence_after();
       if (mine) {
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t w0[16];
+        for (int b4 = 0; b4 < 4; ++b4) {
+          uint32_t w0[2][8];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int t = 32 * q + ((2 * c) & ~7), e = (2 * c) & 7;
-            w0[c] = pack_bf16(kp(t, e), kp(t, e + 1));
+          for (int q = 0; q < 4; ++q) {
+            uint32_t k[4];
+            ldsm_x4_t(kt + kcol + (4 * b4 + q) * 1024, k[0], k[1], k[2], k[3]);
+            float f0, f1;
+            weights(4 * b4 + q, f0, f1);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              w0[x >> 1][2 * q + (x & 1)] = pack_bf16(__uint_as_float(k[x] << 16) * f0,
+                                                      __uint_as_float(k[x] & 0xffff0000u) * f1);
           }
-          tmem_st16(my_lanes + kTmKp + 64 * (m & 1) + 16 * q, w0);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            tmem_st_16x128(my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp + 16 * b4 +
+                               64 * (m & 1),
+                           w0[x]);
         }
         tmem_st_wait();
       }
       tc_fence_before();
       mbar_arrive(kp_full + 8 * (m & 1));
-      mbar_arrive(kv_empty + 8 * st);
+      mbar_arrive(kv_empty + 8 * (ki % L::kSlots));
+      mbar_arrive(kv_empty + 8 * (vi % L::kSlots));
       ++m;
     }
-    if (nch > 0) add_chunk(nch - 1);
+    if (nch > 0) next_state(nch - 1, false);
     if (!ok) {
       set_status(a.status, PHS_ETIMEOUT);
       *abort = 1;
@@ -700,7 +852,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
 template <int D>
 static int launch_linear_prompt_t(const CUtensorMap& tq, const CUtensorMap& tk,
-                                  const CUtensorMap& tv, const LinearArgs& a, cudaStream_t stream) {
+                                  const CUtensorMap& tv, const CUtensorMap& to,
+                                  const LinearArgs& a, cudaStream_t stream) {
   using L = LinLayout<D>;
   auto states = phs_linear_prompt_kernel<D, true>;
   auto rows = phs_linear_prompt_kernel<D, false>;
@@ -708,15 +861,16 @@ static int launch_linear_prompt_t(const CUtensorMap& tq, const CUtensorMap& tk,
       ensure_dynamic_smem(reinterpret_cast<const void*>(states), L::kAlloc) != PHS_OK)
     return PHS_ECUDA;
   if (a.nseg > 1)
-    states<<<dim3(a.B, a.Hkv, a.nseg - 1), kLinThreads, L::kAlloc, stream>>>(tq, tk, tv, a);
-  rows<<<dim3(a.B, a.Hkv, a.nseg), kLinThreads, L::kAlloc, stream>>>(tq, tk, tv, a);
+    states<<<dim3(a.B, a.Hkv, a.nseg - 1), kLinThreads, L::kAlloc, stream>>>(tq, tk, tv, to, a);
+  rows<<<dim3(a.B, a.Hkv, a.nseg), kLinThreads, L::kAlloc, stream>>>(tq, tk, tv, to, a);
   return cudaGetLastError() == cudaSuccess ? PHS_OK : PHS_ECUDA;
 }
 
 int launch_linear_prompt(int D, const CUtensorMap& tq, const CUtensorMap& tk,
-                         const CUtensorMap& tv, const LinearArgs& a, cudaStream_t stream) {
-  return D == 128 ? launch_linear_prompt_t<128>(tq, tk, tv, a, stream)
-                  : launch_linear_prompt_t<64>(tq, tk, tv, a, stream);
+                         const CUtensorMap& tv, const CUtensorMap& to, const LinearArgs& a,
+                         cudaStream_t stream) {
+  return D == 128 ? launch_linear_prompt_t<128>(tq, tk, tv, to, a, stream)
+                  : launch_linear_prompt_t<64>(tq, tk, tv, to, a, stream);
 }
 
 }  // namespace phs

@@ -139,6 +139,7 @@ constexpr int kLinearChunk = 128;  // tokens
 
 int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream);
 int launch_linear_prompt(int D, const CUtensorMap& tq, const CUtensorMap& tk,
-                         const CUtensorMap& tv, const LinearArgs& a, cudaStream_t stream);
+                         const CUtensorMap& tv, const CUtensorMap& to, const LinearArgs& a,
+                         cudaStream_t stream);
 
 }  // namespace phs
