@@ -143,15 +143,18 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // over a long memory would pull the state down.
 //
 // One CTA per (segment, KV head, request) walks its chunks in order:
-//   warps 0-3  rows of the chunk: scores -> P, the inter-chunk part scaled,
-//              the output rows
-//   warps 4-7  rows of the state (one per thread, in registers): state ->
-//              two terms in shared memory, K tile -> K'^T terms
-//   warp 8     TMA loads: a ring of three K and V tiles, one Q tile
-//   warp 9     issues the products: QS, KV, PV, then QK of the next chunk,
-//              so that the state's and P's way through the registers runs
-//              beside them
-//   warp 10    TMA stores of the output tile (warp 11 fills the warpgroup)
+//   warps 0-7   rows of the chunk, two threads a row: scores -> P, the
+//               inter-chunk part scaled, the output rows
+//   warps 8-15  rows of the state, two threads a row, in registers: state ->
+//               two terms in shared memory, K tile -> K'^T terms
+//   warp 16     TMA loads: a ring of three K and V tiles, one Q tile
+//   warp 17     issues the products: QS, KV, PV, then QK of the next chunk,
+//               so that the state's and P's way through the registers runs
+//               beside them
+//   warp 18     TMA stores of the output tile (warp 19 fills the warpgroup)
+// Two warps on each scheduler run each role's code, and its loops are kept
+// small: with one warp and everything unrolled, fetching instructions was
+// the largest stall (3.1 of 10.7 warp-cycles an instruction).
 // What a chunk moves through shared memory bounds the kernel next to HBM: at
 // D = 128 the products read 352 KB, copies and registers move 300 KB, about
 // 5,200 cycles of 128 bytes; its share of HBM (128 KB) takes 5,300.
@@ -159,10 +162,9 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // into segments: a first launch sums up each segment's own state (K and V
 // alone), the second starts each segment from the joined states before it.
 constexpr int kLinC = kLinearChunk;
-constexpr int kLinThreads = 384;
-// registers a thread: 168 at launch; the third warpgroup (copies, products)
-// gives up what the other two take, 88 + 184 + 232 = 3 x 168
-constexpr int kLinRegsRows = 184, kLinRegsState = 232, kLinRegsIssue = 88;
+constexpr int kLinThreads = 640;
+// registers a thread: 96 at launch, five warpgroups; 2 x 88 + 2 x 120 + 64 = 5 x 96
+constexpr int kLinRegsRows = 88, kLinRegsState = 120, kLinRegsIssue = 64;
 constexpr uint32_t kTmU = 0, kTmSc = 128, kTmOut = 256, kTmKp = 384;  // tensor-memory columns
 
 template <int D>
@@ -178,7 +180,7 @@ struct LinLayout {
   static constexpr int kBar = kS + 2 * kSTerm;
   static constexpr int kMisc = kBar + 24 * 8;  // tensor-memory base, abort flag
   static constexpr int kAlloc = kMisc + 16 + 1024;
-  static constexpr int kTables = (2 * (kLinC + 4) + 32) * 4;  // static
+  static constexpr int kTables = (2 * (kLinC + 4) + 32) * 4;  // static: pw, ps and its pad
   static_assert(kAlloc + kTables <= 227 * 1024, "shared memory of the prompt kernel");
 };
 
@@ -242,11 +244,21 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
 
 // Tensor-memory store in the layout that ldmatrix.trans delivers: 16 lanes,
 // 4 N columns; thread 4 r + c holds column 4 i + c of lanes r (word 2 i) and
-// r + 8 (word 2 i + 1).  Here N = 4.
-__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[8]) {
+// r + 8 (word 2 i + 1).  Here N = 2.
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 
@@ -267,8 +279,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                              const __grid_constant__ LinearArgs a) {
   using L = LinLayout<D>;
   extern __shared__ uint8_t smem_raw[];
-  // pw[n] = exp(g n), ps[n] = scale pw[n], col[n] = pw[31 - n]
-  __shared__ float pw[kLinC + 4], ps[kLinC + 4], col[32];
+  // pw[n] = exp(g n), ps[n] = scale pw[n]; ps is read from n = -31 on (unused there)
+  __shared__ float pw[kLinC + 4], ps_pad[32 + kLinC + 4];
+  const float* ps = ps_pad + 32;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -308,32 +321,32 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                  u_done = s_ready + 8, u_free = u_done + 8, y_full = u_free + 8,
                  y_free = y_full + 8, v_ready = y_free + 8, drain = v_ready + 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(sb + L::kMisc, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(kv_full + 8 * i, 1);
-      mbar_init(kv_empty + 8 * i, 129);  // the products, and the 128 state rows
+      mbar_init(kv_empty + 8 * i, 257);  // the products, and the 256 state threads
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(kp_full + 8 * i, 128);
+      mbar_init(kp_full + 8 * i, 256);
       mbar_init(kp_empty + 8 * i, 1);
     }
-    mbar_init(v_ready, 128);
-    mbar_init(y_full, 128);
+    mbar_init(v_ready, 256);
+    mbar_init(y_full, 256);
     mbar_init(y_free, 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(sc_full, 1);
     mbar_init(qs_done, 1);
-    mbar_init(pv_ready, 128);
+    mbar_init(pv_ready, 256);
     mbar_init(o_done, 1);
-    mbar_init(o_free, 128);
-    mbar_init(s_ready, 128);
+    mbar_init(o_free, 256);
+    mbar_init(s_ready, 256);
     mbar_init(u_done, 1);
-    mbar_init(u_free, 128);
+    mbar_init(u_free, 256);
     mbar_init(drain, 1);
     *abort = 0;
     fence_mbar_init();
@@ -341,8 +354,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   for (int n = tid; n <= kLinC; n += kLinThreads) {
     const float p = expf(g * n);
     pw[n] = p;
-    ps[n] = p * a.scale;
-    if (n < 32) col[31 - n] = p;
+    ps_pad[32 + n] = p * a.scale;
+    if (n < 32) ps_pad[n] = 0.f;
   }
   tc_fence_before();
   __syncthreads();
@@ -350,8 +363,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
   const uint32_t my_lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
 
-  if (warp >= 8) regs_dec<kLinRegsIssue>();
-  if (warp == 8) {
+  if (warp >= 16) regs_dec<kLinRegsIssue>();
+  if (warp == 16) {
     // ---------------------------------------------------------------- TMA
     if (lane == 0 && nch > 0) {
       const uint64_t pol = policy_evict_first();
@@ -392,7 +405,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         (void)mbar_wait(kv_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1);
       if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ----------------------------------------------------------- products
     if (lane == 0 && nch > 0) {
       constexpr uint32_t kIdQK = idesc_bf16_f32(128, kLinC, false, false);
@@ -480,7 +493,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int ks = 0; ks < kLinC / 16; ++ks)
-              umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 64 * t + 8 * ks, dv + (ks * 2048 >> 4),
+              umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 16 * ks + 8 * t, dv + (ks * 2048 >> 4),
                            kIdD, 1u);
           umma_commit(o_done);
           if (gq == a.G - 1) free_tile(2 * n + 1);
@@ -497,7 +510,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       umma_commit(drain);  // every product is complete before tensor memory is released
       (void)mbar_wait(drain, 0);
     }
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     // --------------------------------------------- whole output tiles out
     if (!STATES && lane == 0) {
       const int whole = (t1 - t0) / kLinC * a.G;
@@ -518,67 +531,49 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         *abort = 1;
       }
     }
-  } else if (warp < 4) {
+  } else if (warp < 8) {
     // ------------------------------------------------- rows of the chunk
-    regs_inc<kLinRegsRows>();
-    const int i = tid;  // row
-    bool ok = !STATES;
+    regs_dec<kLinRegsRows>();
+    const int qt = warp & 3, half = warp >> 2, i = 32 * qt + lane;  // row
+    bool ok = true;
     int pair = 0;
-    for (int n = 0; ok && n < nch; ++n)
+    const int chunks = STATES ? 0 : nch;
+    for (int n = 0; ok && n < chunks; ++n)
       for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
         ok = lin_wait_warp(sc_full, pair & 1, abort);
         if (!ok) break;
         tc_fence_after();
-        // P: term 0 in columns 0..63 of the scores' place, term 1 in 64..127;
-        // columns 32 c .. of a row i are before the diagonal block (c < warp),
-        // where exp(g (i - j)) = exp(g (i - 32 c - 31)) exp(g (32 c + 31 - j)),
-        // on it, or behind it, where P is zero.
-        // A half is written once the scores under it have been read.
-        uint32_t lo[2][32];
+        // P in place of the scores: 16 columns j of a step of the product
+        // become 8 of term 0 and 8 of term 1
+#pragma unroll 1
+        for (int st = half; st < kLinC / 16; st += 2) {
+          uint32_t p[16];
+          const int d = i - 16 * st;
+          if (16 * st > 32 * qt + 31) {  // behind every row of the warp
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t hi[32];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int c = 2 * hf + q;
-            if (c > warp) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) hi[16 * q + e] = lo[hf][16 * q + e] = 0u;
-              continue;
-            }
-            uint32_t sc[32];
-            tmem_ld32(my_lanes + kTmSc + 32 * c, sc);
+            for (int e = 0; e < 16; ++e) p[e] = 0u;
+          } else {
+            uint32_t sc[16];
+            tmem_ld16(my_lanes + kTmSc + 16 * st, sc);
             tmem_ld_wait();
-            const float rf = ps[max(i - 32 * c - 31, 0)];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float s0 = __uint_as_float(sc[2 * e]), s1 = __uint_as_float(sc[2 * e + 1]);
-              float x0, x1;
-              if (c < warp) {
-                x0 = s0 * (rf * col[2 * e]);
-                x1 = s1 * (rf * col[2 * e + 1]);
-              } else {
-                const int n0 = lane - 2 * e;  // i - j
-                const float f0 = ps[max(n0, 0)], f1 = ps[max(n0 - 1, 0)];
-                x0 = n0 >= 0 ? s0 * f0 : 0.f;
-                x1 = n0 >= 1 ? s1 * f1 : 0.f;
-              }
-              hi[16 * q + e] = take_term(x0, x1);
-              lo[hf][16 * q + e] = pack_bf16(x0, x1);
+            for (int e = 0; e < 8; ++e) {
+              const float y0 = __uint_as_float(sc[2 * e]) * ps[d - 2 * e];
+              const float y1 = __uint_as_float(sc[2 * e + 1]) * ps[d - 2 * e - 1];
+              float x0 = d >= 2 * e ? y0 : 0.f, x1 = d >= 2 * e + 1 ? y1 : 0.f;
+              p[e] = take_term(x0, x1);
+              p[8 + e] = pack_bf16(x0, x1);
             }
           }
-          // (the scores of columns 32.. of the second half's place are read by then)
-          tmem_st32(my_lanes + kTmSc + 32 * hf, hi);
+          tmem_st16(my_lanes + kTmSc + 16 * st, p);
         }
-        tmem_st32(my_lanes + kTmSc + 64, lo[0]);
-        tmem_st32(my_lanes + kTmSc + 96, lo[1]);
         // the part before the chunk, scaled in place
         ok = lin_wait_warp(qs_done, pair & 1, abort);
         if (!ok) break;
         tc_fence_after();
         const float f = ps[i + 1];
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+        for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
           uint32_t o[32];
           tmem_ld32(my_lanes + kTmOut + 32 * c, o);
           tmem_ld_wait();
@@ -589,61 +584,64 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(pv_ready);
-        // output row
-        ok = lin_wait_warp(o_done, pair & 1, abort);
+        // output row: a whole chunk's goes through shared memory and TMA; the
+        // rows behind a last token are another request's
+        const int t = t0 + n * kLinC + i;
+        const bool whole = t0 + (n + 1) * kLinC <= t1;
+        ok = lin_wait_warp(o_done, pair & 1, abort) &&
+             (!whole || pair == 0 || lin_wait_warp(y_free, (pair - 1) & 1, abort));
         if (!ok) break;
         tc_fence_after();
-        uint32_t y[D / 2];
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
+        const uint32_t row = sb + L::kOut + i * 128;
+        uint4* to_row = reinterpret_cast<uint4*>(
+            reinterpret_cast<__nv_bfloat16*>(a.out) +
+            (static_cast<size_t>(t) * a.Hq + h * a.G + gq) * D);
+#pragma unroll 1
+        for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
+          uint32_t o[32], y[16];
           tmem_ld32(my_lanes + kTmOut + 32 * c, o);
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            y[16 * c + e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            y[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int u = 4 * c + k;  // 16 bytes of the row
+            if (whole)
+              sts128(row + (u >> 3) * L::kHalf + (((u ^ i) & 7) << 4), y[4 * k], y[4 * k + 1],
+                     y[4 * k + 2], y[4 * k + 3]);
+            else if (t < t1)
+              to_row[u] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+          }
         }
         tc_fence_before();
         mbar_arrive(o_free);
-        const int t = t0 + n * kLinC + i;
-        if (t0 + (n + 1) * kLinC <= t1) {  // a whole chunk: through shared memory and TMA
-          if (pair >= 1) ok = lin_wait_warp(y_free, (pair - 1) & 1, abort);
-          if (!ok) break;
-          const uint32_t row = sb + L::kOut + i * 128;
-#pragma unroll
-          for (int u = 0; u < D / 8; ++u)
-            sts128(row + (u >> 3) * L::kHalf + (((u ^ i) & 7) << 4), y[4 * u], y[4 * u + 1],
-                   y[4 * u + 2], y[4 * u + 3]);
+        if (whole) {
           fence_proxy_async_smem();
           mbar_arrive(y_full);
-        } else if (t < t1) {  // the rows behind the last are another request's
-          uint4* to_row = reinterpret_cast<uint4*>(
-              reinterpret_cast<__nv_bfloat16*>(a.out) +
-              (static_cast<size_t>(t) * a.Hq + h * a.G + gq) * D);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            to_row[c] = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
         }
       }
-    if (!STATES && !ok) {
+    if (!ok) {
       set_status(a.status, PHS_ETIMEOUT);
       *abort = 1;
     }
-  } else if (warp < 8) {
+  } else if (warp < 16) {
     // ------------------------------------------------- rows of the state
     regs_inc<kLinRegsState>();
-    const int r = tid - 128;  // row (a k index); D = 64: the upper half has none
+    constexpr int N = D / 2;  // columns of a thread
+    const int qt = warp & 3, half = (warp >> 2) & 1;
+    const int r = 32 * qt + lane;  // row (a k index); D = 64: the upper half has none
     const bool mine = r < D;
-    const size_t row = static_cast<size_t>(r) * D;
+    const size_t row = static_cast<size_t>(r) * D + half * N;
     float* pool = a.state + (id * a.Hkv + h) * D * D + row;
     float* ws = a.ws + (static_cast<size_t>(b) * a.Hkv + h) * a.nseg * D * D + row;
     const bool resume = a.resume != nullptr && a.resume[b] != 0;
-    float S[D];
+    float S[N];
 #pragma unroll
-    for (int c = 0; c < D; ++c) S[c] = 0.f;
+    for (int c = 0; c < N; ++c) S[c] = 0.f;
     auto load_row = [&](const float* from, float keep_m1) {  // S <- exp() S + from
 #pragma unroll
-      for (int c = 0; c < D; c += 4) {
+      for (int c = 0; c < N; c += 4) {
         const float4 x = *reinterpret_cast<const float4*>(from + c);
         S[c] = decayed(S[c], keep_m1) + x.x;
         S[c + 1] = decayed(S[c + 1], keep_m1) + x.y;
@@ -653,21 +651,22 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     };
     auto store_row = [&](float* to) {
 #pragma unroll
-      for (int c = 0; c < D; c += 4)
+      for (int c = 0; c < N; c += 4)
         *reinterpret_cast<float4*>(to + c) = make_float4(S[c], S[c + 1], S[c + 2], S[c + 3]);
     };
     if (mine) {
-      if (seg == 0) {
-        // with several segments the pool's state is overwritten by the last
-        // one's CTA: the first launch keeps a copy for the second
-        if (resume) load_row(!STATES && segs > 1 ? ws + (a.nseg - 1) * D * D : pool, 0.f);
-        if (STATES && resume) store_row(ws + (a.nseg - 1) * D * D);
-      } else if (!STATES) {
+      // with several segments the pool's state is overwritten by the last
+      // one's CTA: the first launch keeps a copy for the second
+      float* copy = ws + (a.nseg - 1) * D * D;
+      if (seg > 0 ? !STATES : resume) {
+        const float* from = seg > 0 ? ws : !STATES && segs > 1 ? copy : pool;
         const float keep = expm1f(g * (per * kLinC));
-        for (int s = 0; s < seg; ++s) load_row(ws + s * D * D, keep);
+#pragma unroll 1
+        for (int s = 0; s < max(seg, 1); ++s) load_row(from + s * D * D, keep);
+        if (STATES) store_row(copy);
       }
     }
-    if (!mine) {  // D = 64: rows 64..127 of K'^T are zero
+    if (!mine && half == 0) {  // D = 64: rows 64..127 of K'^T are zero
       uint32_t z[16];
 #pragma unroll
       for (int c = 0; c < 16; ++c) z[c] = 0u;
@@ -690,10 +689,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       if (mine) {
         const uint32_t my_row = sb + L::kS + r * 128;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < N / 32; ++c) {
           if (n >= 0) {
             uint32_t u[32];
-            tmem_ld32(my_lanes + kTmU + 32 * c, u);
+            tmem_ld32(my_lanes + kTmU + half * N + 32 * c, u);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -701,14 +700,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
           if (terms) {
 #pragma unroll
-            for (int u = 4 * c; u < 4 * c + 4; ++u) {
+            for (int k = 0; k < 4; ++k) {
               uint32_t hi[4], lo[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                float x0 = S[8 * u + 2 * e], x1 = S[8 * u + 2 * e + 1];
+                float x0 = S[32 * c + 8 * k + 2 * e], x1 = S[32 * c + 8 * k + 2 * e + 1];
                 hi[e] = take_term(x0, x1);
                 lo[e] = pack_bf16(x0, x1);
               }
+              const int u = half * (N / 8) + 4 * c + k;  // 16 bytes of the row
               const uint32_t at = my_row + (u >> 3) * (D * 128) + (((u ^ r) & 7) << 4);
               sts128(at, hi[0], hi[1], hi[2], hi[3]);
               sts128(at + L::kSTerm, lo[0], lo[1], lo[2], lo[3]);
@@ -723,11 +723,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
       if (terms) mbar_arrive(s_ready);
     };
-    // K'^T of this warp's 32 columns of K: ldmatrix.trans gives thread 4 x + y
-    // tokens 2 y, 2 y + 1 (of 8) of column x of each of 4 groups of 8 columns
-    const int w = warp - 4, kx = lane >> 3;  // matrix kx: columns 32 w + 8 kx ..
-    const uint32_t kcol = (w >> 1) * L::kHalf + (lane & 7) * 128 +
-                          ((((4 * (w & 1) + kx) ^ lane) & 7) << 4);
+    // K'^T of 32 columns of K: ldmatrix.trans gives thread 4 x + y tokens 2 y,
+    // 2 y + 1 (of 8) of column x of each of 4 groups of 8 columns.  The two
+    // warps of a quarter take steps of 16 tokens in turn.
+    const int kx = lane >> 3;  // matrix kx: columns 32 qt + 8 kx ..
+    const uint32_t kcol = (qt >> 1) * L::kHalf + (lane & 7) * 128 +
+                          ((((4 * (qt & 1) + kx) ^ lane) & 7) << 4);
     for (int n = 0; ok && n < nch; ++n) {
       next_state(n - 1, !STATES);
       if (!ok) break;
@@ -743,10 +744,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (!ok) break;
         const uint32_t vt = sb + L::kKV + (vi % L::kSlots) * L::kTile;
         for (int t = v + (lane >> 2); mine && t < kLinC; t += 8)
-          sts128(kt + (w >> 1) * L::kHalf + t * 128 +
-                     ((((4 * (w & 1) + (lane & 3)) ^ t) & 7) << 4),
-                 0, 0, 0, 0);
-        for (int u = r; u < D / 64 * (kLinC - v) * 8; u += 128) {
+          if (((t >> 4) & 1) == half)
+            sts128(kt + (qt >> 1) * L::kHalf + t * 128 +
+                       ((((4 * (qt & 1) + (lane & 3)) ^ t) & 7) << 4),
+                   0, 0, 0, 0);
+        for (int u = tid - 256; u < D / 64 * (kLinC - v) * 8; u += 256) {
           const int hf = u / ((kLinC - v) * 8), x = u % ((kLinC - v) * 8);
           sts128(vt + hf * L::kHalf + v * 128 + x * 16, 0, 0, 0, 0);
         }
@@ -771,14 +773,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       tc_fence_after();
       if (mine) {
 #pragma unroll 1
-        for (int b4 = 0; b4 < 4; ++b4) {  // 32 tokens
-          uint32_t w2[2][8], w1[2][8];
+        for (int st = half; st < kLinC / 16; st += 2) {
+          uint32_t w2[2][4], w1[2][4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             uint32_t k[4];
-            ldsm_x4_t(kt + kcol + (4 * b4 + q) * 1024, k[0], k[1], k[2], k[3]);
+            ldsm_x4_t(kt + kcol + (2 * st + q) * 1024, k[0], k[1], k[2], k[3]);
             float f0, f1;
-            weights(4 * b4 + q, f0, f1);
+            weights(2 * st + q, f0, f1);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               float x0 = __uint_as_float(k[x] << 16) * f0;
@@ -790,7 +792,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t at = my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp + 16 * b4;
+            const uint32_t at = my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp + 8 * st;
             tmem_st_16x128(at + 64 * (m & 1), w2[x]);
             tmem_st_16x128(at + 64 * ((m + 1) & 1), w1[x]);
           }
@@ -807,14 +809,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       tc_fence_after();
       if (mine) {
 #pragma unroll 1
-        for (int b4 = 0; b4 < 4; ++b4) {
-          uint32_t w0[2][8];
+        for (int st = half; st < kLinC / 16; st += 2) {
+          uint32_t w0[2][4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             uint32_t k[4];
-            ldsm_x4_t(kt + kcol + (4 * b4 + q) * 1024, k[0], k[1], k[2], k[3]);
+            ldsm_x4_t(kt + kcol + (2 * st + q) * 1024, k[0], k[1], k[2], k[3]);
             float f0, f1;
-            weights(4 * b4 + q, f0, f1);
+            weights(2 * st + q, f0, f1);
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               w0[x >> 1][2 * q + (x & 1)] = pack_bf16(__uint_as_float(k[x] << 16) * f0,
@@ -822,7 +824,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            tmem_st_16x128(my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp + 16 * b4 +
+            tmem_st_16x128(my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp + 8 * st +
                                64 * (m & 1),
                            w0[x]);
         }
@@ -844,7 +846,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
