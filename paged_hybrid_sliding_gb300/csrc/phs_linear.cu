@@ -137,20 +137,20 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // fp32 one.  They enter as sums of bf16 terms: P and S as two (16 bits of
 // each value; one term would put its 2^-9 beside the output's own rounding),
 // K' as three (24 bits: the state is kept in fp32 and must stay one), and V
-// and Q are exact.  KV is accumulated from its smallest term up, chunk by
-// chunk from zero, and added to the state in fp32 registers: the tensor
-// cores' own sums drop the bits below the running sum's last one, which
-// over a long memory would pull the state down.
+// and Q are exact.  KV is accumulated chunk by chunk from zero and added to
+// the state in fp32 registers: the tensor cores' own sums drop the bits
+// below the running sum's last one, which over a long memory would pull the
+// state down.
 //
 // One CTA per (segment, KV head, request) walks its chunks in order:
 //   warps 0-7   rows of the chunk, two threads a row: scores -> P, the
 //               inter-chunk part scaled, the output rows
 //   warps 8-15  rows of the state, two threads a row, in registers: state ->
 //               two terms in shared memory, K tile -> K'^T terms
-//   warp 16     TMA loads: a ring of three K and V tiles, one Q tile
-//   warp 17     issues the products: QS, KV, PV, then QK of the next chunk,
+//   warp 16     issues the products: half of KV, QK, QS, the rest of KV, PV,
 //               so that the state's and P's way through the registers runs
-//               beside them
+//               beside them (on the scheduler with the least of P's work)
+//   warp 17     TMA loads: a ring of three K and V tiles, one Q tile
 //   warp 18     TMA stores of the output tile (warp 19 fills the warpgroup)
 // Two warps on each scheduler run each role's code, and its loops are kept
 // small: with one warp and everything unrolled, fetching instructions was
@@ -166,6 +166,10 @@ constexpr int kLinThreads = 640;
 // registers a thread: 96 at launch, five warpgroups; 2 x 88 + 2 x 120 + 64 = 5 x 96
 constexpr int kLinRegsRows = 88, kLinRegsState = 120, kLinRegsIssue = 64;
 constexpr uint32_t kTmU = 0, kTmSc = 128, kTmOut = 256, kTmKp = 384;  // tensor-memory columns
+// K'^T goes in quarters of a chunk, 32 tokens at a time: 16 columns for each
+// of the three terms, two buffers
+constexpr int kLinQuarters = 4;
+constexpr uint32_t kTmKpBuf = 48;
 
 template <int D>
 struct LinLayout {
@@ -220,18 +224,58 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-// The value, in a register of its own from here: sums of it with constants
-// are then formed where they are used and not all kept across a loop.
-__device__ __forceinline__ uint64_t here(uint64_t x) {
-  asm volatile("" : "+l"(x));
-  return x;
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
-// bf16 pair of two values; the values keep what it leaves of them
-__device__ __forceinline__ uint32_t take_term(float& x0, float& x1) {
-  const uint32_t w = pack_bf16(x0, x1);
-  x0 -= __uint_as_float(w << 16);
-  x1 -= __uint_as_float(w & 0xffff0000u);
+// Pairs of fp32 values, two to an instruction.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_bf16(uint32_t w) { return f2(w << 16, w & 0xffff0000u); }
+__device__ __forceinline__ float2 f2_get(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// bf16 pair of two values, and with take_term the values keep what it leaves
+__device__ __forceinline__ uint32_t pack_term(uint64_t x) {
+  const float2 v = f2_get(x);
+  return pack_bf16(v.x, v.y);
+}
+__device__ __forceinline__ uint32_t take_term(uint64_t& x) {
+  const uint32_t w = pack_term(x);
+  x = f2_fma(f2_bf16(w), f2(-1.f, -1.f), x);
   return w;
 }
 
@@ -285,7 +329,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
   const int b = blockIdx.x, h = blockIdx.y, seg = blockIdx.z;
 
   // ---- this CTA's chunks
@@ -321,7 +366,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                  u_done = s_ready + 8, u_free = u_done + 8, y_full = u_free + 8,
                  y_free = y_full + 8, v_ready = y_free + 8, drain = v_ready + 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
-  if (warp == 17) {
+  if (warp == 16) {
     tmem_alloc(sb + L::kMisc, 512);
     tmem_relinquish();
   }
@@ -360,11 +405,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
+  const uint32_t tmem =
+      __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + L::kMisc), 0);
   const uint32_t my_lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
 
   if (warp >= 16) regs_dec<kLinRegsIssue>();
-  if (warp == 16) {
+  if (warp < 8) regs_dec<kLinRegsRows>();
+  if (warp == 17) {
     // ---------------------------------------------------------------- TMA
     if (lane == 0 && nch > 0) {
       const uint64_t pol = policy_evict_first();
@@ -405,90 +452,104 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         (void)mbar_wait(kv_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1);
       if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
     }
-  } else if (warp == 17) {
+  } else if (warp == 16) {
     // ----------------------------------------------------------- products
-    if (lane == 0 && nch > 0) {
-      constexpr uint32_t kIdQK = idesc_bf16_f32(128, kLinC, false, false);
-      constexpr uint32_t kIdD = idesc_bf16_f32(128, D, false, true);
-      bool ok = true;
-      int nq = 0;  // (chunk, query head) pairs whose QK has been issued
-      // descriptors; a later part of a tile is `bytes >> 4` further on
-      const uint64_t dq = sdesc_sw128(sb + L::kQ, 16, 1024);
-      const uint64_t ds = sdesc_sw128(sb + L::kS, D * 128, 1024);
-      // tile i of the ring: its place, once it has been loaded
-      auto tile = [&](int i) { return sb + L::kKV + (i % L::kSlots) * L::kTile; };
-      auto wait_tile = [&](int i) {
-        ok = ok && lin_wait(kv_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1, abort);
-      };
-      auto free_tile = [&](int i) {
-        if (ok) umma_commit(kv_empty + 8 * (i % L::kSlots));
-      };
-      auto issue_qk = [&](int n, bool last) {
-        wait_tile(2 * n);
-        ok = ok && lin_wait(q_full, nq & 1, abort) &&
-             (nq == 0 || lin_wait(o_done, (nq - 1) & 1, abort));  // P of the last pair is read
-        if (!ok) return;
+    // The whole warp walks the chunks and one elected lane issues: what the
+    // instructions take is then known to be the same in every lane, and the
+    // compiler keeps it in uniform registers (issued from a lane of its own,
+    // an instruction took 90 cycles and more, whatever its width).
+    constexpr uint32_t kIdQK = idesc_bf16_f32(128, kLinC, false, false);
+    constexpr uint32_t kIdD = idesc_bf16_f32(128, D, false, true);
+    bool ok = true;
+    const bool lead = elect_one();
+    // descriptors; a later part of a tile is `bytes >> 4` further on
+    const uint64_t dq = sdesc_sw128(sb + L::kQ, 16, 1024);
+    const uint64_t ds = sdesc_sw128(sb + L::kS, D * 128, 1024);
+    auto wait = [&](uint32_t bar, int turn) {
+      ok = ok && lin_wait_warp(bar, turn & 1, abort);
+    };
+    // tile i of the ring: its place, once it has been loaded
+    auto tile = [&](int i) { return sb + L::kKV + (i % L::kSlots) * L::kTile; };
+    auto tile_full = [&](int i) { wait(kv_full + 8 * (i % L::kSlots), i / L::kSlots); };
+    auto tile_empty = [&](int i) { return kv_empty + 8 * (i % L::kSlots); };
+    int m = 0;  // K' quarters
+    auto kv_quarter = [&](int j, uint64_t dv) {
+      wait(kp_full + 8 * (m & 1), m >> 1);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t v = dv + (j * 2 * 2048 >> 4);
+      const uint32_t kp = tmem + kTmKp + kTmKpBuf * (m & 1);
+      if (lead) {
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            umma_bf16_ts(tmem + kTmU, kp + 16 * t + 8 * ks, v + (ks * 2048 >> 4), kIdD,
+                         j > 0 || t > 0 || ks > 0);
+        umma_commit(kp_empty + 8 * (m & 1));
+        if (j == kLinQuarters - 1) umma_commit(u_done);
+      }
+      __syncwarp();
+      ++m;
+    };
+    int pair = 0;
+    for (int n = 0; ok && n < nch; ++n) {
+      // the first half of KV needs nothing of this chunk's rows: it runs while
+      // the last chunk's product is still being completed
+      tile_full(2 * n + 1);
+      if (!STATES) wait(v_ready, n);
+      if (n >= 1) wait(u_free, n - 1);
+      const uint64_t dv = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
+#pragma unroll 1
+      for (int j = 0; j < (STATES ? kLinQuarters : kLinQuarters / 2); ++j) kv_quarter(j, dv);
+      if (STATES) {
+        if (ok && lead) {
+          umma_commit(tile_empty(2 * n));
+          umma_commit(tile_empty(2 * n + 1));
+        }
+        continue;
+      }
+      for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
+        const bool last = gq == a.G - 1;
+        if (gq == 0) tile_full(2 * n);
+        wait(q_full, pair);
+        if (pair >= 1) wait(o_done, pair - 1);  // P of the last pair is read
+        if (!ok) break;
         tc_fence_after();
-        const uint64_t q = here(dq), k = here(sdesc_sw128(tile(2 * n), 16, 1024));
+        const uint64_t k = sdesc_sw128(tile(2 * n), 16, 1024);
+        if (lead) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t at = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
-          umma_bf16(tmem + kTmSc, q + at, k + at, kIdQK, ks > 0);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t at = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
+            umma_bf16(tmem + kTmSc, dq + at, k + at, kIdQK, ks > 0);
+          }
+          umma_commit(sc_full);
+          if (last) umma_commit(tile_empty(2 * n));
         }
-        umma_commit(sc_full);
-        if (last) free_tile(2 * n);
-        ++nq;
-      };
-      int m = 0;  // K' terms
-      auto issue_kv = [&](int n) {
-        wait_tile(2 * n + 1);
-        if (n >= 1) ok = ok && lin_wait(u_free, (n - 1) & 1, abort);
-        const uint64_t dv = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
-        for (int t = 0; ok && t < 3; ++t, ++m) {
-          ok = lin_wait(kp_full + 8 * (m & 1), (m >> 1) & 1, abort);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t v = here(dv);
-#pragma unroll
-          for (int ks = 0; ks < kLinC / 16; ++ks)
-            umma_bf16_ts(tmem + kTmU, tmem + kTmKp + 64 * (m & 1) + 8 * ks, v + (ks * 2048 >> 4),
-                         kIdD, t > 0 || ks > 0);
-          umma_commit(kp_empty + 8 * (m & 1));
-        }
-        if (ok) umma_commit(u_done);
-      };
-      if (!STATES) issue_qk(0, a.G == 1);
-      int pair = 0;
-      for (int n = 0; ok && n < nch; ++n) {
-        if (STATES) {
-          issue_kv(n);
-          free_tile(2 * n);
-          free_tile(2 * n + 1);
-          continue;
-        }
-        for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
-          if (gq == 0) ok = lin_wait(s_ready, n & 1, abort);
-          if (pair >= 1) ok = ok && lin_wait(o_free, (pair - 1) & 1, abort);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t q = here(dq), s = here(ds);
+        __syncwarp();
+        if (gq == 0) wait(s_ready, n);
+        if (pair >= 1) wait(o_free, pair - 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (lead) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-              umma_bf16(tmem + kTmOut, q + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4),
-                        s + ((t * L::kSTerm + ks * 2048) >> 4), kIdD, t > 0 || ks > 0);
+              umma_bf16(tmem + kTmOut, dq + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4),
+                        ds + ((t * L::kSTerm + ks * 2048) >> 4), kIdD, t > 0 || ks > 0);
           umma_commit(qs_done);
           umma_commit(q_empty);
-          if (gq == a.G - 1) issue_kv(n);
-          if (gq == 0) {
-            wait_tile(2 * n + 1);
-            ok = ok && lin_wait(v_ready, n & 1, abort);
-          }
-          ok = ok && lin_wait(pv_ready, pair & 1, abort);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t dv = here(sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024));
+        }
+        __syncwarp();
+        if (last) {
+#pragma unroll 1
+          for (int j = kLinQuarters / 2; j < kLinQuarters; ++j) kv_quarter(j, dv);
+        }
+        wait(pv_ready, pair);
+        if (!ok) break;
+        tc_fence_after();
+        if (lead) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -496,20 +557,18 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 16 * ks + 8 * t, dv + (ks * 2048 >> 4),
                            kIdD, 1u);
           umma_commit(o_done);
-          if (gq == a.G - 1) free_tile(2 * n + 1);
-          if (gq + 1 < a.G)
-            issue_qk(n, gq + 2 == a.G);
-          else if (n + 1 < nch)
-            issue_qk(n + 1, a.G == 1);
+          if (last) umma_commit(tile_empty(2 * n + 1));
         }
+        __syncwarp();
       }
-      if (!ok) {
-        set_status(a.status, PHS_ETIMEOUT);
-        *abort = 1;
-      }
-      umma_commit(drain);  // every product is complete before tensor memory is released
-      (void)mbar_wait(drain, 0);
     }
+    if (!ok && lane == 0) {
+      set_status(a.status, PHS_ETIMEOUT);
+      *abort = 1;
+    }
+    if (lead) umma_commit(drain);  // every product is complete before tensor memory is released
+    (void)mbar_wait(drain, 0);
+    __syncwarp();
   } else if (warp == 18) {
     // --------------------------------------------- whole output tiles out
     if (!STATES && lane == 0) {
@@ -531,14 +590,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         *abort = 1;
       }
     }
-  } else if (warp < 8) {
+  } else if (!STATES && warp < 8) {
     // ------------------------------------------------- rows of the chunk
-    regs_dec<kLinRegsRows>();
     const int qt = warp & 3, half = warp >> 2, i = 32 * qt + lane;  // row
+    uint64_t col[8];  // exp(g (15 - e))
+#pragma unroll
+    for (int e = 0; e < 8; ++e) col[e] = f2(pw[15 - 2 * e], pw[14 - 2 * e]);
     bool ok = true;
     int pair = 0;
-    const int chunks = STATES ? 0 : nch;
-    for (int n = 0; ok && n < chunks; ++n)
+    for (int n = 0; ok && n < nch; ++n)
       for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
         ok = lin_wait_warp(sc_full, pair & 1, abort);
         if (!ok) break;
@@ -549,20 +609,30 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int st = half; st < kLinC / 16; st += 2) {
           uint32_t p[16];
           const int d = i - 16 * st;
-          if (16 * st > 32 * qt + 31) {  // behind every row of the warp
+          if (st > 2 * qt + 1) {  // behind every row of the warp
 #pragma unroll
             for (int e = 0; e < 16; ++e) p[e] = 0u;
           } else {
             uint32_t sc[16];
             tmem_ld16(my_lanes + kTmSc + 16 * st, sc);
             tmem_ld_wait();
+            if (st < 2 * qt) {  // before every row: exp(g (d - 15)) exp(g (15 - e))
+              const float rf = ps[d - 15];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float y0 = __uint_as_float(sc[2 * e]) * ps[d - 2 * e];
-              const float y1 = __uint_as_float(sc[2 * e + 1]) * ps[d - 2 * e - 1];
-              float x0 = d >= 2 * e ? y0 : 0.f, x1 = d >= 2 * e + 1 ? y1 : 0.f;
-              p[e] = take_term(x0, x1);
-              p[8 + e] = pack_bf16(x0, x1);
+              for (int e = 0; e < 8; ++e) {
+                uint64_t x = f2_mul(f2_mul(f2(sc[2 * e], sc[2 * e + 1]), f2(rf, rf)), col[e]);
+                p[e] = take_term(x);
+                p[8 + e] = pack_term(x);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float y0 = __uint_as_float(sc[2 * e]) * ps[d - 2 * e];
+                const float y1 = __uint_as_float(sc[2 * e + 1]) * ps[d - 2 * e - 1];
+                uint64_t x = f2(d >= 2 * e ? y0 : 0.f, d >= 2 * e + 1 ? y1 : 0.f);
+                p[e] = take_term(x);
+                p[8 + e] = pack_term(x);
+              }
             }
           }
           tmem_st16(my_lanes + kTmSc + 16 * st, p);
@@ -578,7 +648,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           tmem_ld32(my_lanes + kTmOut + 32 * c, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = f2_get(f2_mul(f2(o[e], o[e + 1]), f2(f, f)));
+            o[e] = __float_as_uint(x.x);
+            o[e + 1] = __float_as_uint(x.y);
+          }
           tmem_st32(my_lanes + kTmOut + 32 * c, o);
         }
         tmem_st_wait();
@@ -625,7 +699,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       set_status(a.status, PHS_ETIMEOUT);
       *abort = 1;
     }
-  } else if (warp < 16) {
+  } else if (warp >= 8 && warp < 16) {
     // ------------------------------------------------- rows of the state
     regs_inc<kLinRegsState>();
     constexpr int N = D / 2;  // columns of a thread
@@ -636,23 +710,24 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     float* pool = a.state + (id * a.Hkv + h) * D * D + row;
     float* ws = a.ws + (static_cast<size_t>(b) * a.Hkv + h) * a.nseg * D * D + row;
     const bool resume = a.resume != nullptr && a.resume[b] != 0;
-    float S[N];
+    uint64_t S[N / 2];  // pairs
 #pragma unroll
-    for (int c = 0; c < N; ++c) S[c] = 0.f;
+    for (int c = 0; c < N / 2; ++c) S[c] = 0ull;
     auto load_row = [&](const float* from, float keep_m1) {  // S <- exp() S + from
+      const uint64_t keep = f2(keep_m1, keep_m1);
 #pragma unroll
       for (int c = 0; c < N; c += 4) {
         const float4 x = *reinterpret_cast<const float4*>(from + c);
-        S[c] = decayed(S[c], keep_m1) + x.x;
-        S[c + 1] = decayed(S[c + 1], keep_m1) + x.y;
-        S[c + 2] = decayed(S[c + 2], keep_m1) + x.z;
-        S[c + 3] = decayed(S[c + 3], keep_m1) + x.w;
+        S[c / 2] = f2_add(f2_fma(S[c / 2], keep, S[c / 2]), f2(x.x, x.y));
+        S[c / 2 + 1] = f2_add(f2_fma(S[c / 2 + 1], keep, S[c / 2 + 1]), f2(x.z, x.w));
       }
     };
     auto store_row = [&](float* to) {
 #pragma unroll
-      for (int c = 0; c < N; c += 4)
-        *reinterpret_cast<float4*>(to + c) = make_float4(S[c], S[c + 1], S[c + 2], S[c + 3]);
+      for (int c = 0; c < N; c += 4) {
+        const float2 x = f2_get(S[c / 2]), y = f2_get(S[c / 2 + 1]);
+        *reinterpret_cast<float4*>(to + c) = make_float4(x.x, x.y, y.x, y.y);
+      }
     };
     if (mine) {
       // with several segments the pool's state is overwritten by the last
@@ -675,16 +750,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     bool ok = true;
     int m = 0;
+    const float keep_chunk = expm1f(g * kLinC);
     // S <- state after chunk n (n >= 0), and where `terms` its two terms to
     // shared memory for the next chunk's QS (the last one has read its own
     // by then: the chunk's sum was issued after it)
     auto next_state = [&](int n, bool terms) {
-      float keep = 0.f;
+      uint64_t keep = 0ull;
       if (n >= 0) {
         ok = ok && lin_wait_warp(u_done, n & 1, abort);
         if (!ok) return;
         tc_fence_after();
-        keep = expm1f(g * min(kLinC, t1 - t0 - n * kLinC));
+        const int v = min(kLinC, t1 - t0 - n * kLinC);
+        const float k = v == kLinC ? keep_chunk : expm1f(g * v);
+        keep = f2(k, k);
       }
       if (mine) {
         const uint32_t my_row = sb + L::kS + r * 128;
@@ -695,8 +773,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             tmem_ld32(my_lanes + kTmU + half * N + 32 * c, u);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              S[32 * c + e] = decayed(S[32 * c + e], keep) + __uint_as_float(u[e]);
+            for (int e = 0; e < 16; ++e)
+              S[16 * c + e] = f2_add(f2_fma(S[16 * c + e], keep, S[16 * c + e]),
+                                     f2(u[2 * e], u[2 * e + 1]));
           }
           if (terms) {
 #pragma unroll
@@ -704,9 +783,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               uint32_t hi[4], lo[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                float x0 = S[32 * c + 8 * k + 2 * e], x1 = S[32 * c + 8 * k + 2 * e + 1];
-                hi[e] = take_term(x0, x1);
-                lo[e] = pack_bf16(x0, x1);
+                uint64_t x = S[16 * c + 4 * k + e];
+                hi[e] = take_term(x);
+                lo[e] = pack_term(x);
               }
               const int u = half * (N / 8) + 4 * c + k;  // 16 bytes of the row
               const uint32_t at = my_row + (u >> 3) * (D * 128) + (((u ^ r) & 7) << 4);
@@ -725,13 +804,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     };
     // K'^T of 32 columns of K: ldmatrix.trans gives thread 4 x + y tokens 2 y,
     // 2 y + 1 (of 8) of column x of each of 4 groups of 8 columns.  The two
-    // warps of a quarter take steps of 16 tokens in turn.
+    // warps of these columns take 16 tokens each of a quarter.
     const int kx = lane >> 3;  // matrix kx: columns 32 qt + 8 kx ..
     const uint32_t kcol = (qt >> 1) * L::kHalf + (lane & 7) * 128 +
                           ((((4 * (qt & 1) + kx) ^ lane) & 7) << 4);
+    next_state(-1, !STATES && nch > 0);
     for (int n = 0; ok && n < nch; ++n) {
-      next_state(n - 1, !STATES);
-      if (!ok) break;
       const int v = min(kLinC, t1 - t0 - n * kLinC);
       const int ki = 2 * n, vi = 2 * n + 1;  // tiles of the ring
       const uint32_t kt = sb + L::kKV + (ki % L::kSlots) * L::kTile;
@@ -744,7 +822,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (!ok) break;
         const uint32_t vt = sb + L::kKV + (vi % L::kSlots) * L::kTile;
         for (int t = v + (lane >> 2); mine && t < kLinC; t += 8)
-          if (((t >> 4) & 1) == half)
+          if (((t >> 4) & 1) == half)  // its own steps
             sts128(kt + (qt >> 1) * L::kHalf + t * 128 +
                        ((((4 * (qt & 1) + (lane & 3)) ^ t) & 7) << 4),
                    0, 0, 0, 0);
@@ -755,86 +833,52 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       }
-      if (!STATES) mbar_arrive(v_ready);
-      auto wait_empty = [&](int mm) {
-        if (mm >= 2) ok = ok && lin_wait_warp(kp_empty + 8 * (mm & 1), ((mm >> 1) - 1) & 1, abort);
-      };
-      // weights of this thread's two tokens of group q (0 behind the last)
-      auto weights = [&](int q, float& w0, float& w1) {
-        const int e = v - 1 - 8 * q - 2 * (lane & 3);
-        const float f0 = pw[max(e, 0)], f1 = pw[max(e - 1, 0)];
-        w0 = e >= 0 ? f0 : 0.f;
-        w1 = e >= 1 ? f1 : 0.f;
-      };
-      // terms lo2 and lo
-      wait_empty(m);
-      wait_empty(m + 1);
-      if (!ok) break;
-      tc_fence_after();
-      if (mine) {
+      // quarter j, as three terms; the first one before the state of the last
+      // chunk is taken up, which waits for that chunk's sum
 #pragma unroll 1
-        for (int st = half; st < kLinC / 16; st += 2) {
-          uint32_t w2[2][4], w1[2][4];
+      for (int j = 0; ok && j < kLinQuarters; ++j, ++m) {
+        if (j == 1) {
+          if (n > 0) next_state(n - 1, !STATES);
+          // (the products' thread waits for the last chunk's before it issues
+          // that chunk's KV, so by now it cannot miss this phase)
+          if (!STATES && ok) mbar_arrive(v_ready);
+        }
+        if (m >= 2) ok = ok && lin_wait_warp(kp_empty + 8 * (m & 1), ((m >> 1) - 1) & 1, abort);
+        if (!ok) break;
+        tc_fence_after();
+        if (mine) {
+          const int st = 2 * j + half;
+          uint32_t w[3][2][4];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             uint32_t k[4];
             ldsm_x4_t(kt + kcol + (2 * st + q) * 1024, k[0], k[1], k[2], k[3]);
-            float f0, f1;
-            weights(2 * st + q, f0, f1);
+            // weights of this thread's two tokens (0 behind the last)
+            const int e = v - 1 - 8 * (2 * st + q) - 2 * (lane & 3);
+            const float p0 = pw[max(e, 0)], p1 = pw[max(e - 1, 0)];
+            const uint64_t f = f2(e >= 0 ? p0 : 0.f, e >= 1 ? p1 : 0.f);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              float x0 = __uint_as_float(k[x] << 16) * f0;
-              float x1 = __uint_as_float(k[x] & 0xffff0000u) * f1;
-              (void)take_term(x0, x1);
-              w1[x >> 1][2 * q + (x & 1)] = take_term(x0, x1);
-              w2[x >> 1][2 * q + (x & 1)] = pack_bf16(x0, x1);
+              uint64_t y = f2_mul(f2_bf16(k[x]), f);
+              w[2][x >> 1][2 * q + (x & 1)] = take_term(y);
+              w[1][x >> 1][2 * q + (x & 1)] = take_term(y);
+              w[0][x >> 1][2 * q + (x & 1)] = pack_term(y);
             }
           }
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t at = my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp + 8 * st;
-            tmem_st_16x128(at + 64 * (m & 1), w2[x]);
-            tmem_st_16x128(at + 64 * ((m + 1) & 1), w1[x]);
-          }
+          for (int t = 0; t < 3; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              tmem_st_16x128(my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp +
+                                 kTmKpBuf * (m & 1) + 16 * t + 8 * half,
+                             w[t][x]);
+          tmem_st_wait();
         }
-        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(kp_full + 8 * (m & 1));
       }
-      tc_fence_before();
-      mbar_arrive(kp_full + 8 * (m & 1));
-      mbar_arrive(kp_full + 8 * ((m + 1) & 1));
-      m += 2;
-      // term hi
-      wait_empty(m);
-      if (!ok) break;
-      tc_fence_after();
-      if (mine) {
-#pragma unroll 1
-        for (int st = half; st < kLinC / 16; st += 2) {
-          uint32_t w0[2][4];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t k[4];
-            ldsm_x4_t(kt + kcol + (2 * st + q) * 1024, k[0], k[1], k[2], k[3]);
-            float f0, f1;
-            weights(2 * st + q, f0, f1);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              w0[x >> 1][2 * q + (x & 1)] = pack_bf16(__uint_as_float(k[x] << 16) * f0,
-                                                      __uint_as_float(k[x] & 0xffff0000u) * f1);
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            tmem_st_16x128(my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp + 8 * st +
-                               64 * (m & 1),
-                           w0[x]);
-        }
-        tmem_st_wait();
-      }
-      tc_fence_before();
-      mbar_arrive(kp_full + 8 * (m & 1));
       mbar_arrive(kv_empty + 8 * (ki % L::kSlots));
       mbar_arrive(kv_empty + 8 * (vi % L::kSlots));
-      ++m;
     }
     if (nch > 0) next_state(nch - 1, false);
     if (!ok) {
@@ -846,7 +890,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
