@@ -188,17 +188,13 @@ struct LinLayout {
   static_assert(kAlloc + kTables <= 227 * 1024, "shared memory of the prompt kernel");
 };
 
-// Bounded wait that also gives up when another role has.
+// Bounded wait that also gives up when another role has.  (4 M tries are
+// a tenth of a second or more; the loop is kept small, since the roles' code
+// competes for the instruction caches.)
 __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63u) == 63u) {
-      if (*abort) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) return false;
-    }
-  }
+  for (uint32_t it = 0; !mbar_try_wait(bar, parity); ++it)
+    if (*abort || it >= (1u << 22)) return false;
+  return true;
 }
 
 // The same by a whole warp, one answer for all its lanes.
@@ -356,15 +352,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const float g0 = a.log_decay[h], g = g0 < -1e4f ? -1e4f : g0;  // exp(g n) is 0 there anyway
 
   // barriers: tile loaded / used, Q, scores, the inter-chunk part, P and that
-  // part ready, output complete / read, K' terms written / used, state terms
-  // written, V's rows behind the last token zero, chunk sum complete / read,
-  // output tile written / stored
+  // part ready, output complete / read, K' terms written / used, state (the
+  // last chunk's sum is read, the state's terms written, V's rows behind the
+  // last token zero), chunk sum complete, output tile written / stored
   const uint32_t kv_full = sb + L::kBar, kv_empty = kv_full + 24, q_full = kv_empty + 24,
                  q_empty = q_full + 8, sc_full = q_empty + 8, qs_done = sc_full + 8,
                  pv_ready = qs_done + 8, o_done = pv_ready + 8, o_free = o_done + 8,
                  kp_full = o_free + 8, kp_empty = kp_full + 16, s_ready = kp_empty + 16,
-                 u_done = s_ready + 8, u_free = u_done + 8, y_full = u_free + 8,
-                 y_free = y_full + 8, v_ready = y_free + 8, drain = v_ready + 8;
+                 u_done = s_ready + 8, y_full = u_done + 8, y_free = y_full + 8,
+                 drain = y_free + 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   if (warp == 16) {
     tmem_alloc(sb + L::kMisc, 512);
@@ -379,7 +375,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       mbar_init(kp_full + 8 * i, 256);
       mbar_init(kp_empty + 8 * i, 1);
     }
-    mbar_init(v_ready, 256);
     mbar_init(y_full, 256);
     mbar_init(y_free, 1);
     mbar_init(q_full, 1);
@@ -391,7 +386,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     mbar_init(o_free, 256);
     mbar_init(s_ready, 256);
     mbar_init(u_done, 1);
-    mbar_init(u_free, 256);
     mbar_init(drain, 1);
     *abort = 0;
     fence_mbar_init();
@@ -497,19 +491,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       // the first half of KV needs nothing of this chunk's rows: it runs while
       // the last chunk's product is still being completed
       tile_full(2 * n + 1);
-      if (!STATES) wait(v_ready, n);
-      if (n >= 1) wait(u_free, n - 1);
+      if (!STATES || n >= 1) wait(s_ready, STATES ? n - 1 : n);
       const uint64_t dv = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
 #pragma unroll 1
       for (int j = 0; j < (STATES ? kLinQuarters : kLinQuarters / 2); ++j) kv_quarter(j, dv);
-      if (STATES) {
-        if (ok && lead) {
-          umma_commit(tile_empty(2 * n));
-          umma_commit(tile_empty(2 * n + 1));
-        }
-        continue;
+      if (STATES && ok && lead) {
+        umma_commit(tile_empty(2 * n));
+        umma_commit(tile_empty(2 * n + 1));
       }
-      for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
+      for (int gq = 0; !STATES && ok && gq < a.G; ++gq, ++pair) {
         const bool last = gq == a.G - 1;
         if (gq == 0) tile_full(2 * n);
         wait(q_full, pair);
@@ -518,7 +508,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         tc_fence_after();
         const uint64_t k = sdesc_sw128(tile(2 * n), 16, 1024);
         if (lead) {
-#pragma unroll
+#pragma unroll 2
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t at = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
             umma_bf16(tmem + kTmSc, dq + at, k + at, kIdQK, ks > 0);
@@ -527,14 +517,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (last) umma_commit(tile_empty(2 * n));
         }
         __syncwarp();
-        if (gq == 0) wait(s_ready, n);
         if (pair >= 1) wait(o_free, pair - 1);
         if (!ok) break;
         tc_fence_after();
         if (lead) {
-#pragma unroll
+#pragma unroll 1
           for (int t = 0; t < 2; ++t)
-#pragma unroll
+#pragma unroll 2
             for (int ks = 0; ks < D / 16; ++ks)
               umma_bf16(tmem + kTmOut, dq + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4),
                         ds + ((t * L::kSTerm + ks * 2048) >> 4), kIdD, t > 0 || ks > 0);
@@ -550,9 +539,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (lead) {
-#pragma unroll
+#pragma unroll 1
           for (int t = 0; t < 2; ++t)
-#pragma unroll
+#pragma unroll 2
             for (int ks = 0; ks < kLinC / 16; ++ks)
               umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 16 * ks + 8 * t, dv + (ks * 2048 >> 4),
                            kIdD, 1u);
@@ -796,11 +785,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         if (terms) fence_proxy_async_smem();
       }
-      if (n >= 0) {
-        tc_fence_before();
-        mbar_arrive(u_free);
-      }
-      if (terms) mbar_arrive(s_ready);
+      tc_fence_before();
+      mbar_arrive(s_ready);
     };
     // K'^T of 32 columns of K: ldmatrix.trans gives thread 4 x + y tokens 2 y,
     // 2 y + 1 (of 8) of column x of each of 4 groups of 8 columns.  The two
@@ -808,7 +794,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int kx = lane >> 3;  // matrix kx: columns 32 qt + 8 kx ..
     const uint32_t kcol = (qt >> 1) * L::kHalf + (lane & 7) * 128 +
                           ((((4 * (qt & 1) + kx) ^ lane) & 7) << 4);
-    next_state(-1, !STATES && nch > 0);
     for (int n = 0; ok && n < nch; ++n) {
       const int v = min(kLinC, t1 - t0 - n * kLinC);
       const int ki = 2 * n, vi = 2 * n + 1;  // tiles of the ring
@@ -837,12 +822,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       // chunk is taken up, which waits for that chunk's sum
 #pragma unroll 1
       for (int j = 0; ok && j < kLinQuarters; ++j, ++m) {
-        if (j == 1) {
-          if (n > 0) next_state(n - 1, !STATES);
-          // (the products' thread waits for the last chunk's before it issues
-          // that chunk's KV, so by now it cannot miss this phase)
-          if (!STATES && ok) mbar_arrive(v_ready);
-        }
+        if (j == 1 && (n > 0 || !STATES)) next_state(n - 1, !STATES);
         if (m >= 2) ok = ok && lin_wait_warp(kp_empty + 8 * (m & 1), ((m >> 1) - 1) & 1, abort);
         if (!ok) break;
         tc_fence_after();
