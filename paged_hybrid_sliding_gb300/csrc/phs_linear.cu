@@ -147,11 +147,12 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 //               inter-chunk part scaled, the output rows
 //   warps 8-15  rows of the state, two threads a row, in registers: state ->
 //               two terms in shared memory, K tile -> K'^T terms
-//   warp 16     issues the products: half of KV, QK, QS, the rest of KV, PV,
-//               so that the state's and P's way through the registers runs
-//               beside them (on the scheduler with the least of P's work)
+//   warp 16     issues KV
 //   warp 17     TMA loads: a ring of three K and V tiles, one Q tile
-//   warp 18     TMA stores of the output tile (warp 19 fills the warpgroup)
+//   warp 18     TMA stores of the output tile
+//   warp 19     issues QK, QS and PV
+// The state's way through the registers and KV, and P's and the other three
+// products, meet once a chunk: the state's terms, and QS done with them.
 // Two warps on each scheduler run each role's code, and its loops are kept
 // small: with one warp and everything unrolled, fetching instructions was
 // the largest stall (3.1 of 10.7 warp-cycles an instruction).
@@ -369,7 +370,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(kv_full + 8 * i, 1);
-      mbar_init(kv_empty + 8 * i, 257);  // the products, and the 256 state threads
+      // the products (two warps'; one where there are states alone), and the
+      // 256 state threads
+      mbar_init(kv_empty + 8 * i, STATES ? 257 : 258);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(kp_full + 8 * i, 256);
@@ -385,8 +388,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     mbar_init(o_done, 1);
     mbar_init(o_free, 256);
     mbar_init(s_ready, 256);
-    mbar_init(u_done, 1);
+    mbar_init(u_done, STATES ? 1 : 2);  // KV, and QS done with the state's terms
     mbar_init(drain, 1);
+    mbar_init(drain + 8, 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -446,9 +450,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         (void)mbar_wait(kv_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1);
       if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
     }
-  } else if (warp == 16) {
+  } else if (warp == 16 || (!STATES && warp == 19)) {
     // ----------------------------------------------------------- products
-    // The whole warp walks the chunks and one elected lane issues: what the
+    // A whole warp walks the chunks and one elected lane issues: what the
     // instructions take is then known to be the same in every lane, and the
     // compiler keeps it in uniform registers (issued from a lane of its own,
     // an instruction took 90 cycles and more, whatever its width).
@@ -456,9 +460,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     constexpr uint32_t kIdD = idesc_bf16_f32(128, D, false, true);
     bool ok = true;
     const bool lead = elect_one();
-    // descriptors; a later part of a tile is `bytes >> 4` further on
-    const uint64_t dq = sdesc_sw128(sb + L::kQ, 16, 1024);
-    const uint64_t ds = sdesc_sw128(sb + L::kS, D * 128, 1024);
     auto wait = [&](uint32_t bar, int turn) {
       ok = ok && lin_wait_warp(bar, turn & 1, abort);
     };
@@ -466,97 +467,102 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     auto tile = [&](int i) { return sb + L::kKV + (i % L::kSlots) * L::kTile; };
     auto tile_full = [&](int i) { wait(kv_full + 8 * (i % L::kSlots), i / L::kSlots); };
     auto tile_empty = [&](int i) { return kv_empty + 8 * (i % L::kSlots); };
-    int m = 0;  // K' quarters
-    auto kv_quarter = [&](int j, uint64_t dv) {
-      wait(kp_full + 8 * (m & 1), m >> 1);
-      if (!ok) return;
-      tc_fence_after();
-      const uint64_t v = dv + (j * 2 * 2048 >> 4);
-      const uint32_t kp = tmem + kTmKp + kTmKpBuf * (m & 1);
-      if (lead) {
-#pragma unroll
-        for (int t = 0; t < 3; ++t)
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
-            umma_bf16_ts(tmem + kTmU, kp + 16 * t + 8 * ks, v + (ks * 2048 >> 4), kIdD,
-                         j > 0 || t > 0 || ks > 0);
-        umma_commit(kp_empty + 8 * (m & 1));
-        if (j == kLinQuarters - 1) umma_commit(u_done);
-      }
-      __syncwarp();
-      ++m;
-    };
-    int pair = 0;
-    for (int n = 0; ok && n < nch; ++n) {
-      // the first half of KV needs nothing of this chunk's rows: it runs while
-      // the last chunk's product is still being completed
-      tile_full(2 * n + 1);
-      if (!STATES || n >= 1) wait(s_ready, STATES ? n - 1 : n);
-      const uint64_t dv = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
+    if (warp == 16) {  // KV
+      int m = 0;       // quarters
+      for (int n = 0; ok && n < nch; ++n) {
+        if (!STATES || n >= 1) wait(s_ready, STATES ? n - 1 : n);
+        tile_full(2 * n + 1);
+        uint64_t v = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
 #pragma unroll 1
-      for (int j = 0; j < (STATES ? kLinQuarters : kLinQuarters / 2); ++j) kv_quarter(j, dv);
-      if (STATES && ok && lead) {
-        umma_commit(tile_empty(2 * n));
-        umma_commit(tile_empty(2 * n + 1));
-      }
-      for (int gq = 0; !STATES && ok && gq < a.G; ++gq, ++pair) {
-        const bool last = gq == a.G - 1;
-        if (gq == 0) tile_full(2 * n);
-        wait(q_full, pair);
-        if (pair >= 1) wait(o_done, pair - 1);  // P of the last pair is read
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t k = sdesc_sw128(tile(2 * n), 16, 1024);
-        if (lead) {
-#pragma unroll 2
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t at = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
-            umma_bf16(tmem + kTmSc, dq + at, k + at, kIdQK, ks > 0);
+        for (int j = 0; j < kLinQuarters; ++j, ++m, v += 2 * 2048 >> 4) {
+          wait(kp_full + 8 * (m & 1), m >> 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t kp = tmem + kTmKp + kTmKpBuf * (m & 1);
+          if (lead) {
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+#pragma unroll
+              for (int ks = 0; ks < 2; ++ks)
+                umma_bf16_ts(tmem + kTmU, kp + 16 * t + 8 * ks, v + (ks * 2048 >> 4), kIdD,
+                             j > 0 || t > 0 || ks > 0);
+            umma_commit(kp_empty + 8 * (m & 1));
           }
-          umma_commit(sc_full);
-          if (last) umma_commit(tile_empty(2 * n));
+          __syncwarp();
         }
-        __syncwarp();
-        if (pair >= 1) wait(o_free, pair - 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (lead) {
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t)
-#pragma unroll 2
-            for (int ks = 0; ks < D / 16; ++ks)
-              umma_bf16(tmem + kTmOut, dq + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4),
-                        ds + ((t * L::kSTerm + ks * 2048) >> 4), kIdD, t > 0 || ks > 0);
-          umma_commit(qs_done);
-          umma_commit(q_empty);
-        }
-        __syncwarp();
-        if (last) {
-#pragma unroll 1
-          for (int j = kLinQuarters / 2; j < kLinQuarters; ++j) kv_quarter(j, dv);
-        }
-        wait(pv_ready, pair);
-        if (!ok) break;
-        tc_fence_after();
-        if (lead) {
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t)
-#pragma unroll 2
-            for (int ks = 0; ks < kLinC / 16; ++ks)
-              umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 16 * ks + 8 * t, dv + (ks * 2048 >> 4),
-                           kIdD, 1u);
-          umma_commit(o_done);
-          if (last) umma_commit(tile_empty(2 * n + 1));
+        if (ok && lead) {
+          umma_commit(u_done);
+          umma_commit(tile_empty(2 * n));
+          umma_commit(tile_empty(2 * n + 1));
         }
         __syncwarp();
       }
+    } else {  // QK, QS, PV
+      // descriptors; a later part of a tile is `bytes >> 4` further on
+      const uint64_t dq = sdesc_sw128(sb + L::kQ, 16, 1024);
+      const uint64_t ds = sdesc_sw128(sb + L::kS, D * 128, 1024);
+      int pair = 0;
+      for (int n = 0; ok && n < nch; ++n)
+        for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
+          const bool last = gq == a.G - 1;
+          if (gq == 0) tile_full(2 * n);
+          wait(q_full, pair);
+          if (pair >= 1) wait(o_done, pair - 1);  // P of the last pair is read
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t k = sdesc_sw128(tile(2 * n), 16, 1024);
+          if (lead) {
+#pragma unroll 2
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t at = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
+              umma_bf16(tmem + kTmSc, dq + at, k + at, kIdQK, ks > 0);
+            }
+            umma_commit(sc_full);
+            if (last) umma_commit(tile_empty(2 * n));
+          }
+          __syncwarp();
+          if (gq == 0) wait(s_ready, n);
+          if (pair >= 1) wait(o_free, pair - 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t)
+#pragma unroll 2
+              for (int ks = 0; ks < D / 16; ++ks)
+                umma_bf16(tmem + kTmOut, dq + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4),
+                          ds + ((t * L::kSTerm + ks * 2048) >> 4), kIdD, t > 0 || ks > 0);
+            umma_commit(qs_done);
+            umma_commit(q_empty);
+            if (last) umma_commit(u_done);  // the state's terms have been read
+          }
+          __syncwarp();
+          if (gq == 0) tile_full(2 * n + 1);
+          wait(pv_ready, pair);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t v = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
+          if (lead) {
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t)
+#pragma unroll 2
+              for (int ks = 0; ks < kLinC / 16; ++ks)
+                umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 16 * ks + 8 * t, v + (ks * 2048 >> 4),
+                             kIdD, 1u);
+            umma_commit(o_done);
+            if (last) umma_commit(tile_empty(2 * n + 1));
+          }
+          __syncwarp();
+        }
     }
     if (!ok && lane == 0) {
       set_status(a.status, PHS_ETIMEOUT);
       *abort = 1;
     }
-    if (lead) umma_commit(drain);  // every product is complete before tensor memory is released
-    (void)mbar_wait(drain, 0);
+    // every product of this warp is complete before tensor memory is released
+    const uint32_t done = warp == 16 ? drain : drain + 8;
+    if (lead) umma_commit(done);
+    (void)mbar_wait(done, 0);
     __syncwarp();
   } else if (warp == 18) {
     // --------------------------------------------- whole output tiles out
