@@ -103,12 +103,13 @@ class PagedPool:
     v: torch.Tensor
 
     def c(self):
-        _need(self.k, torch.bfloat16, "pool.k", 4)
-        _need(self.v, torch.bfloat16, "pool.v", 4)
-        if self.k.shape != self.v.shape:
+        k, v = self.k, self.v
+        _need(k, torch.bfloat16, "pool.k", 4)
+        _need(v, torch.bfloat16, "pool.v", 4)
+        n, h, p, d = shape = k.shape
+        if shape != v.shape:
             raise ValueError("pool.k and pool.v shapes differ")
-        n, h, p, d = self.k.shape
-        return _lib.PagedPoolC(self.k.data_ptr(), self.v.data_ptr(), n, p, h, d)
+        return _lib.PagedPoolC(k.data_ptr(), v.data_ptr(), n, p, h, d)
 
     @staticmethod
     def empty(num_pages, num_kv_heads, head_dim, device="cuda"):
@@ -789,9 +790,13 @@ def _tables(block_table, seq_lens, page_refcount):
 def _pools_of(pools, page_refcount):
     if not pools:
         raise ValueError("pools must name at least one pool")
-    if any(p.k.shape[0] != page_refcount.shape[0] for p in pools):
-        raise ValueError("page_refcount needs one entry per page")
-    return _pool_array(_lib.PagedPoolC, pools)
+    arr = _pool_array(_lib.PagedPoolC, pools)
+    n = page_refcount.shape[0]
+    for p, c in zip(pools, arr):
+        if c.num_pages != n:
+            raise ValueError("page_refcount needs one entry per page")
+        _same_device(page_refcount, p.k, p.v)
+    return arr
 
 
 def pages_free(block_table, seq_lens, page_refcount, rows, status=None, stream=None):
@@ -825,8 +830,7 @@ def pages_fork(pools, block_table, seq_lens, page_refcount, src_rows, dst_rows, 
     arr = _pools_of(pools, page_refcount)
     rows, n = block_table.shape[0], src_rows.shape[0]
     ws = _workspace(workspace, pages_fork_workspace_bytes(rows, n), block_table.device)
-    _same_device(block_table, seq_lens, page_refcount, src_rows, dst_rows, ws, status,
-                 *[t for p in pools for t in (p.k, p.v)])
+    _same_device(block_table, seq_lens, page_refcount, src_rows, dst_rows, ws, status)
     _check(lib().phs_pages_fork(arr, len(pools), _ptr(block_table), rows, block_table.shape[1],
                                 _ptr(seq_lens), _ptr(page_refcount), _ptr(src_rows),
                                 _ptr(dst_rows), n, _ptr(ws), ws.numel(), _ptr(status),
@@ -863,8 +867,7 @@ def pages_compact(pools, block_table, seq_lens, page_refcount, block_table_out=N
     _opt(status, torch.int32, "status")
     ws = _workspace(workspace, pages_compact_workspace_bytes(page_refcount.shape[0]),
                     block_table.device)
-    _same_device(block_table, seq_lens, page_refcount, bt, rc, page_map, num_live, ws, status,
-                 *[t for p in pools for t in (p.k, p.v)])
+    _same_device(block_table, seq_lens, page_refcount, bt, rc, page_map, num_live, ws, status)
     _check(lib().phs_pages_compact(arr, len(pools), _ptr(block_table), block_table.shape[0],
                                    block_table.shape[1], _ptr(seq_lens), _ptr(page_refcount),
                                    _ptr(bt), _ptr(rc), _ptr(page_map), _ptr(num_live), _ptr(ws),

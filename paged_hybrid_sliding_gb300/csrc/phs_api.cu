@@ -1577,6 +1577,44 @@ namespace {
 
 static_assert(kDiffMaxSplit == kMaxSplitTokens, "the split kernel's chunk lists");
 
+// Split length of a call, with P = batch x value heads (x 2 for groups of more
+// than 8 heads) and a wave of W = SMs x CTAs of an SM.
+// Where one wave can hold every split, the length that just does (in whole
+// steps of 128): the call then has one round of CTAs and few partials.  (us:
+// one request of 250,001 tokens, 4 value heads of 64: 147 at 256 tokens a
+// split, 100 at 1,024, 108.9 at 2,048, which is 1.08 waves, 87 at 2,208, 84 at
+// 4,096; 4 requests of 32K on one of 128: 39.2 at 512, 29.5 at 896, 47.1 at
+// 2,048; one of 8K on 4 of 128: 18.9 at 128, 12.6 at 256, 15.9 at 512.)
+// Else, and where a batch may be so ragged that one wave would leave most of
+// it empty (the length above is over four times the one below), the length T
+// that balances what a CTA costs beside its bytes, about 3 us, N / (T W)
+// times in a row for N tokens in all, against half a CTA at the end, T / 2
+// tokens of 8 D bytes on all W at 7.1 TB/s.  N is taken as half of what the
+// stated bound allows.  (64 requests to 32K: 378 at 1,024, 367 at 2,048, 372
+// at 4,096; 16 to 4K: 21.4 at 256, 20.2 at 512, 68 at 4,096, the one wave.)
+int plan_diff_split(int B, int Hv, int G, int D, int max_seq, int sms) {
+  const double pairs = 1.0 * B * Hv * ((G + 7) / 8), wave = 1.0 * sms * diff_ctas_per_sm(D);
+  const double tokens = pairs * max_seq / (B == 1 ? 1 : 2);
+  const double best = std::sqrt(3.0 * tokens * 7.1e6 / (4.0 * D * wave * wave));
+  const int per = static_cast<int>(wave / pairs);  // splits of a request in one wave
+  if (per > 0) {
+    const int one = std::max(1, ((max_seq + per - 1) / per + 127) / 128) * 128;
+    if (one <= kDiffMaxSplit && (B == 1 || one <= 4 * best)) return one;
+  }
+  int T = 128;
+  while (T < kDiffMaxSplit && T * 1.5 < best) T *= 2;  // the nearest power of two
+  return T;
+}
+
+int make_diff_plan(DecodePlan& pl, int B, int H, int Hv, int D, int max_seq, int tps) {
+  int st = make_plan(pl, B, H, Hv, D, max_seq, tps, false);
+  if (st || tps > 0) return st;
+  DevInfo di;
+  if ((st = dev_info(di))) return st;
+  return make_plan(pl, B, H, Hv, D, max_seq, plan_diff_split(B, Hv, pl.G, D, max_seq, di.sms),
+                   false);
+}
+
 // Partials of a split: one 2D-wide row and one (max, sum) for each map of
 // each head.  A call that needs none (one split) still takes a workspace.
 size_t diff_rows(const DecodePlan& pl, int B) {
@@ -1594,8 +1632,8 @@ size_t phs_diff_workspace_bytes(int32_t batch, int32_t num_heads, int32_t num_va
                                 int32_t head_dim, int32_t max_seq_len,
                                 int32_t tokens_per_split) {
   DecodePlan pl;
-  if (make_plan(pl, batch, num_heads, num_value_heads, head_dim, max_seq_len, tokens_per_split,
-                false))
+  if (make_diff_plan(pl, batch, num_heads, num_value_heads, head_dim, max_seq_len,
+                     tokens_per_split))
     return 0;
   return diff_o_bytes(pl, batch) + align256(diff_rows(pl, batch) * 2 * sizeof(float));
 }
@@ -1624,7 +1662,7 @@ int phs_attn_decode_diff_paged(const void* q, int32_t num_heads, const phs_paged
   if (pool->num_kv_heads % 2 != 0) return PHS_ESHAPE;
   const int Hv = pool->num_kv_heads / 2, D = pool->head_dim;
   DecodePlan pl;
-  if ((st = make_plan(pl, batch, num_heads, Hv, D, max_seq_len, tokens_per_split, false)))
+  if ((st = make_diff_plan(pl, batch, num_heads, Hv, D, max_seq_len, tokens_per_split)))
     return st;
   if ((st = check_workspace(workspace, workspace_bytes,
                             phs_diff_workspace_bytes(batch, num_heads, Hv, D, max_seq_len,

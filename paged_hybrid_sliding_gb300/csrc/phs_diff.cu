@@ -86,24 +86,22 @@ __device__ __forceinline__ void finish_head(const DiffArgs& a, int b, int i, flo
   }
 }
 
-#ifndef PHS_DIFF_WARPS_128
-#define PHS_DIFF_WARPS_128 6
-#endif
-#ifndef PHS_DIFF_STAGES_128
-#define PHS_DIFF_STAGES_128 2
-#endif
-#ifndef PHS_DIFF_WARPS_64
-#define PHS_DIFF_WARPS_64 4
-#endif
-#ifndef PHS_DIFF_STAGES_64
-#define PHS_DIFF_STAGES_64 3
-#endif
+// Warps, stages and CTAs of an SM, by the time of a call in us (each at its
+// best split length).  D = 128: 64 requests to 32K / one of 8K / 4 of 32K on
+// one value head: 6 warps x 2 stages x 1 CTA 367 / 12.6 / 30.5, 3 x 2 x 2
+// 371 / 14.8 / 34.2, 2 x 2 x 3 370 / 15.2 / 31.1.  D = 64: one of 250K / 32
+// of 16K: 4 x 2 x 3 83.6 / 158.8, 4 x 3 x 2 85.8 / 161.3, 8 x 3 x 1
+// 84.6 / 168.3.
+template <int D>
+struct DiffShape {
+  static constexpr int NW = D == 128 ? 6 : 4;
+  static constexpr int S = 2;
+  static constexpr int kCtas = diff_ctas_per_sm(D);
+};
 
 template <int D>
 struct DiffLayout {
-  static constexpr int NW = D == 128 ? PHS_DIFF_WARPS_128 : PHS_DIFF_WARPS_64;
-  static constexpr int S = D == 128 ? PHS_DIFF_STAGES_128 : PHS_DIFF_STAGES_64;
-  static constexpr int kCtas = D == 128 ? 1 : 2;     // per SM
+  static constexpr int NW = DiffShape<D>::NW, S = DiffShape<D>::S, kCtas = DiffShape<D>::kCtas;
   static constexpr int kTile = 2 * kPage * D * 2;    // K1 and K2 (or V) of one chunk
   static constexpr int kStage = 2 * kTile;
   static constexpr int kMaxChunks = (kDiffMaxSplit / kPage + NW - 1) / NW;  // of a warp

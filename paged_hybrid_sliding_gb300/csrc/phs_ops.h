@@ -78,6 +78,7 @@ int launch_pages_copy(const PagePools& p, const int32_t* src, const int32_t* dst
 
 // ------------------------------------------------ differential attention --
 constexpr int kDiffMaxSplit = 4096;  // tokens
+constexpr int diff_ctas_per_sm(int D) { return D == 128 ? 1 : 3; }
 
 struct DiffArgs {
   const __nv_bfloat16* q;  // [B][2H][D]
