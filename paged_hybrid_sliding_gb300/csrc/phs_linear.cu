@@ -166,11 +166,25 @@ constexpr int kLinC = kLinearChunk;
 constexpr int kLinThreads = 640;
 // registers a thread: 96 at launch, five warpgroups; 2 x 88 + 2 x 120 + 64 = 5 x 96
 constexpr int kLinRegsRows = 88, kLinRegsState = 120, kLinRegsIssue = 64;
-constexpr uint32_t kTmU = 0, kTmSc = 128, kTmOut = 256, kTmKp = 384;  // tensor-memory columns
 // K'^T goes in quarters of a chunk, 32 tokens at a time: 16 columns for each
-// of the three terms, two buffers
+// of the three terms
 constexpr int kLinQuarters = 4;
 constexpr uint32_t kTmKpBuf = 48;
+
+// Tensor-memory columns: a chunk's sum U, scores (and P), output, and as many
+// buffers of K'^T as there is room for.  The state of the last chunk is taken
+// up (which waits for its sum) before quarter kStateAt: the quarters before
+// it find a buffer while that sum is still being formed.
+template <int D, bool STATES>
+struct LinTmem {
+  static constexpr uint32_t kU = 0;
+  static constexpr uint32_t kOut = D == 64 ? 64 : 256;
+  static constexpr uint32_t kSc = 128;
+  static constexpr uint32_t kKp = STATES ? 128 : D == 64 ? 256 : 384;
+  static constexpr int kBufs = STATES ? 8 : D == 64 ? 4 : 2;
+  static constexpr int kStateAt = kBufs - 1 < kLinQuarters ? kBufs - 1 : kLinQuarters;
+  static_assert(kKp + kBufs * kTmKpBuf <= 512, "tensor memory");
+};
 
 template <int D>
 struct LinLayout {
@@ -183,7 +197,7 @@ struct LinLayout {
   static constexpr int kS = kOut + kTile;      // 2 terms [D / 64][D rows][128 bytes]
   static constexpr int kSTerm = D * D * 2;
   static constexpr int kBar = kS + 2 * kSTerm;
-  static constexpr int kMisc = kBar + 24 * 8;  // tensor-memory base, abort flag
+  static constexpr int kMisc = kBar + 36 * 8;  // tensor-memory base, abort flag
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static constexpr int kTables = (2 * (kLinC + 4) + 32) * 4;  // static: pw, ps and its pad
   static_assert(kAlloc + kTables <= 227 * 1024, "shared memory of the prompt kernel");
@@ -270,9 +284,19 @@ __device__ __forceinline__ uint32_t pack_term(uint64_t x) {
   const float2 v = f2_get(x);
   return pack_bf16(v.x, v.y);
 }
+// (fma with bf16 factors: the terms need no unpacking)
 __device__ __forceinline__ uint32_t take_term(uint64_t& x) {
-  const uint32_t w = pack_term(x);
-  x = f2_fma(f2_bf16(w), f2(-1.f, -1.f), x);
+  const float2 v = f2_get(x);
+  const uint32_t w = pack_bf16(v.x, v.y);
+  float lo, hi;
+  asm("{\n\t.reg .b16 l, h, m;\n\t"
+      "mov.b16 m, 0xBF80;\n\t"  // -1
+      "mov.b32 {l, h}, %2;\n\t"
+      "fma.rn.f32.bf16 %0, l, m, %3;\n\t"
+      "fma.rn.f32.bf16 %1, h, m, %4;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(w), "f"(v.x), "f"(v.y));
+  x = f2(lo, hi);
   return w;
 }
 
@@ -319,6 +343,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                              const __grid_constant__ CUtensorMap to,
                              const __grid_constant__ LinearArgs a) {
   using L = LinLayout<D>;
+  using T = LinTmem<D, STATES>;
+  constexpr uint32_t kTmU = T::kU, kTmSc = T::kSc, kTmOut = T::kOut, kTmKp = T::kKp;
   extern __shared__ uint8_t smem_raw[];
   // pw[n] = exp(g n), ps[n] = scale pw[n]; ps is read from n = -31 on (unused there)
   __shared__ float pw[kLinC + 4], ps_pad[32 + kLinC + 4];
@@ -359,7 +385,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t kv_full = sb + L::kBar, kv_empty = kv_full + 24, q_full = kv_empty + 24,
                  q_empty = q_full + 8, sc_full = q_empty + 8, qs_done = sc_full + 8,
                  pv_ready = qs_done + 8, o_done = pv_ready + 8, o_free = o_done + 8,
-                 kp_full = o_free + 8, kp_empty = kp_full + 16, s_ready = kp_empty + 16,
+                 kp_full = o_free + 8, kp_empty = kp_full + 8 * T::kBufs,
+                 s_ready = kp_empty + 8 * T::kBufs,
                  u_done = s_ready + 8, y_full = u_done + 8, y_free = y_full + 8,
                  drain = y_free + 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
@@ -374,7 +401,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       // 256 state threads
       mbar_init(kv_empty + 8 * i, STATES ? 257 : 258);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < T::kBufs; ++i) {
       mbar_init(kp_full + 8 * i, 256);
       mbar_init(kp_empty + 8 * i, 1);
     }
@@ -475,10 +502,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         uint64_t v = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
 #pragma unroll 1
         for (int j = 0; j < kLinQuarters; ++j, ++m, v += 2 * 2048 >> 4) {
-          wait(kp_full + 8 * (m & 1), m >> 1);
+          const int buf = m % T::kBufs;
+          wait(kp_full + 8 * buf, m / T::kBufs);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t kp = tmem + kTmKp + kTmKpBuf * (m & 1);
+          const uint32_t kp = tmem + kTmKp + kTmKpBuf * buf;
           if (lead) {
 #pragma unroll
             for (int t = 0; t < 3; ++t)
@@ -486,7 +514,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               for (int ks = 0; ks < 2; ++ks)
                 umma_bf16_ts(tmem + kTmU, kp + 16 * t + 8 * ks, v + (ks * 2048 >> 4), kIdD,
                              j > 0 || t > 0 || ks > 0);
-            umma_commit(kp_empty + 8 * (m & 1));
+            umma_commit(kp_empty + 8 * buf);
           }
           __syncwarp();
         }
@@ -740,7 +768,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       uint32_t z[16];
 #pragma unroll
       for (int c = 0; c < 16; ++c) z[c] = 0u;
-      for (int c = 0; c < 8; ++c) tmem_st16(my_lanes + kTmKp + 16 * c, z);
+      for (int c = 0; c < T::kBufs * 3; ++c) tmem_st16(my_lanes + kTmKp + 16 * c, z);
       tmem_st_wait();
     }
     bool ok = true;
@@ -824,12 +852,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       }
-      // quarter j, as three terms; the first one before the state of the last
-      // chunk is taken up, which waits for that chunk's sum
+      // quarter j, as three terms
 #pragma unroll 1
-      for (int j = 0; ok && j < kLinQuarters; ++j, ++m) {
-        if (j == 1 && (n > 0 || !STATES)) next_state(n - 1, !STATES);
-        if (m >= 2) ok = ok && lin_wait_warp(kp_empty + 8 * (m & 1), ((m >> 1) - 1) & 1, abort);
+      for (int j = 0; ok && j <= kLinQuarters; ++j) {
+        if (j == T::kStateAt && (n > 0 || !STATES)) next_state(n - 1, !STATES);
+        if (j == kLinQuarters) break;
+        const int buf = m % T::kBufs, turn = m / T::kBufs;
+        if (turn > 0) ok = ok && lin_wait_warp(kp_empty + 8 * buf, (turn - 1) & 1, abort);
         if (!ok) break;
         tc_fence_after();
         if (mine) {
@@ -856,12 +885,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
               tmem_st_16x128(my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp +
-                                 kTmKpBuf * (m & 1) + 16 * t + 8 * half,
+                                 kTmKpBuf * buf + 16 * t + 8 * half,
                              w[t][x]);
           tmem_st_wait();
         }
         tc_fence_before();
-        mbar_arrive(kp_full + 8 * (m & 1));
+        mbar_arrive(kp_full + 8 * buf);
+        ++m;
       }
       mbar_arrive(kv_empty + 8 * (ki % L::kSlots));
       mbar_arrive(kv_empty + 8 * (vi % L::kSlots));
