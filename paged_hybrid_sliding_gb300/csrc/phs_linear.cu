@@ -148,7 +148,7 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 //   warps 8-15  rows of the state, two threads a row, in registers: state ->
 //               two terms in shared memory, K tile -> K'^T terms
 //   warp 16     issues KV
-//   warp 17     TMA loads: a ring of three K and V tiles, one Q tile
+//   warp 17     TMA loads: a ring of K and V tiles, one Q tile
 //   warp 18     TMA stores of the output tile
 //   warp 19     issues QK, QS and PV
 // The state's way through the registers and KV, and P's and the other three
@@ -166,38 +166,34 @@ constexpr int kLinC = kLinearChunk;
 constexpr int kLinThreads = 640;
 // registers a thread: 96 at launch, five warpgroups; 2 x 88 + 2 x 120 + 64 = 5 x 96
 constexpr int kLinRegsRows = 88, kLinRegsState = 120, kLinRegsIssue = 64;
-// K'^T goes in quarters of a chunk, 32 tokens at a time: 16 columns for each
-// of the three terms
-constexpr int kLinQuarters = 4;
-constexpr uint32_t kTmKpBuf = 48;
-
-// Tensor-memory columns: a chunk's sum U, scores (and P), output, and as many
-// buffers of K'^T as there is room for.  The state of the last chunk is taken
-// up (which waits for its sum) before quarter kStateAt: the quarters before
-// it find a buffer while that sum is still being formed.
+// Tensor-memory columns: a chunk's sum U, scores (and P), output, and two
+// buffers of K'^T, each as much of a chunk as there is room for: all of it in
+// the first launch, half at D = 64, a quarter at D = 128.  Forming the next
+// part then runs beside the product with the last.
 template <int D, bool STATES>
 struct LinTmem {
   static constexpr uint32_t kU = 0;
   static constexpr uint32_t kOut = D == 64 ? 64 : 256;
   static constexpr uint32_t kSc = 128;
   static constexpr uint32_t kKp = STATES ? 128 : D == 64 ? 256 : 384;
-  static constexpr int kBufs = STATES ? 8 : D == 64 ? 4 : 2;
-  static constexpr int kStateAt = kBufs - 1 < kLinQuarters ? kBufs - 1 : kLinQuarters;
-  static_assert(kKp + kBufs * kTmKpBuf <= 512, "tensor memory");
+  static constexpr int kParts = STATES ? 1 : D == 64 ? 2 : 4;
+  static constexpr int kSteps = kLinC / 16 / kParts;  // of 16 tokens, 8 columns a term
+  static constexpr uint32_t kTerm = 8 * kSteps, kBuf = 3 * kTerm;
+  static_assert(kKp + 2 * kBuf <= 512, "tensor memory");
 };
 
-template <int D>
+template <int D, bool STATES>
 struct LinLayout {
   static constexpr int kTile = kLinC * D * 2;  // [D / 64 halves][128 rows][128 bytes]
   static constexpr int kHalf = kLinC * 128;
-  static constexpr int kSlots = 3;             // K(0) V(0) K(1) V(1) ... in turn
-  static constexpr int kQ = 0;
-  static constexpr int kKV = kTile;
-  static constexpr int kOut = kKV + kSlots * kTile;
+  static constexpr int kSlots = STATES || D == 64 ? 6 : 3;  // K(0) V(0) K(1) V(1) ... in turn
+  static constexpr int kKV = 0;
+  static constexpr int kQ = kKV + kSlots * kTile;
+  static constexpr int kOut = kQ + kTile;
   static constexpr int kS = kOut + kTile;      // 2 terms [D / 64][D rows][128 bytes]
   static constexpr int kSTerm = D * D * 2;
-  static constexpr int kBar = kS + 2 * kSTerm;
-  static constexpr int kMisc = kBar + 36 * 8;  // tensor-memory base, abort flag
+  static constexpr int kBar = STATES ? kQ : kS + 2 * kSTerm;
+  static constexpr int kMisc = kBar + 30 * 8;  // tensor-memory base, abort flag
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static constexpr int kTables = (2 * (kLinC + 4) + 32) * 4;  // static: pw, ps and its pad
   static_assert(kAlloc + kTables <= 227 * 1024, "shared memory of the prompt kernel");
@@ -342,9 +338,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                              const __grid_constant__ CUtensorMap tv,
                              const __grid_constant__ CUtensorMap to,
                              const __grid_constant__ LinearArgs a) {
-  using L = LinLayout<D>;
+  using L = LinLayout<D, STATES>;
   using T = LinTmem<D, STATES>;
   constexpr uint32_t kTmU = T::kU, kTmSc = T::kSc, kTmOut = T::kOut, kTmKp = T::kKp;
+  // where there are no rows to work on, their warps help with K'
+  constexpr int kTermWarps = STATES ? 4 : 2;  // of 32 columns of K
+  constexpr int kTermThreads = 128 * kTermWarps;
   extern __shared__ uint8_t smem_raw[];
   // pw[n] = exp(g n), ps[n] = scale pw[n]; ps is read from n = -31 on (unused there)
   __shared__ float pw[kLinC + 4], ps_pad[32 + kLinC + 4];
@@ -382,11 +381,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // part ready, output complete / read, K' terms written / used, state (the
   // last chunk's sum is read, the state's terms written, V's rows behind the
   // last token zero), chunk sum complete, output tile written / stored
-  const uint32_t kv_full = sb + L::kBar, kv_empty = kv_full + 24, q_full = kv_empty + 24,
+  const uint32_t kv_full = sb + L::kBar, kv_empty = kv_full + 8 * L::kSlots,
+                 q_full = kv_empty + 8 * L::kSlots,
                  q_empty = q_full + 8, sc_full = q_empty + 8, qs_done = sc_full + 8,
                  pv_ready = qs_done + 8, o_done = pv_ready + 8, o_free = o_done + 8,
-                 kp_full = o_free + 8, kp_empty = kp_full + 8 * T::kBufs,
-                 s_ready = kp_empty + 8 * T::kBufs,
+                 kp_full = o_free + 8, kp_empty = kp_full + 16, s_ready = kp_empty + 16,
                  u_done = s_ready + 8, y_full = u_done + 8, y_free = y_full + 8,
                  drain = y_free + 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
@@ -397,12 +396,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(kv_full + 8 * i, 1);
-      // the products (two warps'; one where there are states alone), and the
-      // 256 state threads
-      mbar_init(kv_empty + 8 * i, STATES ? 257 : 258);
+      // the threads that form K' and, of a V tile, the products KV and PV; of a
+      // K tile, QK and one of those threads again
+      mbar_init(kv_empty + 8 * i, kTermThreads + (STATES ? 1 : 2));
     }
-    for (int i = 0; i < T::kBufs; ++i) {
-      mbar_init(kp_full + 8 * i, 256);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(kp_full + 8 * i, kTermThreads);
       mbar_init(kp_empty + 8 * i, 1);
     }
     mbar_init(y_full, 256);
@@ -434,187 +433,286 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + L::kMisc), 0);
   const uint32_t my_lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
 
-  if (warp >= 16) regs_dec<kLinRegsIssue>();
-  if (warp < 8) regs_dec<kLinRegsRows>();
-  if (warp == 17) {
-    // ---------------------------------------------------------------- TMA
-    if (lane == 0 && nch > 0) {
-      const uint64_t pol = policy_evict_first();
-      auto load = [&](const CUtensorMap* map, uint32_t dst, int head, int t, uint32_t bar) {
-        for (int hf = 0; hf < D / 64; ++hf)
-          tma_load_2d(dst + hf * (kLinC * 128), map, head * D + 64 * hf, t, bar, pol);
-      };
-      bool ok = true;
-      int nq = 0, tiles = 0;  // Q tiles, K and V tiles issued
-      auto load_kv = [&](const CUtensorMap* map, int t) {
-        const int slot = tiles % L::kSlots, turn = tiles / L::kSlots;
-        if (turn > 0) ok = ok && lin_wait(kv_empty + 8 * slot, (turn - 1) & 1, abort);
-        if (!ok) return;
-        mbar_arrive_expect_tx(kv_full + 8 * slot, L::kTile);
-        load(map, sb + L::kKV + slot * L::kTile, h, t, kv_full + 8 * slot);
-        ++tiles;
-      };
-      auto load_q = [&](int gq, int t) {
-        if (nq >= 1) ok = ok && lin_wait(q_empty, (nq - 1) & 1, abort);
-        if (!ok) return;
-        mbar_arrive_expect_tx(q_full, L::kTile);
-        load(&tq, sb + L::kQ, h * a.G + gq, t, q_full);
-        ++nq;
-      };
-      for (int n = 0; ok && n < nch; ++n) {
-        const int t = t0 + n * kLinC;
-        load_kv(&tk, t);
-        if (!STATES && ok) load_q(0, t);
-        if (ok) load_kv(&tv, t);
-        for (int gq = 1; !STATES && ok && gq < a.G; ++gq) load_q(gq, t);
-      }
-      if (!ok) {
-        set_status(a.status, PHS_ETIMEOUT);
-        *abort = 1;
-      }
-      // copies still in flight land before the CTA ends
-      for (int i = max(0, tiles - L::kSlots); i < tiles; ++i)
-        (void)mbar_wait(kv_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1);
-      if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
+  // ---- K'^T of 32 columns of K, as three terms: ldmatrix.trans gives thread
+  // 4 x + y tokens 2 y, 2 y + 1 (of 8) of column x of each of 4 groups of 8
+  // columns.  The kTermWarps warps of these columns, of which this is number
+  // `which`, take steps of 16 tokens in turn.  `between(p)` is called before part p.
+  auto form_terms = [&](int which, auto&& between) {
+    const int qt = warp & 3, kx = lane >> 3;  // matrix kx: columns 32 qt + 8 kx ..
+    const bool mine = 32 * qt < D;            // D = 64: the upper half has no columns
+    const uint32_t kcol = (qt >> 1) * L::kHalf + (lane & 7) * 128 +
+                          ((((4 * (qt & 1) + kx) ^ lane) & 7) << 4);
+    if (!mine && which == 0) {  // rows 64..127 of K'^T are zero
+      uint32_t z[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) z[c] = 0u;
+      for (uint32_t c = 0; c < 2 * T::kBuf; c += 16) tmem_st16(my_lanes + kTmKp + c, z);
+      tmem_st_wait();
     }
-  } else if (warp == 16 || (!STATES && warp == 19)) {
-    // ----------------------------------------------------------- products
-    // A whole warp walks the chunks and one elected lane issues: what the
-    // instructions take is then known to be the same in every lane, and the
-    // compiler keeps it in uniform registers (issued from a lane of its own,
-    // an instruction took 90 cycles and more, whatever its width).
-    constexpr uint32_t kIdQK = idesc_bf16_f32(128, kLinC, false, false);
-    constexpr uint32_t kIdD = idesc_bf16_f32(128, D, false, true);
     bool ok = true;
-    const bool lead = elect_one();
-    auto wait = [&](uint32_t bar, int turn) {
-      ok = ok && lin_wait_warp(bar, turn & 1, abort);
-    };
-    // tile i of the ring: its place, once it has been loaded
-    auto tile = [&](int i) { return sb + L::kKV + (i % L::kSlots) * L::kTile; };
-    auto tile_full = [&](int i) { wait(kv_full + 8 * (i % L::kSlots), i / L::kSlots); };
-    auto tile_empty = [&](int i) { return kv_empty + 8 * (i % L::kSlots); };
-    if (warp == 16) {  // KV
-      int m = 0;       // quarters
-      for (int n = 0; ok && n < nch; ++n) {
-        if (!STATES || n >= 1) wait(s_ready, STATES ? n - 1 : n);
-        tile_full(2 * n + 1);
-        uint64_t v = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
-#pragma unroll 1
-        for (int j = 0; j < kLinQuarters; ++j, ++m, v += 2 * 2048 >> 4) {
-          const int buf = m % T::kBufs;
-          wait(kp_full + 8 * buf, m / T::kBufs);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t kp = tmem + kTmKp + kTmKpBuf * buf;
-          if (lead) {
-#pragma unroll
-            for (int t = 0; t < 3; ++t)
-#pragma unroll
-              for (int ks = 0; ks < 2; ++ks)
-                umma_bf16_ts(tmem + kTmU, kp + 16 * t + 8 * ks, v + (ks * 2048 >> 4), kIdD,
-                             j > 0 || t > 0 || ks > 0);
-            umma_commit(kp_empty + 8 * buf);
-          }
-          __syncwarp();
+    int m = 0;
+    for (int n = 0; ok && n < nch; ++n) {
+      const int v = min(kLinC, t1 - t0 - n * kLinC);
+      const int ki = 2 * n, vi = 2 * n + 1;  // tiles of the ring
+      const uint32_t kt = sb + L::kKV + (ki % L::kSlots) * L::kTile;
+      ok = lin_wait_warp(kv_full + 8 * (ki % L::kSlots), (ki / L::kSlots) & 1, abort);
+      if (!ok) break;
+      if (v < kLinC) {
+        // rows behind the last token: no 0 * NaN.  K: what this warp reads
+        // itself (QK may read either; those scores are masked); V: all.
+        ok = lin_wait_warp(kv_full + 8 * (vi % L::kSlots), (vi / L::kSlots) & 1, abort);
+        if (!ok) break;
+        const uint32_t vt = sb + L::kKV + (vi % L::kSlots) * L::kTile;
+        for (int t = v + (lane >> 2); mine && t < kLinC; t += 8)
+          if ((t >> 4) % kTermWarps == which)
+            sts128(kt + (qt >> 1) * L::kHalf + t * 128 +
+                       ((((4 * (qt & 1) + (lane & 3)) ^ t) & 7) << 4),
+                   0, 0, 0, 0);
+        for (int u = 128 * which + 32 * qt + lane; u < D / 64 * (kLinC - v) * 8;
+             u += kTermThreads) {
+          const int hf = u / ((kLinC - v) * 8), x = u % ((kLinC - v) * 8);
+          sts128(vt + hf * L::kHalf + v * 128 + x * 16, 0, 0, 0, 0);
         }
-        if (ok && lead) {
-          umma_commit(u_done);
-          umma_commit(tile_empty(2 * n));
-          umma_commit(tile_empty(2 * n + 1));
-        }
+        fence_proxy_async_smem();
         __syncwarp();
       }
-    } else {  // QK, QS, PV
-      // descriptors; a later part of a tile is `bytes >> 4` further on
-      const uint64_t dq = sdesc_sw128(sb + L::kQ, 16, 1024);
-      const uint64_t ds = sdesc_sw128(sb + L::kS, D * 128, 1024);
-      int pair = 0;
-      for (int n = 0; ok && n < nch; ++n)
-        for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
-          const bool last = gq == a.G - 1;
-          if (gq == 0) tile_full(2 * n);
-          wait(q_full, pair);
-          if (pair >= 1) wait(o_done, pair - 1);  // P of the last pair is read
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t k = sdesc_sw128(tile(2 * n), 16, 1024);
-          if (lead) {
-#pragma unroll 2
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t at = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
-              umma_bf16(tmem + kTmSc, dq + at, k + at, kIdQK, ks > 0);
+#pragma unroll 1
+      for (int p = 0; ok && p <= T::kParts; ++p) {
+        if (p == 1) ok = between(n);
+        if (p == T::kParts || !ok) break;
+        if (m >= 2) ok = lin_wait_warp(kp_empty + 8 * (m & 1), ((m >> 1) - 1) & 1, abort);
+        if (!ok) break;
+        tc_fence_after();
+        if (mine) {
+#pragma unroll 1
+          for (int st = which; st < T::kSteps; st += kTermWarps) {
+            const int t = (p * T::kSteps + st) * 16;  // first token
+            uint32_t w[3][2][4];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t k[4];
+              ldsm_x4_t(kt + kcol + (t + 8 * q) * 128, k[0], k[1], k[2], k[3]);
+              // weights of this thread's two tokens (0 behind the last)
+              const int e = v - 1 - t - 8 * q - 2 * (lane & 3);
+              const float p0 = pw[max(e, 0)], p1 = pw[max(e - 1, 0)];
+              const uint64_t f = f2(e >= 0 ? p0 : 0.f, e >= 1 ? p1 : 0.f);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                uint64_t y = f2_mul(f2_bf16(k[x]), f);
+                w[2][x >> 1][2 * q + (x & 1)] = take_term(y);
+                w[1][x >> 1][2 * q + (x & 1)] = take_term(y);
+                w[0][x >> 1][2 * q + (x & 1)] = pack_term(y);
+              }
             }
-            umma_commit(sc_full);
-            if (last) umma_commit(tile_empty(2 * n));
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                tmem_st_16x128(my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp +
+                                   T::kBuf * (m & 1) + T::kTerm * i + 8 * st,
+                               w[i][x]);
           }
-          __syncwarp();
-          if (gq == 0) wait(s_ready, n);
-          if (pair >= 1) wait(o_free, pair - 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (lead) {
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(kp_full + 8 * (m & 1));
+        ++m;
+      }
+      // V's place in the ring was an earlier K's: only once V is there do all of
+      // that tile's users have let go of it, and an arrival counts for V (a warp
+      // that is ahead of the others would else take part in the wrong phase)
+      ok = ok && lin_wait_warp(kv_full + 8 * (vi % L::kSlots), (vi / L::kSlots) & 1, abort);
+      if (!ok) break;
+      mbar_arrive(kv_empty + 8 * (ki % L::kSlots));
+      if (which == 0 && qt == 0 && lane == 0) mbar_arrive(kv_empty + 8 * (ki % L::kSlots));
+      mbar_arrive(kv_empty + 8 * (vi % L::kSlots));
+    }
+    return ok;
+  };
+
+  // (each warpgroup sets its registers at the head of its own branch, so that
+  // the code behind it is compiled for that number)
+  if (warp >= 16) {
+    regs_dec<kLinRegsIssue>();
+    if (warp == 17) {
+      // ---------------------------------------------------------------- TMA
+      if (lane == 0 && nch > 0) {
+        const uint64_t pol = policy_evict_first();
+        auto load = [&](const CUtensorMap* map, uint32_t dst, int head, int t, uint32_t bar) {
+          for (int hf = 0; hf < D / 64; ++hf)
+            tma_load_2d(dst + hf * (kLinC * 128), map, head * D + 64 * hf, t, bar, pol);
+        };
+        bool ok = true;
+        int nq = 0, tiles = 0;  // Q tiles, K and V tiles issued
+        auto load_kv = [&](const CUtensorMap* map, int t) {
+          const int slot = tiles % L::kSlots, turn = tiles / L::kSlots;
+          if (turn > 0) ok = ok && lin_wait(kv_empty + 8 * slot, (turn - 1) & 1, abort);
+          if (!ok) return;
+          mbar_arrive_expect_tx(kv_full + 8 * slot, L::kTile);
+          load(map, sb + L::kKV + slot * L::kTile, h, t, kv_full + 8 * slot);
+          ++tiles;
+        };
+        auto load_q = [&](int gq, int t) {
+          if (nq >= 1) ok = ok && lin_wait(q_empty, (nq - 1) & 1, abort);
+          if (!ok) return;
+          mbar_arrive_expect_tx(q_full, L::kTile);
+          load(&tq, sb + L::kQ, h * a.G + gq, t, q_full);
+          ++nq;
+        };
+        for (int n = 0; ok && n < nch; ++n) {
+          const int t = t0 + n * kLinC;
+          load_kv(&tk, t);
+          if (!STATES && ok) load_q(0, t);
+          if (ok) load_kv(&tv, t);
+          for (int gq = 1; !STATES && ok && gq < a.G; ++gq) load_q(gq, t);
+        }
+        if (!ok) {
+          set_status(a.status, PHS_ETIMEOUT);
+          *abort = 1;
+        }
+        // copies still in flight land before the CTA ends
+        for (int i = max(0, tiles - L::kSlots); i < tiles; ++i)
+          (void)mbar_wait(kv_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1);
+        if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
+      }
+    } else if (warp == 16 || (!STATES && warp == 19)) {
+      // ----------------------------------------------------------- products
+      // A whole warp walks the chunks and one elected lane issues: what the
+      // instructions take is then known to be the same in every lane, and the
+      // compiler keeps it in uniform registers (issued from a lane of its own,
+      // an instruction took 90 cycles and more, whatever its width).
+      constexpr uint32_t kIdQK = idesc_bf16_f32(128, kLinC, false, false);
+      constexpr uint32_t kIdD = idesc_bf16_f32(128, D, false, true);
+      bool ok = true;
+      const bool lead = elect_one();
+      auto wait = [&](uint32_t bar, int turn) {
+        ok = ok && lin_wait_warp(bar, turn & 1, abort);
+      };
+      // tile i of the ring: its place, once it has been loaded
+      auto tile = [&](int i) { return sb + L::kKV + (i % L::kSlots) * L::kTile; };
+      auto tile_full = [&](int i) { wait(kv_full + 8 * (i % L::kSlots), i / L::kSlots); };
+      auto tile_empty = [&](int i) { return kv_empty + 8 * (i % L::kSlots); };
+      if (warp == 16) {  // KV
+        int m = 0;       // parts
+        for (int n = 0; ok && n < nch; ++n) {
+          if (!STATES || n >= 1) wait(s_ready, STATES ? n - 1 : n);
+          tile_full(2 * n + 1);
+          uint64_t v = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
 #pragma unroll 1
-            for (int t = 0; t < 2; ++t)
+          for (int p = 0; p < T::kParts; ++p, ++m, v += T::kSteps * 2048 >> 4) {
+            wait(kp_full + 8 * (m & 1), m >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t kp = tmem + kTmKp + T::kBuf * (m & 1);
+            if (lead) {
+#pragma unroll 1
+              for (int t = 0; t < 3; ++t)
 #pragma unroll 2
-              for (int ks = 0; ks < D / 16; ++ks)
-                umma_bf16(tmem + kTmOut, dq + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4),
-                          ds + ((t * L::kSTerm + ks * 2048) >> 4), kIdD, t > 0 || ks > 0);
-            umma_commit(qs_done);
-            umma_commit(q_empty);
-            if (last) umma_commit(u_done);  // the state's terms have been read
+                for (int ks = 0; ks < T::kSteps; ++ks)
+                  umma_bf16_ts(tmem + kTmU, kp + T::kTerm * t + 8 * ks, v + (ks * 2048 >> 4), kIdD,
+                               p > 0 || t > 0 || ks > 0);
+              umma_commit(kp_empty + 8 * (m & 1));
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          if (gq == 0) tile_full(2 * n + 1);
-          wait(pv_ready, pair);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t v = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
-          if (lead) {
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t)
-#pragma unroll 2
-              for (int ks = 0; ks < kLinC / 16; ++ks)
-                umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 16 * ks + 8 * t, v + (ks * 2048 >> 4),
-                             kIdD, 1u);
-            umma_commit(o_done);
-            if (last) umma_commit(tile_empty(2 * n + 1));
+          if (ok && lead) {
+            umma_commit(u_done);
+            umma_commit(tile_empty(2 * n + 1));
           }
           __syncwarp();
         }
-    }
-    if (!ok && lane == 0) {
-      set_status(a.status, PHS_ETIMEOUT);
-      *abort = 1;
-    }
-    // every product of this warp is complete before tensor memory is released
-    const uint32_t done = warp == 16 ? drain : drain + 8;
-    if (lead) umma_commit(done);
-    (void)mbar_wait(done, 0);
-    __syncwarp();
-  } else if (warp == 18) {
-    // --------------------------------------------- whole output tiles out
-    if (!STATES && lane == 0) {
-      const int whole = (t1 - t0) / kLinC * a.G;
-      bool ok = true;
-      for (int p = 0; ok && p < whole; ++p) {
-        ok = lin_wait(y_full, p & 1, abort);
-        if (!ok) break;
-        for (int hf = 0; hf < D / 64; ++hf)
-          tma_store_2d(&to, sb + L::kOut + hf * L::kHalf, (h * a.G + p % a.G) * D + 64 * hf,
-                       t0 + p / a.G * kLinC);
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        mbar_arrive(y_free);
+      } else {  // QK, QS, PV
+        // descriptors; a later part of a tile is `bytes >> 4` further on
+        const uint64_t dq = sdesc_sw128(sb + L::kQ, 16, 1024);
+        const uint64_t ds = sdesc_sw128(sb + L::kS, D * 128, 1024);
+        int pair = 0;
+        for (int n = 0; ok && n < nch; ++n)
+          for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
+            const bool last = gq == a.G - 1;
+            if (gq == 0) tile_full(2 * n);
+            wait(q_full, pair);
+            if (pair >= 1) wait(o_done, pair - 1);  // P of the last pair is read
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t k = sdesc_sw128(tile(2 * n), 16, 1024);
+            if (lead) {
+#pragma unroll 2
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t at = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
+                umma_bf16(tmem + kTmSc, dq + at, k + at, kIdQK, ks > 0);
+              }
+              umma_commit(sc_full);
+              if (last) umma_commit(tile_empty(2 * n));
+            }
+            __syncwarp();
+            if (gq == 0) wait(s_ready, n);
+            if (pair >= 1) wait(o_free, pair - 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (lead) {
+#pragma unroll 1
+              for (int t = 0; t < 2; ++t)
+#pragma unroll 2
+                for (int ks = 0; ks < D / 16; ++ks)
+                  umma_bf16(tmem + kTmOut, dq + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4),
+                            ds + ((t * L::kSTerm + ks * 2048) >> 4), kIdD, t > 0 || ks > 0);
+              umma_commit(qs_done);
+              umma_commit(q_empty);
+              if (last) umma_commit(u_done);  // the state's terms have been read
+            }
+            __syncwarp();
+            if (gq == 0) tile_full(2 * n + 1);
+            wait(pv_ready, pair);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t v = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
+            if (lead) {
+#pragma unroll 1
+              for (int t = 0; t < 2; ++t)
+#pragma unroll 2
+                for (int ks = 0; ks < kLinC / 16; ++ks)
+                  umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 16 * ks + 8 * t, v + (ks * 2048 >> 4),
+                               kIdD, 1u);
+              umma_commit(o_done);
+              if (last) umma_commit(tile_empty(2 * n + 1));
+            }
+            __syncwarp();
+          }
       }
-      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-      if (!ok) {
+      if (!ok && lane == 0) {
         set_status(a.status, PHS_ETIMEOUT);
         *abort = 1;
+      }
+      // every product of this warp is complete before tensor memory is released
+      const uint32_t done = warp == 16 ? drain : drain + 8;
+      if (lead) umma_commit(done);
+      (void)mbar_wait(done, 0);
+      __syncwarp();
+    } else if (warp == 18) {
+      // --------------------------------------------- whole output tiles out
+      if (!STATES && lane == 0) {
+        const int whole = (t1 - t0) / kLinC * a.G;
+        bool ok = true;
+        for (int p = 0; ok && p < whole; ++p) {
+          ok = lin_wait(y_full, p & 1, abort);
+          if (!ok) break;
+          for (int hf = 0; hf < D / 64; ++hf)
+            tma_store_2d(&to, sb + L::kOut + hf * L::kHalf, (h * a.G + p % a.G) * D + 64 * hf,
+                         t0 + p / a.G * kLinC);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          mbar_arrive(y_free);
+        }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (!ok) {
+          set_status(a.status, PHS_ETIMEOUT);
+          *abort = 1;
+        }
       }
     }
   } else if (!STATES && warp < 8) {
     // ------------------------------------------------- rows of the chunk
+    regs_dec<kLinRegsRows>();
     const int qt = warp & 3, half = warp >> 2, i = 32 * qt + lane;  // row
     uint64_t col[8];  // exp(g (15 - e))
 #pragma unroll
@@ -722,7 +820,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       set_status(a.status, PHS_ETIMEOUT);
       *abort = 1;
     }
-  } else if (warp >= 8 && warp < 16) {
+  } else if (STATES && warp < 8) {
+    regs_dec<kLinRegsRows>();
+    if (!form_terms(2 + (warp >> 2), [](int) { return true; })) {
+      set_status(a.status, PHS_ETIMEOUT);
+      *abort = 1;
+    }
+  } else {
     // ------------------------------------------------- rows of the state
     regs_inc<kLinRegsState>();
     constexpr int N = D / 2;  // columns of a thread
@@ -764,15 +868,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (STATES) store_row(copy);
       }
     }
-    if (!mine && half == 0) {  // D = 64: rows 64..127 of K'^T are zero
-      uint32_t z[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) z[c] = 0u;
-      for (int c = 0; c < T::kBufs * 3; ++c) tmem_st16(my_lanes + kTmKp + 16 * c, z);
-      tmem_st_wait();
-    }
     bool ok = true;
-    int m = 0;
     const float keep_chunk = expm1f(g * kLinC);
     // S <- state after chunk n (n >= 0), and where `terms` its two terms to
     // shared memory for the next chunk's QS (the last one has read its own
@@ -822,80 +918,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       tc_fence_before();
       mbar_arrive(s_ready);
     };
-    // K'^T of 32 columns of K: ldmatrix.trans gives thread 4 x + y tokens 2 y,
-    // 2 y + 1 (of 8) of column x of each of 4 groups of 8 columns.  The two
-    // warps of these columns take 16 tokens each of a quarter.
-    const int kx = lane >> 3;  // matrix kx: columns 32 qt + 8 kx ..
-    const uint32_t kcol = (qt >> 1) * L::kHalf + (lane & 7) * 128 +
-                          ((((4 * (qt & 1) + kx) ^ lane) & 7) << 4);
-    for (int n = 0; ok && n < nch; ++n) {
-      const int v = min(kLinC, t1 - t0 - n * kLinC);
-      const int ki = 2 * n, vi = 2 * n + 1;  // tiles of the ring
-      const uint32_t kt = sb + L::kKV + (ki % L::kSlots) * L::kTile;
-      ok = lin_wait_warp(kv_full + 8 * (ki % L::kSlots), (ki / L::kSlots) & 1, abort);
-      if (!ok) break;
-      if (v < kLinC) {
-        // rows behind the last token: no 0 * NaN.  K: the columns this warp
-        // reads itself (QK may read either; those scores are masked); V: all.
-        ok = lin_wait_warp(kv_full + 8 * (vi % L::kSlots), (vi / L::kSlots) & 1, abort);
-        if (!ok) break;
-        const uint32_t vt = sb + L::kKV + (vi % L::kSlots) * L::kTile;
-        for (int t = v + (lane >> 2); mine && t < kLinC; t += 8)
-          if (((t >> 4) & 1) == half)  // its own steps
-            sts128(kt + (qt >> 1) * L::kHalf + t * 128 +
-                       ((((4 * (qt & 1) + (lane & 3)) ^ t) & 7) << 4),
-                   0, 0, 0, 0);
-        for (int u = tid - 256; u < D / 64 * (kLinC - v) * 8; u += 256) {
-          const int hf = u / ((kLinC - v) * 8), x = u % ((kLinC - v) * 8);
-          sts128(vt + hf * L::kHalf + v * 128 + x * 16, 0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      // quarter j, as three terms
-#pragma unroll 1
-      for (int j = 0; ok && j <= kLinQuarters; ++j) {
-        if (j == T::kStateAt && (n > 0 || !STATES)) next_state(n - 1, !STATES);
-        if (j == kLinQuarters) break;
-        const int buf = m % T::kBufs, turn = m / T::kBufs;
-        if (turn > 0) ok = ok && lin_wait_warp(kp_empty + 8 * buf, (turn - 1) & 1, abort);
-        if (!ok) break;
-        tc_fence_after();
-        if (mine) {
-          const int st = 2 * j + half;
-          uint32_t w[3][2][4];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t k[4];
-            ldsm_x4_t(kt + kcol + (2 * st + q) * 1024, k[0], k[1], k[2], k[3]);
-            // weights of this thread's two tokens (0 behind the last)
-            const int e = v - 1 - 8 * (2 * st + q) - 2 * (lane & 3);
-            const float p0 = pw[max(e, 0)], p1 = pw[max(e - 1, 0)];
-            const uint64_t f = f2(e >= 0 ? p0 : 0.f, e >= 1 ? p1 : 0.f);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint64_t y = f2_mul(f2_bf16(k[x]), f);
-              w[2][x >> 1][2 * q + (x & 1)] = take_term(y);
-              w[1][x >> 1][2 * q + (x & 1)] = take_term(y);
-              w[0][x >> 1][2 * q + (x & 1)] = pack_term(y);
-            }
-          }
-#pragma unroll
-          for (int t = 0; t < 3; ++t)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              tmem_st_16x128(my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp +
-                                 kTmKpBuf * buf + 16 * t + 8 * half,
-                             w[t][x]);
-          tmem_st_wait();
-        }
-        tc_fence_before();
-        mbar_arrive(kp_full + 8 * buf);
-        ++m;
-      }
-      mbar_arrive(kv_empty + 8 * (ki % L::kSlots));
-      mbar_arrive(kv_empty + 8 * (vi % L::kSlots));
-    }
+    ok = form_terms(half, [&](int n) {
+      if (n > 0 || !STATES) next_state(n - 1, !STATES);
+      return ok;
+    });
     if (nch > 0) next_state(nch - 1, false);
     if (!ok) {
       set_status(a.status, PHS_ETIMEOUT);
@@ -916,15 +942,15 @@ template <int D>
 static int launch_linear_prompt_t(const CUtensorMap& tq, const CUtensorMap& tk,
                                   const CUtensorMap& tv, const CUtensorMap& to,
                                   const LinearArgs& a, cudaStream_t stream) {
-  using L = LinLayout<D>;
+  constexpr int kStates = LinLayout<D, true>::kAlloc, kRows = LinLayout<D, false>::kAlloc;
   auto states = phs_linear_prompt_kernel<D, true>;
   auto rows = phs_linear_prompt_kernel<D, false>;
-  if (ensure_dynamic_smem(reinterpret_cast<const void*>(rows), L::kAlloc) != PHS_OK ||
-      ensure_dynamic_smem(reinterpret_cast<const void*>(states), L::kAlloc) != PHS_OK)
+  if (ensure_dynamic_smem(reinterpret_cast<const void*>(rows), kRows) != PHS_OK ||
+      ensure_dynamic_smem(reinterpret_cast<const void*>(states), kStates) != PHS_OK)
     return PHS_ECUDA;
   if (a.nseg > 1)
-    states<<<dim3(a.B, a.Hkv, a.nseg - 1), kLinThreads, L::kAlloc, stream>>>(tq, tk, tv, to, a);
-  rows<<<dim3(a.B, a.Hkv, a.nseg), kLinThreads, L::kAlloc, stream>>>(tq, tk, tv, to, a);
+    states<<<dim3(a.B, a.Hkv, a.nseg - 1), kLinThreads, kStates, stream>>>(tq, tk, tv, to, a);
+  rows<<<dim3(a.B, a.Hkv, a.nseg), kLinThreads, kRows, stream>>>(tq, tk, tv, to, a);
   return cudaGetLastError() == cudaSuccess ? PHS_OK : PHS_ECUDA;
 }
 
