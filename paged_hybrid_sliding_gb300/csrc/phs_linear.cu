@@ -167,19 +167,21 @@ constexpr int kLinThreads = 640;
 // registers a thread: 96 at launch, five warpgroups; 2 x 88 + 2 x 120 + 64 = 5 x 96
 constexpr int kLinRegsRows = 88, kLinRegsState = 120, kLinRegsIssue = 64;
 // Tensor-memory columns: a chunk's sum U, scores (and P), output, and two
-// buffers of K'^T, each as much of a chunk as there is room for: all of it in
-// the first launch, half at D = 64, a quarter at D = 128.  Forming the next
-// part then runs beside the product with the last.
+// buffers of K'^T, each as much of a chunk as there is room for: half, or a
+// quarter beside the rows at D = 128.  Forming the next part then runs beside
+// the product with the last.  Where there are no rows U has two buffers, and
+// a chunk's KV does not wait for the last one's sum to be taken up.
 template <int D, bool STATES>
 struct LinTmem {
   static constexpr uint32_t kU = 0;
+  static constexpr int kUBufs = STATES ? 2 : 1;
   static constexpr uint32_t kOut = D == 64 ? 64 : 256;
   static constexpr uint32_t kSc = 128;
-  static constexpr uint32_t kKp = STATES ? 128 : D == 64 ? 256 : 384;
-  static constexpr int kParts = STATES ? 1 : D == 64 ? 2 : 4;
+  static constexpr uint32_t kKp = STATES || D == 64 ? 256 : 384;
+  static constexpr int kParts = STATES || D == 64 ? 2 : 4;
   static constexpr int kSteps = kLinC / 16 / kParts;  // of 16 tokens, 8 columns a term
   static constexpr uint32_t kTerm = 8 * kSteps, kBuf = 3 * kTerm;
-  static_assert(kKp + 2 * kBuf <= 512, "tensor memory");
+  static_assert(kUBufs * D <= kKp && kKp + 2 * kBuf <= 512, "tensor memory");
 };
 
 template <int D, bool STATES>
@@ -193,7 +195,7 @@ struct LinLayout {
   static constexpr int kS = kOut + kTile;      // 2 terms [D / 64][D rows][128 bytes]
   static constexpr int kSTerm = D * D * 2;
   static constexpr int kBar = STATES ? kQ : kS + 2 * kSTerm;
-  static constexpr int kMisc = kBar + 30 * 8;  // tensor-memory base, abort flag
+  static constexpr int kMisc = kBar + 32 * 8;  // tensor-memory base, abort flag
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static constexpr int kTables = (2 * (kLinC + 4) + 32) * 4;  // static: pw, ps and its pad
   static_assert(kAlloc + kTables <= 227 * 1024, "shared memory of the prompt kernel");
@@ -341,8 +343,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   using L = LinLayout<D, STATES>;
   using T = LinTmem<D, STATES>;
   constexpr uint32_t kTmU = T::kU, kTmSc = T::kSc, kTmOut = T::kOut, kTmKp = T::kKp;
-  // where there are no rows to work on, their warps help with K'
-  constexpr int kTermWarps = STATES ? 4 : 2;  // of 32 columns of K
+  constexpr int kTermWarps = 2;  // that form K' of 32 columns of K
   constexpr int kTermThreads = 128 * kTermWarps;
   extern __shared__ uint8_t smem_raw[];
   // pw[n] = exp(g n), ps[n] = scale pw[n]; ps is read from n = -31 on (unused there)
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                  q_empty = q_full + 8, sc_full = q_empty + 8, qs_done = sc_full + 8,
                  pv_ready = qs_done + 8, o_done = pv_ready + 8, o_free = o_done + 8,
                  kp_full = o_free + 8, kp_empty = kp_full + 16, s_ready = kp_empty + 16,
-                 u_done = s_ready + 8, y_full = u_done + 8, y_free = y_full + 8,
+                 u_done = s_ready + 16, y_full = u_done + 16, y_free = y_full + 8,
                  drain = y_free + 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   if (warp == 16) {
@@ -413,8 +414,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     mbar_init(pv_ready, 256);
     mbar_init(o_done, 1);
     mbar_init(o_free, 256);
-    mbar_init(s_ready, 256);
-    mbar_init(u_done, STATES ? 1 : 2);  // KV, and QS done with the state's terms
+    for (int i = 0; i < T::kUBufs; ++i) {
+      mbar_init(s_ready + 8 * i, 256);
+      mbar_init(u_done + 8 * i, STATES ? 1 : 2);  // KV, and QS done with the state's terms
+    }
     mbar_init(drain, 1);
     mbar_init(drain + 8, 1);
     *abort = 0;
@@ -436,7 +439,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // ---- K'^T of 32 columns of K, as three terms: ldmatrix.trans gives thread
   // 4 x + y tokens 2 y, 2 y + 1 (of 8) of column x of each of 4 groups of 8
   // columns.  The kTermWarps warps of these columns, of which this is number
-  // `which`, take steps of 16 tokens in turn.  `between(p)` is called before part p.
+  // `which`, take steps of 16 tokens in turn.  `between(n)` is called after the
+  // first part of chunk n.
   auto form_terms = [&](int which, auto&& between) {
     const int qt = warp & 3, kx = lane >> 3;  // matrix kx: columns 32 qt + 8 kx ..
     const bool mine = 32 * qt < D;            // D = 64: the upper half has no columns
@@ -595,7 +599,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       if (warp == 16) {  // KV
         int m = 0;       // parts
         for (int n = 0; ok && n < nch; ++n) {
-          if (!STATES || n >= 1) wait(s_ready, STATES ? n - 1 : n);
+          const int ub = n % T::kUBufs;
+          if (!STATES)
+            wait(s_ready, n);
+          else if (n >= 2)  // the sum two chunks ago has been taken up
+            wait(s_ready + 8 * ub, n / 2 - 1);
           tile_full(2 * n + 1);
           uint64_t v = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
 #pragma unroll 1
@@ -609,14 +617,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               for (int t = 0; t < 3; ++t)
 #pragma unroll 2
                 for (int ks = 0; ks < T::kSteps; ++ks)
-                  umma_bf16_ts(tmem + kTmU, kp + T::kTerm * t + 8 * ks, v + (ks * 2048 >> 4), kIdD,
+                  umma_bf16_ts(tmem + kTmU + D * ub, kp + T::kTerm * t + 8 * ks, v + (ks * 2048 >> 4), kIdD,
                                p > 0 || t > 0 || ks > 0);
               umma_commit(kp_empty + 8 * (m & 1));
             }
             __syncwarp();
           }
           if (ok && lead) {
-            umma_commit(u_done);
+            umma_commit(u_done + 8 * ub);
             umma_commit(tile_empty(2 * n + 1));
           }
           __syncwarp();
@@ -822,7 +830,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
   } else if (STATES && warp < 8) {
     regs_dec<kLinRegsRows>();
-    if (!form_terms(2 + (warp >> 2), [](int) { return true; })) {
+    if (!form_terms(warp >> 2, [](int) { return true; })) {
       set_status(a.status, PHS_ETIMEOUT);
       *abort = 1;
     }
@@ -875,8 +883,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // by then: the chunk's sum was issued after it)
     auto next_state = [&](int n, bool terms) {
       uint64_t keep = 0ull;
+      const int ub = n >= 0 ? n % T::kUBufs : 0;
       if (n >= 0) {
-        ok = ok && lin_wait_warp(u_done, n & 1, abort);
+        ok = ok && lin_wait_warp(u_done + 8 * ub, n / T::kUBufs & 1, abort);
         if (!ok) return;
         tc_fence_after();
         const int v = min(kLinC, t1 - t0 - n * kLinC);
@@ -889,7 +898,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int c = 0; c < N / 32; ++c) {
           if (n >= 0) {
             uint32_t u[32];
-            tmem_ld32(my_lanes + kTmU + half * N + 32 * c, u);
+            tmem_ld32(my_lanes + kTmU + D * ub + half * N + 32 * c, u);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -916,13 +925,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (terms) fence_proxy_async_smem();
       }
       tc_fence_before();
-      mbar_arrive(s_ready);
+      mbar_arrive(s_ready + 8 * ub);
     };
-    ok = form_terms(half, [&](int n) {
-      if (n > 0 || !STATES) next_state(n - 1, !STATES);
-      return ok;
-    });
-    if (nch > 0) next_state(nch - 1, false);
+    if (STATES) {
+      for (int n = 0; ok && n < nch; ++n) next_state(n, false);
+    } else {
+      ok = form_terms(half, [&](int n) {
+        next_state(n - 1, true);
+        return ok;
+      });
+      if (nch > 0) next_state(nch - 1, false);
+    }
     if (!ok) {
       set_status(a.status, PHS_ETIMEOUT);
       *abort = 1;
