@@ -488,8 +488,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (mine) {
-#pragma unroll 1
-          for (int st = which; st < T::kSteps; st += kTermWarps) {
+#pragma unroll
+          for (int i2 = 0; i2 < T::kSteps / kTermWarps; ++i2) {
+            const int st = which + i2 * kTermWarps;
             const int t = (p * T::kSteps + st) * 16;  // first token
             uint32_t w[3][2][4];
 #pragma unroll
