@@ -151,8 +151,7 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 //   warp 17     TMA loads: a ring of K and V tiles, one Q tile
 //   warp 18     TMA stores of the output tile
 //   warp 19     issues QK, QS and PV
-// The state's way through the registers and KV, and P's and the other three
-// products, meet once a chunk: the state's terms, and QS done with them.
+// KV is issued before PV: its sum's way into the state then runs beside PV.
 // Two warps on each scheduler run each role's code, and its loops are kept
 // small: with one warp and everything unrolled, fetching instructions was
 // the largest stall (3.1 of 10.7 warp-cycles an instruction).
@@ -195,7 +194,8 @@ struct LinLayout {
   static constexpr int kS = kOut + kTile;      // 2 terms [D / 64][D rows][128 bytes]
   static constexpr int kSTerm = D * D * 2;
   static constexpr int kBar = STATES ? kQ : kS + 2 * kSTerm;
-  static constexpr int kMisc = kBar + 32 * 8;  // tensor-memory base, abort flag
+  static constexpr int kBars = 2 * kSlots + 21;
+  static constexpr int kMisc = kBar + kBars * 8;  // tensor-memory base, abort flag
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static constexpr int kTables = (2 * (kLinC + 4) + 32) * 4;  // static: pw, ps and its pad
   static_assert(kAlloc + kTables <= 227 * 1024, "shared memory of the prompt kernel");
@@ -381,14 +381,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // barriers: tile loaded / used, Q, scores, the inter-chunk part, P and that
   // part ready, output complete / read, K' terms written / used, state (the
   // last chunk's sum is read, the state's terms written, V's rows behind the
-  // last token zero), chunk sum complete, output tile written / stored
-  const uint32_t kv_full = sb + L::kBar, kv_empty = kv_full + 8 * L::kSlots,
-                 q_full = kv_empty + 8 * L::kSlots,
-                 q_empty = q_full + 8, sc_full = q_empty + 8, qs_done = sc_full + 8,
-                 pv_ready = qs_done + 8, o_done = pv_ready + 8, o_free = o_done + 8,
-                 kp_full = o_free + 8, kp_empty = kp_full + 16, s_ready = kp_empty + 16,
-                 u_done = s_ready + 16, y_full = u_done + 16, y_free = y_full + 8,
-                 drain = y_free + 8;
+  // last token zero), chunk sum complete, output tile written / stored, all
+  // of a chunk's KV issued, its last PV issued
+  auto bar = [sb](int i) { return sb + L::kBar + 8 * i; };
+  constexpr int kB = 2 * L::kSlots;
+  const uint32_t kv_full = bar(0), kv_empty = bar(L::kSlots), q_full = bar(kB),
+                 q_empty = bar(kB + 1), sc_full = bar(kB + 2), qs_done = bar(kB + 3),
+                 pv_ready = bar(kB + 4), o_done = bar(kB + 5), o_free = bar(kB + 6),
+                 kp_full = bar(kB + 7), kp_empty = bar(kB + 9), s_ready = bar(kB + 11),
+                 u_done = bar(kB + 13), y_full = bar(kB + 15), y_free = bar(kB + 16),
+                 kv_all = bar(kB + 17), pv_issued = bar(kB + 18), drain = bar(kB + 19);
+  static_assert(kB + 21 == L::kBars, "barriers (the last is a pair)");
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   if (warp == 16) {
     tmem_alloc(sb + L::kMisc, 512);
@@ -418,6 +421,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       mbar_init(s_ready + 8 * i, 256);
       mbar_init(u_done + 8 * i, STATES ? 1 : 2);  // KV, and QS done with the state's terms
     }
+    mbar_init(kv_all, 1);
+    mbar_init(pv_issued, 1);
     mbar_init(drain, 1);
     mbar_init(drain + 8, 1);
     *abort = 0;
@@ -624,7 +629,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             __syncwarp();
           }
+          // (the other warp has issued the last chunk's PV, so it has waited for
+          // that chunk's phase)
+          if (!STATES && n >= 1) wait(pv_issued, n - 1);
           if (ok && lead) {
+            if (!STATES) mbar_arrive(kv_all);
             umma_commit(u_done + 8 * ub);
             umma_commit(tile_empty(2 * n + 1));
           }
@@ -671,6 +680,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             __syncwarp();
             if (gq == 0) tile_full(2 * n + 1);
+            if (last) wait(kv_all, n);
             wait(pv_ready, pair);
             if (!ok) break;
             tc_fence_after();
@@ -683,7 +693,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                   umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 16 * ks + 8 * t, v + (ks * 2048 >> 4),
                                kIdD, 1u);
               umma_commit(o_done);
-              if (last) umma_commit(tile_empty(2 * n + 1));
+              if (last) {
+                umma_commit(tile_empty(2 * n + 1));
+                mbar_arrive(pv_issued);
+              }
             }
             __syncwarp();
           }
@@ -735,6 +748,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         tc_fence_after();
         // P in place of the scores: 16 columns j of a step of the product
         // become 8 of term 0 and 8 of term 1
+        uint32_t next[16];
+        if (half <= 2 * qt + 1) tmem_ld16(my_lanes + kTmSc + 16 * half, next);
 #pragma unroll 1
         for (int st = half; st < kLinC / 16; st += 2) {
           uint32_t p[16];
@@ -744,8 +759,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             for (int e = 0; e < 16; ++e) p[e] = 0u;
           } else {
             uint32_t sc[16];
-            tmem_ld16(my_lanes + kTmSc + 16 * st, sc);
             tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sc[e] = next[e];
+            if (st + 2 <= 2 * qt + 1) tmem_ld16(my_lanes + kTmSc + 16 * st + 32, next);
             if (st < 2 * qt) {  // before every row: exp(g (d - 15)) exp(g (15 - e))
               const float rf = ps[d - 15];
 #pragma unroll
