@@ -1765,16 +1765,31 @@ int phs_linear_attn_decode(const void* q, int32_t num_q_heads, const phs_state_p
 
 namespace {
 
-// Segments of the longest prompt: as many as fill the SMs once where the
-// (request, KV head) pairs alone do not, each of at least 8 chunks.
-#ifndef PHS_LINEAR_SEG_CHUNKS
-#define PHS_LINEAR_SEG_CHUNKS 8
-#endif
-int linear_segments(int B, int Hkv, int max_seq, int sms) {
+// Segments of the longest prompt.  Its n chunks in s segments take about
+// n / s chunks' time and, for the last segment, joining s states, of half a
+// chunk's time each: least at s = sqrt(2 n).  (One prompt, s = sqrt(n) / 2,
+// sqrt(n), sqrt(2 n) and 4 sqrt(n): 60, 43, 40 and - us for 2,048 tokens, 8
+// heads of 128; -, 134, 131 and 194 us for 32,768 tokens, 8 heads on one.)  No more
+// than fill the SMs once, nor than leave each 2 chunks.  Then CTAs that share
+// a KV head's query heads, as long as SMs are left -- or, where no prompt is
+// longer than 8 chunks and a batch's lengths decide, up to two for each SM.
+struct LinearPlan {
+  int nseg = 1, ngrp = 1;
+  size_t need = 256;
+};
+LinearPlan linear_plan(int B, int G, int Hkv, int D, int max_seq, int sms) {
+  LinearPlan p;
   const long long pairs = std::max(1LL, 1LL * B * Hkv);
   const long long chunks = (max_seq + kLinearChunk - 1LL) / kLinearChunk;
-  return static_cast<int>(
-      std::max(1LL, std::min(sms / pairs, chunks / PHS_LINEAR_SEG_CHUNKS)));
+  long long nseg = 1;
+  while ((nseg + 1) * (nseg + 1) <= 2 * chunks) ++nseg;
+  p.nseg = static_cast<int>(std::max(1LL, std::min({nseg, sms / pairs, chunks / 2})));
+  const long long room = (chunks <= 8 ? 2 : 1) * sms / (pairs * p.nseg);
+  for (int g = 1; g <= G && g <= room; ++g)
+    if (G % g == 0) p.ngrp = g;
+  if (p.nseg > 1 || p.ngrp > 1)
+    p.need = static_cast<size_t>(pairs) * p.nseg * D * D * sizeof(float);
+  return p;
 }
 
 // [tokens][heads * D] bf16; boxes of 128 tokens x 64 columns
@@ -1803,9 +1818,9 @@ size_t phs_linear_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads,
     return 0;
   DevInfo di;
   if (dev_info(di)) return 0;
-  const int nseg = linear_segments(batch, num_kv_heads, max_seq_len, di.sms);
-  const size_t state = static_cast<size_t>(head_dim) * head_dim * sizeof(float);
-  return nseg > 1 ? static_cast<size_t>(batch) * num_kv_heads * nseg * state : 256;
+  return linear_plan(batch, num_q_heads / num_kv_heads, num_kv_heads, head_dim, max_seq_len,
+                     di.sms)
+      .need;
 }
 
 int phs_linear_attn_prompt(const void* q, int32_t num_q_heads, const void* k, const void* v,
@@ -1831,7 +1846,10 @@ int phs_linear_attn_prompt(const void* q, int32_t num_q_heads, const void* k, co
   a.max_seq = max_seq_len;
   DevInfo di;
   if ((st = dev_info(di))) return st;
-  a.nseg = linear_segments(batch, a.Hkv, max_seq_len, di.sms);
+  const LinearPlan plan =
+      linear_plan(batch, a.G, a.Hkv, pool->head_dim, max_seq_len, di.sms);
+  a.nseg = plan.nseg;
+  a.ngrp = plan.ngrp;
   a.ws = reinterpret_cast<float*>(workspace);
   CUtensorMap tq, tk, tv, to;
   std::memset(&tq, 0, sizeof(tq));

@@ -161,6 +161,9 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // Where there are fewer (request, KV head) pairs than SMs, prompts are cut
 // into segments: a first launch sums up each segment's own state (K and V
 // alone), the second starts each segment from the joined states before it.
+// Where SMs are left, a group's query heads go to several CTAs (`ngrp`), each
+// of which forms the states for itself.  As the pool's state is overwritten
+// by one of these CTAs, they all start from a copy.
 constexpr int kLinC = kLinearChunk;
 constexpr int kLinThreads = 640;
 // registers a thread: 96 at launch, five warpgroups; 2 x 88 + 2 x 120 + 64 = 5 x 96
@@ -354,7 +357,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
-  const int b = blockIdx.x, h = blockIdx.y, seg = blockIdx.z;
+  const int b = blockIdx.x, h = blockIdx.y;
+  const int seg = STATES ? blockIdx.z : blockIdx.z / a.ngrp;
+  const int grp = STATES ? 0 : blockIdx.z % a.ngrp, G = a.G / a.ngrp;
+  const int head0 = h * a.G + grp * G;  // first of this CTA's query heads
 
   // ---- this CTA's chunks
   const int64_t id = request_state(a, b);
@@ -368,9 +374,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   t1 = min(t1, t0 + per * kLinC);
   if (id < 0) {  // no state: zero rows
     if (!STATES)
-      for (int64_t e = tid; e < static_cast<int64_t>(t1 - t0) * a.G * D; e += kLinThreads) {
-        const int64_t t = t0 + e / (a.G * D);
-        reinterpret_cast<__nv_bfloat16*>(a.out)[(t * a.Hq + h * a.G) * D + e % (a.G * D)] =
+      for (int64_t e = tid; e < static_cast<int64_t>(t1 - t0) * G * D; e += kLinThreads) {
+        const int64_t t = t0 + e / (G * D);
+        reinterpret_cast<__nv_bfloat16*>(a.out)[(t * a.Hq + head0) * D + e % (G * D)] =
             __float2bfloat16_rn(0.f);
       }
     return;
@@ -547,6 +553,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (warp == 17) {
       // ---------------------------------------------------------------- TMA
       if (lane == 0 && nch > 0) {
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+        if (!STATES) prefetch_tmap(&tq);
         const uint64_t pol = policy_evict_first();
         auto load = [&](const CUtensorMap* map, uint32_t dst, int head, int t, uint32_t bar) {
           for (int hf = 0; hf < D / 64; ++hf)
@@ -566,7 +575,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (nq >= 1) ok = ok && lin_wait(q_empty, (nq - 1) & 1, abort);
           if (!ok) return;
           mbar_arrive_expect_tx(q_full, L::kTile);
-          load(&tq, sb + L::kQ, h * a.G + gq, t, q_full);
+          load(&tq, sb + L::kQ, head0 + gq, t, q_full);
           ++nq;
         };
         for (int n = 0; ok && n < nch; ++n) {
@@ -574,7 +583,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           load_kv(&tk, t);
           if (!STATES && ok) load_q(0, t);
           if (ok) load_kv(&tv, t);
-          for (int gq = 1; !STATES && ok && gq < a.G; ++gq) load_q(gq, t);
+          for (int gq = 1; !STATES && ok && gq < G; ++gq) load_q(gq, t);
         }
         if (!ok) {
           set_status(a.status, PHS_ETIMEOUT);
@@ -645,8 +654,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const uint64_t ds = sdesc_sw128(sb + L::kS, D * 128, 1024);
         int pair = 0;
         for (int n = 0; ok && n < nch; ++n)
-          for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
-            const bool last = gq == a.G - 1;
+          for (int gq = 0; ok && gq < G; ++gq, ++pair) {
+            const bool last = gq == G - 1;
             if (gq == 0) tile_full(2 * n);
             wait(q_full, pair);
             if (pair >= 1) wait(o_done, pair - 1);  // P of the last pair is read
@@ -713,14 +722,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     } else if (warp == 18) {
       // --------------------------------------------- whole output tiles out
       if (!STATES && lane == 0) {
-        const int whole = (t1 - t0) / kLinC * a.G;
+        const int whole = (t1 - t0) / kLinC * G;
         bool ok = true;
         for (int p = 0; ok && p < whole; ++p) {
           ok = lin_wait(y_full, p & 1, abort);
           if (!ok) break;
           for (int hf = 0; hf < D / 64; ++hf)
-            tma_store_2d(&to, sb + L::kOut + hf * L::kHalf, (h * a.G + p % a.G) * D + 64 * hf,
-                         t0 + p / a.G * kLinC);
+            tma_store_2d(&to, sb + L::kOut + hf * L::kHalf, (head0 + p % G) * D + 64 * hf,
+                         t0 + p / G * kLinC);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           mbar_arrive(y_free);
@@ -742,7 +751,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     bool ok = true;
     int pair = 0;
     for (int n = 0; ok && n < nch; ++n)
-      for (int gq = 0; ok && gq < a.G; ++gq, ++pair) {
+      for (int gq = 0; ok && gq < G; ++gq, ++pair) {
         ok = lin_wait_warp(sc_full, pair & 1, abort);
         if (!ok) break;
         tc_fence_after();
@@ -816,7 +825,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const uint32_t row = sb + L::kOut + i * 128;
         uint4* to_row = reinterpret_cast<uint4*>(
             reinterpret_cast<__nv_bfloat16*>(a.out) +
-            (static_cast<size_t>(t) * a.Hq + h * a.G + gq) * D);
+            (static_cast<size_t>(t) * a.Hq + head0 + gq) * D);
 #pragma unroll 1
         for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
           uint32_t o[32], y[16];
@@ -883,11 +892,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
     };
     if (mine) {
-      // with several segments the pool's state is overwritten by the last
-      // one's CTA: the first launch keeps a copy for the second
+      // with several segments or groups of heads the pool's state is
+      // overwritten by another CTA: an earlier launch has kept a copy
       float* copy = ws + (a.nseg - 1) * D * D;
       if (seg > 0 ? !STATES : resume) {
-        const float* from = seg > 0 ? ws : !STATES && segs > 1 ? copy : pool;
+        const float* from = seg > 0 ? ws : !STATES && (segs > 1 || a.ngrp > 1) ? copy : pool;
         const float keep = expm1f(g * (per * kLinC));
 #pragma unroll 1
         for (int s = 0; s < max(seg, 1); ++s) load_row(from + s * D * D, keep);
@@ -957,7 +966,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (!ok) {
       set_status(a.status, PHS_ETIMEOUT);
       *abort = 1;
-    } else if (mine && (STATES || seg + 1 == segs)) {
+    } else if (mine && (STATES || (seg + 1 == segs && grp == 0))) {
       store_row(STATES ? ws + seg * D * D : pool);
     }
   }
@@ -967,6 +976,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// The states that requests start from, into the last slot of their workspace.
+__global__ void __launch_bounds__(256) phs_linear_keep_states_kernel(const LinearArgs a, int vecs) {
+  const int b = blockIdx.x, h = blockIdx.y;
+  const int64_t id = request_state(a, b);
+  if (id < 0 || a.resume[b] == 0) return;
+  const float4* from = reinterpret_cast<const float4*>(a.state) + (id * a.Hkv + h) * vecs;
+  float4* to = reinterpret_cast<float4*>(a.ws) +
+               ((static_cast<size_t>(b) * a.Hkv + h) * a.nseg + a.nseg - 1) * vecs;
+  for (int i = threadIdx.x; i < vecs; i += 256) to[i] = from[i];
 }
 
 template <int D>
@@ -979,9 +999,11 @@ static int launch_linear_prompt_t(const CUtensorMap& tq, const CUtensorMap& tk,
   if (ensure_dynamic_smem(reinterpret_cast<const void*>(rows), kRows) != PHS_OK ||
       ensure_dynamic_smem(reinterpret_cast<const void*>(states), kStates) != PHS_OK)
     return PHS_ECUDA;
+  if (a.ngrp > 1 && a.resume)
+    phs_linear_keep_states_kernel<<<dim3(a.B, a.Hkv), 256, 0, stream>>>(a, D * D / 4);
   if (a.nseg > 1)
     states<<<dim3(a.B, a.Hkv, a.nseg - 1), kLinThreads, kStates, stream>>>(tq, tk, tv, to, a);
-  rows<<<dim3(a.B, a.Hkv, a.nseg), kLinThreads, kRows, stream>>>(tq, tk, tv, to, a);
+  rows<<<dim3(a.B, a.Hkv, a.nseg * a.ngrp), kLinThreads, kRows, stream>>>(tq, tk, tv, to, a);
   return cudaGetLastError() == cudaSuccess ? PHS_OK : PHS_ECUDA;
 }
 

@@ -133,6 +133,7 @@ struct LinearArgs {
   const int32_t* resume;      // [B] or null: from a zero state
   int total_tokens, max_seq;
   int nseg;                   // segments of the longest prompt
+  int ngrp;                   // CTAs that share a KV head's query heads, a divisor of G
   float* ws;                  // [B][Hkv][nseg][D][D]: segment sums, then the first state
 };
 

@@ -127,6 +127,36 @@ def test_long_prompt_few_heads():
     close(pool.s[0], S, bs, "state")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,lens", [
+    (16, 1, [1100]),                 # segments, and the heads of a group on several CTAs
+    (6, 1, [700, 0, 1, 1300]),       # requests of one segment and of none beside longer ones
+    (12, 4, [200, 129]),             # groups of heads, no segments
+    (8, 8, [2100]), (5, 1, [515, 513])])
+def test_segments_and_groups_of_heads(D, Hq, Hkv, lens):
+    B = len(lens)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T = int(cu[-1])
+    q = synth.normal_bf16((T, Hq, D), 31, device="cuda")
+    k = synth.normal_bf16((T, Hkv, D), 32, device="cuda")
+    v = synth.normal_bf16((T, Hkv, D), 33, device="cuda")
+    g = decays(Hkv, lo=1e-3)
+    for resume in ([1] * B, [0] * B, [r % 2 for r in range(B)], None):
+        pool = state_pool(B, Hkv, D, 34)
+        start = pool.s.clone()
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = phs.linear_attn_prompt(q, k, v, dev(cu), max(lens), pool, g,
+                                     resume=None if resume is None else dev(resume), status=st)
+        assert int(st.item()) == 0
+        for b in range(B):
+            a, e = int(cu[b]), int(cu[b + 1])
+            s0 = start[b] if resume and resume[b] else torch.zeros_like(start[b])
+            r, S, m, A = ops_ref.linear(q[a:e], k[a:e], v[a:e], s0, g, 1 / math.sqrt(D))
+            bo, bs = bounds(r, m, S, A, torch.bfloat16, e - a, D)
+            close(out[a:e], r, bo, f"out of request {b}")
+            close(pool.s[b], S, bs, f"state of request {b}")
+
+
 @pytest.mark.parametrize("value", [0.0, -1e-7, -3.0, -80.0, -1e6, -math.inf])
 def test_prompt_decay_extremes(value):
     D, T = 64, 200
