@@ -1765,14 +1765,14 @@ int phs_linear_attn_decode(const void* q, int32_t num_q_heads, const phs_state_p
 
 namespace {
 
-// Segments of the longest prompt.  Its n chunks in s segments take about
-// n / s chunks' time and, for the last segment, joining s states, of half a
-// chunk's time each: least at s = sqrt(2 n).  (One prompt, s = sqrt(n) / 2,
-// sqrt(n), sqrt(2 n) and 4 sqrt(n): 60, 43, 40 and - us for 2,048 tokens, 8
-// heads of 128; -, 134, 131 and 194 us for 32,768 tokens, 8 heads on one.)  No more
-// than fill the SMs once, nor than leave each 2 chunks.  Then CTAs that share
-// a KV head's query heads, as long as SMs are left -- or, where no prompt is
-// longer than 8 chunks and a batch's lengths decide, up to two for each SM.
+// How a prompt call is spread over the SMs: segments of the longest prompt,
+// and CTAs that share a KV head's query heads.  The time of a plan at D = 128,
+// in half microseconds a chunk of the longest segment: 4 for its state (4 more
+// where a first launch has to sum it up too) and 3 for each query head of a
+// CTA; two more launches take about 10 us.  Of the plans with one CTA for
+// each SM at most the shortest is taken, with few heads first; where no
+// prompt is longer than 8 chunks, and a batch's lengths decide, up to two
+// CTAs for each SM.
 struct LinearPlan {
   int nseg = 1, ngrp = 1;
   size_t need = 256;
@@ -1781,12 +1781,20 @@ LinearPlan linear_plan(int B, int G, int Hkv, int D, int max_seq, int sms) {
   LinearPlan p;
   const long long pairs = std::max(1LL, 1LL * B * Hkv);
   const long long chunks = (max_seq + kLinearChunk - 1LL) / kLinearChunk;
-  long long nseg = 1;
-  while ((nseg + 1) * (nseg + 1) <= 2 * chunks) ++nseg;
-  p.nseg = static_cast<int>(std::max(1LL, std::min({nseg, sms / pairs, chunks / 2})));
-  const long long room = (chunks <= 8 ? 2 : 1) * sms / (pairs * p.nseg);
-  for (int g = 1; g <= G && g <= room; ++g)
-    if (G % g == 0) p.ngrp = g;
+  const long long room = (chunks <= 8 ? 2 : 1) * sms / pairs;
+  long long best = -1;
+  for (int g = 1; g <= G && (g == 1 || g <= room); ++g) {
+    if (G % g != 0) continue;
+    const long long most = std::max(1LL, std::min(sms / (pairs * g), chunks / 2));
+    for (const long long s : {1LL, most}) {
+      const long long per = (chunks + s - 1) / s;
+      const long long time = per * ((s > 1 ? 8 : 4) + 3 * (G / g)) + (s > 1 ? 20 : 0);
+      if (best >= 0 && time >= best) continue;
+      best = time;
+      p.nseg = static_cast<int>(s);
+      p.ngrp = g;
+    }
+  }
   if (p.nseg > 1 || p.ngrp > 1)
     p.need = static_cast<size_t>(pairs) * p.nseg * D * D * sizeof(float);
   return p;

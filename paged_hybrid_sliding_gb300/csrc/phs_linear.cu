@@ -160,10 +160,11 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // 5,200 cycles of 128 bytes; its share of HBM (128 KB) takes 5,300.
 // Where there are fewer (request, KV head) pairs than SMs, prompts are cut
 // into segments: a first launch sums up each segment's own state (K and V
-// alone), the second starts each segment from the joined states before it.
-// Where SMs are left, a group's query heads go to several CTAs (`ngrp`), each
-// of which forms the states for itself.  As the pool's state is overwritten
-// by one of these CTAs, they all start from a copy.
+// alone), a small one joins these sums into the states that the segments
+// start from, and the last one forms the rows.  Where SMs are left, a group's
+// query heads go to several CTAs (`ngrp`), each of which forms the states for
+// itself.  As the pool's state is overwritten by one of these CTAs, they all
+// start from a copy.
 constexpr int kLinC = kLinearChunk;
 constexpr int kLinThreads = 640;
 // registers a thread: 96 at launch, five warpgroups; 2 x 88 + 2 x 120 + 64 = 5 x 96
@@ -335,6 +336,12 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
                : "memory");
 }
 
+// Chunks of each segment of a request but its last.
+__device__ __forceinline__ int segment_chunks(const LinearArgs& a, int tokens) {
+  const int chunks = (tokens + kLinC - 1) / kLinC;
+  return max(1, (chunks + a.nseg - 1) / a.nseg);
+}
+
 // STATES: the first launch (sums of each segment but the last, no outputs)
 template <int D, bool STATES>
 __global__ void __launch_bounds__(kLinThreads, 1)
@@ -362,14 +369,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int grp = STATES ? 0 : blockIdx.z % a.ngrp, G = a.G / a.ngrp;
   const int head0 = h * a.G + grp * G;  // first of this CTA's query heads
 
+  if (STATES) pdl_launch_dependents();  // the join waits for this grid's end
+
   // ---- this CTA's chunks
   const int64_t id = request_state(a, b);
   int t0, t1;
-  if (!request_tokens(a, b, t0, t1)) return;
-  const int all = (t1 - t0 + kLinC - 1) / kLinC;             // chunks of the request
-  const int per = max(1, (all + a.nseg - 1) / a.nseg);       // of a segment
-  const int segs = max(1, (all + per - 1) / per);
-  if (seg >= segs || (STATES && seg + 1 >= segs)) return;
+  if (!request_tokens(a, b, t0, t1)) {
+    pdl_wait_prior_grid();
+    return;
+  }
+  const int per = segment_chunks(a, t1 - t0);
+  const int segs = max(1, (t1 - t0 + per * kLinC - 1) / (per * kLinC));
+  if (seg >= segs || (STATES && seg + 1 >= segs)) {
+    pdl_wait_prior_grid();
+    return;
+  }
   t0 += seg * per * kLinC;
   t1 = min(t1, t0 + per * kLinC);
   if (id < 0) {  // no state: zero rows
@@ -379,6 +393,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         reinterpret_cast<__nv_bfloat16*>(a.out)[(t * a.Hq + head0) * D + e % (G * D)] =
             __float2bfloat16_rn(0.f);
       }
+    pdl_wait_prior_grid();
     return;
   }
   const int nch = (t1 - t0 + kLinC - 1) / kLinC;
@@ -875,15 +890,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint64_t S[N / 2];  // pairs
 #pragma unroll
     for (int c = 0; c < N / 2; ++c) S[c] = 0ull;
-    auto load_row = [&](const float* from, float keep_m1) {  // S <- exp() S + from
-      const uint64_t keep = f2(keep_m1, keep_m1);
-#pragma unroll
-      for (int c = 0; c < N; c += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(from + c);
-        S[c / 2] = f2_add(f2_fma(S[c / 2], keep, S[c / 2]), f2(x.x, x.y));
-        S[c / 2 + 1] = f2_add(f2_fma(S[c / 2 + 1], keep, S[c / 2 + 1]), f2(x.z, x.w));
-      }
-    };
     auto store_row = [&](float* to) {
 #pragma unroll
       for (int c = 0; c < N; c += 4) {
@@ -891,16 +897,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         *reinterpret_cast<float4*>(to + c) = make_float4(x.x, x.y, y.x, y.y);
       }
     };
-    if (mine) {
-      // with several segments or groups of heads the pool's state is
-      // overwritten by another CTA: an earlier launch has kept a copy
-      float* copy = ws + (a.nseg - 1) * D * D;
-      if (seg > 0 ? !STATES : resume) {
-        const float* from = seg > 0 ? ws : !STATES && (segs > 1 || a.ngrp > 1) ? copy : pool;
-        const float keep = expm1f(g * (per * kLinC));
-#pragma unroll 1
-        for (int s = 0; s < max(seg, 1); ++s) load_row(from + s * D * D, keep);
-        if (STATES) store_row(copy);
+    if (!STATES) pdl_wait_prior_grid();  // for the join: the one reader of an earlier launch's output
+    if (mine && !STATES && (seg > 0 || resume)) {
+      const float* from = a.nseg > 1 || a.ngrp > 1 ? ws + seg * D * D : pool;
+#pragma unroll
+      for (int c = 0; c < N; c += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(from + c);
+        S[c / 2] = f2(x.x, x.y);
+        S[c / 2 + 1] = f2(x.z, x.w);
       }
     }
     bool ok = true;
@@ -978,15 +982,38 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
 }
 
-// The states that requests start from, into the last slot of their workspace.
-__global__ void __launch_bounds__(256) phs_linear_keep_states_kernel(const LinearArgs a, int vecs) {
-  const int b = blockIdx.x, h = blockIdx.y;
+// Sums of segments -> the states that they start from, in their place: a
+// thread holds 4 elements of a state and walks the segments, 8 loads at once.
+// (Joined by each segment for itself instead, a state cost it 2.2 us.)
+__global__ void __launch_bounds__(128) phs_linear_join_kernel(const LinearArgs a, int vecs) {
+  const int b = blockIdx.x, h = blockIdx.y, i = blockIdx.z * 128 + threadIdx.x;
+  pdl_launch_dependents();
   const int64_t id = request_state(a, b);
-  if (id < 0 || a.resume[b] == 0) return;
-  const float4* from = reinterpret_cast<const float4*>(a.state) + (id * a.Hkv + h) * vecs;
-  float4* to = reinterpret_cast<float4*>(a.ws) +
-               ((static_cast<size_t>(b) * a.Hkv + h) * a.nseg + a.nseg - 1) * vecs;
-  for (int i = threadIdx.x; i < vecs; i += 256) to[i] = from[i];
+  int t0, t1;
+  const bool good = request_tokens(a, b, t0, t1) && id >= 0;
+  pdl_wait_prior_grid();
+  if (!good) return;
+  const int tokens = segment_chunks(a, t1 - t0) * kLinC;
+  const int segs = max(1, (t1 - t0 + tokens - 1) / tokens);
+  const float g = a.log_decay[h], keep = expm1f((g < -1e4f ? -1e4f : g) * tokens);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.resume && a.resume[b] != 0)
+    s = reinterpret_cast<const float4*>(a.state)[(id * a.Hkv + h) * vecs + i];
+  float4* at = reinterpret_cast<float4*>(a.ws) +
+               (static_cast<size_t>(b) * a.Hkv + h) * a.nseg * vecs + i;
+  for (int n = 0; n < segs; n += 8) {
+    float4 x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n + j + 1 < segs) x[j] = at[static_cast<size_t>(n + j) * vecs];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (n + j < segs) at[static_cast<size_t>(n + j) * vecs] = s;
+      if (n + j + 1 < segs)
+        s = make_float4(decayed(s.x, keep) + x[j].x, decayed(s.y, keep) + x[j].y,
+                        decayed(s.z, keep) + x[j].z, decayed(s.w, keep) + x[j].w);
+    }
+  }
 }
 
 template <int D>
@@ -999,11 +1026,36 @@ static int launch_linear_prompt_t(const CUtensorMap& tq, const CUtensorMap& tk,
   if (ensure_dynamic_smem(reinterpret_cast<const void*>(rows), kRows) != PHS_OK ||
       ensure_dynamic_smem(reinterpret_cast<const void*>(states), kStates) != PHS_OK)
     return PHS_ECUDA;
-  if (a.ngrp > 1 && a.resume)
-    phs_linear_keep_states_kernel<<<dim3(a.B, a.Hkv), 256, 0, stream>>>(a, D * D / 4);
-  if (a.nseg > 1)
-    states<<<dim3(a.B, a.Hkv, a.nseg - 1), kLinThreads, kStates, stream>>>(tq, tk, tv, to, a);
-  rows<<<dim3(a.B, a.Hkv, a.nseg * a.ngrp), kLinThreads, kRows, stream>>>(tq, tk, tv, to, a);
+  // The launches after the first may start before the one in front of them has
+  // ended (they wait for it where they read what it wrote).
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cudaError_t err = cudaSuccess;
+  if (a.nseg > 1) {
+    cfg.gridDim = dim3(a.B, a.Hkv, a.nseg - 1);
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = kStates;
+    err = cudaLaunchKernelEx(&cfg, states, tq, tk, tv, to, a);
+    cfg.numAttrs = 1;
+  }
+  if (err == cudaSuccess && (a.nseg > 1 || (a.ngrp > 1 && a.resume))) {
+    cfg.gridDim = dim3(a.B, a.Hkv, D * D / 512);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    err = cudaLaunchKernelEx(&cfg, phs_linear_join_kernel, a, D * D / 4);
+    cfg.numAttrs = 1;
+  }
+  if (err == cudaSuccess) {
+    cfg.gridDim = dim3(a.B, a.Hkv, a.nseg * a.ngrp);
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = kRows;
+    err = cudaLaunchKernelEx(&cfg, rows, tq, tk, tv, to, a);
+  }
+  if (err != cudaSuccess) return PHS_ECUDA;
   return cudaGetLastError() == cudaSuccess ? PHS_OK : PHS_ECUDA;
 }
 

@@ -134,7 +134,7 @@ struct LinearArgs {
   int total_tokens, max_seq;
   int nseg;                   // segments of the longest prompt
   int ngrp;                   // CTAs that share a KV head's query heads, a divisor of G
-  float* ws;                  // [B][Hkv][nseg][D][D]: segment sums, then the first state
+  float* ws;                  // [B][Hkv][nseg][D][D]: segment sums, then first states
 };
 
 constexpr int kLinearChunk = 128;  // tokens
