@@ -1766,29 +1766,30 @@ int phs_linear_attn_decode(const void* q, int32_t num_q_heads, const phs_state_p
 namespace {
 
 // How a prompt call is spread over the SMs: segments of the longest prompt,
-// and CTAs that share a KV head's query heads.  The time of a plan at D = 128,
-// in half microseconds a chunk of the longest segment: 4 for its state (4 more
-// where a first launch has to sum it up too) and 3 for each query head of a
-// CTA; two more launches take about 10 us.  Of the plans with one CTA for
-// each SM at most the shortest is taken, with few heads first; where no
-// prompt is longer than 8 chunks, and a batch's lengths decide, up to two
-// CTAs for each SM.
+// and CTAs that share a KV head's query heads.  Of the plans the one with the
+// least time is taken, by these costs at D = 128 in half microseconds: 16 for
+// a CTA; for each chunk 4 for its state (4 more where a first launch has to
+// sum it up too) and 3 for each query head of the CTA; 20 for two more
+// launches.  Without segments a call takes as long as its longest prompt, or
+// as all CTAs' work spread over the SMs; segments are only made while each CTA
+// has an SM to itself.
 struct LinearPlan {
   int nseg = 1, ngrp = 1;
   size_t need = 256;
 };
-LinearPlan linear_plan(int B, int G, int Hkv, int D, int max_seq, int sms) {
+LinearPlan linear_plan(int B, int G, int Hkv, int D, int total, int max_seq, int sms) {
   LinearPlan p;
-  const long long pairs = std::max(1LL, 1LL * B * Hkv);
-  const long long chunks = (max_seq + kLinearChunk - 1LL) / kLinearChunk;
-  const long long room = (chunks <= 8 ? 2 : 1) * sms / pairs;
+  const long long pairs = std::max(1LL, 1LL * B * Hkv), C = kLinearChunk;
+  const long long chunks = (std::min(total, max_seq) + C - 1) / C;
   long long best = -1;
-  for (int g = 1; g <= G && (g == 1 || g <= room); ++g) {
+  for (int g = 1; g <= G; ++g) {
     if (G % g != 0) continue;
     const long long most = std::max(1LL, std::min(sms / (pairs * g), chunks / 2));
     for (const long long s : {1LL, most}) {
-      const long long per = (chunks + s - 1) / s;
-      const long long time = per * ((s > 1 ? 8 : 4) + 3 * (G / g)) + (s > 1 ? 20 : 0);
+      const long long per = (chunks + s - 1) / s, chunk = (s > 1 ? 8 : 4) + 3 * (G / g);
+      long long time = 16 + per * chunk + (s > 1 ? 20 : 0);
+      if (s == 1)  // (a request's last chunk is half full on average)
+        time = std::max(time, g * (pairs * 16 + Hkv * chunk * (total / C + B / 2)) / sms);
       if (best >= 0 && time >= best) continue;
       best = time;
       p.nseg = static_cast<int>(s);
@@ -1826,8 +1827,8 @@ size_t phs_linear_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads,
     return 0;
   DevInfo di;
   if (dev_info(di)) return 0;
-  return linear_plan(batch, num_q_heads / num_kv_heads, num_kv_heads, head_dim, max_seq_len,
-                     di.sms)
+  return linear_plan(batch, num_q_heads / num_kv_heads, num_kv_heads, head_dim, total_tokens,
+                     max_seq_len, di.sms)
       .need;
 }
 
@@ -1855,9 +1856,12 @@ int phs_linear_attn_prompt(const void* q, int32_t num_q_heads, const void* k, co
   DevInfo di;
   if ((st = dev_info(di))) return st;
   const LinearPlan plan =
-      linear_plan(batch, a.G, a.Hkv, pool->head_dim, max_seq_len, di.sms);
+      linear_plan(batch, a.G, a.Hkv, pool->head_dim, total_tokens, max_seq_len, di.sms);
   a.nseg = plan.nseg;
   a.ngrp = plan.ngrp;
+  const int64_t ctas = int64_t{batch} * a.Hkv * a.nseg * a.ngrp;
+  if (ctas > INT32_MAX) return PHS_EUNSUPPORTED;
+  a.longest_first = ctas > di.sms && batch > 1 && batch <= kLinearSort;
   a.ws = reinterpret_cast<float*>(workspace);
   CUtensorMap tq, tk, tv, to;
   std::memset(&tq, 0, sizeof(tq));

@@ -342,6 +342,28 @@ __device__ __forceinline__ int segment_chunks(const LinearArgs& a, int tokens) {
   return max(1, (chunks + a.nseg - 1) / a.nseg);
 }
 
+// The request that comes `at`-th when the longest come first.  Where there are
+// more CTAs than SMs, the last ones to start then end soon.  All threads of the
+// CTA call it.
+__device__ __forceinline__ int request_by_length(const LinearArgs& a, int at) {
+  __shared__ int found;
+  static_assert(kLinearSort <= kLinThreads, "a thread for each request");
+  const int j = threadIdx.x;
+  if (j < a.B) {
+    const int64_t len = int64_t{a.cu_seqlens[j + 1]} - a.cu_seqlens[j];
+    int before = 0;
+    int64_t from = a.cu_seqlens[0];
+    for (int i = 0; i < a.B; ++i) {
+      const int64_t to = a.cu_seqlens[i + 1];
+      before += to - from > len || (to - from == len && i < j);
+      from = to;
+    }
+    if (before == at) found = j;
+  }
+  __syncthreads();
+  return found;
+}
+
 // STATES: the first launch (sums of each segment but the last, no outputs)
 template <int D, bool STATES>
 __global__ void __launch_bounds__(kLinThreads, 1)
@@ -364,9 +386,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
-  const int b = blockIdx.x, h = blockIdx.y;
-  const int seg = STATES ? blockIdx.z : blockIdx.z / a.ngrp;
-  const int grp = STATES ? 0 : blockIdx.z % a.ngrp, G = a.G / a.ngrp;
+  int b = blockIdx.x, h = blockIdx.y, seg = blockIdx.z, grp = 0;
+  if (!STATES) {
+    const int of_b = a.Hkv * a.nseg * a.ngrp, i = blockIdx.x % of_b;
+    b = blockIdx.x / of_b;
+    h = i % a.Hkv;
+    seg = i / a.Hkv / a.ngrp;
+    grp = i / a.Hkv % a.ngrp;
+    if (a.longest_first) b = request_by_length(a, b);
+  }
+  const int G = a.G / a.ngrp;
   const int head0 = h * a.G + grp * G;  // first of this CTA's query heads
 
   if (STATES) pdl_launch_dependents();  // the join waits for this grid's end
@@ -1050,7 +1079,7 @@ static int launch_linear_prompt_t(const CUtensorMap& tq, const CUtensorMap& tk,
     cfg.numAttrs = 1;
   }
   if (err == cudaSuccess) {
-    cfg.gridDim = dim3(a.B, a.Hkv, a.nseg * a.ngrp);
+    cfg.gridDim = dim3(a.B * a.Hkv * a.nseg * a.ngrp);
     cfg.blockDim = dim3(kLinThreads);
     cfg.dynamicSmemBytes = kRows;
     err = cudaLaunchKernelEx(&cfg, rows, tq, tk, tv, to, a);

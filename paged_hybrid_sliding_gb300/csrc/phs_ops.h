@@ -134,10 +134,12 @@ struct LinearArgs {
   int total_tokens, max_seq;
   int nseg;                   // segments of the longest prompt
   int ngrp;                   // CTAs that share a KV head's query heads, a divisor of G
+  bool longest_first;         // CTAs in order of their requests' lengths (B <= kLinearSort)
   float* ws;                  // [B][Hkv][nseg][D][D]: segment sums, then first states
 };
 
-constexpr int kLinearChunk = 128;  // tokens
+constexpr int kLinearChunk = 128;
+constexpr int kLinearSort = 256;  // requests of a call that are put in order, at most  // tokens
 
 int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream);
 int launch_linear_prompt(int D, const CUtensorMap& tq, const CUtensorMap& tk,

@@ -173,6 +173,43 @@ def test_prompt_decay_extremes(value):
     close(pool.s[0], S, bs, "state")
 
 
+@pytest.mark.parametrize("B", [40, 256, 257])
+def test_many_short_prompts(B):
+    """More CTAs than SMs, with and without an order by length."""
+    D, Hq, Hkv = 64, 8, 4
+    lens = np.random.RandomState(B).randint(0, 180, B)
+    lens[B // 2], lens[B // 3] = 700, 0
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T = int(cu[-1])
+    q = synth.normal_bf16((T, Hq, D), 35, device="cuda")
+    k = synth.normal_bf16((T, Hkv, D), 36, device="cuda")
+    v = synth.normal_bf16((T, Hkv, D), 37, device="cuda")
+    g = decays(Hkv, lo=1e-3)
+    pool = state_pool(B, Hkv, D, 38)
+    start = pool.s.clone()
+    ids = np.random.RandomState(1).permutation(B).astype(np.int32)
+    ids[5] = -1
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = phs.linear_attn_prompt(q, k, v, dev(cu), 700, pool, g, state_ids=dev(ids),
+                                 resume=dev(np.arange(B) % 2), status=st)
+    assert int(st.item()) == 0
+    assert not out[cu[5]:cu[6]].any()
+    for b in [b for b in range(B) if b != 5 and (b < 12 or b > B - 6 or lens[b] in (0, 700))]:
+        a, e = int(cu[b]), int(cu[b + 1])
+        s0 = start[ids[b]] if b % 2 else torch.zeros_like(start[0])
+        r, S, m, A = ops_ref.linear(q[a:e], k[a:e], v[a:e], s0, g, 1 / math.sqrt(D))
+        bo, bs = bounds(r, m, S, A, torch.bfloat16, e - a, D)
+        close(out[a:e], r, bo, f"out of request {b}")
+        close(pool.s[ids[b]], S, bs, f"state of request {b}")
+    # the others against calls of their own
+    for b in range(12, B - 6, 7):
+        a, e = int(cu[b]), int(cu[b + 1])
+        one = phs.StatePool(start[ids[b]][None].clone())
+        ref = phs.linear_attn_prompt(q[a:e], k[a:e], v[a:e], dev([0, e - a]), max(e - a, 1), one,
+                                     g, resume=dev([b % 2]))
+        assert torch.allclose(out[a:e].float(), ref.float(), rtol=2**-7, atol=1e-3)
+
+
 def test_prompt_in_parts_then_decode_is_one_prompt():
     """A prompt in two calls, then single tokens, against one recurrence."""
     D, Hq, Hkv, T = 128, 4, 2, 391
