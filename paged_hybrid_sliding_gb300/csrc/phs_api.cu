@@ -1765,16 +1765,16 @@ int phs_linear_attn_decode(const void* q, int32_t num_q_heads, const phs_state_p
 
 namespace {
 
-// How a prompt call is spread over the SMs: segments of the longest prompt,
-// and CTAs that share a KV head's query heads.  Of the plans the one with the
-// least time is taken, by these costs at D = 128 in half microseconds: 16 for
-// a CTA; for each chunk 4 for its state (4 more where a first launch has to
-// sum it up too) and 3 for each query head of the CTA; 20 for two more
-// launches.  Without segments a call takes as long as its longest prompt, or
-// as all CTAs' work spread over the SMs; segments are only made while each CTA
-// has an SM to itself.
+// How a prompt call is spread over the SMs: segments of each prompt, parts
+// that a first launch sums a segment up in, and CTAs that share a KV head's
+// query heads.  Of the plans the one with the least time is taken, by these
+// costs at D = 128 in half microseconds: 16 for a CTA; for each chunk 4 for
+// its state (in either launch) and 3 for each query head of the CTA; 20 for
+// two more launches.  Without segments a call takes as long as its longest
+// prompt, or as all CTAs' work spread over the SMs; segments are only made
+// while each CTA has an SM to itself.
 struct LinearPlan {
-  int nseg = 1, ngrp = 1;
+  int nseg = 1, nsub = 1, ngrp = 1;
   size_t need = 256;
 };
 LinearPlan linear_plan(int B, int G, int Hkv, int D, int total, int max_seq, int sms) {
@@ -1786,18 +1786,30 @@ LinearPlan linear_plan(int B, int G, int Hkv, int D, int total, int max_seq, int
     if (G % g != 0) continue;
     const long long most = std::max(1LL, std::min(sms / (pairs * g), chunks / 2));
     for (const long long s : {1LL, most}) {
-      const long long per = (chunks + s - 1) / s, chunk = (s > 1 ? 8 : 4) + 3 * (G / g);
-      long long time = 16 + per * chunk + (s > 1 ? 20 : 0);
-      if (s == 1)  // (a request's last chunk is half full on average)
+      const long long per = (chunks + s - 1) / s, chunk = 4 + 3 * (G / g);
+      long long time = 16 + per * chunk, sub = 1;
+      if (s == 1) {  // (a request's last chunk is half full on average)
         time = std::max(time, g * (pairs * 16 + Hkv * chunk * (total / C + B / 2)) / sms);
+      } else {
+        long long sums = -1;
+        for (long long n = 1; n <= 8 && n <= per; ++n) {
+          const long long waves = ((s - 1) * pairs * n + sms - 1) / sms;
+          const long long t = waves * (16 + 4 * ((per + n - 1) / n));
+          if (sums >= 0 && t >= sums) continue;
+          sums = t;
+          sub = n;
+        }
+        time += sums + 4;
+      }
       if (best >= 0 && time >= best) continue;
       best = time;
       p.nseg = static_cast<int>(s);
+      p.nsub = static_cast<int>(sub);
       p.ngrp = g;
     }
   }
   if (p.nseg > 1 || p.ngrp > 1)
-    p.need = static_cast<size_t>(pairs) * p.nseg * D * D * sizeof(float);
+    p.need = static_cast<size_t>(pairs) * p.nseg * p.nsub * D * D * sizeof(float);
   return p;
 }
 
@@ -1858,6 +1870,7 @@ int phs_linear_attn_prompt(const void* q, int32_t num_q_heads, const void* k, co
   const LinearPlan plan =
       linear_plan(batch, a.G, a.Hkv, pool->head_dim, total_tokens, max_seq_len, di.sms);
   a.nseg = plan.nseg;
+  a.nsub = plan.nsub;
   a.ngrp = plan.ngrp;
   const int64_t ctas = int64_t{batch} * a.Hkv * a.nseg * a.ngrp;
   if (ctas > INT32_MAX) return PHS_EUNSUPPORTED;

@@ -159,9 +159,10 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // D = 128 the products read 352 KB, copies and registers move 300 KB, about
 // 5,200 cycles of 128 bytes; its share of HBM (128 KB) takes 5,300.
 // Where there are fewer (request, KV head) pairs than SMs, prompts are cut
-// into segments: a first launch sums up each segment's own state (K and V
-// alone), a small one joins these sums into the states that the segments
-// start from, and the last one forms the rows.  Where SMs are left, a group's
+// into segments: a first launch sums up their own states (K and V alone; a
+// segment in `nsub` parts, as this launch has fewer CTAs), a small one joins
+// these sums into the states that the segments start from, and the last one
+// forms the rows.  Where SMs are left, a group's
 // query heads go to several CTAs (`ngrp`), each of which forms the states for
 // itself.  As the pool's state is overwritten by one of these CTAs, they all
 // start from a copy.
@@ -336,10 +337,10 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
                : "memory");
 }
 
-// Chunks of each segment of a request but its last.
-__device__ __forceinline__ int segment_chunks(const LinearArgs& a, int tokens) {
-  const int chunks = (tokens + kLinC - 1) / kLinC;
-  return max(1, (chunks + a.nseg - 1) / a.nseg);
+// First chunk of part p of a request's `chunks`; a segment is nsub parts, and
+// part nseg * nsub is the end.
+__device__ __forceinline__ int part_chunk(const LinearArgs& a, int chunks, int p) {
+  return static_cast<int>(static_cast<int64_t>(chunks) * p / (a.nseg * a.nsub));
 }
 
 // The request that comes `at`-th when the longest come first.  Where there are
@@ -386,12 +387,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
-  int b = blockIdx.x, h = blockIdx.y, seg = blockIdx.z, grp = 0;
+  // part: the segment's first one, with STATES the one to sum up
+  int b = blockIdx.x, h = blockIdx.y, part = blockIdx.z, grp = 0;
   if (!STATES) {
     const int of_b = a.Hkv * a.nseg * a.ngrp, i = blockIdx.x % of_b;
     b = blockIdx.x / of_b;
     h = i % a.Hkv;
-    seg = i / a.Hkv / a.ngrp;
+    part = i / a.Hkv / a.ngrp * a.nsub;
     grp = i / a.Hkv % a.ngrp;
     if (a.longest_first) b = request_by_length(a, b);
   }
@@ -407,14 +409,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     pdl_wait_prior_grid();
     return;
   }
-  const int per = segment_chunks(a, t1 - t0);
-  const int segs = max(1, (t1 - t0 + per * kLinC - 1) / (per * kLinC));
-  if (seg >= segs || (STATES && seg + 1 >= segs)) {
+  const int all = (t1 - t0 + kLinC - 1) / kLinC, parts = a.nseg * a.nsub;
+  const int next = part + (STATES ? 1 : a.nsub);
+  const bool last = next == parts;
+  const int c0 = part_chunk(a, all, part), c1 = part_chunk(a, all, next);
+  if (c0 == c1 && !last) {
     pdl_wait_prior_grid();
     return;
   }
-  t0 += seg * per * kLinC;
-  t1 = min(t1, t0 + per * kLinC);
+  t1 = min(t1, t0 + c1 * kLinC);
+  t0 += c0 * kLinC;
   if (id < 0) {  // no state: zero rows
     if (!STATES)
       for (int64_t e = tid; e < static_cast<int64_t>(t1 - t0) * G * D; e += kLinThreads) {
@@ -914,7 +918,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const bool mine = r < D;
     const size_t row = static_cast<size_t>(r) * D + half * N;
     float* pool = a.state + (id * a.Hkv + h) * D * D + row;
-    float* ws = a.ws + (static_cast<size_t>(b) * a.Hkv + h) * a.nseg * D * D + row;
+    float* ws = a.ws + (static_cast<size_t>(b) * a.Hkv + h) * parts * D * D + row;
     const bool resume = a.resume != nullptr && a.resume[b] != 0;
     uint64_t S[N / 2];  // pairs
 #pragma unroll
@@ -927,8 +931,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
     };
     if (!STATES) pdl_wait_prior_grid();  // for the join: the one reader of an earlier launch's output
-    if (mine && !STATES && (seg > 0 || resume)) {
-      const float* from = a.nseg > 1 || a.ngrp > 1 ? ws + seg * D * D : pool;
+    if (mine && !STATES && (part > 0 || resume)) {
+      const float* from = a.nseg > 1 || a.ngrp > 1 ? ws + part * D * D : pool;
 #pragma unroll
       for (int c = 0; c < N; c += 4) {
         const float4 x = *reinterpret_cast<const float4*>(from + c);
@@ -999,8 +1003,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (!ok) {
       set_status(a.status, PHS_ETIMEOUT);
       *abort = 1;
-    } else if (mine && (STATES || (seg + 1 == segs && grp == 0))) {
-      store_row(STATES ? ws + seg * D * D : pool);
+    } else if (mine && (STATES || (last && grp == 0))) {
+      store_row(STATES ? ws + part * D * D : pool);
     }
   }
   tc_fence_before();
@@ -1011,36 +1015,51 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
 }
 
-// Sums of segments -> the states that they start from, in their place: a
-// thread holds 4 elements of a state and walks the segments, 8 loads at once.
-// (Joined by each segment for itself instead, a state cost it 2.2 us.)
+// Sums of parts -> the states that segments start from, in the place of their
+// first part's: a thread holds 4 elements of a state and walks the parts, 8
+// loads at once.  (Joined by each segment for itself instead, a state cost
+// it 2.2 us.)
 __global__ void __launch_bounds__(128) phs_linear_join_kernel(const LinearArgs a, int vecs) {
-  const int b = blockIdx.x, h = blockIdx.y, i = blockIdx.z * 128 + threadIdx.x;
+  const int b = blockIdx.x, h = blockIdx.y;
   pdl_launch_dependents();
   const int64_t id = request_state(a, b);
   int t0, t1;
   const bool good = request_tokens(a, b, t0, t1) && id >= 0;
   pdl_wait_prior_grid();
   if (!good) return;
-  const int tokens = segment_chunks(a, t1 - t0) * kLinC;
-  const int segs = max(1, (t1 - t0 + tokens - 1) / tokens);
-  const float g = a.log_decay[h], keep = expm1f((g < -1e4f ? -1e4f : g) * tokens);
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (a.resume && a.resume[b] != 0)
-    s = reinterpret_cast<const float4*>(a.state)[(id * a.Hkv + h) * vecs + i];
-  float4* at = reinterpret_cast<float4*>(a.ws) +
-               (static_cast<size_t>(b) * a.Hkv + h) * a.nseg * vecs + i;
-  for (int n = 0; n < segs; n += 8) {
-    float4 x[8];
+  const int chunks = (t1 - t0 + kLinC - 1) / kLinC, parts = a.nseg * a.nsub;
+  const int small = chunks / parts, rest = chunks % parts;  // a part: so many chunks, or one more
+  const float g0 = a.log_decay[h], g = g0 < -1e4f ? -1e4f : g0;
+  const float keep0 = expm1f(g * (small * kLinC)), keep1 = expm1f(g * ((small + 1) * kLinC));
+  for (int i = blockIdx.z * 128 + threadIdx.x; i < vecs; i += gridDim.z * 128) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.resume && a.resume[b] != 0)
+      s = reinterpret_cast<const float4*>(a.state)[(id * a.Hkv + h) * vecs + i];
+    float4* at = reinterpret_cast<float4*>(a.ws) +
+                 (static_cast<size_t>(b) * a.Hkv + h) * parts * vecs + i;
+    const int sums = parts - a.nsub;  // the last segment has none
+    int frac = 0, sub = 0;            // part_chunk's fraction; number of the part in its segment
+    for (int n = 0; n <= sums; n += 8) {
+      float4 x[8];
+      bool more[8], sum[8];  // of small + 1 chunks; not empty
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (n + j + 1 < segs) x[j] = at[static_cast<size_t>(n + j) * vecs];
+      for (int j = 0; j < 8; ++j) {
+        frac += rest;
+        more[j] = frac >= parts;
+        if (more[j]) frac -= parts;
+        sum[j] = n + j < sums && (small > 0 || more[j]);
+        if (sum[j]) x[j] = at[static_cast<size_t>(n + j) * vecs];
+      }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (n + j < segs) at[static_cast<size_t>(n + j) * vecs] = s;
-      if (n + j + 1 < segs)
-        s = make_float4(decayed(s.x, keep) + x[j].x, decayed(s.y, keep) + x[j].y,
-                        decayed(s.z, keep) + x[j].z, decayed(s.w, keep) + x[j].w);
+      for (int j = 0; j < 8; ++j) {
+        if (n + j <= sums && sub == 0) at[static_cast<size_t>(n + j) * vecs] = s;
+        if (++sub == a.nsub) sub = 0;
+        if (sum[j]) {
+          const float k = more[j] ? keep1 : keep0;
+          s = make_float4(decayed(s.x, k) + x[j].x, decayed(s.y, k) + x[j].y,
+                          decayed(s.z, k) + x[j].z, decayed(s.w, k) + x[j].w);
+        }
+      }
     }
   }
 }
@@ -1065,14 +1084,15 @@ static int launch_linear_prompt_t(const CUtensorMap& tq, const CUtensorMap& tk,
   cfg.attrs = &early;
   cudaError_t err = cudaSuccess;
   if (a.nseg > 1) {
-    cfg.gridDim = dim3(a.B, a.Hkv, a.nseg - 1);
+    cfg.gridDim = dim3(a.B, a.Hkv, (a.nseg - 1) * a.nsub);
     cfg.blockDim = dim3(kLinThreads);
     cfg.dynamicSmemBytes = kStates;
     err = cudaLaunchKernelEx(&cfg, states, tq, tk, tv, to, a);
     cfg.numAttrs = 1;
   }
   if (err == cudaSuccess && (a.nseg > 1 || (a.ngrp > 1 && a.resume))) {
-    cfg.gridDim = dim3(a.B, a.Hkv, D * D / 512);
+    // (nothing to join: a copy, by fewer CTAs)
+    cfg.gridDim = dim3(a.B, a.Hkv, D * D / (a.nseg > 1 ? 512 : 2048));
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
     err = cudaLaunchKernelEx(&cfg, phs_linear_join_kernel, a, D * D / 4);

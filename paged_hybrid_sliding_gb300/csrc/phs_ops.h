@@ -132,10 +132,10 @@ struct LinearArgs {
   const int32_t* cu_seqlens;  // [B + 1]
   const int32_t* resume;      // [B] or null: from a zero state
   int total_tokens, max_seq;
-  int nseg;                   // segments of the longest prompt
+  int nseg, nsub;             // segments of each prompt, parts of a segment
   int ngrp;                   // CTAs that share a KV head's query heads, a divisor of G
   bool longest_first;         // CTAs in order of their requests' lengths (B <= kLinearSort)
-  float* ws;                  // [B][Hkv][nseg][D][D]: segment sums, then first states
+  float* ws;                  // [B][Hkv][nseg * nsub][D][D]: sums of parts, then first states
 };
 
 constexpr int kLinearChunk = 128;
