@@ -1,7 +1,8 @@
 // phs_api.cu -- the extern "C" entry points declared in include/phs.h:
 // argument validation, TMA tensor-map encoding, split planning, and the
 // hybrid layer-stack driver.  All compute happens in the kernels of
-// phs_decode.cu, phs_swa.cu, phs_append.cu and phs_quant.cu.
+// phs_decode.cu, phs_swa.cu, phs_prefix.cu, phs_append.cu, phs_quant.cu,
+// phs_pages.cu, phs_diff.cu and phs_linear.cu.
 #include <algorithm>
 #include <cmath>
 #include <cstring>

@@ -24,6 +24,14 @@
 // Each map has its own running maximum and sum, the difference is only
 // taken when both are complete.
 //
+// Measured, both launches: 64 requests to 32K tokens, 4 value heads of 128, 368
+// us against 358.5 for their bytes at the rate of a plain copy; one request
+// of 250,001 on 4 of 64, 87 against 75; 16 of 1 to 4,097, 20.5 against 5.8,
+// where the longest request's CTAs and the two launches' latency count. (Equal
+// ranges over all requests, which each CTA finds from the lengths, were slower
+// but for batches of equal lengths: 47 and 395 us for the ragged two, 52
+// against 63 for 16 of 4,097 each.)
+//
 // Weights are split into bf16 terms, p = hi + lo (+ lo2 for fp32 outputs):
 // 16 (24) bits of each weight.  The output is a difference of two averages
 // that may nearly cancel, which would blow up the 2^-9 of a single term.

@@ -48,7 +48,12 @@ __device__ __forceinline__ bool request_tokens(const LinearArgs& a, int b, int& 
 }
 
 // One CTA per (request, KV head).  A row of the state (one k index) is D/4
-// threads of one float4 each.
+// threads of one float4 each, read, updated and written back in registers; the
+// outputs' sums over rows meet in shared memory once.  The step reads and
+// writes each state once and computes 2 to 3 operations a byte, so it is bound
+// by memory, and small CTAs with many loads in flight carry it: 256 requests of
+// 32 heads of 128 (1.07 GB) take 169.7 us, 6.4 TB/s, against 159.4 for those
+// bytes at the rate of a plain copy; 2 requests 3.3 us, a launch.
 template <int D, int GM>
 __global__ void __launch_bounds__(256) phs_linear_decode_kernel(const LinearArgs a) {
   constexpr int TR = D / 4, RT = 256 / TR;  // threads of a row, rows at once
@@ -155,9 +160,17 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // Two warps on each scheduler run each role's code, and its loops are kept
 // small: with one warp and everything unrolled, fetching instructions was
 // the largest stall (3.1 of 10.7 warp-cycles an instruction).
-// What a chunk moves through shared memory bounds the kernel next to HBM: at
-// D = 128 the products read 352 KB, copies and registers move 300 KB, about
-// 5,200 cycles of 128 bytes; its share of HBM (128 KB) takes 5,300.
+//
+// What bounds it: a chunk at D = 128 takes 4.1 us (7,700 cycles) of a CTA, in
+// which it has the tensor cores busy for 51 %, issues 0.57 instructions a
+// cycle and moves 128 KB, 2.9 us at an SM's share of HBM.  What is left is the
+// chain from one chunk's state to the next one's (terms to shared memory, KV,
+// its sum back) and, beside it, scores, P, PV and the rows.  One prompt of
+// 32,751 tokens and 32 heads of 128: 355 us (89 for the sums of segments, 262
+// for the rows) against 158 for its bytes; of 32,768 tokens and heads of 64,
+// 235 against 79.  Steps that did not help: six warpgroups instead of five
+// (300 against 265 us for the rows), other forms of the waits, P's loads a
+// step ahead; single bf16 terms of P or S would, and are too coarse.
 // Where there are fewer (request, KV head) pairs than SMs, prompts are cut
 // into segments: a first launch sums up their own states (K and V alone; a
 // segment in `nsub` parts, as this launch has fewer CTAs), a small one joins
@@ -331,10 +344,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(src)
-               : "memory");
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(src)
+      : "memory");
 }
 
 // First chunk of part p of a request's `chunks`; a segment is nsub parts, and
@@ -344,8 +358,9 @@ __device__ __forceinline__ int part_chunk(const LinearArgs& a, int chunks, int p
 }
 
 // The request that comes `at`-th when the longest come first.  Where there are
-// more CTAs than SMs, the last ones to start then end soon.  All threads of the
-// CTA call it.
+// more CTAs than SMs, the last ones to start then end soon: 48.5 us against 61
+// for 16 prompts of 1 to 517 tokens, 32 heads on 8.  All threads of the CTA
+// call it.
 __device__ __forceinline__ int request_by_length(const LinearArgs& a, int at) {
   __shared__ int found;
   static_assert(kLinearSort <= kLinThreads, "a thread for each request");
@@ -680,8 +695,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               for (int t = 0; t < 3; ++t)
 #pragma unroll 2
                 for (int ks = 0; ks < T::kSteps; ++ks)
-                  umma_bf16_ts(tmem + kTmU + D * ub, kp + T::kTerm * t + 8 * ks, v + (ks * 2048 >> 4), kIdD,
-                               p > 0 || t > 0 || ks > 0);
+                  umma_bf16_ts(tmem + kTmU + D * ub, kp + T::kTerm * t + 8 * ks,
+                               v + (ks * 2048 >> 4), kIdD, p > 0 || t > 0 || ks > 0);
               umma_commit(kp_empty + 8 * (m & 1));
             }
             __syncwarp();
@@ -930,7 +945,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         *reinterpret_cast<float4*>(to + c) = make_float4(x.x, x.y, y.x, y.y);
       }
     };
-    if (!STATES) pdl_wait_prior_grid();  // for the join: the one reader of an earlier launch's output
+    if (!STATES) pdl_wait_prior_grid();  // the join's states are read here alone
     if (mine && !STATES && (part > 0 || resume)) {
       const float* from = a.nseg > 1 || a.ngrp > 1 ? ws + part * D * D : pool;
 #pragma unroll
@@ -1018,7 +1033,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // Sums of parts -> the states that segments start from, in the place of their
 // first part's: a thread holds 4 elements of a state and walks the parts, 8
 // loads at once.  (Joined by each segment for itself instead, a state cost
-// it 2.2 us.)
+// it 2.2 us: one prompt of 32,768 tokens, 8 heads on one, 139 us against 76.)
+// 8 us for 12 parts of 32 heads.
 __global__ void __launch_bounds__(128) phs_linear_join_kernel(const LinearArgs a, int vecs) {
   const int b = blockIdx.x, h = blockIdx.y;
   pdl_launch_dependents();
