@@ -568,8 +568,9 @@ int phs_attn_decode_diff_paged(const void *q, int32_t num_heads, const phs_paged
  * out bf16 [total_tokens][Hq][D]; rows of no request are left as they were.
  * A request with a bad token range (outside the tokens, or beginning before
  * an earlier one's end) or a length above max_seq_len records PHS_ERANGE and
- * is left out whole.  workspace:
- * phs_linear_prompt_workspace_bytes, 256-byte aligned.
+ * is left out whole.  workspace: phs_linear_prompt_workspace_bytes of the
+ * same sizes (a call with fewer requests may need more: its prompts are cut
+ * finer), 256-byte aligned; calls that may run at once need one each.
  * ---------------------------------------------------------------------- */
 typedef struct {
     float *s;             /* device, fp32 [num_states][Hkv][D][D] */

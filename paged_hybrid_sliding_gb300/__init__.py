@@ -286,11 +286,21 @@ def _append_args(k_new, v_new, page_refcount, B, Hkv, D):
     _opt(page_refcount, torch.int32, "page_refcount", 1)
 
 
-def _workspace(workspace, nbytes, device):
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream` (None: the current one), from that
+    stream's own: what the current stream has let go of may still be in use
+    there, and what this call uses must not be handed on before it is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(workspace, nbytes, device, stream=None):
     if workspace is None:
         # a zero size means the library rejects the shape: let the call
         # report the precise status
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+        return _empty((max(nbytes, 1),), torch.uint8, device, stream)
     _need(workspace, torch.uint8, "workspace", 1)
     return workspace
 
@@ -829,7 +839,7 @@ def pages_fork(pools, block_table, seq_lens, page_refcount, src_rows, dst_rows, 
     _opt(status, torch.int32, "status")
     arr = _pools_of(pools, page_refcount)
     rows, n = block_table.shape[0], src_rows.shape[0]
-    ws = _workspace(workspace, pages_fork_workspace_bytes(rows, n), block_table.device)
+    ws = _workspace(workspace, pages_fork_workspace_bytes(rows, n), block_table.device, stream)
     _same_device(block_table, seq_lens, page_refcount, src_rows, dst_rows, ws, status)
     _check(lib().phs_pages_fork(arr, len(pools), _ptr(block_table), rows, block_table.shape[1],
                                 _ptr(seq_lens), _ptr(page_refcount), _ptr(src_rows),
@@ -852,9 +862,9 @@ def pages_compact(pools, block_table, seq_lens, page_refcount, block_table_out=N
     bt = block_table if block_table_out is None else block_table_out
     rc = page_refcount if page_refcount_out is None else page_refcount_out
     if page_map is None:
-        page_map = torch.empty_like(page_refcount)
+        page_map = _empty(page_refcount.shape, torch.int32, block_table.device, stream)
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=block_table.device)
+        num_live = _empty((1,), torch.int32, block_table.device, stream)
     for t, like, name in ((bt, block_table, "block_table_out"),
                           (rc, page_refcount, "page_refcount_out"),
                           (page_map, page_refcount, "page_map")):
@@ -866,7 +876,7 @@ def pages_compact(pools, block_table, seq_lens, page_refcount, block_table_out=N
         raise ValueError("num_live must be [1]")
     _opt(status, torch.int32, "status")
     ws = _workspace(workspace, pages_compact_workspace_bytes(page_refcount.shape[0]),
-                    block_table.device)
+                    block_table.device, stream)
     _same_device(block_table, seq_lens, page_refcount, bt, rc, page_map, num_live, ws, status)
     _check(lib().phs_pages_compact(arr, len(pools), _ptr(block_table), block_table.shape[0],
                                    block_table.shape[1], _ptr(seq_lens), _ptr(page_refcount),
@@ -936,7 +946,7 @@ def attn_decode_diff_paged(q, pool: PagedPool, block_table, seq_lens, max_seq_le
         raise ValueError("block_table and seq_lens need one row per request")
     H = H2 // 2
     if out is None:
-        out = torch.empty((B, H, 2 * D), dtype=out_dtype, device=q.device)
+        out = _empty((B, H, 2 * D), out_dtype, q.device, stream)
     _need(out, out.dtype, "out", 3)
     if out.shape != (B, H, 2 * D):
         raise ValueError("out must be [batch, H, 2 head_dim]")
@@ -946,7 +956,7 @@ def attn_decode_diff_paged(q, pool: PagedPool, block_table, seq_lens, max_seq_le
     wc = weights.c(H, D)
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
     ws = _workspace(workspace, diff_workspace_bytes(B, H, heads // 2, D, max_seq_len,
-                                                    tokens_per_split), q.device)
+                                                    tokens_per_split), q.device, stream)
     _same_device(q, pool.k, pool.v, block_table, seq_lens, out, ws, k_new, v_new, page_refcount,
                  status, weights.lambda_q1, weights.lambda_k1, weights.lambda_q2,
                  weights.lambda_k2, weights.norm_weight)
@@ -997,9 +1007,9 @@ def _linear_args(q, k, v, pool, log_decay, state_ids, batch, status):
     return pc
 
 
-def _linear_out(out, q, dtype):
+def _linear_out(out, q, dtype, stream):
     if out is None:
-        return torch.empty(q.shape, dtype=dtype, device=q.device)
+        return _empty(q.shape, dtype, q.device, stream)
     _need(out, out.dtype, "out", 3)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
@@ -1012,7 +1022,7 @@ def linear_attn_decode(q, k_new, v_new, pool: StatePool, log_decay, state_ids=No
     [B, Hkv, D] bf16; updates the states and returns out [B, Hq, D]."""
     B = q.shape[0]
     pc = _linear_args(q, k_new, v_new, pool, log_decay, state_ids, B, status)
-    out = _linear_out(out, q, out_dtype)
+    out = _linear_out(out, q, out_dtype, stream)
     _same_device(q, k_new, v_new, pool.s, log_decay, state_ids, out, status)
     scale = 1.0 / math.sqrt(q.shape[2]) if scale is None else float(scale)
     _check(lib().phs_linear_attn_decode(_ptr(q), q.shape[1], ctypes.byref(pc), _ptr(k_new),
@@ -1024,7 +1034,8 @@ def linear_attn_decode(q, k_new, v_new, pool: StatePool, log_decay, state_ids=No
 
 def linear_prompt_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, total_tokens,
                                   max_seq_len) -> int:
-    """Workspace bytes for linear_attn_prompt; 0 if unsupported."""
+    """Workspace bytes for linear_attn_prompt; 0 if unsupported.  For a call
+    of these very sizes: one with fewer requests may need more."""
     return int(lib().phs_linear_prompt_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim,
                                                        total_tokens, max_seq_len))
 
@@ -1045,12 +1056,12 @@ def linear_attn_prompt(q, k, v, cu_seqlens, max_seq_len: int, pool: StatePool, l
     _opt(resume, torch.int32, "resume", 1)
     if resume is not None and resume.shape[0] != B:
         raise ValueError("resume must be [batch]")
-    out = _linear_out(out, q, torch.bfloat16)
+    out = _linear_out(out, q, torch.bfloat16, stream)
     if out.dtype != torch.bfloat16:
         raise ValueError("out must be bfloat16")
     T, Hq, D = q.shape
     ws = _workspace(workspace, linear_prompt_workspace_bytes(B, Hq, pool.s.shape[1], D, T,
-                                                             max_seq_len), q.device)
+                                                             max_seq_len), q.device, stream)
     _same_device(q, k, v, cu_seqlens, pool.s, log_decay, state_ids, resume, out, ws, status)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     _check(lib().phs_linear_attn_prompt(_ptr(q), Hq, _ptr(k), _ptr(v), _ptr(cu_seqlens), T,

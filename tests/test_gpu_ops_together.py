@@ -209,3 +209,29 @@ def test_two_graphs_with_their_own_workspaces_replayed_at_once():
     for w, (_, out, _) in zip(want, runs):
         assert torch.equal(w, out)
     assert torch.equal(states, pool.s)
+
+
+def test_memory_of_a_call_on_another_stream():
+    """What the current stream has let go of, but is still to write, is not
+    what a call on another stream gets for its output and workspace."""
+    D, Hq, Hkv, T = 128, 4, 2, 1200
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    mk = lambda *shape: torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)
+    q, k, v = mk(T, Hq, D), mk(T, Hkv, D), mk(T, Hkv, D)
+    decay = -torch.logspace(-4, -0.5, Hkv, device="cuda")
+    cu = dev([0, T])
+    need = phs.linear_prompt_workspace_bytes(1, Hq, Hkv, D, T, T)
+    want = phs.linear_attn_prompt(q, k, v, cu, T, phs.StatePool.zeros(1, Hkv, D), decay)
+    side = torch.cuda.Stream()
+    pool = phs.StatePool.zeros(1, Hkv, D)
+    torch.cuda.synchronize()
+    # (sleeps about 20 ms, far longer than the call)
+    waste = [torch.empty(n, dtype=torch.uint8, device="cuda")
+             for n in (need, want.numel() * 2) for _ in range(4)]
+    torch.cuda._sleep(40_000_000)
+    for w in waste:
+        w.fill_(255)
+    del waste, w
+    got = phs.linear_attn_prompt(q, k, v, cu, T, pool, decay, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
