@@ -286,21 +286,11 @@ def _append_args(k_new, v_new, page_refcount, B, Hkv, D):
     _opt(page_refcount, torch.int32, "page_refcount", 1)
 
 
-def _empty(shape, dtype, device, stream):
-    """Memory for a call on `stream` (None: the current one), from that
-    stream's own: what the current stream has let go of may still be in use
-    there, and what this call uses must not be handed on before it is done."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _workspace(workspace, nbytes, device, stream=None):
+def _workspace(workspace, nbytes, device):
     if workspace is None:
         # a zero size means the library rejects the shape: let the call
         # report the precise status
-        return _empty((max(nbytes, 1),), torch.uint8, device, stream)
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
     _need(workspace, torch.uint8, "workspace", 1)
     return workspace
 
@@ -777,48 +767,102 @@ def window_safe_len(swa_valid, match_len: int, window: int, align: int = 1) -> i
 
 
 # ---------------------------------------------------------- page operations --
-def _same_device(first, *others):
-    """The tensors of one call live on the device that the call runs on."""
-    device = torch.cuda.current_device()
-    if first.get_device() == device:
-        for t in others:
-            if t is not None and t.get_device() != device:
-                break
-        else:
-            return
-    raise ValueError("all tensors must be on the current CUDA device")
+# A small call costs the GPU less than its checks cost the host, so the calls
+# below look at each tensor once.
+_DEVICE_ERROR = "all tensors must be on the current CUDA device"
+
+
+def _device(t, dtype, name):
+    """The device that a call with t runs on: t's, and the current one."""
+    if isinstance(t, torch.Tensor):
+        dev = t.get_device()
+        if dev >= 0:
+            if torch._C._cuda_getDevice() != dev:
+                raise ValueError(_DEVICE_ERROR)
+            return dev
+    return _need(t, dtype, name).get_device()
+
+
+def _shape(t, dtype, dev, name, dims):
+    """Shape of t: a contiguous `dtype` tensor of `dims` dimensions on `dev`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev \
+            and t.is_contiguous():
+        shape = t.shape
+        if len(shape) == dims:
+            return shape
+    _need(t, dtype, name, dims)
+    raise ValueError(_DEVICE_ERROR)
+
+
+def _status_ptr(status, dev):
+    if status is None:
+        return None
+    if _need(status, torch.int32, "status").get_device() != dev:
+        raise ValueError(_DEVICE_ERROR)
+    return status.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream` (None: the current one), from that
+    stream's own: what the current stream has let go of may still be in use
+    there, and what this call uses must not be handed on before it is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call_memory(workspace, nbytes, dev, stream):
+    """(pointer, bytes) of a call's workspace, and the tensor that holds it."""
+    if workspace is None:
+        # (a zero size means the library rejects the shape: it says how)
+        workspace = _empty((max(nbytes, 1),), torch.uint8, dev, stream)
+        return workspace.data_ptr(), nbytes, workspace
+    n, = _shape(workspace, torch.uint8, dev, "workspace", 1)
+    return workspace.data_ptr(), n, workspace
 
 
 def _tables(block_table, seq_lens, page_refcount):
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
-    _need(page_refcount, torch.int32, "page_refcount", 1)
-    if seq_lens.shape[0] != block_table.shape[0]:
+    """(device, rows, pages of a row, pages of the pool)"""
+    dev = _device(block_table, torch.int32, "block_table")
+    rows, width = _shape(block_table, torch.int32, dev, "block_table", 2)
+    n, = _shape(seq_lens, torch.int32, dev, "seq_lens", 1)
+    pages, = _shape(page_refcount, torch.int32, dev, "page_refcount", 1)
+    if n != rows:
         raise ValueError("seq_lens needs one entry per row of block_table")
+    return dev, rows, width, pages
 
 
-def _pools_of(pools, page_refcount):
+def _pool_c(pool, dev):
+    shape = n, h, p, d = _shape(pool.k, torch.bfloat16, dev, "pool.k", 4)
+    if _shape(pool.v, torch.bfloat16, dev, "pool.v", 4) != shape:
+        raise ValueError("pool.k and pool.v shapes differ")
+    return _lib.PagedPoolC(pool.k.data_ptr(), pool.v.data_ptr(), n, p, h, d)
+
+
+def _pools_of(pools, dev, num_pages):
     if not pools:
         raise ValueError("pools must name at least one pool")
-    arr = _pool_array(_lib.PagedPoolC, pools)
-    n = page_refcount.shape[0]
-    for p, c in zip(pools, arr):
-        if c.num_pages != n:
+    arr = (_lib.PagedPoolC * len(pools))()
+    for i, p in enumerate(pools):
+        arr[i] = c = _pool_c(p, dev)
+        if c.num_pages != num_pages:
             raise ValueError("page_refcount needs one entry per page")
-        _same_device(page_refcount, p.k, p.v)
     return arr
 
 
 def pages_free(block_table, seq_lens, page_refcount, rows, status=None, stream=None):
     """Free the listed rows of the block table: one reference less on each
     of their pages, their lengths zero."""
-    _tables(block_table, seq_lens, page_refcount)
-    _need(rows, torch.int32, "rows", 1)
-    _opt(status, torch.int32, "status")
-    _same_device(block_table, seq_lens, page_refcount, rows, status)
-    _check(lib().phs_pages_free(_ptr(block_table), block_table.shape[0], block_table.shape[1],
-                                _ptr(seq_lens), _ptr(page_refcount), page_refcount.shape[0],
-                                _ptr(rows), rows.shape[0], _ptr(status), _stream(stream)),
+    dev, num_rows, width, pages = _tables(block_table, seq_lens, page_refcount)
+    n, = _shape(rows, torch.int32, dev, "rows", 1)
+    _check(lib().phs_pages_free(block_table.data_ptr(), num_rows, width, seq_lens.data_ptr(),
+                                page_refcount.data_ptr(), pages, rows.data_ptr(), n,
+                                _status_ptr(status, dev), _raw_stream(stream, dev)),
            "pages_free")
 
 
@@ -831,20 +875,17 @@ def pages_fork(pools, block_table, seq_lens, page_refcount, src_rows, dst_rows, 
     """Continue row src_rows[i] in the free row dst_rows[i]: whole pages
     shared, a partly filled last page copied into the lowest free page, in
     every pool of `pools` (list of PagedPool sharing the block table)."""
-    _tables(block_table, seq_lens, page_refcount)
-    _need(src_rows, torch.int32, "src_rows", 1)
-    _need(dst_rows, torch.int32, "dst_rows", 1)
-    if src_rows.shape != dst_rows.shape:
+    dev, rows, width, pages = _tables(block_table, seq_lens, page_refcount)
+    n, = _shape(src_rows, torch.int32, dev, "src_rows", 1)
+    if _shape(dst_rows, torch.int32, dev, "dst_rows", 1) != (n,):
         raise ValueError("src_rows and dst_rows go together")
-    _opt(status, torch.int32, "status")
-    arr = _pools_of(pools, page_refcount)
-    rows, n = block_table.shape[0], src_rows.shape[0]
-    ws = _workspace(workspace, pages_fork_workspace_bytes(rows, n), block_table.device, stream)
-    _same_device(block_table, seq_lens, page_refcount, src_rows, dst_rows, ws, status)
-    _check(lib().phs_pages_fork(arr, len(pools), _ptr(block_table), rows, block_table.shape[1],
-                                _ptr(seq_lens), _ptr(page_refcount), _ptr(src_rows),
-                                _ptr(dst_rows), n, _ptr(ws), ws.numel(), _ptr(status),
-                                _stream(stream)), "pages_fork")
+    arr = _pools_of(pools, dev, pages)
+    ws, ws_bytes, _held = _call_memory(workspace, pages_fork_workspace_bytes(rows, n), dev, stream)
+    _check(lib().phs_pages_fork(arr, len(pools), block_table.data_ptr(), rows, width,
+                                seq_lens.data_ptr(), page_refcount.data_ptr(),
+                                src_rows.data_ptr(), dst_rows.data_ptr(), n, ws, ws_bytes,
+                                _status_ptr(status, dev), _raw_stream(stream, dev)),
+           "pages_fork")
 
 
 def pages_compact_workspace_bytes(num_pages) -> int:
@@ -857,31 +898,30 @@ def pages_compact(pools, block_table, seq_lens, page_refcount, block_table_out=N
     """Move the live pages to the lowest page ids in every pool of `pools`;
     returns (page_map [num_pages]: new id or -1, num_live [1]).  The tables
     and counts are rewritten in place unless *_out are given."""
-    _tables(block_table, seq_lens, page_refcount)
-    arr = _pools_of(pools, page_refcount)
+    dev, rows, width, pages = _tables(block_table, seq_lens, page_refcount)
+    arr = _pools_of(pools, dev, pages)
     bt = block_table if block_table_out is None else block_table_out
     rc = page_refcount if page_refcount_out is None else page_refcount_out
     if page_map is None:
-        page_map = _empty(page_refcount.shape, torch.int32, block_table.device, stream)
+        page_map = _empty((pages,), torch.int32, dev, stream)
     if num_live is None:
-        num_live = _empty((1,), torch.int32, block_table.device, stream)
-    for t, like, name in ((bt, block_table, "block_table_out"),
-                          (rc, page_refcount, "page_refcount_out"),
-                          (page_map, page_refcount, "page_map")):
-        _need(t, torch.int32, name, like.dim())
-        if t.shape != like.shape:
-            raise ValueError(f"{name} must be {tuple(like.shape)}")
-    _need(num_live, torch.int32, "num_live", 1)
-    if num_live.shape[0] != 1:
+        num_live = _empty((1,), torch.int32, dev, stream)
+    if bt is not block_table and \
+            _shape(bt, torch.int32, dev, "block_table_out", 2) != (rows, width):
+        raise ValueError(f"block_table_out must be [{rows}, {width}]")
+    if rc is not page_refcount and \
+            _shape(rc, torch.int32, dev, "page_refcount_out", 1) != (pages,):
+        raise ValueError(f"page_refcount_out must be [{pages}]")
+    if _shape(page_map, torch.int32, dev, "page_map", 1) != (pages,):
+        raise ValueError(f"page_map must be [{pages}]")
+    if _shape(num_live, torch.int32, dev, "num_live", 1) != (1,):
         raise ValueError("num_live must be [1]")
-    _opt(status, torch.int32, "status")
-    ws = _workspace(workspace, pages_compact_workspace_bytes(page_refcount.shape[0]),
-                    block_table.device, stream)
-    _same_device(block_table, seq_lens, page_refcount, bt, rc, page_map, num_live, ws, status)
-    _check(lib().phs_pages_compact(arr, len(pools), _ptr(block_table), block_table.shape[0],
-                                   block_table.shape[1], _ptr(seq_lens), _ptr(page_refcount),
-                                   _ptr(bt), _ptr(rc), _ptr(page_map), _ptr(num_live), _ptr(ws),
-                                   ws.numel(), _ptr(status), _stream(stream)), "pages_compact")
+    ws, ws_bytes, _held = _call_memory(workspace, pages_compact_workspace_bytes(pages), dev, stream)
+    _check(lib().phs_pages_compact(arr, len(pools), block_table.data_ptr(), rows, width,
+                                   seq_lens.data_ptr(), page_refcount.data_ptr(), bt.data_ptr(),
+                                   rc.data_ptr(), page_map.data_ptr(), num_live.data_ptr(), ws,
+                                   ws_bytes, _status_ptr(status, dev), _raw_stream(stream, dev)),
+           "pages_compact")
     return page_map, num_live
 
 
@@ -899,21 +939,20 @@ class DiffWeights:
     norm_weight: torch.Tensor | None = None
     norm_eps: float = 1e-5
 
-    def c(self, num_heads, head_dim):
-        vecs = (self.lambda_q1, self.lambda_k1, self.lambda_q2, self.lambda_k2)
+    def c(self, num_heads, head_dim, dev):
         per_head = self.lambda_q1.dim() == 2
         want = (num_heads, head_dim) if per_head else (head_dim,)
+        vecs = (self.lambda_q1, self.lambda_k1, self.lambda_q2, self.lambda_k2)
         for t in vecs:
-            _need(t, torch.float32, "lambda vectors")
-            if t.shape != want:
+            if _shape(t, torch.float32, dev, "lambda vectors", len(want)) != want:
                 raise ValueError(f"lambda vectors must be [{head_dim}] or "
                                  f"[{num_heads}, {head_dim}], all alike")
-        _opt(self.norm_weight, torch.float32, "norm_weight", 1)
-        if self.norm_weight is not None and self.norm_weight.shape[0] != 2 * head_dim:
+        norm = self.norm_weight
+        if norm is not None and \
+                _shape(norm, torch.float32, dev, "norm_weight", 1) != (2 * head_dim,):
             raise ValueError(f"norm_weight must be [{2 * head_dim}]")
-        return _lib.DiffWeightsC(*(t.data_ptr() for t in vecs),
-                                 0 if self.norm_weight is None else self.norm_weight.data_ptr(),
-                                 float(self.lambda_init), float(self.norm_eps), int(per_head))
+        return _lib.DiffWeightsC(*[t.data_ptr() for t in vecs], _ptr(norm),
+                                 float(self.lambda_init), float(self.norm_eps), per_head)
 
 
 def diff_workspace_bytes(batch, num_heads, num_value_heads, head_dim, max_seq_len,
@@ -931,40 +970,41 @@ def attn_decode_diff_paged(q, pool: PagedPool, block_table, seq_lens, max_seq_le
     queries of the two maps), pool of 2 Hv heads of width D; returns out
     [B, H, 2D].  k_new / v_new ([B, 2 Hv, D] bf16): append token
     seq_lens[b] - 1 in the same call."""
-    _need(q, torch.bfloat16, "q", 3)
-    pc = pool.c()
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
-    _opt(status, torch.int32, "status")
-    B, H2, D = q.shape
-    heads = pool.k.shape[1]
+    dev = _device(q, torch.bfloat16, "q")
+    B, H2, D = _shape(q, torch.bfloat16, dev, "q", 3)
+    pc = _pool_c(pool, dev)
+    rows, width = _shape(block_table, torch.int32, dev, "block_table", 2)
+    n, = _shape(seq_lens, torch.int32, dev, "seq_lens", 1)
+    heads = pc.num_kv_heads
     if H2 % 2 != 0 or heads % 2 != 0:
         raise ValueError("q and the pool need an even number of heads (two maps)")
-    if D != pool.k.shape[3]:
+    if D != pc.head_dim:
         raise ValueError("q and the pool differ in head_dim")
-    if block_table.shape[0] != B or seq_lens.shape[0] != B:
+    if rows != B or n != B:
         raise ValueError("block_table and seq_lens need one row per request")
     H = H2 // 2
     if out is None:
-        out = _empty((B, H, 2 * D), out_dtype, q.device, stream)
-    _need(out, out.dtype, "out", 3)
-    if out.shape != (B, H, 2 * D):
+        out = _empty((B, H, 2 * D), out_dtype, dev, stream)
+    elif _shape(out, out.dtype, dev, "out", 3) != (B, H, 2 * D):
         raise ValueError("out must be [batch, H, 2 head_dim]")
-    _append_args(k_new, v_new, page_refcount, B, heads, D)
-    if page_refcount is not None and page_refcount.shape[0] != pool.k.shape[0]:
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    if k_new is not None and (_shape(k_new, torch.bfloat16, dev, "k_new", 3) != (B, heads, D) or
+                              _shape(v_new, torch.bfloat16, dev, "v_new", 3) != (B, heads, D)):
+        raise ValueError("k_new and v_new must be [batch, heads of the pool, D]")
+    if page_refcount is not None and \
+            _shape(page_refcount, torch.int32, dev, "page_refcount", 1) != (pc.num_pages,):
         raise ValueError("page_refcount needs one entry per page")
-    wc = weights.c(H, D)
+    wc = weights.c(H, D, dev)
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    ws = _workspace(workspace, diff_workspace_bytes(B, H, heads // 2, D, max_seq_len,
-                                                    tokens_per_split), q.device, stream)
-    _same_device(q, pool.k, pool.v, block_table, seq_lens, out, ws, k_new, v_new, page_refcount,
-                 status, weights.lambda_q1, weights.lambda_k1, weights.lambda_q2,
-                 weights.lambda_k2, weights.norm_weight)
+    ws, ws_bytes, _held = _call_memory(
+        workspace, diff_workspace_bytes(B, H, heads // 2, D, max_seq_len, tokens_per_split), dev,
+        stream)
     _check(lib().phs_attn_decode_diff_paged(
-        _ptr(q), H, ctypes.byref(pc), _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-        int(max_seq_len), B, ctypes.byref(wc), scale, int(tokens_per_split), _ptr(out),
-        _out_code(out.dtype), _ptr(ws), ws.numel(), _ptr(k_new), _ptr(v_new),
-        _ptr(page_refcount), _ptr(status), _stream(stream)), "attn_decode_diff_paged")
+        q.data_ptr(), H, pc, block_table.data_ptr(), width, seq_lens.data_ptr(), int(max_seq_len),
+        B, wc, scale, int(tokens_per_split), out.data_ptr(), _out_code(out.dtype), ws, ws_bytes,
+        _ptr(k_new), _ptr(v_new), _ptr(page_refcount), _status_ptr(status, dev),
+        _raw_stream(stream, dev)), "attn_decode_diff_paged")
     return out
 
 
@@ -974,9 +1014,8 @@ class StatePool:
     """States of linear attention: s fp32 [num_states, Hkv, D (k), D (v)]."""
     s: torch.Tensor
 
-    def c(self):
-        _need(self.s, torch.float32, "state.s", 4)
-        n, h, d, d2 = self.s.shape
+    def c(self, dev):
+        n, h, d, d2 = _shape(self.s, torch.float32, dev, "state.s", 4)
         if d != d2:
             raise ValueError("state.s must be [num_states, Hkv, D, D]")
         return _lib.StatePoolC(self.s.data_ptr(), n, h, d)
@@ -987,31 +1026,29 @@ class StatePool:
                                      dtype=torch.float32, device=device))
 
 
-def _linear_args(q, k, v, pool, log_decay, state_ids, batch, status):
-    pc = pool.c()
-    _need(q, torch.bfloat16, "q", 3)
-    Hkv, D = pool.s.shape[1], pool.s.shape[2]
-    for t, name in ((k, "k"), (v, "v")):
-        _need(t, torch.bfloat16, name, 3)
-        if t.shape != (q.shape[0], Hkv, D):
-            raise ValueError(f"{name} must be [tokens, Hkv, head_dim]")
-    if q.shape[2] != D:
+def _linear_args(q, k, v, pool, log_decay, state_ids, batch, dev):
+    """(T, Hq, D) of q and the pool's descriptor, all arguments checked."""
+    T, Hq, D = _shape(q, torch.bfloat16, dev, "q", 3)
+    pc = pool.c(dev)
+    Hkv = pc.num_kv_heads
+    if _shape(k, torch.bfloat16, dev, "k", 3) != (T, Hkv, D) or \
+            _shape(v, torch.bfloat16, dev, "v", 3) != (T, Hkv, D):
+        raise ValueError("k and v must be [tokens, Hkv, head_dim]")
+    if D != pc.head_dim:
         raise ValueError("q and the state pool differ in head_dim")
-    _need(log_decay, torch.float32, "log_decay", 1)
-    if log_decay.shape[0] != Hkv:
+    if _shape(log_decay, torch.float32, dev, "log_decay", 1) != (Hkv,):
         raise ValueError("log_decay must be [Hkv]")
-    _opt(state_ids, torch.int32, "state_ids", 1)
-    if state_ids is not None and state_ids.shape[0] != batch:
+    batch = T if batch is None else batch
+    if state_ids is not None and \
+            _shape(state_ids, torch.int32, dev, "state_ids", 1) != (batch,):
         raise ValueError("state_ids must be [batch]")
-    _opt(status, torch.int32, "status")
-    return pc
+    return T, Hq, D, pc
 
 
-def _linear_out(out, q, dtype, stream):
+def _linear_out(out, T, Hq, D, dtype, dev, stream):
     if out is None:
-        return _empty(q.shape, dtype, q.device, stream)
-    _need(out, out.dtype, "out", 3)
-    if out.shape != q.shape:
+        return _empty((T, Hq, D), dtype, dev, stream)
+    if _shape(out, out.dtype, dev, "out", 3) != (T, Hq, D):
         raise ValueError("out must have q's shape")
     return out
 
@@ -1020,15 +1057,15 @@ def linear_attn_decode(q, k_new, v_new, pool: StatePool, log_decay, state_ids=No
                        out=None, out_dtype=torch.bfloat16, status=None, stream=None):
     """One token of linear attention per request: q [B, Hq, D], k_new, v_new
     [B, Hkv, D] bf16; updates the states and returns out [B, Hq, D]."""
-    B = q.shape[0]
-    pc = _linear_args(q, k_new, v_new, pool, log_decay, state_ids, B, status)
-    out = _linear_out(out, q, out_dtype, stream)
-    _same_device(q, k_new, v_new, pool.s, log_decay, state_ids, out, status)
-    scale = 1.0 / math.sqrt(q.shape[2]) if scale is None else float(scale)
-    _check(lib().phs_linear_attn_decode(_ptr(q), q.shape[1], ctypes.byref(pc), _ptr(k_new),
-                                        _ptr(v_new), _ptr(log_decay), _ptr(state_ids), B, scale,
-                                        _ptr(out), _out_code(out.dtype), _ptr(status),
-                                        _stream(stream)), "linear_attn_decode")
+    dev = _device(q, torch.bfloat16, "q")
+    B, Hq, D, pc = _linear_args(q, k_new, v_new, pool, log_decay, state_ids, None, dev)
+    out = _linear_out(out, B, Hq, D, out_dtype, dev, stream)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    _check(lib().phs_linear_attn_decode(q.data_ptr(), Hq, pc, k_new.data_ptr(), v_new.data_ptr(),
+                                        log_decay.data_ptr(), _ptr(state_ids), B, scale,
+                                        out.data_ptr(), _out_code(out.dtype),
+                                        _status_ptr(status, dev), _raw_stream(stream, dev)),
+           "linear_attn_decode")
     return out
 
 
@@ -1048,25 +1085,24 @@ def linear_attn_prompt(q, k, v, cu_seqlens, max_seq_len: int, pool: StatePool, l
     bf16, starts from its state where resume[b] != 0 (else from zero) and
     leaves its last state in the pool.  Returns out bf16 [T, Hq, D]; rows of
     no request are left as they were (unset in an output made here)."""
-    _need(cu_seqlens, torch.int32, "cu_seqlens", 1)
-    B = cu_seqlens.shape[0] - 1
+    dev = _device(q, torch.bfloat16, "q")
+    B = _shape(cu_seqlens, torch.int32, dev, "cu_seqlens", 1)[0] - 1
     if B < 0:
         raise ValueError("cu_seqlens must be [batch + 1]")
-    pc = _linear_args(q, k, v, pool, log_decay, state_ids, B, status)
-    _opt(resume, torch.int32, "resume", 1)
-    if resume is not None and resume.shape[0] != B:
+    T, Hq, D, pc = _linear_args(q, k, v, pool, log_decay, state_ids, B, dev)
+    if resume is not None and _shape(resume, torch.int32, dev, "resume", 1) != (B,):
         raise ValueError("resume must be [batch]")
-    out = _linear_out(out, q, torch.bfloat16, stream)
+    out = _linear_out(out, T, Hq, D, torch.bfloat16, dev, stream)
     if out.dtype != torch.bfloat16:
         raise ValueError("out must be bfloat16")
-    T, Hq, D = q.shape
-    ws = _workspace(workspace, linear_prompt_workspace_bytes(B, Hq, pool.s.shape[1], D, T,
-                                                             max_seq_len), q.device, stream)
-    _same_device(q, k, v, cu_seqlens, pool.s, log_decay, state_ids, resume, out, ws, status)
+    ws, ws_bytes, _held = _call_memory(
+        workspace, linear_prompt_workspace_bytes(B, Hq, pc.num_kv_heads, D, T, max_seq_len), dev,
+        stream)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    _check(lib().phs_linear_attn_prompt(_ptr(q), Hq, _ptr(k), _ptr(v), _ptr(cu_seqlens), T,
-                                        int(max_seq_len), ctypes.byref(pc), _ptr(state_ids),
-                                        _ptr(resume), _ptr(log_decay), B, scale, _ptr(out),
-                                        _ptr(ws), ws.numel(), _ptr(status), _stream(stream)),
+    _check(lib().phs_linear_attn_prompt(q.data_ptr(), Hq, k.data_ptr(), v.data_ptr(),
+                                        cu_seqlens.data_ptr(), T, int(max_seq_len), pc,
+                                        _ptr(state_ids), _ptr(resume), log_decay.data_ptr(), B,
+                                        scale, out.data_ptr(), ws, ws_bytes,
+                                        _status_ptr(status, dev), _raw_stream(stream, dev)),
            "linear_attn_prompt")
     return out
