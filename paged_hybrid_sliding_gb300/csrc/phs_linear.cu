@@ -609,6 +609,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     return ok;
   };
 
+  // The first tiles are on their way while an earlier launch ends; all else
+  // waits for that end here, not in a wait of limited length.
+  if (!STATES && warp != 17) pdl_wait_prior_grid();
+
   // (each warpgroup sets its registers at the head of its own branch, so that
   // the code behind it is compiled for that number)
   if (warp >= 16) {
@@ -646,6 +650,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           load_kv(&tk, t);
           if (!STATES && ok) load_q(0, t);
           if (ok) load_kv(&tv, t);
+          if (!STATES && n == 0) pdl_wait_prior_grid();
           for (int gq = 1; !STATES && ok && gq < G; ++gq) load_q(gq, t);
         }
         if (!ok) {
@@ -945,7 +950,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         *reinterpret_cast<float4*>(to + c) = make_float4(x.x, x.y, y.x, y.y);
       }
     };
-    if (!STATES) pdl_wait_prior_grid();  // the join's states are read here alone
     if (mine && !STATES && (part > 0 || resume)) {
       const float* from = a.nseg > 1 || a.ngrp > 1 ? ws + part * D * D : pool;
 #pragma unroll
