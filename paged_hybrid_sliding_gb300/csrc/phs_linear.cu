@@ -161,16 +161,18 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // small: with one warp and everything unrolled, fetching instructions was
 // the largest stall (3.1 of 10.7 warp-cycles an instruction).
 //
-// What bounds it: a chunk at D = 128 takes 4.1 us (7,700 cycles) of a CTA, in
-// which it has the tensor cores busy for 51 %, issues 0.57 instructions a
-// cycle and moves 128 KB, 2.9 us at an SM's share of HBM.  What is left is the
-// chain from one chunk's state to the next one's (terms to shared memory, KV,
-// its sum back) and, beside it, scores, P, PV and the rows.  One prompt of
-// 32,751 tokens and 32 heads of 128: 355 us (89 for the sums of segments, 262
-// for the rows) against 158 for its bytes; of 32,768 tokens and heads of 64,
-// 235 against 79.  Steps that did not help: six warpgroups instead of five
-// (300 against 265 us for the rows), other forms of the waits, P's loads a
-// step ahead; single bf16 terms of P or S would, and are too coarse.
+// What bounds it: a chunk at D = 128 takes 3.8 us (7,200 cycles) of a CTA, in
+// which it has the tensor cores busy for 54 %, issues 0.6 instructions a cycle,
+// the integer and conversion units for 45 % of the time, and moves 128 KB, 2.9
+// us at an SM's share of HBM.  What is left is the chain from one chunk's state
+// to the next one's (terms to shared memory, KV, its sum back) and, beside it,
+// scores, P, PV and the rows.  One prompt of 32,751 tokens and 32 heads of 128:
+// 337 us (89 for the sums of segments, 243 for the rows) against 158 for its
+// bytes; of 32,768 tokens and heads of 64, 226 against 79.  Steps that did not
+// help: six warpgroups instead of five (300 against 265 us for the rows), other
+// forms of the waits, P's loads a step ahead, terms cut off instead of rounded
+// (391 against 348 us), K' formed before the wait for its buffer (345 against
+// 337).  Single bf16 terms of P or S would help, and are too coarse.
 // Where there are fewer (request, KV head) pairs than SMs, prompts are cut
 // into segments: a first launch sums up their own states (K and V alone; a
 // segment in `nsub` parts, as this launch has fewer CTAs), a small one joins
@@ -215,7 +217,7 @@ struct LinLayout {
   static constexpr int kBars = 2 * kSlots + 21;
   static constexpr int kMisc = kBar + kBars * 8;  // tensor-memory base, abort flag
   static constexpr int kAlloc = kMisc + 16 + 1024;
-  static constexpr int kTables = (2 * (kLinC + 4) + 32) * 4;  // static: pw, ps and its pad
+  static constexpr int kTables = (3 * kLinC + 4 + 32) * 4;  // static: back, ps and its pad
   static_assert(kAlloc + kTables <= 227 * 1024, "shared memory of the prompt kernel");
 };
 
@@ -273,7 +275,19 @@ __device__ __forceinline__ uint64_t f2(uint32_t lo, uint32_t hi) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
   return r;
 }
-__device__ __forceinline__ uint64_t f2_bf16(uint32_t w) { return f2(w << 16, w & 0xffff0000u); }
+// (by fma with bf16 factors, here and below: shifts and masks would run on the
+// units that the conversions keep busy)
+__device__ __forceinline__ uint64_t f2_bf16(uint32_t w) {
+  float lo, hi;
+  asm("{\n\t.reg .b16 l, h, m;\n\t"
+      "mov.b16 m, 0x3F80;\n\t"  // 1
+      "mov.b32 {l, h}, %2;\n\t"
+      "fma.rn.f32.bf16 %0, l, m, %3;\n\t"
+      "fma.rn.f32.bf16 %1, h, m, %3;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(w), "f"(0.f));
+  return f2(lo, hi);
+}
 __device__ __forceinline__ float2 f2_get(uint64_t v) {
   float2 r;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
@@ -300,7 +314,6 @@ __device__ __forceinline__ uint32_t pack_term(uint64_t x) {
   const float2 v = f2_get(x);
   return pack_bf16(v.x, v.y);
 }
-// (fma with bf16 factors: the terms need no unpacking)
 __device__ __forceinline__ uint32_t take_term(uint64_t& x) {
   const float2 v = f2_get(x);
   const uint32_t w = pack_bf16(v.x, v.y);
@@ -394,8 +407,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   constexpr int kTermWarps = 2;  // that form K' of 32 columns of K
   constexpr int kTermThreads = 128 * kTermWarps;
   extern __shared__ uint8_t smem_raw[];
-  // pw[n] = exp(g n), ps[n] = scale pw[n]; ps is read from n = -31 on (unused there)
-  __shared__ float pw[kLinC + 4], ps_pad[32 + kLinC + 4];
+  // back[x]: the decay of token x of a whole chunk up to its last one, exp(g
+  // (127 - x)), then zeros for tokens behind the last; ps[n] = scale exp(g n),
+  // read from n = -31 on (unused there)
+  __shared__ float back[2 * kLinC], ps_pad[32 + kLinC + 4];
   const float* ps = ps_pad + 32;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -499,7 +514,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
   for (int n = tid; n <= kLinC; n += kLinThreads) {
     const float p = expf(g * n);
-    pw[n] = p;
+    if (n < kLinC) {
+      back[kLinC - 1 - n] = p;
+      back[kLinC + n] = 0.f;
+    }
     ps_pad[32 + n] = p * a.scale;
     if (n < 32) ps_pad[n] = 0.f;
   }
@@ -513,8 +531,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // ---- K'^T of 32 columns of K, as three terms: ldmatrix.trans gives thread
   // 4 x + y tokens 2 y, 2 y + 1 (of 8) of column x of each of 4 groups of 8
   // columns.  The kTermWarps warps of these columns, of which this is number
-  // `which`, take steps of 16 tokens in turn.  `between(n)` is called after the
-  // first part of chunk n.
+  // `which`, take steps of 16 tokens in turn.  `between(n)` is called before the
+  // chunk's first part, at D = 64 after it (the state is what the others wait
+  // for: 348 against 355 us for 32,751 tokens of 32 heads; but 239 against 234
+  // at 64).
   auto form_terms = [&](int which, auto&& between) {
     const int qt = warp & 3, kx = lane >> 3;  // matrix kx: columns 32 qt + 8 kx ..
     const bool mine = 32 * qt < D;            // D = 64: the upper half has no columns
@@ -533,6 +553,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int v = min(kLinC, t1 - t0 - n * kLinC);
       const int ki = 2 * n, vi = 2 * n + 1;  // tiles of the ring
       const uint32_t kt = sb + L::kKV + (ki % L::kSlots) * L::kTile;
+      const float* decay = back + kLinC - v + 2 * (lane & 3);  // of this thread's two tokens
       ok = lin_wait_warp(kv_full + 8 * (ki % L::kSlots), (ki / L::kSlots) & 1, abort);
       if (!ok) break;
       if (v < kLinC) {
@@ -556,7 +577,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
 #pragma unroll 1
       for (int p = 0; ok && p <= T::kParts; ++p) {
-        if (p == 1) ok = between(n);
+        if (p == (D == 64 ? 1 : 0)) ok = between(n);
         if (p == T::kParts || !ok) break;
         if (m >= 2) ok = lin_wait_warp(kp_empty + 8 * (m & 1), ((m >> 1) - 1) & 1, abort);
         if (!ok) break;
@@ -571,10 +592,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             for (int q = 0; q < 2; ++q) {
               uint32_t k[4];
               ldsm_x4_t(kt + kcol + (t + 8 * q) * 128, k[0], k[1], k[2], k[3]);
-              // weights of this thread's two tokens (0 behind the last)
-              const int e = v - 1 - t - 8 * q - 2 * (lane & 3);
-              const float p0 = pw[max(e, 0)], p1 = pw[max(e - 1, 0)];
-              const uint64_t f = f2(e >= 0 ? p0 : 0.f, e >= 1 ? p1 : 0.f);
+              const uint64_t f = f2(decay[t + 8 * q], decay[t + 8 * q + 1]);
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 uint64_t y = f2_mul(f2_bf16(k[x]), f);
@@ -815,7 +833,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int qt = warp & 3, half = warp >> 2, i = 32 * qt + lane;  // row
     uint64_t col[8];  // exp(g (15 - e))
 #pragma unroll
-    for (int e = 0; e < 8; ++e) col[e] = f2(pw[15 - 2 * e], pw[14 - 2 * e]);
+    for (int e = 0; e < 8; ++e) col[e] = f2(back[112 + 2 * e], back[113 + 2 * e]);
     bool ok = true;
     int pair = 0;
     for (int n = 0; ok && n < nch; ++n)
@@ -825,8 +843,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         tc_fence_after();
         // P in place of the scores: 16 columns j of a step of the product
         // become 8 of term 0 and 8 of term 1
-        uint32_t next[16];
-        if (half <= 2 * qt + 1) tmem_ld16(my_lanes + kTmSc + 16 * half, next);
 #pragma unroll 1
         for (int st = half; st < kLinC / 16; st += 2) {
           uint32_t p[16];
@@ -836,10 +852,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             for (int e = 0; e < 16; ++e) p[e] = 0u;
           } else {
             uint32_t sc[16];
+            tmem_ld16(my_lanes + kTmSc + 16 * st, sc);
             tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sc[e] = next[e];
-            if (st + 2 <= 2 * qt + 1) tmem_ld16(my_lanes + kTmSc + 16 * st + 32, next);
             if (st < 2 * qt) {  // before every row: exp(g (d - 15)) exp(g (15 - e))
               const float rf = ps[d - 15];
 #pragma unroll
