@@ -167,12 +167,13 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // us at an SM's share of HBM.  What is left is the chain from one chunk's state
 // to the next one's (terms to shared memory, KV, its sum back) and, beside it,
 // scores, P, PV and the rows.  One prompt of 32,751 tokens and 32 heads of 128:
-// 337 us (89 for the sums of segments, 243 for the rows) against 158 for its
-// bytes; of 32,768 tokens and heads of 64, 226 against 79.  Steps that did not
+// 342 us (89 for the sums of segments, 246 for the rows) against 158 for its
+// bytes; of 32,768 tokens and heads of 64, 221 against 79.  Steps that did not
 // help: six warpgroups instead of five (300 against 265 us for the rows), other
 // forms of the waits, P's loads a step ahead, terms cut off instead of rounded
-// (391 against 348 us), K' formed before the wait for its buffer (345 against
-// 337).  Single bf16 terms of P or S would help, and are too coarse.
+// (391 against 348 us) or rounded by two fma (339 against 337), K' formed before
+// the wait for its buffer (345 against 337).  Single bf16 terms of P or S would
+// help, and are too coarse.
 // Where there are fewer (request, KV head) pairs than SMs, prompts are cut
 // into segments: a first launch sums up their own states (K and V alone; a
 // segment in `nsub` parts, as this launch has fewer CTAs), a small one joins
@@ -221,12 +222,13 @@ struct LinLayout {
   static_assert(kAlloc + kTables <= 227 * 1024, "shared memory of the prompt kernel");
 };
 
-// Bounded wait that also gives up when another role has.  (4 M tries are
-// a tenth of a second or more; the loop is kept small, since the roles' code
-// competes for the instruction caches.)
+// Bounded wait that also gives up when another role has.  (The loop is kept
+// small, since the roles' code competes for the instruction caches.)
 __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  for (uint32_t it = 0; !mbar_try_wait(bar, parity); ++it)
-    if (*abort || it >= (1u << 22)) return false;
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (*abort || global_timer_ns() - t0 > kWaitLimitNs) return false;
   return true;
 }
 

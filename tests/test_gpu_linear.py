@@ -339,7 +339,8 @@ def test_refusals():
                 lambda: phs.linear_attn_decode(q, q, q, pool, g[:1]),
                 lambda: phs.linear_attn_decode(q, q, q, pool, g, state_ids=dev([0])),
                 lambda: phs.linear_attn_decode(q[:, :, ::2], q, q, pool, g),
-                lambda: phs.linear_attn_prompt(q, q, q, dev([0, 2]), 2, pool, g, resume=dev([1, 1])),
+                lambda: phs.linear_attn_prompt(q, q, q, dev([0, 2]), 2, pool, g,
+                                               resume=dev([1, 1])),
                 lambda: phs.linear_attn_prompt(q, q, q, dev([0, 2]), 2, pool, g,
                                                out=torch.empty_like(q, dtype=torch.float32))):
         with pytest.raises(ValueError):

@@ -74,9 +74,10 @@ class Server:
         q, lq = self.bf16(n, 2 * H, D), self.bf16(n, LQ, D)
         lk, lv = self.bf16(n, LKV, D), self.bf16(n, LKV, D)
         self.lens[rows] += 1
-        out = phs.attn_decode_diff_paged(q, self.pool, self.table[rows], self.lens[rows], WIDTH * 16, self.weights,
-                                         out_dtype=torch.float32, k_new=k, v_new=v,
-                                         page_refcount=self.counts, status=self.status)
+        out = phs.attn_decode_diff_paged(q, self.pool, self.table[rows], self.lens[rows],
+                                         WIDTH * 16, self.weights, out_dtype=torch.float32,
+                                         k_new=k, v_new=v, page_refcount=self.counts,
+                                         status=self.status)
         lin = phs.linear_attn_decode(lq, lk, lv, self.states, self.decay, state_ids=dev(rows),
                                      out_dtype=torch.float32, status=self.status)
         for i, r in enumerate(rows):
