@@ -161,14 +161,13 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // small: with one warp and everything unrolled, fetching instructions was
 // the largest stall (3.1 of 10.7 warp-cycles an instruction).
 //
-// What bounds it: a chunk at D = 128 takes 3.8 us (7,200 cycles) of a CTA, in
-// which it has the tensor cores busy for 54 %, issues 0.6 instructions a cycle,
-// the integer and conversion units for 45 % of the time, and moves 128 KB, 2.9
-// us at an SM's share of HBM.  What is left is the chain from one chunk's state
+// What bounds it: a chunk at D = 128 takes 3.6 us (6,900 cycles) of a CTA, in
+// which it has the tensor cores busy for 57 %, issues 0.6 instructions a cycle,
+// and moves 128 KB, 2.9 us at an SM's share of HBM.  What is left is the chain from one chunk's state
 // to the next one's (terms to shared memory, KV, its sum back) and, beside it,
 // scores, P, PV and the rows.  One prompt of 32,751 tokens and 32 heads of 128:
-// 342 us (89 for the sums of segments, 246 for the rows) against 158 for its
-// bytes; of 32,768 tokens and heads of 64, 221 against 79.  Steps that did not
+// 323 us (85 for the sums of segments, 230 for the rows) against 158 for its
+// bytes; of 32,768 tokens and heads of 64, 207 against 79.  Steps that did not
 // help: six warpgroups instead of five (300 against 265 us for the rows), other
 // forms of the waits, P's loads a step ahead, terms cut off instead of rounded
 // (391 against 348 us) or rounded by two fma (339 against 337), K' formed before
@@ -186,11 +185,14 @@ constexpr int kLinC = kLinearChunk;
 constexpr int kLinThreads = 640;
 // registers a thread: 96 at launch, five warpgroups; 2 x 88 + 2 x 120 + 64 = 5 x 96
 constexpr int kLinRegsRows = 88, kLinRegsState = 120, kLinRegsIssue = 64;
-// Tensor-memory columns: a chunk's sum U, scores (and P), output, and two
-// buffers of K'^T, each as much of a chunk as there is room for: half, or a
-// quarter beside the rows at D = 128.  Forming the next part then runs beside
-// the product with the last.  Where there are no rows U has two buffers, and
-// a chunk's KV does not wait for the last one's sum to be taken up.
+// Tensor-memory columns: a chunk's sum U, scores (and P), output, and a ring
+// of parts of K'^T: beside the rows at D = 128 parts of 16 tokens, 5 of a
+// chunk's 8; else two of 64.  Forming the next parts runs beside the product
+// with the last.  (8 prompts of 4,096 tokens, 32 heads of 128: 250 us, against
+// 262 with two parts of 32 tokens.  One of 32,768 and heads of 64: 207 us with
+// parts of 64, 236 of 32, 261 of 16.)  Where there are no rows U has two
+// buffers, and a chunk's KV does not wait for the last one's sum to be taken
+// up.
 template <int D, bool STATES>
 struct LinTmem {
   static constexpr uint32_t kU = 0;
@@ -198,10 +200,10 @@ struct LinTmem {
   static constexpr uint32_t kOut = D == 64 ? 64 : 256;
   static constexpr uint32_t kSc = 128;
   static constexpr uint32_t kKp = STATES || D == 64 ? 256 : 384;
-  static constexpr int kParts = STATES || D == 64 ? 2 : 4;
-  static constexpr int kSteps = kLinC / 16 / kParts;  // of 16 tokens, 8 columns a term
-  static constexpr uint32_t kTerm = 8 * kSteps, kBuf = 3 * kTerm;
-  static_assert(kUBufs * D <= kKp && kKp + 2 * kBuf <= 512, "tensor memory");
+  static constexpr int kSteps = STATES || D == 64 ? 4 : 1;  // of 16 tokens
+  static constexpr uint32_t kPart = 24 * kSteps;  // a step: 3 terms of 8 columns
+  static constexpr int kRing = (512 - kKp) / kPart;
+  static_assert(kUBufs * D <= kKp, "tensor memory");
 };
 
 template <int D, bool STATES>
@@ -215,7 +217,7 @@ struct LinLayout {
   static constexpr int kS = kOut + kTile;      // 2 terms [D / 64][D rows][128 bytes]
   static constexpr int kSTerm = D * D * 2;
   static constexpr int kBar = STATES ? kQ : kS + 2 * kSTerm;
-  static constexpr int kBars = 2 * kSlots + 21;
+  static constexpr int kBars = 2 * kSlots + 2 * LinTmem<D, STATES>::kRing + 17;
   static constexpr int kMisc = kBar + kBars * 8;  // tensor-memory base, abort flag
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static constexpr int kTables = (3 * kLinC + 4 + 32) * 4;  // static: back, ps and its pad
@@ -408,6 +410,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   constexpr uint32_t kTmU = T::kU, kTmSc = T::kSc, kTmOut = T::kOut, kTmKp = T::kKp;
   constexpr int kTermWarps = 2;  // that form K' of 32 columns of K
   constexpr int kTermThreads = 128 * kTermWarps;
+  constexpr int kBefore = D == 64 ? 1 : 0;  // parts of a warp before the state, see below
   extern __shared__ uint8_t smem_raw[];
   // back[x]: the decay of token x of a whole chunk up to its last one, exp(g
   // (127 - x)), then zeros for tokens behind the last; ps[n] = scale exp(g n),
@@ -474,10 +477,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t kv_full = bar(0), kv_empty = bar(L::kSlots), q_full = bar(kB),
                  q_empty = bar(kB + 1), sc_full = bar(kB + 2), qs_done = bar(kB + 3),
                  pv_ready = bar(kB + 4), o_done = bar(kB + 5), o_free = bar(kB + 6),
-                 kp_full = bar(kB + 7), kp_empty = bar(kB + 9), s_ready = bar(kB + 11),
-                 u_done = bar(kB + 13), y_full = bar(kB + 15), y_free = bar(kB + 16),
-                 kv_all = bar(kB + 17), pv_issued = bar(kB + 18), drain = bar(kB + 19);
-  static_assert(kB + 21 == L::kBars, "barriers (the last is a pair)");
+                 s_ready = bar(kB + 7), u_done = bar(kB + 9), y_full = bar(kB + 11),
+                 y_free = bar(kB + 12), kv_all = bar(kB + 13), pv_issued = bar(kB + 14),
+                 drain = bar(kB + 15), kp_full = bar(kB + 17), kp_empty = bar(kB + 17 + T::kRing);
+  static_assert(kB + 17 + 2 * T::kRing == L::kBars, "barriers (s_ready, u_done, drain: pairs)");
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   if (warp == 16) {
     tmem_alloc(sb + L::kMisc, 512);
@@ -490,8 +493,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       // K tile, QK and one of those threads again
       mbar_init(kv_empty + 8 * i, kTermThreads + (STATES ? 1 : 2));
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(kp_full + 8 * i, kTermThreads);
+    for (int i = 0; i < T::kRing; ++i) {
+      mbar_init(kp_full + 8 * i, 128);
       mbar_init(kp_empty + 8 * i, 1);
     }
     mbar_init(y_full, 256);
@@ -533,10 +536,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // ---- K'^T of 32 columns of K, as three terms: ldmatrix.trans gives thread
   // 4 x + y tokens 2 y, 2 y + 1 (of 8) of column x of each of 4 groups of 8
   // columns.  The kTermWarps warps of these columns, of which this is number
-  // `which`, take steps of 16 tokens in turn.  `between(n)` is called before the
-  // chunk's first part, at D = 64 after it (the state is what the others wait
-  // for: 348 against 355 us for 32,751 tokens of 32 heads; but 239 against 234
-  // at 64).
+  // `which`, take parts in turn.  `between(n)` is called before the first of
+  // them, at D = 64 after it (the state is what the others wait for: 327 us for
+  // 32,751 tokens of 32 heads, 348 after the first; but 230 and 211 at 64).
   auto form_terms = [&](int which, auto&& between) {
     const int qt = warp & 3, kx = lane >> 3;  // matrix kx: columns 32 qt + 8 kx ..
     const bool mine = 32 * qt < D;            // D = 64: the upper half has no columns
@@ -546,11 +548,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       uint32_t z[16];
 #pragma unroll
       for (int c = 0; c < 16; ++c) z[c] = 0u;
-      for (uint32_t c = 0; c < 2 * T::kBuf; c += 16) tmem_st16(my_lanes + kTmKp + c, z);
+      static_assert(D == 128 || T::kRing * T::kPart % 16 == 0, "in stores of 16 columns");
+      for (uint32_t c = 0; c < T::kRing * T::kPart; c += 16) tmem_st16(my_lanes + kTmKp + c, z);
       tmem_st_wait();
     }
     bool ok = true;
-    int m = 0;
+    int place = which, turn = 0;  // in the ring, of this warp's next part
     for (int n = 0; ok && n < nch; ++n) {
       const int v = min(kLinC, t1 - t0 - n * kLinC);
       const int ki = 2 * n, vi = 2 * n + 1;  // tiles of the ring
@@ -577,18 +580,18 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       }
+      constexpr int kParts = kLinC / 16 / T::kSteps;
 #pragma unroll 1
-      for (int p = 0; ok && p <= T::kParts; ++p) {
-        if (p == (D == 64 ? 1 : 0)) ok = between(n);
-        if (p == T::kParts || !ok) break;
-        if (m >= 2) ok = lin_wait_warp(kp_empty + 8 * (m & 1), ((m >> 1) - 1) & 1, abort);
+      for (int p = which; ok && p < kParts + kTermWarps; p += kTermWarps) {
+        if (p / kTermWarps == kBefore) ok = between(n);
+        if (!ok || p >= kParts) break;
+        if (turn > 0) ok = lin_wait_warp(kp_empty + 8 * place, (turn - 1) & 1, abort);
         if (!ok) break;
         tc_fence_after();
         if (mine) {
 #pragma unroll
-          for (int i2 = 0; i2 < T::kSteps / kTermWarps; ++i2) {
-            const int st = which + i2 * kTermWarps;
-            const int t = (p * T::kSteps + st) * 16;  // first token
+          for (int st = 0; st < T::kSteps; ++st) {
+            const int t = 16 * (T::kSteps * p + st);  // first token
             uint32_t w[3][2][4];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -608,14 +611,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
               for (int x = 0; x < 2; ++x)
                 tmem_st_16x128(my_lanes + (static_cast<uint32_t>(16 * x) << 16) + kTmKp +
-                                   T::kBuf * (m & 1) + T::kTerm * i + 8 * st,
+                                   T::kPart * place + 24 * st + 8 * i,
                                w[i][x]);
           }
           tmem_st_wait();
         }
         tc_fence_before();
-        mbar_arrive(kp_full + 8 * (m & 1));
-        ++m;
+        mbar_arrive(kp_full + 8 * place);
+        if ((place += kTermWarps) >= T::kRing) {
+          place -= T::kRing;
+          ++turn;
+        }
       }
       // V's place in the ring was an earlier K's: only once V is there do all of
       // that tile's users have let go of it, and an arrival counts for V (a warp
@@ -700,7 +706,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       auto tile_full = [&](int i) { wait(kv_full + 8 * (i % L::kSlots), i / L::kSlots); };
       auto tile_empty = [&](int i) { return kv_empty + 8 * (i % L::kSlots); };
       if (warp == 16) {  // KV
-        int m = 0;       // parts
+        int place = 0, turn = 0;  // of the next part of K'
         for (int n = 0; ok && n < nch; ++n) {
           const int ub = n % T::kUBufs;
           if (!STATES)
@@ -710,21 +716,25 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           tile_full(2 * n + 1);
           uint64_t v = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
 #pragma unroll 1
-          for (int p = 0; p < T::kParts; ++p, ++m, v += T::kSteps * 2048 >> 4) {
-            wait(kp_full + 8 * (m & 1), m >> 1);
+          for (int p = 0; p < kLinC / 16; p += T::kSteps, v += T::kSteps * 2048 >> 4) {
+            wait(kp_full + 8 * place, turn);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t kp = tmem + kTmKp + T::kBuf * (m & 1);
             if (lead) {
-#pragma unroll 1
+              const uint32_t kp = tmem + kTmKp + T::kPart * place;
+#pragma unroll
               for (int t = 0; t < 3; ++t)
-#pragma unroll 2
-                for (int ks = 0; ks < T::kSteps; ++ks)
-                  umma_bf16_ts(tmem + kTmU + D * ub, kp + T::kTerm * t + 8 * ks,
-                               v + (ks * 2048 >> 4), kIdD, p > 0 || t > 0 || ks > 0);
-              umma_commit(kp_empty + 8 * (m & 1));
+#pragma unroll
+                for (int st = 0; st < T::kSteps; ++st)
+                  umma_bf16_ts(tmem + kTmU + D * ub, kp + 24 * st + 8 * t, v + (st * 2048 >> 4),
+                               kIdD, p > 0 || t > 0 || st > 0);
+              umma_commit(kp_empty + 8 * place);
             }
             __syncwarp();
+            if (++place == T::kRing) {
+              place = 0;
+              ++turn;
+            }
           }
           // (the other warp has issued the last chunk's PV, so it has waited for
           // that chunk's phase)
@@ -737,6 +747,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           __syncwarp();
         }
       } else {  // QK, QS, PV
+        // (for 32,751 tokens: 323 us at 4, 327 at 2; at D = 64 213 and 207)
+        constexpr int kIssue = D == 64 ? 2 : 4;
         // descriptors; a later part of a tile is `bytes >> 4` further on
         const uint64_t dq = sdesc_sw128(sb + L::kQ, 16, 1024);
         const uint64_t ds = sdesc_sw128(sb + L::kS, D * 128, 1024);
@@ -751,7 +763,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             tc_fence_after();
             const uint64_t k = sdesc_sw128(tile(2 * n), 16, 1024);
             if (lead) {
-#pragma unroll 2
+#pragma unroll kIssue
               for (int ks = 0; ks < D / 16; ++ks) {
                 const uint32_t at = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
                 umma_bf16(tmem + kTmSc, dq + at, k + at, kIdQK, ks > 0);
@@ -767,7 +779,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (lead) {
 #pragma unroll 1
               for (int t = 0; t < 2; ++t)
-#pragma unroll 2
+#pragma unroll kIssue
                 for (int ks = 0; ks < D / 16; ++ks)
                   umma_bf16(tmem + kTmOut, dq + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4),
                             ds + ((t * L::kSTerm + ks * 2048) >> 4), kIdD, t > 0 || ks > 0);
@@ -785,7 +797,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (lead) {
 #pragma unroll 1
               for (int t = 0; t < 2; ++t)
-#pragma unroll 2
+#pragma unroll kIssue
                 for (int ks = 0; ks < kLinC / 16; ++ks)
                   umma_bf16_ts(tmem + kTmOut, tmem + kTmSc + 16 * ks + 8 * t, v + (ks * 2048 >> 4),
                                kIdD, 1u);
