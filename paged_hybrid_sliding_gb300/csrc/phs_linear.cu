@@ -153,8 +153,8 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 //   warps 8-15  rows of the state, two threads a row, in registers: state ->
 //               two terms in shared memory, K tile -> K'^T terms
 //   warp 16     issues KV
-//   warp 17     TMA loads: a ring of K and V tiles, one Q tile
-//   warp 18     TMA stores of the output tile
+//   warp 17     TMA loads: a ring of K and V tiles, two Q tiles
+//   warp 18     TMA stores of the output tiles, in Q's place
 //   warp 19     issues QK, QS and PV
 // KV is issued before PV: its sum's way into the state then runs beside PV.
 // Two warps on each scheduler run each role's code, and its loops are kept
@@ -213,11 +213,12 @@ struct LinLayout {
   static constexpr int kSlots = STATES || D == 64 ? 6 : 3;  // K(0) V(0) K(1) V(1) ... in turn
   static constexpr int kKV = 0;
   static constexpr int kQ = kKV + kSlots * kTile;
-  static constexpr int kOut = kQ + kTile;
-  static constexpr int kS = kOut + kTile;      // 2 terms [D / 64][D rows][128 bytes]
+  // two tiles in turn, each for a pair's Q and then for its output: the next Q
+  // is loaded a pair ahead
+  static constexpr int kS = kQ + 2 * kTile;    // 2 terms [D / 64][D rows][128 bytes]
   static constexpr int kSTerm = D * D * 2;
   static constexpr int kBar = STATES ? kQ : kS + 2 * kSTerm;
-  static constexpr int kBars = 2 * kSlots + 2 * LinTmem<D, STATES>::kRing + 17;
+  static constexpr int kBars = 2 * kSlots + 2 * LinTmem<D, STATES>::kRing + 19;
   static constexpr int kMisc = kBar + kBars * 8;  // tensor-memory base, abort flag
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static constexpr int kTables = (3 * kLinC + 4 + 32) * 4;  // static: back, ps and its pad
@@ -475,12 +476,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   auto bar = [sb](int i) { return sb + L::kBar + 8 * i; };
   constexpr int kB = 2 * L::kSlots;
   const uint32_t kv_full = bar(0), kv_empty = bar(L::kSlots), q_full = bar(kB),
-                 q_empty = bar(kB + 1), sc_full = bar(kB + 2), qs_done = bar(kB + 3),
-                 pv_ready = bar(kB + 4), o_done = bar(kB + 5), o_free = bar(kB + 6),
-                 s_ready = bar(kB + 7), u_done = bar(kB + 9), y_full = bar(kB + 11),
-                 y_free = bar(kB + 12), kv_all = bar(kB + 13), pv_issued = bar(kB + 14),
-                 drain = bar(kB + 15), kp_full = bar(kB + 17), kp_empty = bar(kB + 17 + T::kRing);
-  static_assert(kB + 17 + 2 * T::kRing == L::kBars, "barriers (s_ready, u_done, drain: pairs)");
+                 y_full = bar(kB + 2), y_free = bar(kB + 4), s_ready = bar(kB + 6),
+                 u_done = bar(kB + 8), drain = bar(kB + 10), sc_full = bar(kB + 12),
+                 qs_done = bar(kB + 13), pv_ready = bar(kB + 14), o_done = bar(kB + 15),
+                 o_free = bar(kB + 16), kv_all = bar(kB + 17), pv_issued = bar(kB + 18),
+                 kp_full = bar(kB + 19), kp_empty = bar(kB + 19 + T::kRing);
+  static_assert(kB + 19 + 2 * T::kRing == L::kBars, "barriers (the first six: pairs)");
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   if (warp == 16) {
     tmem_alloc(sb + L::kMisc, 512);
@@ -497,10 +498,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       mbar_init(kp_full + 8 * i, 128);
       mbar_init(kp_empty + 8 * i, 1);
     }
-    mbar_init(y_full, 256);
-    mbar_init(y_free, 1);
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 1);
+      mbar_init(y_full + 8 * i, 256);
+      mbar_init(y_free + 8 * i, 1);
+    }
     mbar_init(sc_full, 1);
     mbar_init(qs_done, 1);
     mbar_init(pv_ready, 256);
@@ -665,10 +667,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           ++tiles;
         };
         auto load_q = [&](int gq, int t) {
-          if (nq >= 1) ok = ok && lin_wait(q_empty, (nq - 1) & 1, abort);
+          const int at = nq & 1;
+          if (nq >= 2) ok = ok && lin_wait(y_free + 8 * at, ((nq >> 1) - 1) & 1, abort);
           if (!ok) return;
-          mbar_arrive_expect_tx(q_full, L::kTile);
-          load(&tq, sb + L::kQ, head0 + gq, t, q_full);
+          mbar_arrive_expect_tx(q_full + 8 * at, L::kTile);
+          load(&tq, sb + L::kQ + at * L::kTile, head0 + gq, t, q_full + 8 * at);
           ++nq;
         };
         for (int n = 0; ok && n < nch; ++n) {
@@ -686,7 +689,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         // copies still in flight land before the CTA ends
         for (int i = max(0, tiles - L::kSlots); i < tiles; ++i)
           (void)mbar_wait(kv_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1);
-        if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
+        for (int i = max(0, nq - 2); i < nq; ++i)
+          (void)mbar_wait(q_full + 8 * (i & 1), (i >> 1) & 1);
       }
     } else if (warp == 16 || (!STATES && warp == 19)) {
       // ----------------------------------------------------------- products
@@ -750,14 +754,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         // (for 32,751 tokens: 323 us at 4, 327 at 2; at D = 64 213 and 207)
         constexpr int kIssue = D == 64 ? 2 : 4;
         // descriptors; a later part of a tile is `bytes >> 4` further on
-        const uint64_t dq = sdesc_sw128(sb + L::kQ, 16, 1024);
+        const uint64_t dq0 = sdesc_sw128(sb + L::kQ, 16, 1024);
         const uint64_t ds = sdesc_sw128(sb + L::kS, D * 128, 1024);
         int pair = 0;
         for (int n = 0; ok && n < nch; ++n)
           for (int gq = 0; ok && gq < G; ++gq, ++pair) {
             const bool last = gq == G - 1;
             if (gq == 0) tile_full(2 * n);
-            wait(q_full, pair);
+            wait(q_full + 8 * (pair & 1), pair >> 1);
+            const uint64_t dq = dq0 + (pair & 1) * (L::kTile >> 4);
             if (pair >= 1) wait(o_done, pair - 1);  // P of the last pair is read
             if (!ok) break;
             tc_fence_after();
@@ -784,7 +789,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                   umma_bf16(tmem + kTmOut, dq + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4),
                             ds + ((t * L::kSTerm + ks * 2048) >> 4), kIdD, t > 0 || ks > 0);
               umma_commit(qs_done);
-              umma_commit(q_empty);
               if (last) umma_commit(u_done);  // the state's terms have been read
             }
             __syncwarp();
@@ -822,17 +826,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     } else if (warp == 18) {
       // --------------------------------------------- whole output tiles out
       if (!STATES && lane == 0) {
-        const int whole = (t1 - t0) / kLinC * G;
+        const int whole = (t1 - t0) / kLinC * G;  // (the others' rows are stored by the threads)
         bool ok = true;
-        for (int p = 0; ok && p < whole; ++p) {
-          ok = lin_wait(y_full, p & 1, abort);
+        for (int p = 0; ok && p < nch * G; ++p) {
+          ok = lin_wait(y_full + 8 * (p & 1), (p >> 1) & 1, abort);
           if (!ok) break;
-          for (int hf = 0; hf < D / 64; ++hf)
-            tma_store_2d(&to, sb + L::kOut + hf * L::kHalf, (head0 + p % G) * D + 64 * hf,
-                         t0 + p / G * kLinC);
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          mbar_arrive(y_free);
+          if (p < whole) {
+            for (int hf = 0; hf < D / 64; ++hf)
+              tma_store_2d(&to, sb + L::kQ + (p & 1) * L::kTile + hf * L::kHalf,
+                           (head0 + p % G) * D + 64 * hf, t0 + p / G * kLinC);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          }
+          mbar_arrive(y_free + 8 * (p & 1));
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!ok) {
@@ -914,11 +920,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         // rows behind a last token are another request's
         const int t = t0 + n * kLinC + i;
         const bool whole = t0 + (n + 1) * kLinC <= t1;
-        ok = lin_wait_warp(o_done, pair & 1, abort) &&
-             (!whole || pair == 0 || lin_wait_warp(y_free, (pair - 1) & 1, abort));
+        ok = lin_wait_warp(o_done, pair & 1, abort);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t row = sb + L::kOut + i * 128;
+        const uint32_t row = sb + L::kQ + (pair & 1) * L::kTile + i * 128;
         uint4* to_row = reinterpret_cast<uint4*>(
             reinterpret_cast<__nv_bfloat16*>(a.out) +
             (static_cast<size_t>(t) * a.Hq + head0 + gq) * D);
@@ -942,10 +947,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(o_free);
-        if (whole) {
-          fence_proxy_async_smem();
-          mbar_arrive(y_full);
-        }
+        if (whole) fence_proxy_async_smem();
+        mbar_arrive(y_full + 8 * (pair & 1));
       }
     if (!ok) {
       set_status(a.status, PHS_ETIMEOUT);
