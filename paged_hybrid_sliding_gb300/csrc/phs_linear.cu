@@ -161,18 +161,19 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // small: with one warp and everything unrolled, fetching instructions was
 // the largest stall (3.1 of 10.7 warp-cycles an instruction).
 //
-// What bounds it: a chunk at D = 128 takes 3.6 us (6,900 cycles) of a CTA, in
-// which it has the tensor cores busy for 57 %, issues 0.6 instructions a cycle,
+// What bounds it: a chunk at D = 128 takes 3.5 us (6,600 cycles) of a CTA, in
+// which it has the tensor cores busy for 59 %, issues 0.6 instructions a cycle,
 // and moves 128 KB, 2.9 us at an SM's share of HBM.  What is left is the chain from one chunk's state
 // to the next one's (terms to shared memory, KV, its sum back) and, beside it,
 // scores, P, PV and the rows.  One prompt of 32,751 tokens and 32 heads of 128:
-// 323 us (85 for the sums of segments, 230 for the rows) against 158 for its
+// 313 us (85 for the sums of segments, 220 for the rows) against 158 for its
 // bytes; of 32,768 tokens and heads of 64, 207 against 79.  Steps that did not
 // help: six warpgroups instead of five (300 against 265 us for the rows), other
-// forms of the waits, P's loads a step ahead, terms cut off instead of rounded
-// (391 against 348 us) or rounded by two fma (339 against 337), K' formed before
-// the wait for its buffer (345 against 337).  Single bf16 terms of P or S would
-// help, and are too coarse.
+// forms of the waits, one arrival for a warp instead of its threads' (331
+// against 321), P's loads a step ahead, terms cut off instead of rounded (391
+// against 348) or rounded by two fma (339 against 337), K' formed before the
+// wait for its buffer (345 against 337), PV not held behind KV (326 against
+// 321).  Single bf16 terms of P or S would help, and are too coarse.
 // Where there are fewer (request, KV head) pairs than SMs, prompts are cut
 // into segments: a first launch sums up their own states (K and V alone; a
 // segment in `nsub` parts, as this launch has fewer CTAs), a small one joins
@@ -535,6 +536,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + L::kMisc), 0);
   const uint32_t my_lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
 
+  // parts of a chunk whose places in the ring are free when the state is there
+  constexpr int kKnownFree = !STATES && kBefore == 0 ? T::kRing : 0;
+
   // ---- K'^T of 32 columns of K, as three terms: ldmatrix.trans gives thread
   // 4 x + y tokens 2 y, 2 y + 1 (of 8) of column x of each of 4 groups of 8
   // columns.  The kTermWarps warps of these columns, of which this is number
@@ -587,7 +591,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       for (int p = which; ok && p < kParts + kTermWarps; p += kTermWarps) {
         if (p / kTermWarps == kBefore) ok = between(n);
         if (!ok || p >= kParts) break;
-        if (turn > 0) ok = lin_wait_warp(kp_empty + 8 * place, (turn - 1) & 1, abort);
+        // (a wait costs 100 cycles even where it has nothing to wait for: what
+        // the last chunk had in the ring is known to be read once its sum is there)
+        if (turn > 0 && p >= kKnownFree)
+          ok = lin_wait_warp(kp_empty + 8 * place, (turn - 1) & 1, abort);
         if (!ok) break;
         tc_fence_after();
         if (mine) {
@@ -713,11 +720,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         int place = 0, turn = 0;  // of the next part of K'
         for (int n = 0; ok && n < nch; ++n) {
           const int ub = n % T::kUBufs;
+          tile_full(2 * n + 1);
           if (!STATES)
             wait(s_ready, n);
           else if (n >= 2)  // the sum two chunks ago has been taken up
             wait(s_ready + 8 * ub, n / 2 - 1);
-          tile_full(2 * n + 1);
           uint64_t v = sdesc_sw128(tile(2 * n + 1), L::kHalf, 1024);
 #pragma unroll 1
           for (int p = 0; p < kLinC / 16; p += T::kSteps, v += T::kSteps * 2048 >> 4) {
