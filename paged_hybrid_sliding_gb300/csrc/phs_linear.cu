@@ -166,7 +166,7 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // and moves 128 KB, 2.9 us at an SM's share of HBM.  What is left is the chain from one chunk's state
 // to the next one's (terms to shared memory, KV, its sum back) and, beside it,
 // scores, P, PV and the rows.  One prompt of 32,751 tokens and 32 heads of 128:
-// 313 us (85 for the sums of segments, 220 for the rows) against 158 for its
+// 313 us (77 for the sums of segments, 231 for the rows) against 158 for its
 // bytes; of 32,768 tokens and heads of 64, 207 against 79.  Steps that did not
 // help: six warpgroups instead of five (300 against 265 us for the rows), other
 // forms of the waits, one arrival for a warp instead of its threads' (331
@@ -1089,34 +1089,45 @@ __global__ void __launch_bounds__(128) phs_linear_join_kernel(const LinearArgs a
   const int small = chunks / parts, rest = chunks % parts;  // a part: so many chunks, or one more
   const float g0 = a.log_decay[h], g = g0 < -1e4f ? -1e4f : g0;
   const float keep0 = expm1f(g * (small * kLinC)), keep1 = expm1f(g * ((small + 1) * kLinC));
-  for (int i = blockIdx.z * 128 + threadIdx.x; i < vecs; i += gridDim.z * 128) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.resume && a.resume[b] != 0)
-      s = reinterpret_cast<const float4*>(a.state)[(id * a.Hkv + h) * vecs + i];
-    float4* at = reinterpret_cast<float4*>(a.ws) +
-                 (static_cast<size_t>(b) * a.Hkv + h) * parts * vecs + i;
-    const int sums = parts - a.nsub;  // the last segment has none
-    int frac = 0, sub = 0;            // part_chunk's fraction; number of the part in its segment
-    for (int n = 0; n <= sums; n += 8) {
-      float4 x[8];
-      bool more[8], sum[8];  // of small + 1 chunks; not empty
+  if (parts == 1) {  // nothing to join: a copy for the groups of heads, 4 loads at once
+    if (!a.resume || a.resume[b] == 0) return;
+    const float4* from = reinterpret_cast<const float4*>(a.state) + (id * a.Hkv + h) * vecs;
+    float4* to = reinterpret_cast<float4*>(a.ws) + (static_cast<size_t>(b) * a.Hkv + h) * vecs;
+    const int i0 = blockIdx.z * 512 + threadIdx.x;
+    float4 x[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        frac += rest;
-        more[j] = frac >= parts;
-        if (more[j]) frac -= parts;
-        sum[j] = n + j < sums && (small > 0 || more[j]);
-        if (sum[j]) x[j] = at[static_cast<size_t>(n + j) * vecs];
-      }
+    for (int j = 0; j < 4; ++j) x[j] = from[i0 + 128 * j];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (n + j <= sums && sub == 0) at[static_cast<size_t>(n + j) * vecs] = s;
-        if (++sub == a.nsub) sub = 0;
-        if (sum[j]) {
-          const float k = more[j] ? keep1 : keep0;
-          s = make_float4(decayed(s.x, k) + x[j].x, decayed(s.y, k) + x[j].y,
-                          decayed(s.z, k) + x[j].z, decayed(s.w, k) + x[j].w);
-        }
+    for (int j = 0; j < 4; ++j) to[i0 + 128 * j] = x[j];
+    return;
+  }
+  const int i = blockIdx.z * 128 + threadIdx.x;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.resume && a.resume[b] != 0)
+    s = reinterpret_cast<const float4*>(a.state)[(id * a.Hkv + h) * vecs + i];
+  float4* at = reinterpret_cast<float4*>(a.ws) +
+               (static_cast<size_t>(b) * a.Hkv + h) * parts * vecs + i;
+  const int sums = parts - a.nsub;  // the last segment has none
+  int frac = 0, sub = 0;            // part_chunk's fraction; number of the part in its segment
+  for (int n = 0; n <= sums; n += 8) {
+    float4 x[8];
+    bool more[8], sum[8];  // of small + 1 chunks; not empty
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      frac += rest;
+      more[j] = frac >= parts;
+      if (more[j]) frac -= parts;
+      sum[j] = n + j < sums && (small > 0 || more[j]);
+      if (sum[j]) x[j] = at[static_cast<size_t>(n + j) * vecs];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (n + j <= sums && sub == 0) at[static_cast<size_t>(n + j) * vecs] = s;
+      if (++sub == a.nsub) sub = 0;
+      if (sum[j]) {
+        const float k = more[j] ? keep1 : keep0;
+        s = make_float4(decayed(s.x, k) + x[j].x, decayed(s.y, k) + x[j].y,
+                        decayed(s.z, k) + x[j].z, decayed(s.w, k) + x[j].w);
       }
     }
   }
@@ -1149,8 +1160,7 @@ static int launch_linear_prompt_t(const CUtensorMap& tq, const CUtensorMap& tk,
     cfg.numAttrs = 1;
   }
   if (err == cudaSuccess && (a.nseg > 1 || (a.ngrp > 1 && a.resume))) {
-    // (nothing to join: a copy, by fewer CTAs)
-    cfg.gridDim = dim3(a.B, a.Hkv, D * D / (a.nseg > 1 ? 512 : 2048));
+    cfg.gridDim = dim3(a.B, a.Hkv, D * D / (a.nseg > 1 ? 512 : 2048));  // (1 or 4 vectors a thread)
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
     err = cudaLaunchKernelEx(&cfg, phs_linear_join_kernel, a, D * D / 4);
