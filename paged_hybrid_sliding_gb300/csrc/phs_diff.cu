@@ -420,7 +420,10 @@ __global__ void __launch_bounds__(kDiffMergeWarps * 32)
   __shared__ float sO[NW][2][2 * D], sM[NW][2], sL[NW][2];
   const int b = blockIdx.x, i = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = max(0, min(a.seq_lens[b], a.n_clamp)), ns = (n + a.T - 1) / a.T;
-  if (ns <= 1) return;
+  if (ns <= 1) {  // (this grid must not end before the one in front of it)
+    pdl_wait_prior_grid();
+    return;
+  }
   const float lambda = warp == 0 ? diff_lambda<D>(a, i, lane) : 0.f;
   const int j = i / a.G;
   const size_t row0 = (static_cast<size_t>(b) * a.Hv + j) * a.max_splits * a.G + i % a.G;

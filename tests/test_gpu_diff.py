@@ -163,6 +163,35 @@ def test_side_stream_and_graph():
         check(out, pool, q, bt, np.array([650, 20]), w)
 
 
+def test_what_follows_a_call_of_one_split_waits_for_it():
+    """Where no request is split the second launch has nothing to do, and must
+    not let the next work of a stream or graph start before the first is done."""
+    pool, q, bt, lens, w = make([4000, 3500, 3999], 4, 2, 128, 9)
+    args = (q, pool, dev(bt), dev(lens), 4096, w)
+    kw = dict(out_dtype=torch.float32, tokens_per_split=4096)
+    want = phs.attn_decode_diff_paged(*args, **kw)
+    need = phs.diff_workspace_bytes(3, 4, 2, 128, 4096, 4096)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out, copy = torch.empty_like(want), torch.empty_like(want)
+
+    def step():
+        out.zero_()
+        phs.attn_decode_diff_paged(*args, out=out, workspace=ws, **kw)
+        copy.copy_(out)
+
+    step()
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(5):
+        copy.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want)
+
+
 def test_refusals():
     pool, q, bt, lens, w = make([40], 4, 2, 64, 13)
     a = (dev(bt), dev(lens), 40)
