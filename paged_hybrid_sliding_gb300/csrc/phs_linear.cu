@@ -151,7 +151,8 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 //   warps 0-7   rows of the chunk, two threads a row: scores -> P, the
 //               inter-chunk part scaled, the output rows
 //   warps 8-15  rows of the state, two threads a row, in registers: state ->
-//               two terms in shared memory, K tile -> K'^T terms
+//               two terms in shared memory, K tile -> K'^T terms (by warps 0-7
+//               where only sums are formed, which have no rows)
 //   warp 16     issues KV
 //   warp 17     TMA loads: a ring of K and V tiles, two Q tiles
 //   warp 18     TMA stores of the output tiles, in Q's place
@@ -163,25 +164,26 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 //
 // What bounds it: a chunk at D = 128 takes 3.5 us (6,600 cycles) of a CTA, in
 // which it has the tensor cores busy for 59 %, issues 0.6 instructions a cycle,
-// and moves 128 KB, 2.9 us at an SM's share of HBM.  What is left is the chain from one chunk's state
-// to the next one's (terms to shared memory, KV, its sum back) and, beside it,
-// scores, P, PV and the rows.  One prompt of 32,751 tokens and 32 heads of 128:
-// 313 us (77 for the sums of segments, 231 for the rows) against 158 for its
-// bytes; of 32,768 tokens and heads of 64, 207 against 79.  Steps that did not
-// help: six warpgroups instead of five (300 against 265 us for the rows), other
-// forms of the waits, one arrival for a warp instead of its threads' (331
-// against 321), P's loads a step ahead, terms cut off instead of rounded (391
-// against 348) or rounded by two fma (339 against 337), K' formed before the
-// wait for its buffer (345 against 337), PV not held behind KV (326 against
-// 321).  Single bf16 terms of P or S would help, and are too coarse.
+// and moves 128 KB, 2.9 us at an SM's share of HBM.  What is left is the chain
+// from one chunk's state to the next one's (terms to shared memory, K' and KV,
+// its sum back) and, beside it, scores, P, PV and the rows.  One prompt of
+// 32,751 tokens and 32 heads of 128: 313 us (77 for the sums of segments, 231
+// for the rows) against 158 for its bytes; of 32,768 tokens and heads of 64, 207
+// against 79.  Steps that did not help: six warpgroups instead of five (300
+// against 265 us for the rows), other forms of the waits, one arrival for a
+// warp instead of its threads' (331 against 321), P's loads a step ahead, terms
+// cut off instead of rounded (391 against 348) or rounded by two fma (339
+// against 337), K' formed before the wait for its buffer (345 against 337), PV
+// not held behind KV (326 against 321), fewer parts of K' for a last chunk (325
+// against 310).  Single bf16 terms of P or S would help, and are too coarse.
+//
 // Where there are fewer (request, KV head) pairs than SMs, prompts are cut
 // into segments: a first launch sums up their own states (K and V alone; a
 // segment in `nsub` parts, as this launch has fewer CTAs), a small one joins
 // these sums into the states that the segments start from, and the last one
-// forms the rows.  Where SMs are left, a group's
-// query heads go to several CTAs (`ngrp`), each of which forms the states for
-// itself.  As the pool's state is overwritten by one of these CTAs, they all
-// start from a copy.
+// forms the rows.  Where SMs are left, a group's query heads go to several
+// CTAs (`ngrp`), each of which forms the states for itself.  As the pool's
+// state is overwritten by one of these CTAs, they all start from a copy.
 constexpr int kLinC = kLinearChunk;
 constexpr int kLinThreads = 640;
 // registers a thread: 96 at launch, five warpgroups; 2 x 88 + 2 x 120 + 64 = 5 x 96
