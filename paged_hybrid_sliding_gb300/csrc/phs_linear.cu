@@ -571,12 +571,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       if (!ok) break;
       if (v < kLinC) {
         // rows behind the last token: no 0 * NaN.  K: what this warp reads
-        // itself (QK may read either; those scores are masked); V: all.
+        // itself, its own parts' rows, since nothing orders it with the others
+        // here (QK may read either; those scores are masked); V: all.
         ok = lin_wait_warp(kv_full + 8 * (vi % L::kSlots), (vi / L::kSlots) & 1, abort);
         if (!ok) break;
         const uint32_t vt = sb + L::kKV + (vi % L::kSlots) * L::kTile;
         for (int t = v + (lane >> 2); mine && t < kLinC; t += 8)
-          if ((t >> 4) % kTermWarps == which)
+          if (t / (16 * T::kSteps) % kTermWarps == which)
             sts128(kt + (qt >> 1) * L::kHalf + t * 128 +
                        ((((4 * (qt & 1) + (lane & 3)) ^ t) & 7) << 4),
                    0, 0, 0, 0);
