@@ -67,7 +67,8 @@ __device__ __forceinline__ void finish_head(const DiffArgs& a, int b, int i, flo
                                             const float (&o)[2][D / 16], const float (&l)[2],
                                             int lane) {
   constexpr int V = D / 16;
-  const float i1 = l[0] > 0.f ? 1.f / l[0] : 0.f, i2 = l[1] > 0.f ? lambda / l[1] : 0.f;
+  // (a sum of NaN scores is NaN, and so is the row)
+  const float i1 = l[0] == 0.f ? 0.f : 1.f / l[0], i2 = l[1] == 0.f ? 0.f : lambda / l[1];
   float x[V];
 #pragma unroll
   for (int c = 0; c < V; ++c) x[c] = o[0][c] * i1 - o[1][c] * i2;
@@ -462,7 +463,11 @@ __global__ void __launch_bounds__(kDiffMergeWarps * 32)
       float top = M[m];
 #pragma unroll
       for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u][m].x);
-      if (top == -INFINITY) continue;  // nothing attended so far
+      if (top == -INFINITY) {  // nothing attended so far, or NaN scores alone
+#pragma unroll
+        for (int u = 0; u < U; ++u) l[m] += ml[u][m].y;  // zeros, or NaN
+        continue;
+      }
       const float keep = exp2f(M[m] - top);
       l[m] *= keep;
 #pragma unroll
