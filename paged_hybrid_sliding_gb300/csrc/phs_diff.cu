@@ -77,10 +77,10 @@ __device__ __forceinline__ void finish_head(const DiffArgs& a, int b, int i, flo
 #pragma unroll
     for (int c = 0; c < V; ++c) sq = fmaf(x[c], x[c], sq);
     sq = warp_sum(sq);
-    const float f = (1.f - a.lambda_init) / sqrtf(sq / (2 * D) + a.norm_eps);
+    const float mean = sq / (2 * D) + a.norm_eps;
+    const float f = mean == 0.f ? 0.f : (1.f - a.lambda_init) / sqrtf(mean);  // eps may be 0
 #pragma unroll
-    for (int c = 0; c < V; ++c)
-      x[c] = sq == 0.f ? 0.f : x[c] * f * __ldg(a.norm_weight + V * lane + c);  // eps may be 0
+    for (int c = 0; c < V; ++c) x[c] = x[c] * f * __ldg(a.norm_weight + V * lane + c);
   }
   const size_t at = (static_cast<size_t>(b) * a.H + i) * 2 * D + V * lane;
   if (a.out_f32) {

@@ -1,10 +1,11 @@
-"""Differential attention decode with values that are not finite."""
+"""Differential attention decode with values that are not finite, or hardly
+above zero."""
 import pytest
 import torch
 
 import paged_hybrid_sliding_gb300 as phs
 from gpu_util import dev
-from test_gpu_diff import make
+from test_gpu_diff import check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,20 @@ def test_a_nan_key_gives_nan_however_the_request_is_split(tps):
     out = phs.attn_decode_diff_paged(q, pool, dev(bt), dev(lens), 700, w, **kw)
     assert torch.isnan(out[0, 2:]).all()
     assert torch.equal(out[0, :2], want[0, :2]) and torch.equal(out[1], want[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [9, 500])
+def test_norm_of_rows_whose_squares_underflow(D, n):
+    """Values of 2^-85: their squares are zero in fp32, they themselves are not,
+    and the root of eps is what the norm divides by."""
+    pool, q, bt, lens, w = make([n], 4, 2, D, 23)
+    pool.v.mul_(2.0**-85)
+    out = phs.attn_decode_diff_paged(q, pool, dev(bt), dev(lens), n, w, out_dtype=torch.float32)
+    check(out, pool, q, bt, lens, w)
+    assert bool((out != 0).any())
+    # with eps 0 and no value at all the row is zero
+    pool.v.zero_()
+    w.norm_eps = 0.0
+    out = phs.attn_decode_diff_paged(q, pool, dev(bt), dev(lens), n, w, out_dtype=torch.float32)
+    assert not out.any()
