@@ -40,7 +40,7 @@ struct PageForkArgs {
   int32_t* first_dst;  // [num_rows] first entry that names the row as its destination
   int32_t* is_src;     // [num_rows]
   int32_t* rank;       // [n] rank among the entries that need a fresh page, -1 none, -2 refused
-  int32_t* fresh;      // [n] the lowest free pages, ascending
+  int32_t* fresh;      // [n] the pages given out: the lowest free ones, ascending, then INT32_MAX
   int32_t* copy_src;   // [n] page to copy, or -1
   int32_t* copy_dst;   // [n]
   int share_ctas;

@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(1024) phs_pages_fork_plan_kernel(const PageFor
         a.fresh[found + rank[k]] = static_cast<int32_t>(base + tile_id(k));
     found += total;
   }
+  for (int i = min(found, need) + tid; i < a.n; i += 1024) a.fresh[i] = INT32_MAX;
   __syncthreads();
   for (int i = tid; i < a.n; i += 1024) {
     const int rank = a.rank[i];
@@ -233,6 +234,22 @@ int launch_pages_fork_plan(const PageForkArgs& a, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? PHS_OK : PHS_ECUDA;
 }
 
+// Whether the plan has given out page pg: it then counts 1, as a live page may,
+// but an entry that names it named no live page.  (fresh: n ids, ascending.)
+__device__ __forceinline__ bool given_out(const int32_t* fresh, int n, int pg) {
+  int lo = 0;
+  for (int len = n; len > 0;) {
+    const int half = len >> 1;
+    if (fresh[lo + half] < pg) {
+      lo += half + 1;
+      len -= half + 1;
+    } else {
+      len = half;
+    }
+  }
+  return lo < n && fresh[lo] == pg;
+}
+
 // Share and copy, side by side in one launch: CTAs [0, n) write a child's
 // table row and add a reference on each whole page, the others copy the
 // partly filled pages.  192 children, 10 layers, 234 MB read and written: 27 us
@@ -253,7 +270,8 @@ __global__ void __launch_bounds__(256) phs_pages_fork_kernel(const __grid_consta
   for (int j = threadIdx.x; j < n / kPage; j += blockDim.x) {
     const int pg = from[j];
     to[j] = pg;
-    if (pg < 0 || pg >= a.num_pages || a.refcount[pg] <= 0)
+    const int count = pg < 0 || pg >= a.num_pages ? 0 : a.refcount[pg];
+    if (count <= 0 || (count == 1 && given_out(a.fresh, a.n, pg)))
       set_status(a.status, PHS_ERANGE);
     else
       atomicAdd(a.refcount + pg, 1);
