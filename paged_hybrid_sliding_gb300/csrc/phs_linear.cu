@@ -11,10 +11,20 @@
 
 namespace phs {
 
-// exp(g) s as s + (exp(g) - 1) s: the rounding of exp(g) itself, off by up to
-// 2^-25, would come back in every step and grow with the memory of the head
-// (a rate of 2e-4 holds 5,000 tokens: 1.5e-4 of the state).
-__device__ __forceinline__ float decayed(float s, float expm1_g) { return fmaf(s, expm1_g, s); }
+// A state's decay over some tokens whose log decays add up to x, as one factor.
+// Small ones (-1/2 < x <= 0) as exp(x) - 1, of negative sign, and the state as s +
+// factor s: the rounding of exp(x) itself, off by up to 2^-25, would come back in
+// every step and grow with the memory of the head (a rate of 2e-4 holds 5,000
+// tokens: 1.5e-4 of the state).  Strong ones as exp(x): there the rounding of
+// exp(x) - 1, off by up to 2^-25 too, would be more than what is left (10 % of it
+// at x = -15).
+__device__ __forceinline__ float decay_factor(float x) {
+  return x > -0.5f && x <= 0.f ? copysignf(expm1f(x), -1.f) : expf(x);
+}
+__device__ __forceinline__ bool is_small_decay(float factor) { return signbit(factor); }
+__device__ __forceinline__ float decayed(float s, float factor) {
+  return fmaf(s, factor, is_small_decay(factor) ? s : 0.f);
+}
 
 // The state of request b, or -1 where it has none: a negative id (an
 // inactive request), one outside the pool, or one that an earlier request
@@ -76,7 +86,7 @@ __global__ void __launch_bounds__(256) phs_linear_decode_kernel(const LinearArgs
   v.y = __bfloat162float(a.v[krow + 4 * c + 1]);
   v.z = __bfloat162float(a.v[krow + 4 * c + 2]);
   v.w = __bfloat162float(a.v[krow + 4 * c + 3]);
-  const float decay = expm1f(a.log_decay[h]);
+  const float decay = decay_factor(a.log_decay[h]);
   float4* S = reinterpret_cast<float4*>(a.state + (id * a.Hkv + h) * D * D);
   __syncthreads();
   float4 o[GM];
@@ -224,7 +234,7 @@ struct LinLayout {
   static constexpr int kBars = 2 * kSlots + 2 * LinTmem<D, STATES>::kRing + 19;
   static constexpr int kMisc = kBar + kBars * 8;  // tensor-memory base, abort flag
   static constexpr int kAlloc = kMisc + 16 + 1024;
-  static constexpr int kTables = (3 * kLinC + 4 + 32) * 4;  // static: back, ps and its pad
+  static constexpr int kTables = (3 * kLinC + 4 + 32 + 2) * 4;  // static: back, ps and its pad, factors
   static_assert(kAlloc + kTables <= 227 * 1024, "shared memory of the prompt kernel");
 };
 
@@ -420,6 +430,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // (127 - x)), then zeros for tokens behind the last; ps[n] = scale exp(g n),
   // read from n = -31 on (unused there)
   __shared__ float back[2 * kLinC], ps_pad[32 + kLinC + 4];
+  __shared__ float factors[2];  // decay factors of a whole chunk and of the last one
   const float* ps = ps_pad + 32;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -531,6 +542,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     ps_pad[32 + n] = p * a.scale;
     if (n < 32) ps_pad[n] = 0.f;
   }
+  // (by threads that have no part in the tables)
+  if (tid == 160) factors[0] = decay_factor(g * kLinC);
+  if (tid == 192) factors[1] = decay_factor(g * (t1 - t0 - (nch - 1) * kLinC));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1001,20 +1015,20 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
     }
     bool ok = true;
-    const float keep_chunk = expm1f(g * kLinC);
+    const float chunk_decay = factors[0], last_decay = factors[1];
     // S <- state after chunk n (n >= 0), and where `terms` its two terms to
     // shared memory for the next chunk's QS (the last one has read its own
     // by then: the chunk's sum was issued after it)
     auto next_state = [&](int n, bool terms) {
-      uint64_t keep = 0ull;
       const int ub = n >= 0 ? n % T::kUBufs : 0;
+      const float d = n == nch - 1 ? last_decay : chunk_decay;
+      const uint64_t factor = f2(d, d);
+      const float one = is_small_decay(d) ? 1.f : 0.f;
+      const uint64_t base = f2(one, one);
       if (n >= 0) {
         ok = ok && lin_wait_warp(u_done + 8 * ub, n / T::kUBufs & 1, abort);
         if (!ok) return;
         tc_fence_after();
-        const int v = min(kLinC, t1 - t0 - n * kLinC);
-        const float k = v == kLinC ? keep_chunk : expm1f(g * v);
-        keep = f2(k, k);
       }
       if (mine) {
         const uint32_t my_row = sb + L::kS + r * 128;
@@ -1026,8 +1040,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              S[16 * c + e] = f2_add(f2_fma(S[16 * c + e], keep, S[16 * c + e]),
-                                     f2(u[2 * e], u[2 * e + 1]));
+              // (the first is a shorter way from the sum to the state, the second
+              // fewer instructions: 311 and 317 us for 32,751 tokens of 32 heads of
+              // 128, 213 and 210 at 64)
+              if constexpr (D == 128)
+                S[16 * c + e] = f2_add(f2_fma(S[16 * c + e], factor, f2_mul(S[16 * c + e], base)),
+                                       f2(u[2 * e], u[2 * e + 1]));
+              else
+                S[16 * c + e] = f2_fma(S[16 * c + e], factor,
+                                       f2_fma(S[16 * c + e], base, f2(u[2 * e], u[2 * e + 1])));
           }
           if (terms) {
 #pragma unroll
@@ -1086,12 +1107,13 @@ __global__ void __launch_bounds__(128) phs_linear_join_kernel(const LinearArgs a
   const int64_t id = request_state(a, b);
   int t0, t1;
   const bool good = request_tokens(a, b, t0, t1) && id >= 0;
-  pdl_wait_prior_grid();
-  if (!good) return;
-  const int chunks = (t1 - t0 + kLinC - 1) / kLinC, parts = a.nseg * a.nsub;
+  const int chunks = good ? (t1 - t0 + kLinC - 1) / kLinC : 0, parts = a.nseg * a.nsub;
   const int small = chunks / parts, rest = chunks % parts;  // a part: so many chunks, or one more
   const float g0 = a.log_decay[h], g = g0 < -1e4f ? -1e4f : g0;
-  const float keep0 = expm1f(g * (small * kLinC)), keep1 = expm1f(g * ((small + 1) * kLinC));
+  const float decay0 = decay_factor(g * (small * kLinC));
+  const float decay1 = decay_factor(g * ((small + 1) * kLinC));
+  pdl_wait_prior_grid();
+  if (!good) return;
   if (parts == 1) {  // nothing to join: a copy for the groups of heads, 4 loads at once
     if (!a.resume || a.resume[b] == 0) return;
     const float4* from = reinterpret_cast<const float4*>(a.state) + (id * a.Hkv + h) * vecs;
@@ -1128,7 +1150,7 @@ __global__ void __launch_bounds__(128) phs_linear_join_kernel(const LinearArgs a
       if (n + j <= sums && sub == 0) at[static_cast<size_t>(n + j) * vecs] = s;
       if (++sub == a.nsub) sub = 0;
       if (sum[j]) {
-        const float k = more[j] ? keep1 : keep0;
+        const float k = more[j] ? decay1 : decay0;
         s = make_float4(decayed(s.x, k) + x[j].x, decayed(s.y, k) + x[j].y,
                         decayed(s.z, k) + x[j].z, decayed(s.w, k) + x[j].w);
       }

@@ -84,3 +84,61 @@ def test_a_chunk_of_bad_rows_behind_a_prompt_in_segments(D, n):
     r, S, bo, bs = reference(q[:n], k[:n], v[:n], start, g)
     close(out[:n], r, bo, "out")
     close(pool.s[0], S, bs, "state")
+
+
+# A state that strongly decays is exp(g n) of itself, not what is left of it after
+# 1 - (1 - exp(g n)) has been rounded: at g n = -12 half a step of fp32 below 1 is
+# 0.5 % of exp(g n).  The bounds are those of the other tests: some 2^-22 a token of
+# the decayed absolute sums.  exp(g n) stays far above the smallest fp32 numbers.
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (24, 8)])
+def test_decode_keeps_what_a_strong_decay_leaves(D, Hq, Hkv):
+    pool = state_pool(3, Hkv, D, 51)
+    start = pool.s.clone()
+    q, k, v = (synth.normal_bf16((3, h, D), s, device="cuda")
+               for h, s in ((Hq, 52), (Hkv, 53), (Hkv, 54)))
+    k[:2] = 0                                # nothing comes in
+    k[2] *= 2.0**-40                         # next to nothing
+    g = -torch.tensor([0.3, 0.6, 1.0, 3.0, 8.0, 12.0, 20.0, 50.0], device="cuda")
+    out = phs.linear_attn_decode(q, k, v, pool, g, out_dtype=torch.float32)
+    for b in range(3):
+        r, S, m, A = ops_ref.linear(q[b:b + 1], k[b:b + 1], v[b:b + 1], start[b], g,
+                                    1 / math.sqrt(D))
+        bo, bs = bounds(r, m, S, A, torch.float32, 1, D)
+        close(out[b], r[0], bo[0], f"out {b}")
+        close(pool.s[b], S, bs, f"state {b}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [1, 100, 128, 200, 300])
+def test_prompt_keeps_what_a_strong_decay_leaves(D, T):
+    """A padded prompt: keys of zero behind its first tokens, or from the start."""
+    H = 6
+    q, k, v = (synth.normal_bf16((2 * T, H, D), s, device="cuda") for s in (55, 56, 57))
+    k[:T] = 0
+    k[T + 2:] = 0
+    g = -torch.tensor([1e-3, 6e-3, 0.03, 0.08, 0.15, 0.2], device="cuda")
+    pool = state_pool(2, H, D, 58)
+    start = pool.s.clone()
+    out = phs.linear_attn_prompt(q, k, v, dev([0, T, 2 * T]), T, pool, g, resume=dev([1, 0]))
+    for b in range(2):
+        a, e = b * T, (b + 1) * T
+        s0 = torch.zeros_like(start[0]) if b else start[0]
+        r, S, bo, bs = reference(q[a:e], k[a:e], v[a:e], s0, g)
+        close(out[a:e], r, bo, f"out {b}")
+        close(pool.s[b], S, bs, f"state {b}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [640, 1800])
+def test_segments_keep_what_a_strong_decay_leaves(D, T):
+    H = 2
+    q, k, v = (synth.normal_bf16((T, H, D), s, device="cuda") for s in (59, 60, 61))
+    k[:] = 0
+    g = -torch.tensor([20 / T, 58 / T], device="cuda")
+    pool = state_pool(1, H, D, 62)
+    start = pool.s[0].clone()
+    out = phs.linear_attn_prompt(q, k, v, dev([0, T]), T, pool, g, resume=dev([1]))
+    r, S, bo, bs = reference(q, k, v, start, g)
+    close(out, r, bo, "out")
+    close(pool.s[0], S, bs, "state")
