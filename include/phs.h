@@ -710,8 +710,9 @@ int phs_radix_evict(phs_radix_tree *t, int64_t pages, int64_t *out_freed);
 int64_t phs_radix_cached_pages(phs_radix_tree *t);
 /* Renames the tree's Full pages by page_map (host int32 [num_pages], the map
  * phs_pages_compact wrote): page p becomes page_map[p].  PHS_ERANGE, and no
- * change, if a cached page has no new id.  References are not touched: the
- * moved counts come with phs_page_load_refcounts. */
+ * change, if a cached page has no new id; PHS_EWORKSPACE, and no change, if
+ * the host has no memory for the list of the tree's nodes.  References are
+ * not touched: the moved counts come with phs_page_load_refcounts. */
 int phs_radix_remap(phs_radix_tree *t, const int32_t *page_map, int64_t num_pages);
 /* Window-safe length as a plain function: the largest L <= match_len, L a
  * multiple of align, with swa_valid[t] != 0 (host uint8) for every t in

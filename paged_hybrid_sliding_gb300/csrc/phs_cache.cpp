@@ -28,6 +28,7 @@
 #include <map>
 #include <memory>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "phs.h"
@@ -492,16 +493,18 @@ int phs_radix_remap(phs_radix_tree* t, const int32_t* page_map, int64_t num_page
     std::lock_guard<std::mutex> alock(t->alloc->mu);
     if (static_cast<size_t>(num_pages) != t->alloc->rc.size()) return PHS_ESHAPE;
   }
-  std::vector<Node*> nodes, stack{&t->root};
-  while (!stack.empty()) {
-    Node* n = stack.back();
-    stack.pop_back();
-    nodes.push_back(n);
-    for (auto& kv : n->children) stack.push_back(kv.second.get());
+  std::vector<Node*> nodes;  // all of them, before any is changed
+  try {
+    nodes.push_back(&t->root);
+    for (size_t i = 0; i < nodes.size(); ++i)
+      for (auto& kv : nodes[i]->children) nodes.push_back(kv.second.get());
+  } catch (const std::bad_alloc&) {
+    return PHS_EWORKSPACE;
+  }
+  for (const Node* n : nodes)
     for (int32_t p : n->pages)
       if (p < 0 || p >= num_pages || page_map[p] < 0 || page_map[p] >= num_pages)
         return PHS_ERANGE;
-  }
   for (Node* n : nodes)
     for (int32_t& p : n->pages) p = page_map[p];
   return PHS_OK;
