@@ -138,8 +138,8 @@ struct LinearArgs {
   float* ws;                  // [B][Hkv][nseg * nsub][D][D]: sums of parts, then first states
 };
 
-constexpr int kLinearChunk = 128;
-constexpr int kLinearSort = 256;  // requests of a call that are put in order, at most  // tokens
+constexpr int kLinearChunk = 128;  // tokens
+constexpr int kLinearSort = 256;   // requests of a call that are put in order, at most
 
 int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream);
 int launch_linear_prompt(int D, const CUtensorMap& tq, const CUtensorMap& tk,

@@ -229,11 +229,6 @@ __global__ void __launch_bounds__(1024) phs_pages_fork_plan_kernel(const PageFor
   }
 }
 
-int launch_pages_fork_plan(const PageForkArgs& a, cudaStream_t stream) {
-  phs_pages_fork_plan_kernel<<<1, 1024, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PHS_OK : PHS_ECUDA;
-}
-
 // Whether the plan has given out page pg: it then counts 1, as a live page may,
 // but an entry that names it named no live page.  (fresh: n ids, ascending.)
 __device__ __forceinline__ bool given_out(const int32_t* fresh, int n, int pg) {
