@@ -142,3 +142,51 @@ def test_segments_keep_what_a_strong_decay_leaves(D, T):
     r, S, bo, bs = reference(q, k, v, start, g)
     close(out, r, bo, "out")
     close(pool.s[0], S, bs, "state")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("value", ["nan", "inf"])
+def test_how_far_a_bad_value_reaches(D, value):
+    """An infinite or NaN row of v at token 300: the outputs of the chunks of 128
+    tokens before its own, and of the other requests, are as without it; from its
+    own on they are not finite."""
+    H, T = 2, 500
+    q, k, v = (synth.normal_bf16((2 * T, H, D), s, device="cuda") for s in (63, 64, 65))
+    g = decays(H, lo=1e-3, hi=0.02)
+
+    def run():
+        pool = state_pool(2, H, D, 66)
+        return phs.linear_attn_prompt(q, k, v, dev([0, T, 2 * T]), T, pool, g), pool.s
+
+    out, s = run()
+    v[300] = float(value)
+    bad, bad_s = run()
+    assert torch.equal(bad[:256], out[:256]) and torch.equal(bad[T:], out[T:])
+    assert torch.equal(bad_s[1], s[1])
+    assert not torch.isfinite(bad[300:T].float()).any() and not torch.isfinite(bad_s[0]).any()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_segments_beside_inactive_and_refused_requests(D):
+    """Long prompts in segments, with a request without a state, one of a state
+    that another has, one of a range beginning before the last one's end."""
+    H, n = 1, 1400
+    cu = [0, n, 2 * n, 3 * n, 4 * n, 4 * n - 300]
+    ids = [2, -1, 2, 0, 1]
+    T = 4 * n
+    q, k, v = (synth.normal_bf16((T, H, D), s, device="cuda") for s in (67, 68, 69))
+    g = decays(H, lo=1e-3, hi=1e-3)
+    pool = state_pool(4, H, D, 70)
+    start = pool.s.clone()
+    out = torch.full((T, H, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    phs.linear_attn_prompt(q, k, v, dev(cu), n, pool, g, state_ids=dev(ids),
+                           resume=dev([1] * 5), out=out, status=st)
+    assert int(st.item()) in (-1, -3)
+    assert not out[n:3 * n].any()          # without a state, and of one that is taken
+    for b, i in ((0, 2), (3, 0)):
+        a, e = cu[b], cu[b + 1]
+        r, S, bo, bs = reference(q[a:e], k[a:e], v[a:e], start[i], g)
+        close(out[a:e], r, bo, f"out of request {b}")
+        close(pool.s[i], S, bs, f"state {i}")
+    assert torch.equal(pool.s[[1, 3]], start[[1, 3]])
