@@ -447,7 +447,10 @@ size_t phs_hybrid_stack_fused_workspace_bytes(int32_t batch, int32_t num_q_heads
  * block_table is int32 [num_rows][max_pages_per_seq], seq_lens int32
  * [num_rows]; row r holds pages block_table[r][0 .. ceil(seq_lens[r] / 16)).
  * pools: host array of num_layers descriptors that share the block table
- * (same num_pages, Hkv and head_dim).
+ * (same num_pages, Hkv and head_dim).  Only rows whose tokens are all in bf16
+ * pages are taken: the calls know nothing of an INT8 region (its table
+ * entries, which the decode does not read, would be taken as pages), nor of
+ * SWA rings or linear attention states.
  *
  * phs_pages_free: for each i < n, takes one reference off every page of row
  * rows[i] (a page that reaches 0 is free) and sets seq_lens[rows[i]] = 0;
@@ -507,7 +510,8 @@ int phs_pages_compact(const phs_paged_pool *pools, int32_t num_layers,
  * of value head j, and the same two heads of V hold the first and the last
  * D of its 2D value columns (so a [..][Hv][2D] value is a [..][2 Hv][D]
  * one, and append, copies and page operations take the pool as any other).
- * Head i reads value head i / (num_heads / Hv); num_heads / Hv <= 16.
+ * Head i reads value head i / (num_heads / Hv); num_heads / Hv <= 16 (up to
+ * 8 share one read of K and V).
  *   q    bf16 [batch][2 num_heads][D]: rows 2i and 2i + 1 are head i's
  *        queries of the two maps
  *   out  [batch][num_heads][2D], bf16 or fp32
@@ -516,6 +520,7 @@ int phs_pages_compact(const phs_paged_pool *pools, int32_t num_layers,
  *              / sqrt(mean(out_i^2) + norm_eps).
  * The lambda vectors are fp32 [D] (lambda_per_head 0) or [num_heads][D]
  * (1), device memory.  Sums, softmax statistics and the norm are fp32.
+ * Softmax weights enter the value product to 16 bits (24 for fp32 outputs).
  * Splits, workspace, k_new / v_new / page_refcount (bf16
  * [batch][2 Hv][D]) and errors as for phs_attn_decode_full_paged; a request
  * of length 0 gets a zero row.
@@ -566,6 +571,10 @@ int phs_attn_decode_diff_paged(const void *q, int32_t num_heads, const phs_paged
  * its last token in the pool, ready for the next part of the prompt or for
  * phs_linear_attn_decode.  max_seq_len (host) bounds the requests' lengths.
  * out bf16 [total_tokens][Hq][D]; rows of no request are left as they were.
+ * Tokens go in chunks of 128, whose products take states and weights to 16
+ * bits (the state itself is kept in fp32).  A value row that is infinite or NaN
+ * reaches the request's outputs from the start of its chunk on, up to 127
+ * tokens before its own; other requests are not reached.
  * A request with a bad token range (outside the tokens, or beginning before
  * an earlier one's end) or a length above max_seq_len records PHS_ERANGE and
  * is left out whole.  workspace: phs_linear_prompt_workspace_bytes of the

@@ -874,7 +874,9 @@ def pages_fork(pools, block_table, seq_lens, page_refcount, src_rows, dst_rows, 
                status=None, stream=None):
     """Continue row src_rows[i] in the free row dst_rows[i]: whole pages
     shared, a partly filled last page copied into the lowest free page, in
-    every pool of `pools` (list of PagedPool sharing the block table)."""
+    every pool of `pools` (list of PagedPool sharing the block table).  Pages
+    of the block table only: an INT8 region, SWA rings and linear attention
+    states are the caller's to copy."""
     dev, rows, width, pages = _tables(block_table, seq_lens, page_refcount)
     n, = _shape(src_rows, torch.int32, dev, "src_rows", 1)
     if _shape(dst_rows, torch.int32, dev, "dst_rows", 1) != (n,):

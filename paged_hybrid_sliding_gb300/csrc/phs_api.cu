@@ -1769,7 +1769,7 @@ namespace {
 // How a prompt call is spread over the SMs: segments of each prompt, parts
 // that a first launch sums a segment up in, and CTAs that share a KV head's
 // query heads.  Of the plans the one with the least time is taken, by these
-// costs at D = 128 in half microseconds: 16 for a CTA (of either launch); for
+// costs at D = 128 (taken at 64 too) in half microseconds: 16 for a CTA (of either launch); for
 // each chunk 4 for its state (in either launch) and 3 for each query head of
 // the CTA; 4 for joining the sums.  Without segments a call takes as long as
 // its longest prompt, or as all CTAs' work spread over the SMs; segments are

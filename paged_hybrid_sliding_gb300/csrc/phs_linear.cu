@@ -62,7 +62,7 @@ __device__ __forceinline__ bool request_tokens(const LinearArgs& a, int b, int& 
 // outputs' sums over rows meet in shared memory once.  The step reads and
 // writes each state once and computes 2 to 3 operations a byte, so it is bound
 // by memory, and small CTAs with many loads in flight carry it: 256 requests of
-// 32 heads of 128 (1.07 GB) take 169.7 us, 6.4 TB/s, against 159.4 for those
+// 32 heads of 128 (1.07 GB) take 170.1 us, 6.4 TB/s, against 159.4 for those
 // bytes at the rate of a plain copy; 2 requests 3.3 us, a launch.
 template <int D, int GM>
 __global__ void __launch_bounds__(256) phs_linear_decode_kernel(const LinearArgs a) {
@@ -173,13 +173,12 @@ int launch_linear_decode(int D, const LinearArgs& a, cudaStream_t stream) {
 // the largest stall (3.1 of 10.7 warp-cycles an instruction).
 //
 // What bounds it: a chunk at D = 128 takes 3.5 us (6,600 cycles) of a CTA, in
-// which it has the tensor cores busy for 59 %, issues 0.6 instructions a cycle,
-// and moves 128 KB, 2.9 us at an SM's share of HBM.  What is left is the chain
+// which it has the tensor cores busy for 55 %, its schedulers issue in 56 %, and
+// it moves 128 KB, 2.9 us at an SM's share of HBM.  What is left is the chain
 // from one chunk's state to the next one's (terms to shared memory, K' and KV,
 // its sum back) and, beside it, scores, P, PV and the rows.  One prompt of
-// 32,751 tokens and 32 heads of 128: 313 us (77 for the sums of segments, 231
-// for the rows) against 158 for its bytes; of 32,768 tokens and heads of 64, 207
-// against 79.  Steps that did not help: six warpgroups instead of five (300
+// 32,751 tokens and 32 heads of 128: 315 us (a quarter for the sums of segments)
+// against 158 for its bytes; of 32,768 tokens and heads of 64, 211 against 79.  Steps that did not help: six warpgroups instead of five (300
 // against 265 us for the rows), other forms of the waits, one arrival for a
 // warp instead of its threads' (331 against 321), P's loads a step ahead, terms
 // cut off instead of rounded (391 against 348) or rounded by two fma (339
