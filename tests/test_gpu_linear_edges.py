@@ -190,3 +190,22 @@ def test_segments_beside_inactive_and_refused_requests(D):
         close(out[a:e], r, bo, f"out of request {b}")
         close(pool.s[i], S, bs, f"state {i}")
     assert torch.equal(pool.s[[1, 3]], start[[1, 3]])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(3, 3), (12, 2), (16, 1)])
+def test_a_single_token_is_rounded_once(D, Hq, Hkv):
+    """Its products are fp32 ones: a bf16 output is off by half a step of its own
+    beside what the fp32 output is off by."""
+    B = 4
+    q, k, v = (synth.normal_bf16((B, h, D), s, device="cuda")
+               for h, s in ((Hq, 71), (Hkv, 72), (Hkv, 73)))
+    g = decays(Hkv)
+    pool = state_pool(B, Hkv, D, 74)
+    start = pool.s.clone()
+    out = phs.linear_attn_decode(q, k, v, pool, g)
+    for b in range(B):
+        r, S, m, A = ops_ref.linear(q[b:b + 1], k[b:b + 1], v[b:b + 1], start[b], g,
+                                    1 / math.sqrt(D))
+        bo, _ = bounds(r, m, S, A, torch.float32, 1, D)
+        close(out[b], r[0], (bo + (r.abs() + bo) * 2.0**-8)[0], f"out {b}")
