@@ -602,6 +602,187 @@ int phs_linear_attn_prompt(const void *q, int32_t num_q_heads, const void *k, co
                            float scale, void *out, void *workspace, size_t workspace_bytes,
                            int32_t *dev_status, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions, and the tokens of whole prompts (or one token each) on
+ * their way into the paged cache.
+ *
+ * Pair i of a head turns by the angle 2 pi turns[i] / 2^64 for each position:
+ *     (x, y) -> factor (x cos - y sin, y cos + x sin)
+ * turns (device, uint64 [rotary_dim / 2]) is the share of a full turn as a
+ * 64-bit fraction, so a position's angle is one integer product, exact to
+ * 2^-64 of a turn whatever the position.  The first rotary_dim elements of a
+ * head are rotated (a multiple of 16, at most D), the others copied: pair i
+ * is elements i and i + rotary_dim / 2, with `interleaved` 2 i and 2 i + 1.
+ * Scalings for long contexts change turns and factor.  Angles are taken to 32
+ * bits of a turn, products in fp32, rounded once to bf16.
+ *
+ * Rows: x_stride is the number of elements from one token's row to the next
+ * one's, at least heads * D, a multiple of 8; heads and their elements lie
+ * side by side, pointers 16-byte aligned (a part of a wider projection's rows
+ * will do).
+ *
+ * phs_rope_rotate: q_out[t] = q[t] rotated by positions[t] (device int32
+ * [tokens]), k likewise (k NULL: q alone).  An output may be its own input
+ * (same pointer and stride); else they must not overlap.
+ *
+ * phs_kv_write_paged: request b brings tokens [cu_seqlens[b],
+ * cu_seqlens[b + 1]) (device int32 [batch + 1], not decreasing, within
+ * [0, tokens]) of k and v; cu_seqlens NULL: one token each, token b (tokens =
+ * batch).  seq_lens[b] counts the request's tokens AFTER the call, so its
+ * new ones are the last; a token's position is its place in the request.
+ * With rope k is rotated, and q (NULL: none) into q_out, dense bf16
+ * [tokens][num_q_heads][D].  Tokens go to their pages as in
+ * phs_kv_append_paged, page_refcount included.
+ *   With int8: the request's first qlens[b] tokens (a multiple of 32) are
+ * held in 8 bits after the call, its first qlens_before[b] were before it.
+ * Each block of 32 between the two is quantised as by
+ * phs_kv_quant_int8_block32 (bit for bit what a bf16 write and that call
+ * give), new tokens straight from k and v without touching their pages,
+ * earlier ones from their pages.  At most max_qblocks blocks a request.
+ *   Device errors: a bad cu_seqlens refuses the whole call (PHS_ERANGE, no
+ * cache is written); seq_lens below the new tokens, qlens_before or qlens bad
+ * (negative, not a multiple of 32, qlens_before above qlens or above the
+ * earlier tokens, qlens above seq_lens, more blocks than max_qblocks) refuse
+ * the request (PHS_ERANGE); its q_out rows are zero.  A page or block outside
+ * its pool or table (PHS_ERANGE) or a shared page (PHS_ESHARED) is not
+ * written.  Without cu_seqlens a request of length 0 is inactive: nothing is
+ * written, its q_out row is zero.  q_out rows of no request are left as they
+ * were.
+ *
+ * phs_kv_read_paged: tokens [starts[b], starts[b] + n) of request b, n =
+ * cu_seqlens[b + 1] - cu_seqlens[b], back as dense rows [cu_seqlens[b], ...)
+ * of k_out and v_out, bf16 [tokens][Hkv][D]: copies of bf16 pages, and where
+ * int8 is given tokens below qlens[b] as code * scale, rounded to bf16.
+ * max_tokens (host) bounds n.  Bad ranges (PHS_ERANGE): a bad cu_seqlens
+ * refuses the call, n above max_tokens, a negative start or a qlens that is
+ * negative or no multiple of 32 the request (rows left as they were); rows
+ * of a page outside its pool or table are zero.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    const uint64_t *turns;    /* device, [rotary_dim / 2] */
+    int32_t rotary_dim;
+    int32_t interleaved;
+    float factor;
+} phs_rope;
+
+int phs_rope_rotate(const void *q, int64_t q_stride, int32_t num_q_heads, const void *k,
+                    int64_t k_stride, int32_t num_kv_heads, int32_t head_dim, int32_t tokens,
+                    const int32_t *positions, const phs_rope *rope, void *q_out,
+                    int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream);
+int phs_kv_write_paged(const phs_paged_pool *pool, const void *k, int64_t k_stride, const void *v,
+                       int64_t v_stride, int32_t tokens, const int32_t *cu_seqlens,
+                       const int32_t *block_table, int32_t max_pages_per_seq,
+                       const int32_t *seq_lens, int32_t batch, const phs_rope *rope,
+                       const void *q, int64_t q_stride, int32_t num_q_heads, void *q_out,
+                       const phs_int8_pool *int8, const int32_t *qtable,
+                       int32_t max_qpages_per_seq, const int32_t *qlens_before,
+                       const int32_t *qlens, int32_t max_qblocks, const int32_t *page_refcount,
+                       int32_t *dev_status, void *stream);
+int phs_kv_read_paged(const phs_paged_pool *pool, const int32_t *block_table,
+                      int32_t max_pages_per_seq, const int32_t *starts,
+                      const int32_t *cu_seqlens, int32_t batch, int32_t tokens,
+                      int32_t max_tokens, const phs_int8_pool *int8, const int32_t *qtable,
+                      int32_t max_qpages_per_seq, const int32_t *qlens, void *k_out, void *v_out,
+                      int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The recurrent parts of a selective state space layer.  A request's cache is
+ * the last width - 1 inputs of each channel of a short convolution and one
+ * state for each head of a scan.  Rows with a stride as above; state_ids,
+ * resume, cu_seqlens, max_seq_len and batch as for linear attention: a
+ * negative id marks an inactive request; an id outside the pool (PHS_ERANGE)
+ * or one that an earlier request of the call has (PHS_EINVAL) is recorded;
+ * such a request updates nothing and its output rows are zero.  Rows of no
+ * request are left as they were.
+ *
+ * Causal convolution, one filter for each channel:
+ *     y[t][c] = act(bias[c] + sum_k weight[c][k] x[t - width + 1 + k][c])
+ * act(y) = y / (1 + exp(-y)) with `silu`, else y.  Inputs before a request's
+ * first token are the pool's (oldest first) where resume[b] != 0 and in
+ * phs_causal_conv_decode, else zero; the pool gets the last width - 1.  x and
+ * out bf16 (out dense [tokens][channels]), sums fp32.  channels a multiple of
+ * 8, width 2 to 4.  A cu_seqlens that decreases or leaves [0, total_tokens]
+ * refuses the whole call (PHS_ERANGE, nothing is written).
+ *
+ * Selective scan: state S [P][N] of head h, group g = h / (H / G),
+ *     s   = softplus(dt[t][h] + dt_bias[h])
+ *     S_t = exp(s a[h]) S_{t-1} + s x[t][h] b[t][g]^T
+ *     y_t = S_t c[t][g] + skip[h] x[t][h]
+ * a (fp32 [H], <= 0) the rate, skip and dt_bias fp32 [H] or NULL (zero).  x
+ * bf16 [tokens][H][P], b and c bf16 [tokens][G][N], dt bf16 or fp32
+ * [tokens][H] (any stride of at least H); out dense [tokens][H][P].  P and N
+ * 64 or 128.  softplus(x) = x above 20.  States are fp32 and stay so;
+ * phs_selective_scan_prompt takes states and weights into its products to 16
+ * bits (24 for what goes into the state).  In a prompt an infinite or NaN
+ * value reaches the request's rows from the start of its chunk of 128 tokens
+ * on, up to 127 tokens before its own; other requests are not reached.  A
+ * request with a bad token range (outside the tokens, or beginning before an
+ * earlier one's end) or a length above max_seq_len records PHS_ERANGE and is
+ * left out whole.  workspace: phs_scan_prompt_workspace_bytes of the same
+ * sizes (a call with fewer requests may need more), 256-byte aligned; calls
+ * that may run at once need one each.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    const float *weight;  /* device, fp32 [channels][width] */
+    const float *bias;    /* device, fp32 [channels], or NULL */
+    int32_t silu;
+} phs_conv_weights;
+
+typedef struct {
+    void *c;              /* device, bf16 [num_states][width - 1][channels] */
+    int64_t num_states;
+    int32_t channels;
+    int32_t width;
+} phs_conv_pool;
+
+int phs_causal_conv_decode(const void *x, int64_t x_stride, const phs_conv_pool *pool,
+                           const phs_conv_weights *weights, const int32_t *state_ids,
+                           int32_t batch, void *out, int32_t *dev_status, void *stream);
+int phs_causal_conv_prompt(const void *x, int64_t x_stride, const int32_t *cu_seqlens,
+                           int32_t total_tokens, const phs_conv_pool *pool,
+                           const phs_conv_weights *weights, const int32_t *state_ids,
+                           const int32_t *resume, int32_t batch, void *out, int32_t *dev_status,
+                           void *stream);
+
+typedef struct {
+    const float *a;       /* device, fp32 [H] */
+    const float *skip;    /* or NULL */
+    const float *dt_bias; /* or NULL */
+} phs_scan_weights;
+
+typedef struct {
+    float *s;             /* device, fp32 [num_states][H][P][N] */
+    int64_t num_states;
+    int32_t num_heads;    /* H */
+    int32_t head_dim;     /* P: 64 or 128 */
+    int32_t state_dim;    /* N: 64 or 128 */
+} phs_scan_pool;
+
+/* a token's inputs */
+typedef struct {
+    const void *x;        /* device, bf16 [tokens][H][P] */
+    const void *b;        /* device, bf16 [tokens][G][N] */
+    const void *c;
+    const void *dt;       /* device, bf16 or fp32 [tokens][H] */
+    int64_t x_stride, b_stride, c_stride, dt_stride;
+    int32_t num_groups;   /* G */
+    int32_t dt_dtype;     /* PHS_OUT_BF16 or PHS_OUT_F32 */
+} phs_scan_inputs;
+
+int phs_selective_scan_decode(const phs_scan_inputs *in, const phs_scan_pool *pool,
+                              const phs_scan_weights *weights, const int32_t *state_ids,
+                              int32_t batch, void *out, int32_t out_dtype, int32_t *dev_status,
+                              void *stream);
+size_t phs_scan_prompt_workspace_bytes(int32_t batch, int32_t num_heads, int32_t num_groups,
+                                       int32_t head_dim, int32_t state_dim, int32_t total_tokens,
+                                       int32_t max_seq_len);
+int phs_selective_scan_prompt(const phs_scan_inputs *in, const int32_t *cu_seqlens,
+                              int32_t total_tokens, int32_t max_seq_len,
+                              const phs_scan_pool *pool, const phs_scan_weights *weights,
+                              const int32_t *state_ids, const int32_t *resume, int32_t batch,
+                              void *out, void *workspace, size_t workspace_bytes,
+                              int32_t *dev_status, void *stream);
+
 /* KV tokens held by a hybrid stack (host arrays in, host results out):
  * Full layers hold seq_lens[b] tokens per request, SWA layers
  * min(seq_lens[b], window).  Source: MiMo page, section 1 (the 10/60 stack

@@ -33,6 +33,10 @@ __all__ = [
     "pages_compact_workspace_bytes",
     "DiffWeights", "attn_decode_diff_paged", "diff_workspace_bytes",
     "StatePool", "linear_attn_decode", "linear_attn_prompt", "linear_prompt_workspace_bytes",
+    "Rope", "rope_frequencies", "rope_rotate", "kv_write_paged", "kv_read_paged",
+    "ConvPool", "ConvWeights", "causal_conv_decode", "causal_conv_prompt",
+    "ScanPool", "ScanWeights", "selective_scan_decode", "selective_scan_prompt",
+    "scan_prompt_workspace_bytes",
 ]
 
 PAGE = 16
@@ -1107,4 +1111,429 @@ def linear_attn_prompt(q, k, v, cu_seqlens, max_seq_len: int, pool: StatePool, l
                                         scale, out.data_ptr(), ws, ws_bytes,
                                         _status_ptr(status, dev), _raw_stream(stream, dev)),
            "linear_attn_prompt")
+    return out
+
+
+# ------------------------------------------- rotary positions, cache writes --
+def _rows(t, dtype, dev, name, dims):
+    """(shape, row stride) of t: rows of a token side by side in memory, at
+    any stride (a part of a wider projection's output)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.dim() == dims):
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == dims:
+            raise ValueError(_DEVICE_ERROR)
+        _need(t, dtype, name, dims)
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape = t.shape
+    cols = shape[1] if dims == 2 else shape[1] * shape[2]
+    if t.is_contiguous():
+        return shape, cols
+    strides = t.stride()
+    if (strides[-1] != 1 and shape[-1] != 1) or \
+            (dims == 3 and shape[1] != 1 and strides[1] != shape[2]):
+        raise ValueError(f"{name}: a token's elements must lie side by side")
+    return shape, strides[0] if shape[0] > 1 else cols
+
+
+@dataclass
+class Rope:
+    """Rotary positions: turns int64 [rotary_dim / 2], the share of a full
+    turn that each position adds to pair i's angle, as a 64-bit fraction
+    (stored in the int64's bits); pairs of elements i and i + rotary_dim / 2,
+    with `interleaved` 2 i and 2 i + 1; cos and sin are multiplied by
+    `factor`.  `make` lays out the usual ones."""
+    turns: torch.Tensor
+    interleaved: bool = False
+    factor: float = 1.0
+
+    def c(self, dev):
+        half, = _shape(self.turns, torch.int64, dev, "rope.turns", 1)
+        return _lib.RopeC(self.turns.data_ptr(), 2 * half, self.interleaved, self.factor)
+
+    @staticmethod
+    def make(rotary_dim, base=10000.0, interleaved=False, scaling=None, scale=1.0,
+             trained_len=None, low=None, high=None, factor=None, device="cuda"):
+        """Pair i turns by base^(-2 i / rotary_dim) radians a position.
+        Scalings to contexts `scale` times as long:
+          "linear"       all pairs `scale` times slower;
+          "base"         the base raised so that the slowest pair is `scale`
+                         times slower and the fastest as it was;
+          "parts"        pairs of more than `high` (32) rotations in trained_len
+                         as they were, of fewer than `low` (1) `scale` times
+                         slower, between them by their index; factor
+                         0.1 ln(scale) + 1;
+          "wavelengths"  the same with 4 and 1, between them by their
+                         rotations.
+        factor: the one of cos and sin, where it is not the scaling's."""
+        freq, mag = rope_frequencies(rotary_dim, base, scaling, scale, trained_len, low, high)
+        import numpy as np
+        turns = np.array([round(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 for f in freq.tolist()],
+                         dtype=np.uint64)
+        return Rope(torch.from_numpy(turns.view(np.int64)).to(device), interleaved,
+                    float(mag if factor is None else factor))
+
+
+def rope_frequencies(rotary_dim, base=10000.0, scaling=None, scale=1.0, trained_len=None, low=None,
+                     high=None):
+    """(radians a position of each pair, host fp64 [rotary_dim / 2]; factor of
+    cos and sin) of Rope.make's scalings."""
+    import numpy as np
+    if rotary_dim <= 0 or rotary_dim % 2 or not base > 1 or not scale >= 1:
+        raise ValueError("rotary_dim must be even and positive, base above 1, scale at least 1")
+    half = rotary_dim // 2
+    i = np.arange(half)
+    if scaling == "base":
+        if half < 2:
+            raise ValueError("scaling of the base needs at least two pairs")
+        base = base * scale ** (half / (half - 1))
+    freq = float(base) ** (-i / half)
+    if scaling in (None, "base"):
+        return freq, 1.0
+    if scaling == "linear":
+        return freq / scale, 1.0
+    if scaling not in ("parts", "wavelengths"):
+        raise ValueError("scaling must be linear, base, parts or wavelengths")
+    low = 1.0 if low is None else float(low)
+    high = (32.0 if scaling == "parts" else 4.0) if high is None else float(high)
+    if trained_len is None or trained_len <= 0 or not 0 < low < high:
+        raise ValueError(f"scaling by {scaling} needs trained_len and 0 < low < high")
+    if scaling == "parts":
+        # index of the pair that makes so many rotations in trained_len
+        at = [half * math.log(trained_len / (2 * math.pi * r)) / math.log(base)
+              for r in (high, low)]
+        first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), half - 1)
+        slow = np.clip((i - first) / max(last - first, 0.001), 0, 1)
+        return freq * (1 - slow) + freq / scale * slow, 0.1 * math.log(scale) + 1
+    keep = np.clip((trained_len * freq / (2 * math.pi) - low) / (high - low), 0, 1)
+    return freq * keep + freq / scale * (1 - keep), 1.0
+
+
+def rope_rotate(q, k, positions, rope: Rope, q_out=None, k_out=None, stream=None):
+    """q [T, Hq, D] and k [T, Hkv, D] (None: q alone) bf16, rotated by
+    positions int32 [T] into q_out, k_out (may be the inputs themselves);
+    returns (q_out, k_out).  For layers whose attention call appends k itself."""
+    dev = _device(q, torch.bfloat16, "q")
+    (T, Hq, D), qs = _rows(q, torch.bfloat16, dev, "q", 3)
+    Hk = ks = kos = 0
+    if k is not None:
+        (Tk, Hk, Dk), ks = _rows(k, torch.bfloat16, dev, "k", 3)
+        if Tk != T or Dk != D:
+            raise ValueError("q and k differ in tokens or head_dim")
+    if _shape(positions, torch.int32, dev, "positions", 1) != (T,):
+        raise ValueError("positions must be [tokens]")
+    if q_out is None:
+        q_out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
+    shape, qos = _rows(q_out, torch.bfloat16, dev, "q_out", 3)
+    if shape != (T, Hq, D):
+        raise ValueError("q_out must have q's shape")
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+    else:
+        if k_out is None:
+            k_out = _empty((T, Hk, D), torch.bfloat16, dev, stream)
+        shape, kos = _rows(k_out, torch.bfloat16, dev, "k_out", 3)
+        if shape != (T, Hk, D):
+            raise ValueError("k_out must have k's shape")
+    _check(lib().phs_rope_rotate(q.data_ptr(), qs, Hq, _ptr(k), ks, Hk, D, T,
+                                 positions.data_ptr(), rope.c(dev), q_out.data_ptr(), qos,
+                                 _ptr(k_out), kos, _raw_stream(stream, dev)), "rope_rotate")
+    return q_out, k_out
+
+
+def _int8_c(int8, dev):
+    n, h, q, d = _shape(int8.k, torch.uint8, dev, "int8.k", 4)
+    if q != QBLOCK or \
+            _shape(int8.v, torch.uint8, dev, "int8.v", 5) != (n, h, 2, d, QBLOCK // 2) or \
+            _shape(int8.k_scale, torch.float32, dev, "int8.k_scale", 2) != (n, h) or \
+            _shape(int8.v_scale, torch.float32, dev, "int8.v_scale", 2) != (n, h):
+        raise ValueError("inconsistent INT8 pool shapes")
+    return _lib.Int8PoolC(int8.k.data_ptr(), int8.v.data_ptr(), int8.k_scale.data_ptr(),
+                          int8.v_scale.data_ptr(), n, h, d)
+
+
+def _per_request(t, dev, name, batch):
+    if _shape(t, torch.int32, dev, name, 1) != (batch,):
+        raise ValueError(f"{name} needs one entry per request")
+    return t.data_ptr()
+
+
+def kv_write_paged(pool: PagedPool, k, v, block_table, seq_lens, cu_seqlens=None,
+                   rope: Rope | None = None, q=None, q_out=None, int8: Int8Pool | None = None,
+                   qtable=None, qlens_before=None, qlens=None, max_qblocks=0, page_refcount=None,
+                   status=None, stream=None):
+    """Write the new tokens of every request into the paged cache: k, v bf16
+    [T, Hkv, D], request b's rows [cu_seqlens[b], cu_seqlens[b + 1]) (None: one
+    token each), the last of its seq_lens[b] tokens.  With rope k is rotated by
+    each token's place in its request, and q [T, Hq, D] into q_out, which is
+    returned (None without q).  With int8 the blocks of 32 tokens from
+    qlens_before[b] to qlens[b] (at most max_qblocks) are quantised, new tokens
+    straight from k and v, earlier ones from their pages."""
+    dev = _device(k, torch.bfloat16, "k")
+    (T, H, D), ks = _rows(k, torch.bfloat16, dev, "k", 3)
+    shape, vs = _rows(v, torch.bfloat16, dev, "v", 3)
+    pc = _pool_c(pool, dev)
+    if shape != (T, H, D) or H != pc.num_kv_heads or D != pc.head_dim:
+        raise ValueError("k and v must be [tokens, Hkv of the pool, head_dim]")
+    B, width = _shape(block_table, torch.int32, dev, "block_table", 2)
+    lens = _per_request(seq_lens, dev, "seq_lens", B)
+    cu = None
+    if cu_seqlens is not None:
+        cu = _per_request(cu_seqlens, dev, "cu_seqlens", B + 1)
+    elif T != B:
+        raise ValueError("without cu_seqlens one token per request")
+    Hq = qs = 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        if rope is None:
+            raise ValueError("q goes with rope")
+        (Tq, Hq, Dq), qs = _rows(q, torch.bfloat16, dev, "q", 3)
+        if Tq != T or Dq != D:
+            raise ValueError("q must be [tokens, Hq, head_dim]")
+        if q_out is None:
+            q_out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
+        elif _shape(q_out, torch.bfloat16, dev, "q_out", 3) != (T, Hq, D):
+            raise ValueError("q_out must have q's shape")
+    ic = qt = qb = ql = None
+    qw = 0
+    if int8 is not None:
+        ic = _int8_c(int8, dev)
+        rows, qw = _shape(qtable, torch.int32, dev, "qtable", 2)
+        if rows != B:
+            raise ValueError("qtable needs one row per request")
+        qt = qtable.data_ptr()
+        qb = _per_request(qlens_before, dev, "qlens_before", B)
+        ql = _per_request(qlens, dev, "qlens", B)
+    elif qtable is not None or qlens is not None or qlens_before is not None:
+        raise ValueError("qtable and qlens go with int8")
+    if page_refcount is not None and \
+            _shape(page_refcount, torch.int32, dev, "page_refcount", 1) != (pc.num_pages,):
+        raise ValueError("page_refcount needs one entry per page")
+    _check(lib().phs_kv_write_paged(
+        pc, k.data_ptr(), ks, v.data_ptr(), vs, T, cu, block_table.data_ptr(), width, lens, B,
+        None if rope is None else rope.c(dev), _ptr(q), qs, Hq, _ptr(q_out), ic, qt, qw, qb, ql,
+        int(max_qblocks), _ptr(page_refcount), _status_ptr(status, dev), _raw_stream(stream, dev)),
+        "kv_write_paged")
+    return q_out
+
+
+def kv_read_paged(pool: PagedPool, block_table, starts, cu_seqlens, total_tokens: int,
+                  max_tokens: int, int8: Int8Pool | None = None, qtable=None, qlens=None,
+                  k_out=None, v_out=None, status=None, stream=None):
+    """Tokens [starts[b], starts[b] + n) of every request, n = cu_seqlens[b + 1]
+    - cu_seqlens[b] <= max_tokens, back from the cache as rows [cu_seqlens[b],
+    ...) of bf16 [total_tokens, Hkv, D]; those below qlens[b] from their 8-bit
+    blocks.  Returns (k_out, v_out)."""
+    dev = _device(block_table, torch.int32, "block_table")
+    B, width = _shape(block_table, torch.int32, dev, "block_table", 2)
+    pc = _pool_c(pool, dev)
+    at = _per_request(starts, dev, "starts", B)
+    cu = _per_request(cu_seqlens, dev, "cu_seqlens", B + 1)
+    shape = (int(total_tokens), pc.num_kv_heads, pc.head_dim)
+    if k_out is None:
+        k_out = _empty(shape, torch.bfloat16, dev, stream)
+    if v_out is None:
+        v_out = _empty(shape, torch.bfloat16, dev, stream)
+    if _shape(k_out, torch.bfloat16, dev, "k_out", 3) != shape or \
+            _shape(v_out, torch.bfloat16, dev, "v_out", 3) != shape:
+        raise ValueError("k_out and v_out must be [total_tokens, Hkv, head_dim]")
+    ic = qt = ql = None
+    qw = 0
+    if int8 is not None:
+        ic = _int8_c(int8, dev)
+        rows, qw = _shape(qtable, torch.int32, dev, "qtable", 2)
+        if rows != B:
+            raise ValueError("qtable needs one row per request")
+        qt = qtable.data_ptr()
+        ql = _per_request(qlens, dev, "qlens", B)
+    elif qtable is not None or qlens is not None:
+        raise ValueError("qtable and qlens go with int8")
+    _check(lib().phs_kv_read_paged(pc, block_table.data_ptr(), width, at, cu, B, shape[0],
+                                   int(max_tokens), ic, qt, qw, ql, k_out.data_ptr(),
+                                   v_out.data_ptr(), _status_ptr(status, dev),
+                                   _raw_stream(stream, dev)), "kv_read_paged")
+    return k_out, v_out
+
+
+# ------------------------------------------------------- causal convolution --
+@dataclass
+class ConvPool:
+    """Last inputs of a causal convolution: c bf16 [num_states, width - 1,
+    channels], oldest first."""
+    c: torch.Tensor
+
+    @staticmethod
+    def zeros(num_states, channels, width, device="cuda"):
+        return ConvPool(torch.zeros((num_states, width - 1, channels), dtype=torch.bfloat16,
+                                    device=device))
+
+
+@dataclass
+class ConvWeights:
+    """Filters of a causal convolution: weight fp32 [channels, width], bias
+    fp32 [channels] or None; with silu the sum y goes out as y / (1 + exp(-y))."""
+    weight: torch.Tensor
+    bias: torch.Tensor | None = None
+    silu: bool = True
+
+
+def _conv_args(x, pool, weights, state_ids, batch, out, dev, stream):
+    """(row stride, descriptors of pool and weights, pointer of the ids, out)"""
+    (T, C), stride = _rows(x, torch.bfloat16, dev, "x", 2)
+    n, w1, channels = _shape(pool.c, torch.bfloat16, dev, "pool.c", 3)
+    if C != channels:
+        raise ValueError("x must be [tokens, channels of the pool]")
+    if _shape(weights.weight, torch.float32, dev, "weight", 2) != (C, w1 + 1):
+        raise ValueError("weight must be [channels, width]")
+    bias = weights.bias
+    if bias is not None and _shape(bias, torch.float32, dev, "bias", 1) != (C,):
+        raise ValueError("bias must be [channels]")
+    ids = None if state_ids is None else _per_request(state_ids, dev, "state_ids", batch)
+    if out is None:
+        out = _empty((T, C), torch.bfloat16, dev, stream)
+    elif _shape(out, torch.bfloat16, dev, "out", 2) != (T, C):
+        raise ValueError("out must have x's shape")
+    return (stride, _lib.ConvPoolC(pool.c.data_ptr(), n, C, w1 + 1),
+            _lib.ConvWeightsC(weights.weight.data_ptr(), _ptr(bias), weights.silu), ids, out)
+
+
+def causal_conv_decode(x, pool: ConvPool, weights: ConvWeights, state_ids=None, out=None,
+                       status=None, stream=None):
+    """One token per request: x [B, channels] bf16; returns out [B, channels]
+    and moves the requests' last inputs on by one."""
+    dev = _device(x, torch.bfloat16, "x")
+    B = x.shape[0]
+    stride, pc, wc, ids, out = _conv_args(x, pool, weights, state_ids, B, out, dev, stream)
+    _check(lib().phs_causal_conv_decode(x.data_ptr(), stride, pc, wc, ids, B, out.data_ptr(),
+                                        _status_ptr(status, dev), _raw_stream(stream, dev)),
+           "causal_conv_decode")
+    return out
+
+
+def causal_conv_prompt(x, cu_seqlens, pool: ConvPool, weights: ConvWeights, state_ids=None,
+                       resume=None, out=None, status=None, stream=None):
+    """The convolution over packed prompts: request b has rows [cu_seqlens[b],
+    cu_seqlens[b + 1]) of x [T, channels] bf16, behind its last inputs in the
+    pool where resume[b] != 0 (else behind zeros), and leaves its own there.
+    Returns out [T, channels]; rows of no request are left as they were (unset
+    in an output made here)."""
+    dev = _device(x, torch.bfloat16, "x")
+    B = _shape(cu_seqlens, torch.int32, dev, "cu_seqlens", 1)[0] - 1
+    if B < 0:
+        raise ValueError("cu_seqlens must be [batch + 1]")
+    stride, pc, wc, ids, out = _conv_args(x, pool, weights, state_ids, B, out, dev, stream)
+    again = None if resume is None else _per_request(resume, dev, "resume", B)
+    _check(lib().phs_causal_conv_prompt(x.data_ptr(), stride, cu_seqlens.data_ptr(), x.shape[0],
+                                        pc, wc, ids, again, B, out.data_ptr(),
+                                        _status_ptr(status, dev), _raw_stream(stream, dev)),
+           "causal_conv_prompt")
+    return out
+
+
+# ----------------------------------------------------------- selective scan --
+@dataclass
+class ScanPool:
+    """States of a selective scan: s fp32 [num_states, H, P, N]."""
+    s: torch.Tensor
+
+    @staticmethod
+    def zeros(num_states, num_heads, head_dim, state_dim, device="cuda"):
+        return ScanPool(torch.zeros((num_states, num_heads, head_dim, state_dim),
+                                    dtype=torch.float32, device=device))
+
+
+@dataclass
+class ScanWeights:
+    """Weights of a selective scan, fp32 [H] each: the rate (<= 0), and where
+    there are any the skip of x past the scan and the bias of the steps."""
+    rate: torch.Tensor
+    skip: torch.Tensor | None = None
+    dt_bias: torch.Tensor | None = None
+
+
+def _scan_args(x, dt, b, c, pool, weights, dev):
+    """(tokens, groups, descriptors of inputs, pool and weights)"""
+    shape, xs = _rows(x, torch.bfloat16, dev, "x", 3)
+    T, H, P = shape
+    bshape, bs = _rows(b, torch.bfloat16, dev, "b", 3)
+    cshape, cs = _rows(c, torch.bfloat16, dev, "c", 3)
+    kind = torch.float32 if isinstance(dt, torch.Tensor) and dt.dtype is torch.float32 \
+        else torch.bfloat16
+    dshape, ds = _rows(dt, kind, dev, "dt", 2)
+    n, Hs, Ps, N = _shape(pool.s, torch.float32, dev, "pool.s", 4)
+    if (Hs, Ps) != (H, P):
+        raise ValueError("x must be [tokens, H, P] of the pool")
+    if bshape != cshape or bshape[0] != T or bshape[2] != N:
+        raise ValueError("b and c must be [tokens, groups, N of the pool]")
+    if dshape != (T, H):
+        raise ValueError("dt must be [tokens, H]")
+    rate = _shape(weights.rate, torch.float32, dev, "rate", 1)
+    if rate != (H,):
+        raise ValueError("rate must be [H]")
+    skip, bias = weights.skip, weights.dt_bias
+    if skip is not None and _shape(skip, torch.float32, dev, "skip", 1) != rate or \
+            bias is not None and _shape(bias, torch.float32, dev, "dt_bias", 1) != rate:
+        raise ValueError("skip and dt_bias must be [H]")
+    return (T, bshape[1],
+            _lib.ScanInputsC(x.data_ptr(), b.data_ptr(), c.data_ptr(), dt.data_ptr(), xs, bs, cs,
+                             ds, bshape[1], OUT_F32 if kind is torch.float32 else OUT_BF16),
+            _lib.ScanPoolC(pool.s.data_ptr(), n, H, P, N),
+            _lib.ScanWeightsC(weights.rate.data_ptr(), _ptr(skip), _ptr(bias)))
+
+
+def selective_scan_decode(x, dt, b, c, pool: ScanPool, weights: ScanWeights, state_ids=None,
+                          out=None, out_dtype=torch.bfloat16, status=None, stream=None):
+    """One token of a selective scan per request: x [B, H, P], b, c [B, G, N]
+    bf16, dt [B, H] bf16 or fp32; updates the states and returns out
+    [B, H, P]."""
+    dev = _device(x, torch.bfloat16, "x")
+    B, _, ic, pc, wc = _scan_args(x, dt, b, c, pool, weights, dev)
+    ids = None if state_ids is None else _per_request(state_ids, dev, "state_ids", B)
+    if out is None:
+        out = _empty(x.shape, out_dtype, dev, stream)
+    elif _shape(out, out.dtype, dev, "out", 3) != x.shape:
+        raise ValueError("out must have x's shape")
+    _check(lib().phs_selective_scan_decode(ic, pc, wc, ids, B, out.data_ptr(),
+                                           _out_code(out.dtype), _status_ptr(status, dev),
+                                           _raw_stream(stream, dev)), "selective_scan_decode")
+    return out
+
+
+def scan_prompt_workspace_bytes(batch, num_heads, num_groups, head_dim, state_dim, total_tokens,
+                                max_seq_len) -> int:
+    """Workspace bytes for selective_scan_prompt; 0 if unsupported.  For a call
+    of these very sizes: one with fewer requests may need more."""
+    return int(lib().phs_scan_prompt_workspace_bytes(batch, num_heads, num_groups, head_dim,
+                                                     state_dim, total_tokens, max_seq_len))
+
+
+def selective_scan_prompt(x, dt, b, c, cu_seqlens, max_seq_len: int, pool: ScanPool,
+                          weights: ScanWeights, state_ids=None, resume=None, out=None,
+                          workspace=None, status=None, stream=None):
+    """A selective scan over packed prompts: request b has tokens
+    [cu_seqlens[b], cu_seqlens[b + 1]) of x [T, H, P], b, c [T, G, N] bf16 and
+    dt [T, H] bf16 or fp32, starts from its state where resume[b] != 0 (else
+    from zero) and leaves its last state in the pool.  Returns out bf16
+    [T, H, P]; rows of no request are left as they were (unset in an output
+    made here)."""
+    dev = _device(x, torch.bfloat16, "x")
+    B = _shape(cu_seqlens, torch.int32, dev, "cu_seqlens", 1)[0] - 1
+    if B < 0:
+        raise ValueError("cu_seqlens must be [batch + 1]")
+    T, G, ic, pc, wc = _scan_args(x, dt, b, c, pool, weights, dev)
+    ids = None if state_ids is None else _per_request(state_ids, dev, "state_ids", B)
+    again = None if resume is None else _per_request(resume, dev, "resume", B)
+    if out is None:
+        out = _empty(x.shape, torch.bfloat16, dev, stream)
+    elif _shape(out, torch.bfloat16, dev, "out", 3) != x.shape:
+        raise ValueError("out must have x's shape")
+    ws, ws_bytes, _held = _call_memory(
+        workspace, scan_prompt_workspace_bytes(B, pc.num_heads, G, pc.head_dim, pc.state_dim, T,
+                                               max_seq_len), dev, stream)
+    _check(lib().phs_selective_scan_prompt(ic, cu_seqlens.data_ptr(), T, int(max_seq_len), pc, wc,
+                                           ids, again, B, out.data_ptr(), ws, ws_bytes,
+                                           _status_ptr(status, dev), _raw_stream(stream, dev)),
+           "selective_scan_prompt")
     return out

@@ -49,6 +49,33 @@ class StatePoolC(ctypes.Structure):
     _fields_ = [("s", c_vp), ("num_states", c_i64), ("num_kv_heads", c_i32), ("head_dim", c_i32)]
 
 
+class RopeC(ctypes.Structure):
+    _fields_ = [("turns", c_vp), ("rotary_dim", c_i32), ("interleaved", c_i32), ("factor", c_f32)]
+
+
+class ConvPoolC(ctypes.Structure):
+    _fields_ = [("c", c_vp), ("num_states", c_i64), ("channels", c_i32), ("width", c_i32)]
+
+
+class ConvWeightsC(ctypes.Structure):
+    _fields_ = [("weight", c_vp), ("bias", c_vp), ("silu", c_i32)]
+
+
+class ScanPoolC(ctypes.Structure):
+    _fields_ = [("s", c_vp), ("num_states", c_i64), ("num_heads", c_i32), ("head_dim", c_i32),
+                ("state_dim", c_i32)]
+
+
+class ScanWeightsC(ctypes.Structure):
+    _fields_ = [("a", c_vp), ("skip", c_vp), ("dt_bias", c_vp)]
+
+
+class ScanInputsC(ctypes.Structure):
+    _fields_ = [("x", c_vp), ("b", c_vp), ("c", c_vp), ("dt", c_vp), ("x_stride", c_i64),
+                ("b_stride", c_i64), ("c_stride", c_i64), ("dt_stride", c_i64),
+                ("num_groups", c_i32), ("dt_dtype", c_i32)]
+
+
 _P = ctypes.POINTER
 _SIGS = {
     "phs_version": (c_i32, []),
@@ -113,6 +140,26 @@ _SIGS = {
     "phs_linear_attn_prompt": (ctypes.c_int, [c_vp, c_i32, c_vp, c_vp, c_vp, c_i32, c_i32,
                                               _P(StatePoolC), c_vp, c_vp, c_vp, c_i32, c_f32, c_vp,
                                               c_vp, c_size, c_vp, c_vp]),
+    "phs_rope_rotate": (ctypes.c_int, [c_vp, c_i64, c_i32, c_vp, c_i64, c_i32, c_i32, c_i32, c_vp,
+                                       _P(RopeC), c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "phs_kv_write_paged": (ctypes.c_int, [_P(PagedPoolC), c_vp, c_i64, c_vp, c_i64, c_i32, c_vp,
+                                          c_vp, c_i32, c_vp, c_i32, _P(RopeC), c_vp, c_i64, c_i32,
+                                          c_vp, _P(Int8PoolC), c_vp, c_i32, c_vp, c_vp, c_i32,
+                                          c_vp, c_vp, c_vp]),
+    "phs_kv_read_paged": (ctypes.c_int, [_P(PagedPoolC), c_vp, c_i32, c_vp, c_vp, c_i32, c_i32,
+                                         c_i32, _P(Int8PoolC), c_vp, c_i32, c_vp, c_vp, c_vp, c_vp,
+                                         c_vp]),
+    "phs_causal_conv_decode": (ctypes.c_int, [c_vp, c_i64, _P(ConvPoolC), _P(ConvWeightsC), c_vp,
+                                              c_i32, c_vp, c_vp, c_vp]),
+    "phs_causal_conv_prompt": (ctypes.c_int, [c_vp, c_i64, c_vp, c_i32, _P(ConvPoolC),
+                                              _P(ConvWeightsC), c_vp, c_vp, c_i32, c_vp, c_vp,
+                                              c_vp]),
+    "phs_selective_scan_decode": (ctypes.c_int, [_P(ScanInputsC), _P(ScanPoolC), _P(ScanWeightsC),
+                                                 c_vp, c_i32, c_vp, c_i32, c_vp, c_vp]),
+    "phs_scan_prompt_workspace_bytes": (c_size, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32]),
+    "phs_selective_scan_prompt": (ctypes.c_int, [_P(ScanInputsC), c_vp, c_i32, c_i32,
+                                                 _P(ScanPoolC), _P(ScanWeightsC), c_vp, c_vp,
+                                                 c_i32, c_vp, c_vp, c_size, c_vp, c_vp]),
     "phs_page_load_refcounts": (ctypes.c_int, [c_vp, c_vp]),
     "phs_radix_remap": (ctypes.c_int, [c_vp, c_vp, c_i64]),
     "phs_page_allocator_create": (c_vp, [c_i64]),

@@ -2,7 +2,7 @@
 // argument validation, TMA tensor-map encoding, split planning, and the
 // hybrid layer-stack driver.  All compute happens in the kernels of
 // phs_decode.cu, phs_swa.cu, phs_prefix.cu, phs_append.cu, phs_quant.cu,
-// phs_pages.cu, phs_diff.cu and phs_linear.cu.
+// phs_pages.cu, phs_diff.cu, phs_linear.cu, phs_write.cu, phs_conv.cu and phs_scan.cu.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -12,6 +12,7 @@
 #include <utility>
 
 #include "phs_internal.h"
+#include "phs_layers.h"
 #include "phs_ops.h"
 
 namespace phs {
@@ -1892,6 +1893,347 @@ int phs_linear_attn_prompt(const void* q, int32_t num_q_heads, const void* k, co
   }
   return launch_linear_prompt(pool->head_dim, tq, tk, tv, to, a,
                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ----------------------------------------- rotary positions, cache writes --
+namespace {
+
+// Rows of `cols` elements at a stride: 16-byte pieces.
+bool bad_rows(int64_t stride, int64_t cols) { return stride < cols || stride % 8 != 0; }
+
+int check_rope(const phs_rope* rope, int D) {
+  if (!rope->turns || rope->rotary_dim <= 0 || !std::isfinite(rope->factor)) return PHS_EINVAL;
+  if (rope->rotary_dim > D) return PHS_ESHAPE;
+  if (rope->rotary_dim % 16 != 0) return PHS_EUNSUPPORTED;
+  return PHS_OK;
+}
+
+void set_rope(WriteArgs& a, const phs_rope* rope) {
+  a.turns = rope->turns;
+  a.rotary = rope->rotary_dim;
+  a.interleaved = rope->interleaved != 0;
+  a.factor = rope->factor;
+}
+
+int run_write(int D, const WriteArgs& a, void* stream) {
+  DevInfo di;
+  const int st = dev_info(di);
+  return st ? st : launch_write(D, a, di.sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int phs_rope_rotate(const void* q, int64_t q_stride, int32_t num_q_heads, const void* k,
+                    int64_t k_stride, int32_t num_kv_heads, int32_t head_dim, int32_t tokens,
+                    const int32_t* positions, const phs_rope* rope, void* q_out,
+                    int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+  if (tokens < 0 || !rope || num_q_heads <= 0 || (k && num_kv_heads <= 0)) return PHS_EINVAL;
+  if ((k == nullptr) != (k_out == nullptr)) return PHS_EINVAL;
+  if (tokens > 0 && (!q || !q_out || !positions)) return PHS_EINVAL;
+  if (head_dim != 64 && head_dim != 128) return PHS_EUNSUPPORTED;
+  const int st = check_rope(rope, head_dim);
+  if (st) return st;
+  const int64_t qc = int64_t{num_q_heads} * head_dim, kc = int64_t{num_kv_heads} * head_dim;
+  if (bad_rows(q_stride, qc) || bad_rows(q_out_stride, qc)) return PHS_ESHAPE;
+  if (k && (bad_rows(k_stride, kc) || bad_rows(k_out_stride, kc))) return PHS_ESHAPE;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out)) return PHS_EALIGN;
+  if (tokens == 0) return PHS_OK;
+  WriteArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  a.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
+  a.k_out = reinterpret_cast<__nv_bfloat16*>(k_out);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_out_stride = k_out_stride;
+  a.positions = positions;
+  a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
+  a.tokens = tokens;
+  set_rope(a, rope);
+  return run_write(head_dim, a, stream);
+}
+
+int phs_kv_write_paged(const phs_paged_pool* pool, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, int32_t tokens, const int32_t* cu_seqlens,
+                       const int32_t* block_table, int32_t max_pages_per_seq,
+                       const int32_t* seq_lens, int32_t batch, const phs_rope* rope,
+                       const void* q, int64_t q_stride, int32_t num_q_heads, void* q_out,
+                       const phs_int8_pool* int8, const int32_t* qtable,
+                       int32_t max_qpages_per_seq, const int32_t* qlens_before,
+                       const int32_t* qlens, int32_t max_qblocks, const int32_t* page_refcount,
+                       int32_t* dev_status, void* stream) {
+  int st = check_paged(pool);
+  if (st) return st;
+  if (tokens < 0 || batch < 0 || max_pages_per_seq <= 0) return PHS_EINVAL;
+  if (tokens > 0 && (!k || !v)) return PHS_EINVAL;
+  if (batch > 0 && (!block_table || !seq_lens)) return PHS_EINVAL;
+  if (!cu_seqlens && tokens != batch) return PHS_ESHAPE;
+  const int D = pool->head_dim;
+  const int64_t kc = int64_t{pool->num_kv_heads} * D;
+  if (tokens > 0 && (bad_rows(k_stride, kc) || bad_rows(v_stride, kc))) return PHS_ESHAPE;
+  if (!aligned16(k) || !aligned16(v)) return PHS_EALIGN;
+  if (rope && (st = check_rope(rope, D))) return st;
+  if (q) {
+    if (!rope || !q_out || num_q_heads <= 0) return PHS_EINVAL;
+    if (bad_rows(q_stride, int64_t{num_q_heads} * D)) return PHS_ESHAPE;
+    if (!aligned16(q) || !aligned16(q_out)) return PHS_EALIGN;
+  }
+  WriteArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (int8) {
+    if ((st = check_int8(int8))) return st;
+    if (int8->num_kv_heads != pool->num_kv_heads || int8->head_dim != D) return PHS_ESHAPE;
+    if (batch > 0 && (!qtable || !qlens_before || !qlens)) return PHS_EINVAL;
+    if (max_qpages_per_seq <= 0 || max_qblocks < 0) return PHS_EINVAL;
+    if (batch > 65535 || max_qblocks > INT32_MAX / 64) return PHS_EUNSUPPORTED;  // the grid
+    a.k_codes = int8->k;
+    a.v_codes = int8->v;
+    a.k_scale = int8->k_scale;
+    a.v_scale = int8->v_scale;
+    a.qtable = qtable;
+    a.qlens_before = qlens_before;
+    a.qlens = qlens;
+    a.num_qpages = int8->num_qpages;
+    a.max_qpages = max_qpages_per_seq;
+    a.max_qblocks = max_qblocks;
+  }
+  if (batch == 0) return PHS_OK;
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  a.v = reinterpret_cast<const __nv_bfloat16*>(v);
+  a.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out_stride = int64_t{num_q_heads} * D;
+  a.cu_seqlens = cu_seqlens;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.page_refcount = page_refcount;
+  a.status = dev_status;
+  a.pool_k = reinterpret_cast<__nv_bfloat16*>(pool->k);
+  a.pool_v = reinterpret_cast<__nv_bfloat16*>(pool->v);
+  a.num_pages = pool->num_pages;
+  a.Hq = q ? num_q_heads : 0;
+  a.Hkv = pool->num_kv_heads;
+  a.tokens = tokens;
+  a.B = batch;
+  a.max_pages = max_pages_per_seq;
+  if (rope) set_rope(a, rope);
+  return run_write(D, a, stream);
+}
+
+int phs_kv_read_paged(const phs_paged_pool* pool, const int32_t* block_table,
+                      int32_t max_pages_per_seq, const int32_t* starts,
+                      const int32_t* cu_seqlens, int32_t batch, int32_t tokens,
+                      int32_t max_tokens, const phs_int8_pool* int8, const int32_t* qtable,
+                      int32_t max_qpages_per_seq, const int32_t* qlens, void* k_out, void* v_out,
+                      int32_t* dev_status, void* stream) {
+  int st = check_paged(pool);
+  if (st) return st;
+  if (batch < 0 || tokens < 0 || max_tokens < 0 || max_pages_per_seq <= 0) return PHS_EINVAL;
+  if (batch > 0 && (!block_table || !starts || !cu_seqlens)) return PHS_EINVAL;
+  if (tokens > 0 && (!k_out || !v_out)) return PHS_EINVAL;
+  if (!aligned16(k_out) || !aligned16(v_out)) return PHS_EALIGN;
+  if (batch > 65535) return PHS_EUNSUPPORTED;  // grid y
+  ReadArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (int8) {
+    if ((st = check_int8(int8))) return st;
+    if (int8->num_kv_heads != pool->num_kv_heads || int8->head_dim != pool->head_dim)
+      return PHS_ESHAPE;
+    if (max_qpages_per_seq <= 0 || (batch > 0 && (!qtable || !qlens))) return PHS_EINVAL;
+    a.k_codes = int8->k;
+    a.v_codes = int8->v;
+    a.k_scale = int8->k_scale;
+    a.v_scale = int8->v_scale;
+    a.qtable = qtable;
+    a.qlens = qlens;
+    a.num_qpages = int8->num_qpages;
+    a.max_qpages = max_qpages_per_seq;
+  }
+  if (batch == 0) return PHS_OK;
+  a.pool_k = reinterpret_cast<const __nv_bfloat16*>(pool->k);
+  a.pool_v = reinterpret_cast<const __nv_bfloat16*>(pool->v);
+  a.block_table = block_table;
+  a.starts = starts;
+  a.cu_seqlens = cu_seqlens;
+  a.status = dev_status;
+  a.k_out = reinterpret_cast<__nv_bfloat16*>(k_out);
+  a.v_out = reinterpret_cast<__nv_bfloat16*>(v_out);
+  a.num_pages = pool->num_pages;
+  a.Hkv = pool->num_kv_heads;
+  a.B = batch;
+  a.tokens = tokens;
+  // (no request has more tokens than there are)
+  a.max_tokens = std::min(max_tokens, tokens);
+  a.max_pages = max_pages_per_seq;
+  return launch_read_back(pool->head_dim, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------- causal convolution, selective scan --
+namespace {
+
+int conv_args(ConvArgs& a, const void* x, int64_t x_stride, const phs_conv_pool* pool,
+              const phs_conv_weights* weights, const int32_t* state_ids, int32_t batch,
+              int32_t tokens, void* out, int32_t* dev_status) {
+  if (!pool || !pool->c || pool->num_states <= 0 || pool->channels <= 0) return PHS_EINVAL;
+  if (!weights || !weights->weight || batch < 0 || tokens < 0) return PHS_EINVAL;
+  if (tokens > 0 && (!x || !out)) return PHS_EINVAL;
+  if (pool->width < 2 || pool->width > 4 || pool->channels % 8 != 0) return PHS_EUNSUPPORTED;
+  if (tokens > 0 && bad_rows(x_stride, pool->channels)) return PHS_ESHAPE;
+  if (!state_ids && batch > pool->num_states) return PHS_ESHAPE;
+  if (!aligned16(x) || !aligned16(out) || !aligned16(pool->c) || !aligned16(weights->weight) ||
+      !aligned16(weights->bias))
+    return PHS_EALIGN;
+  std::memset(&a, 0, sizeof(a));
+  a.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  a.x_stride = x_stride;
+  a.state = reinterpret_cast<__nv_bfloat16*>(pool->c);
+  a.weight = weights->weight;
+  a.bias = weights->bias;
+  a.silu = weights->silu != 0;
+  a.state_ids = state_ids;
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.status = dev_status;
+  a.num_states = pool->num_states;
+  a.channels = pool->channels;
+  a.B = batch;
+  a.tokens = tokens;
+  return PHS_OK;
+}
+
+int scan_args(ScanArgs& a, const phs_scan_inputs* in, const phs_scan_pool* pool,
+              const phs_scan_weights* weights, const int32_t* state_ids, int32_t batch,
+              int32_t tokens, void* out, int32_t out_dtype, int32_t* dev_status) {
+  if (!in || !pool || !pool->s || pool->num_states <= 0 || pool->num_heads <= 0) return PHS_EINVAL;
+  if (!weights || !weights->a || batch < 0 || tokens < 0 || in->num_groups <= 0) return PHS_EINVAL;
+  if (tokens > 0 && (!in->x || !in->b || !in->c || !in->dt || !out)) return PHS_EINVAL;
+  if (out_dtype != PHS_OUT_BF16 && out_dtype != PHS_OUT_F32) return PHS_EINVAL;
+  if (in->dt_dtype != PHS_OUT_BF16 && in->dt_dtype != PHS_OUT_F32) return PHS_EINVAL;
+  const int H = pool->num_heads, G = in->num_groups, P = pool->head_dim, N = pool->state_dim;
+  if (H % G != 0) return PHS_ESHAPE;
+  if ((P != 64 && P != 128) || (N != 64 && N != 128)) return PHS_EUNSUPPORTED;
+  if (H > 65535) return PHS_EUNSUPPORTED;  // grid y
+  if (tokens > 0 && (bad_rows(in->x_stride, int64_t{H} * P) ||
+                     bad_rows(in->b_stride, int64_t{G} * N) ||
+                     bad_rows(in->c_stride, int64_t{G} * N) || in->dt_stride < H))
+    return PHS_ESHAPE;
+  if (!state_ids && batch > pool->num_states) return PHS_ESHAPE;
+  if (!aligned16(in->x) || !aligned16(in->b) || !aligned16(in->c) || !aligned16(out) ||
+      !aligned16(pool->s))
+    return PHS_EALIGN;
+  std::memset(&a, 0, sizeof(a));
+  a.x = reinterpret_cast<const __nv_bfloat16*>(in->x);
+  a.b = reinterpret_cast<const __nv_bfloat16*>(in->b);
+  a.c = reinterpret_cast<const __nv_bfloat16*>(in->c);
+  a.dt = in->dt;
+  a.x_stride = in->x_stride;
+  a.b_stride = in->b_stride;
+  a.c_stride = in->c_stride;
+  a.dt_stride = in->dt_stride;
+  a.dt_f32 = in->dt_dtype == PHS_OUT_F32;
+  a.state = pool->s;
+  a.rate = weights->a;
+  a.skip = weights->skip;
+  a.dt_bias = weights->dt_bias;
+  a.state_ids = state_ids;
+  a.out = out;
+  a.status = dev_status;
+  a.num_states = pool->num_states;
+  a.H = H;
+  a.G = G;
+  a.B = batch;
+  a.out_f32 = out_dtype == PHS_OUT_F32;
+  return PHS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int phs_causal_conv_decode(const void* x, int64_t x_stride, const phs_conv_pool* pool,
+                           const phs_conv_weights* weights, const int32_t* state_ids,
+                           int32_t batch, void* out, int32_t* dev_status, void* stream) {
+  ConvArgs a;
+  const int st =
+      conv_args(a, x, x_stride, pool, weights, state_ids, batch, batch, out, dev_status);
+  if (st) return st;
+  if (batch > 65535) return PHS_EUNSUPPORTED;  // grid y
+  if (batch == 0) return PHS_OK;
+  return launch_conv_decode(pool->width, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int phs_causal_conv_prompt(const void* x, int64_t x_stride, const int32_t* cu_seqlens,
+                           int32_t total_tokens, const phs_conv_pool* pool,
+                           const phs_conv_weights* weights, const int32_t* state_ids,
+                           const int32_t* resume, int32_t batch, void* out, int32_t* dev_status,
+                           void* stream) {
+  ConvArgs a;
+  const int st =
+      conv_args(a, x, x_stride, pool, weights, state_ids, batch, total_tokens, out, dev_status);
+  if (st) return st;
+  if (!cu_seqlens) return PHS_EINVAL;
+  if (batch == 0) return PHS_OK;
+  a.cu_seqlens = cu_seqlens;
+  a.resume = resume;
+  return launch_conv_prompt(pool->width, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int phs_selective_scan_decode(const phs_scan_inputs* in, const phs_scan_pool* pool,
+                              const phs_scan_weights* weights, const int32_t* state_ids,
+                              int32_t batch, void* out, int32_t out_dtype, int32_t* dev_status,
+                              void* stream) {
+  ScanArgs a;
+  const int st = scan_args(a, in, pool, weights, state_ids, batch, batch, out, out_dtype,
+                           dev_status);
+  if (st || batch == 0) return st;
+  return launch_scan_decode(pool->head_dim, pool->state_dim, a,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t phs_scan_prompt_workspace_bytes(int32_t batch, int32_t num_heads, int32_t num_groups,
+                                       int32_t head_dim, int32_t state_dim, int32_t total_tokens,
+                                       int32_t max_seq_len) {
+  if (batch < 0 || total_tokens < 0 || max_seq_len < 0 || num_heads <= 0 || num_groups <= 0 ||
+      num_heads % num_groups != 0 || (head_dim != 64 && head_dim != 128) ||
+      (state_dim != 64 && state_dim != 128))
+    return 0;
+  return 256;
+}
+
+int phs_selective_scan_prompt(const phs_scan_inputs* in, const int32_t* cu_seqlens,
+                              int32_t total_tokens, int32_t max_seq_len,
+                              const phs_scan_pool* pool, const phs_scan_weights* weights,
+                              const int32_t* state_ids, const int32_t* resume, int32_t batch,
+                              void* out, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream) {
+  ScanArgs a;
+  int st = scan_args(a, in, pool, weights, state_ids, batch, total_tokens, out, PHS_OUT_BF16,
+                     dev_status);
+  if (st) return st;
+  if (!cu_seqlens || max_seq_len < 0) return PHS_EINVAL;
+  if (batch == 0) return PHS_OK;
+  if ((st = check_workspace(workspace, workspace_bytes,
+                            phs_scan_prompt_workspace_bytes(
+                                batch, a.H, a.G, pool->head_dim, pool->state_dim, total_tokens,
+                                max_seq_len))))
+    return st;
+  a.cu_seqlens = cu_seqlens;
+  a.resume = resume;
+  a.total_tokens = total_tokens;
+  a.max_seq = max_seq_len;
+  return launch_scan_prompt(pool->head_dim, pool->state_dim, a,
+                            reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

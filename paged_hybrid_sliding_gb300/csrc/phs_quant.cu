@@ -22,54 +22,9 @@
 // in shared memory and writes its half (2 KB, contiguous).
 #include "phs_common.cuh"
 #include "phs_internal.h"
+#include "phs_quant.cuh"
 
 namespace phs {
-
-// Magic-number rounding: for |y| < 2^22, fl(y + 1.5 * 2^23) rounds y to the
-// nearest integer (ties to even, the default rounding) and keeps it in the
-// low mantissa bits.  With 128 added to the constant (128 is even, so the
-// ties still go to even) the low byte of the sum's bits is the stored byte
-// x + 128.
-constexpr float kRoundMagicOffset = 12582912.0f + 128.0f;
-
-// Packed fp32 pairs (two lanes of work per instruction on the FMA pipe,
-// each rounded to nearest as the scalar instruction would) and the
-// three-input min / max.
-__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f2_unpack(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float fmin3(float a, float b, float c) {
-  float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 
 template <int D>
 // CTAs per SM: each holds its four source pages in shared memory (20.6 KB
@@ -156,17 +111,8 @@ __global__ void __launch_bounds__(128, PHS_QUANT_MIN_CTAS) phs_quant_kernel(cons
   amax = fmaxf(s_amax[2 * which], s_amax[2 * which + 1]);  // whole 32-token group
   const float s = __fdiv_rn(amax, 127.0f);
   const float rs = s != 0.f ? __fdiv_rn(1.0f, s) : 0.f;
-  // code = rint(x / s) with x / s the IEEE quotient.  y = x * fl(1/s) is
-  // within |x/s| * (2^-23 + 2^-48) + ulp/2 <= 1.9e-5 of that quotient (|x/s|
-  // <= 127.5), so rint(y) equals rint(x / s) unless y lies within 1.9e-5 of
-  // a half-integer: a group of 8 codes holding such an element takes the
-  // IEEE division for all 8 (rare).  A scale so small that 1/s overflows
-  // (subnormal groups) always divides.  |rint(x / s)| <= 127 by
-  // construction, so no clamp is needed.  s == 0 gives rs == 0 and every
-  // code 0.  The rounding steps run on packed pairs (two elements per
-  // instruction, each rounded as the scalar operation would be).
   const bool always_divide = !(rs < INFINITY);
-  const uint64_t rs2 = f2_pack(rs, rs), magic2 = f2_pack(kRoundMagicOffset, kRoundMagicOffset);
+  const uint64_t rs2 = f2_pack(rs, rs);
   const size_t block = static_cast<size_t>(qp) * a.Hkv + h;  // (block, head) of 32 x D codes
   // K: straight to the pool; V: into the shared token-major tile
   uint2* out = which ? reinterpret_cast<uint2*>(s_v + kPage * half * D)
@@ -175,36 +121,7 @@ __global__ void __launch_bounds__(128, PHS_QUANT_MIN_CTAS) phs_quant_kernel(cons
   for (int it = 0; it < kIters; ++it) {
     const uint4 xv = stile[it * 32 + lane];
     const uint32_t* v = reinterpret_cast<const uint32_t*>(&xv);
-    uint32_t t[8];  // fl(rint(code) + 1.5 * 2^23): the code in the low byte
-    float dmax = 0.f, dmin = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      // bf16 pair -> fp32 pair: the bf16 bits are the high half of the fp32
-      const uint64_t f = f2_pack(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xFFFF0000u));
-      const uint64_t y = f2_mul(f, rs2);
-      const uint64_t tt = f2_add(y, magic2);
-      const uint64_t d = f2_sub(y, f2_sub(tt, magic2));  // y - rint(y), in [-1/2, 1/2]
-      const float2 dd = f2_unpack(d), tf = f2_unpack(tt);
-      dmax = fmax3(dmax, dd.x, dd.y);
-      dmin = fmin3(dmin, dd.x, dd.y);
-      t[2 * k] = __float_as_uint(tf.x);
-      t[2 * k + 1] = __float_as_uint(tf.y);
-    }
-    if (always_divide || dmax > 0.4999f || dmin < -0.4999f) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xv = __uint_as_float(e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16);
-        t[e] = __float_as_uint(__fadd_rn(rintf(__fdiv_rn(xv, s)), kRoundMagicOffset));
-      }
-    }
-    uint32_t w[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t lo = __byte_perm(t[4 * k], t[4 * k + 1], 0x0040);
-      const uint32_t hi = __byte_perm(t[4 * k + 2], t[4 * k + 3], 0x0040);
-      w[k] = __byte_perm(lo, hi, 0x5410);
-    }
-    out[it * 32 + lane] = make_uint2(w[0], w[1]);
+    out[it * 32 + lane] = quant_codes8(v, s, rs2, always_divide);
   }
   if (threadIdx.x == 64 * which && half == 0) scales[block] = s;
   if (which) {
