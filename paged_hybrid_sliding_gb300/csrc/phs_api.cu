@@ -2157,6 +2157,69 @@ int scan_args(ScanArgs& a, const phs_scan_inputs* in, const phs_scan_pool* pool,
   return PHS_OK;
 }
 
+// How a prompt call is spread over the SMs: 64-wide heads in pairs where a
+// group has an even number of them, segments of each prompt, and parts that a
+// first launch sums a segment up in.  Of no segments and as many as leave each
+// CTA an SM to itself the plan with the least time is taken, by these costs in
+// half microseconds: 16 for a CTA (of either launch); for each chunk 4 for
+// its state (in either launch) and 4 for the rows of each slot; 4 for joining
+// the sums.
+struct ScanPlan {
+  int slots = 1, units = 1, nseg = 1, nsub = 1;
+  size_t tables = 0, sums = 0, need = 0;  // bytes
+};
+ScanPlan scan_plan(int B, int H, int G, int P, int N, int total, int max_seq, int sms) {
+  ScanPlan p;
+  p.slots = P == 128 || H / G % 2 == 0 ? 2 : 1;
+  p.units = H * (P / 64) / p.slots;
+  const long long pairs = std::max(1LL, 1LL * B * p.units), C = kScanChunk;
+  const long long chunks = (std::min(total, max_seq) + C - 1) / C, chunk = 4 + 4 * p.slots;
+  const long long most = std::max(1LL, std::min(sms / pairs, chunks / 2));
+  long long best = -1;
+  for (const long long s : {1LL, most}) {
+    const long long per = (chunks + s - 1) / s;
+    long long time = 16 + per * chunk, sub = 1;
+    if (s == 1) {  // (a request's last chunk is half full on average)
+      time = std::max(time, (pairs * 16 + p.units * chunk * (total / C + B / 2)) / sms);
+    } else {
+      long long sums = -1;
+      for (long long n = 1; n <= 8 && n <= per; ++n) {
+        const long long waves = ((s - 1) * pairs * n + sms - 1) / sms;
+        const long long t = waves * (16 + 4 * ((per + n - 1) / n));
+        if (sums >= 0 && t >= sums) continue;
+        sums = t;
+        sub = n;
+      }
+      time += sums + 4;
+    }
+    if (best >= 0 && time >= best) continue;
+    best = time;
+    p.nseg = static_cast<int>(s);
+    p.nsub = static_cast<int>(sub);
+  }
+  p.tables = align256((total / C + B + 1) * H * kScanTable * sizeof(float));
+  if (p.nseg > 1)
+    p.sums = align256(static_cast<size_t>(pairs) * p.nseg * p.nsub * 64 * p.slots * N * sizeof(float));
+  p.need = p.tables + p.sums;
+  if (p.nseg > 1) p.need += align256(static_cast<size_t>(pairs) * p.nseg * p.nsub * 2 * sizeof(float));
+  return p;
+}
+
+// [tokens] rows of `cols` bf16 at a stride; boxes of 128 tokens x 64 columns
+int map_bf16_strided(CUtensorMap* m, const void* base, int64_t tokens, int64_t cols,
+                     int64_t stride) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return PHS_ECUDA;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[2] = {64, kScanChunk};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PHS_OK : PHS_ECUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -2208,7 +2271,11 @@ size_t phs_scan_prompt_workspace_bytes(int32_t batch, int32_t num_heads, int32_t
       num_heads % num_groups != 0 || (head_dim != 64 && head_dim != 128) ||
       (state_dim != 64 && state_dim != 128))
     return 0;
-  return 256;
+  DevInfo di;
+  if (dev_info(di)) return 0;
+  return scan_plan(batch, num_heads, num_groups, head_dim, state_dim, total_tokens, max_seq_len,
+                   di.sms)
+      .need;
 }
 
 int phs_selective_scan_prompt(const phs_scan_inputs* in, const int32_t* cu_seqlens,
@@ -2232,8 +2299,36 @@ int phs_selective_scan_prompt(const phs_scan_inputs* in, const int32_t* cu_seqle
   a.resume = resume;
   a.total_tokens = total_tokens;
   a.max_seq = max_seq_len;
-  return launch_scan_prompt(pool->head_dim, pool->state_dim, a,
-                            reinterpret_cast<cudaStream_t>(stream));
+  DevInfo di;
+  if ((st = dev_info(di))) return st;
+  const int P = pool->head_dim, N = pool->state_dim;
+  const ScanPlan plan = scan_plan(batch, a.H, a.G, P, N, total_tokens, max_seq_len, di.sms);
+  a.P = P;
+  a.slots = plan.slots;
+  a.units = plan.units;
+  a.nseg = plan.nseg;
+  a.nsub = plan.nsub;
+  a.max_chunks = (std::min(total_tokens, max_seq_len) + kScanChunk - 1) / kScanChunk;
+  const int64_t ctas = int64_t{batch} * a.units * a.nseg;
+  // (grids: rows along x, tables and sums along y and z)
+  if (ctas > INT32_MAX || batch > 65535 || a.units > 65535) return PHS_EUNSUPPORTED;
+  a.longest_first = ctas > di.sms && batch > 1 && batch <= kScanSort;
+  char* ws = reinterpret_cast<char*>(workspace);
+  a.tables = reinterpret_cast<float*>(ws);
+  a.ws = reinterpret_cast<float*>(ws + plan.tables);
+  a.ws_log = reinterpret_cast<float*>(ws + plan.tables + plan.sums);
+  CUtensorMap tb, tc, tx, to;
+  std::memset(&tb, 0, sizeof(tb));
+  if (total_tokens > 0) {
+    const int64_t hp = int64_t{a.H} * P, gn = int64_t{a.G} * N;
+    if ((st = map_bf16_strided(&tb, a.b, total_tokens, gn, a.b_stride))) return st;
+    if ((st = map_bf16_strided(&tc, a.c, total_tokens, gn, a.c_stride))) return st;
+    if ((st = map_bf16_strided(&tx, a.x, total_tokens, hp, a.x_stride))) return st;
+    if ((st = map_bf16_strided(&to, out, total_tokens, hp, hp))) return st;
+  } else {
+    tc = tx = to = tb;  // no chunk, no copy
+  }
+  return launch_scan_prompt(N, tb, tc, tx, to, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

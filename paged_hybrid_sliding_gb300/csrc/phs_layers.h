@@ -107,9 +107,22 @@ struct ScanArgs {
   const int32_t* cu_seqlens;
   const int32_t* resume;
   int total_tokens, max_seq;
+  int P;
+  int slots, units;     // 64 columns of x each, that go together; such units of a request
+  int nseg, nsub;       // segments of each prompt, parts of a segment
+  int max_chunks;       // of a request
+  bool longest_first;   // CTAs in order of their requests' lengths (B <= kScanSort)
+  float* tables;        // [tokens / 128 + B + 1][H][kScanTable]
+  float* ws;            // [B][units][nseg * nsub][64 slots][N]: sums of parts, then first states
+  float* ws_log;        // [B][units][nseg * nsub][2]: log decays of the parts
 };
 
+constexpr int kScanChunk = 128;  // tokens
+constexpr int kScanTable = 528;  // floats
+constexpr int kScanSort = 256;   // requests of a call that are put in order, at most
+
 int launch_scan_decode(int P, int N, const ScanArgs& a, cudaStream_t stream);
-int launch_scan_prompt(int P, int N, const ScanArgs& a, cudaStream_t stream);
+int launch_scan_prompt(int N, const CUtensorMap& tb, const CUtensorMap& tc, const CUtensorMap& tx,
+                       const CUtensorMap& to, const ScanArgs& a, cudaStream_t stream);
 
 }  // namespace phs
