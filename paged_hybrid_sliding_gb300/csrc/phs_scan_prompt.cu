@@ -24,7 +24,7 @@
 // Sums of l that an exponential is taken of are formed over just their own
 // tokens, never as differences of long sums (but within 32 tokens, for the
 // blocks on the diagonal): exp(L_last - L_j) from sums from the end, the
-// others by blocks of 16 tokens, exp(L_i - L_j) = exp(L_i - L_e) exp(L_e -
+// others by blocks of 32 tokens, exp(L_i - L_j) = exp(L_i - L_e) exp(L_e -
 // L_j), e the last token of j's block.
 //
 // One CTA per (segment, pair of heads, request) walks its chunks in order:
@@ -45,25 +45,30 @@
 #include "phs_prompt.cuh"
 #include "phs_scan.cuh"
 
+#ifndef PHS_SCAN_BEFORE
+#define PHS_SCAN_BEFORE 1
+#endif
+
 namespace phs {
 
 namespace {
 
 constexpr int kScanC = kScanChunk;
 constexpr int kScanThreads = 640;
-// registers a thread: 96 at launch, five warpgroups; 2 x 88 + 2 x 120 + 64 = 5 x 96
-constexpr int kRegsRows = 88, kRegsState = 120, kRegsIssue = 64;
+// registers a thread: 96 at launch, five warpgroups; 2 x 96 + 2 x 120 + 48 = 5 x 96
+constexpr int kRegsRows = 96, kRegsState = 120, kRegsIssue = 48;
 constexpr int kHalf = kScanC * 128;   // 64 columns of a tile: [128 rows][128 bytes]
 constexpr int kTile = 2 * kHalf;      // a place of the ring
 
 // A chunk's table of a head (floats).  Exponents of P in powers of two.
 constexpr int kTabLoc = 0;      // sum of l from its 32 tokens' first one on
-constexpr int kTabStep = 128;   // s_j
-constexpr int kTabCol = 256;    // exp(L_e - L_j) s_j, e the last of j's 16 tokens
+constexpr int kTabDiag = 128;   // the same less log2 s_j
+constexpr int kTabCol = 256;    // exp(L_e - L_j) s_j, e the last of j's 32 tokens
 constexpr int kTabEnd = 384;    // exp(L_last - L_j) s_j
-constexpr int kTabBlock = 512;  // [8] sum of l of 16 tokens
-constexpr int kTabBase = 520;   // [4] sum of l before each 32 tokens
-constexpr int kTabTotal = 524;  // sum of l, natural
+constexpr int kTabBlock = 512;  // [4] sum of l of 32 tokens
+constexpr int kTabBase = 516;   // [4] sum of l before them
+constexpr int kTabTotal = 520;  // sum of l, natural
+constexpr int kTabDecay = 521;  // its decay_factor
 static_assert(kScanTable == 528, "a table");
 
 // Tensor-memory columns: a chunk's sum U, scores (and P), the outputs of both
@@ -83,14 +88,14 @@ struct ScanTmem {
 template <int N, bool STATES>
 struct ScanLayout {
   static constexpr int kPer = STATES ? 2 : 3;  // tiles of a chunk: B, X (C between them)
-  static constexpr int kSlots = STATES || N == 64 ? 6 : 5;
-  static constexpr int kS = kSlots * kTile;  // 2 terms [N / 64][128 rows][128 bytes]
-  static constexpr int kSTerm = kScanC * N * 2;
-  static constexpr int kBar = STATES ? kS : kS + 2 * kSTerm;
+  static constexpr int kSlots = 6;
+  static constexpr int kS = kSlots * kTile;  // the state [N / 64][128 rows][128 bytes]
+  static constexpr int kBar = STATES ? kS : kS + kScanC * N * 2;
   static constexpr int kBars = 2 * kSlots + 2 * ScanTmem<N, STATES>::kRing + 17;
-  static constexpr int kMisc = kBar + kBars * 8;  // tensor-memory base, abort flag
-  static constexpr int kAlloc = kMisc + 16 + 1024;
-  static_assert(kAlloc + 64 <= 227 * 1024, "shared memory of the prompt kernel");
+  static constexpr int kMisc = kBar + kBars * 8;  // tensor-memory base, abort flag, request
+  static constexpr int kCols = (kMisc + 16 + 15) / 16 * 16;  // a rows' warp: 2 rows of 32 floats
+  static constexpr int kAlloc = kCols + (STATES ? 0 : 8 * 256);
+  static_assert(kAlloc <= 227 * 1024, "shared memory of the prompt kernel");
 };
 
 // First chunk of part p of a request's `chunks`; a segment is nsub parts, and
@@ -106,8 +111,7 @@ __device__ __forceinline__ int64_t table_row(int b, int t0) { return t0 / kScanC
 // The request that comes `at`-th when the longest come first.  Where there are
 // more CTAs than SMs, the last ones to start then end soon.  All threads of
 // the CTA call it.
-__device__ __forceinline__ int scan_by_length(const ScanArgs& a, int at) {
-  __shared__ int found;
+__device__ __forceinline__ int scan_by_length(const ScanArgs& a, int at, volatile int* found) {
   static_assert(kScanSort <= kScanThreads, "a thread for each request");
   const int j = threadIdx.x;
   if (j < a.B) {
@@ -119,10 +123,10 @@ __device__ __forceinline__ int scan_by_length(const ScanArgs& a, int at) {
       before += to - from > len || (to - from == len && i < j);
       from = to;
     }
-    if (before == at) found = j;
+    if (before == at) *found = j;
   }
   __syncthreads();
-  return found;
+  return *found;
 }
 
 // ------------------------------------------------------------------ tables --
@@ -155,18 +159,15 @@ __global__ void __launch_bounds__(256) phs_scan_table_kernel(const __grid_consta
       l[e] = 4 * lane + e < v ? fmaxf(s[e] * rate, -128.f) : 0.f;
       own += l[e];
     }
-    // sums of whole lanes: before this one within its 8 (32 tokens), behind it
-    // within its 4 (16 tokens) and within all
-    float pre = own, back16 = own, back = own;
+    // sums of whole lanes: up to this one within its 8 (32 tokens), from it on
+    // within its 8 and within all
+    float pre = own, back32 = own, back = own;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
       const float x = __shfl_up_sync(0xffffffffu, pre, o, 8);
       if ((lane & 7) >= o) pre += x;
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      const float x = __shfl_down_sync(0xffffffffu, back16, o, 4);
-      if ((lane & 3) + o < 4) back16 += x;
+      const float y = __shfl_down_sync(0xffffffffu, back32, o, 8);
+      if ((lane & 7) + o < 8) back32 += y;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -174,44 +175,49 @@ __global__ void __launch_bounds__(256) phs_scan_table_kernel(const __grid_consta
       if (lane + o < 32) back += x;
     }
     const float total = __shfl_sync(0xffffffffu, back, 0);
-    const float block = __shfl_sync(0xffffffffu, back16, lane & 28);  // of these 16 tokens
+    const float block = __shfl_sync(0xffffffffu, pre, lane | 7);  // of these 32 tokens
     // the same without this lane's own tokens
-    float after16 = __shfl_down_sync(0xffffffffu, back16, 1, 4);
+    float after32 = __shfl_down_sync(0xffffffffu, back32, 1, 8);
     float after = __shfl_down_sync(0xffffffffu, back, 1);
     float before = __shfl_up_sync(0xffffffffu, pre, 1, 8);
-    if ((lane & 3) == 3) after16 = 0.f;
+    if ((lane & 7) == 7) after32 = 0.f;
     if (lane == 31) after = 0.f;
     if ((lane & 7) == 0) before = 0.f;
     // before each 32 tokens
-    float base = pre;
-    base = __shfl_sync(0xffffffffu, base, lane | 7);  // of these 32 tokens
     float sum = 0.f;
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
-      const float x = __shfl_sync(0xffffffffu, base, 8 * q + 7);
+      const float x = __shfl_sync(0xffffffffu, block, 8 * q);
       if (lane / 8 > q) sum += x;
     }
-    float loc[4], col[4], end[4], run = 0.f;
+    float loc[4], diag[4], col[4], end[4], run = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       run += l[e];
       loc[e] = (before + run) * kLog2e;
+      diag[e] = loc[e] - log2f(s[e]);
     }
     run = 0.f;
 #pragma unroll
     for (int e = 3; e >= 0; --e) {  // sums behind the token
-      col[e] = expf(after16 + run) * s[e];
+      col[e] = expf(after32 + run) * s[e];
       end[e] = expf(after + run) * s[e];
       run += l[e];
     }
     float* tab = a.tables + (row * a.H + h) * kScanTable;
     reinterpret_cast<float4*>(tab + kTabLoc)[lane] = make_float4(loc[0], loc[1], loc[2], loc[3]);
-    reinterpret_cast<float4*>(tab + kTabStep)[lane] = s4;
+    reinterpret_cast<float4*>(tab + kTabDiag)[lane] =
+        make_float4(diag[0], diag[1], diag[2], diag[3]);
     reinterpret_cast<float4*>(tab + kTabCol)[lane] = make_float4(col[0], col[1], col[2], col[3]);
     reinterpret_cast<float4*>(tab + kTabEnd)[lane] = make_float4(end[0], end[1], end[2], end[3]);
-    if ((lane & 3) == 0) tab[kTabBlock + lane / 4] = block * kLog2e;
-    if ((lane & 7) == 0) tab[kTabBase + lane / 8] = sum * kLog2e;
-    if (lane == 0) tab[kTabTotal] = total;
+    if ((lane & 7) == 0) {
+      tab[kTabBlock + lane / 8] = block * kLog2e;
+      tab[kTabBase + lane / 8] = sum * kLog2e;
+    }
+    if (lane == 0) {
+      tab[kTabTotal] = total;
+      tab[kTabDecay] = decay_factor(total);
+    }
   }
 }
 
@@ -228,9 +234,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   using T = ScanTmem<N, STATES>;
   constexpr int kTermWarps = 2;  // that form X' of 32 columns of x
   constexpr int kTermThreads = 128 * kTermWarps;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // (there is no other shared memory)
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
@@ -242,7 +246,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     b = blockIdx.x / of_b;
     unit = i % a.units;
     part = i / a.units * a.nsub;
-    if (a.longest_first) b = scan_by_length(a, b);
+    if (a.longest_first)
+      b = scan_by_length(a, b, reinterpret_cast<volatile int*>(smem + L::kMisc + 8));
   }
   const int col0 = unit * rows;                       // first column of x and of the output
   auto head = [&](int slot) { return (col0 + 64 * slot) / a.P; };
@@ -278,23 +283,26 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     return;
   }
   const int nch = (t1 - t0 + kScanC - 1) / kScanC;
+  const int head0 = head(0), head1 = head(S - 1);
   auto table = [&](int n, int slot) {
-    return tables + (static_cast<int64_t>(n) * a.H + head(slot)) * kScanTable;
+    return tables + (static_cast<int64_t>(n) * a.H + (slot ? head1 : head0)) * kScanTable;
   };
 
-  // barriers: tile loaded / used, X' terms written / used, output tile written,
-  // output of a slot complete, state (the last chunk's sum is read, the state's
-  // terms written, rows behind the last token zero), chunk sum complete, drain,
-  // scores, the inter-chunk part, P and that part ready, outputs read, all of a
-  // chunk's KV issued, its last PV issued
+  // barriers: tile loaded / used, X' terms written / used; of a half of the
+  // scores' columns: scores complete, P (and with the first half the
+  // inter-chunk part) ready, P read; output tile written; state (the last
+  // chunk's sum is read, the state's terms written, rows behind the last token
+  // zero), chunk sum complete; drain; inter-chunk part complete, outputs
+  // complete, outputs read, all of the last chunk's KV issued
   auto bar = [sb](int i) { return sb + L::kBar + 8 * i; };
   constexpr int kB = 2 * L::kSlots, kR = kB + 2 * T::kRing;
   const uint32_t full = bar(0), empty = bar(L::kSlots), xp_full = bar(kB),
-                 xp_empty = bar(kB + T::kRing), y_full = bar(kR), o_done = bar(kR + 2),
-                 s_ready = bar(kR + 4), u_done = bar(kR + 6), drain = bar(kR + 8),
-                 sc_full = bar(kR + 10), qs_done = bar(kR + 11), pv_ready = bar(kR + 12),
-                 o_free = bar(kR + 13), kv_all = bar(kR + 14), pv_issued = bar(kR + 15);
-  static_assert(kR + 17 == L::kBars, "barriers (the first five of these: pairs)");
+                 xp_empty = bar(kB + T::kRing), sc_full = bar(kR), pv_ready = bar(kR + 2),
+                 pv_done = bar(kR + 4), y_full = bar(kR + 6), s_ready = bar(kR + 8),
+                 u_done = bar(kR + 10), drain = bar(kR + 12), qs_done = bar(kR + 14),
+                 o_free = bar(kR + 15), kv_all = bar(kR + 16);
+  const uint32_t o_done = pv_done + 8;  // (PV of the second half is the last)
+  static_assert(kR + 17 == L::kBars, "barriers (the first seven of these: pairs)");
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   if (warp == 16) {
     tmem_alloc(sb + L::kMisc, 512);
@@ -312,20 +320,19 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       mbar_init(xp_empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(sc_full + 8 * i, 1);
+      mbar_init(pv_ready + 8 * i, 256);
+      mbar_init(pv_done + 8 * i, 1);
       mbar_init(y_full + 8 * i, 256);
-      mbar_init(o_done + 8 * i, 1);
       mbar_init(drain + 8 * i, 1);
     }
     for (int i = 0; i < T::kUBufs; ++i) {
       mbar_init(s_ready + 8 * i, 256);
       mbar_init(u_done + 8 * i, STATES ? 1 : 2);  // KV, and QS done with the state's terms
     }
-    mbar_init(sc_full, 1);
     mbar_init(qs_done, 1);
-    mbar_init(pv_ready, 256);
     mbar_init(o_free, 256);
     mbar_init(kv_all, 1);
-    mbar_init(pv_issued, 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -344,6 +351,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   auto tile_c = [](int n) { return L::kPer * n + 1; };
   auto tile_x = [](int n) { return L::kPer * n + L::kPer - 1; };
 
+  constexpr int kBefore = STATES ? 0 : PHS_SCAN_BEFORE;  // parts of a warp before the state
   // parts of a chunk whose places in the ring are free when the state is there
   constexpr int kKnownFree = STATES ? 0 : T::kRing;
 
@@ -393,27 +401,39 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       }
-      ok = before(n);
       constexpr int kParts = kScanC / 16 / T::kSteps;
+      // weights of a step's tokens, a step ahead
+      float2 ahead[2];
+      auto weights_of = [&](int t) {
+        if (mine)
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            ahead[q] = *reinterpret_cast<const float2*>(weight + t + 8 * q);
+      };
+      weights_of(16 * T::kSteps * which);
 #pragma unroll 1
-      for (int p = which; ok && p < kParts; p += kTermWarps) {
+      for (int p = which; ok && p < kParts + kTermWarps; p += kTermWarps) {
+        if (p / kTermWarps == kBefore) ok = before(n);
+        if (!ok || p >= kParts) break;
         // (a wait costs 100 cycles even where it has nothing to wait for: what
         // the last chunk had in the ring is known to be read once its sum is there)
-        if (turn > 0 && p >= kKnownFree)
+        if (turn > 0 && (p / kTermWarps < kBefore || p >= kKnownFree))
           ok = lin_wait_warp(xp_empty + 8 * place, (turn - 1) & 1, abort);
         if (!ok) break;
         tc_fence_after();
         if (mine) {
-#pragma unroll
+#pragma unroll 1
           for (int st = 0; st < T::kSteps; ++st) {
             const int t = 16 * (T::kSteps * p + st);  // first token
+            const float2 now[2] = {ahead[0], ahead[1]};
+            const int t_next = st + 1 < T::kSteps ? t + 16 : t + 16 + 16 * T::kSteps * (kTermWarps - 1);
+            if (t_next < kScanC) weights_of(t_next);
             uint32_t w[3][2][4];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               uint32_t k[4];
               ldsm_x4_t(xt + kcol + (t + 8 * q) * 128, k[0], k[1], k[2], k[3]);
-              const float2 f2w = *reinterpret_cast<const float2*>(weight + t + 8 * q);
-              const uint64_t f = f2(f2w.x, f2w.y);
+              const uint64_t f = f2(now[q].x, now[q].y);
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 uint64_t y = f2_mul(f2_bf16(k[x]), f);
@@ -469,8 +489,18 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             tma_load_2d(place_of(tiles) + hf * kHalf, map, col + 64 * hf, t, full_of(tiles), pol);
           ++tiles;
         };
+        // The ring has no place for a whole chunk ahead: what comes next is
+        // brought as far as L2.
+        auto fetch = [&](const CUtensorMap* map, int col, int halves, int t) {
+          for (int hf = 0; hf < halves; ++hf) tma_prefetch_2d(map, col + 64 * hf, t);
+        };
         for (int n = 0; ok && n < nch; ++n) {
           const int t = t0 + n * kScanC;
+          for (int m = n ? n + 2 : 1; m <= n + 2 && m < nch; ++m) {
+            fetch(&tb, group * N, N / 64, t0 + m * kScanC);
+            if (!STATES) fetch(&tc, group * N, N / 64, t0 + m * kScanC);
+            fetch(&tx, col0, S, t0 + m * kScanC);
+          }
           load(&tb, group * N, N / 64, t);
           if (!STATES && ok) load(&tc, group * N, N / 64, t);
           if (ok) load(&tx, col0, S, t);
@@ -488,11 +518,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       // ----------------------------------------------------------- products
       // (a whole warp walks the chunks and one elected lane issues, so that the
       // compiler keeps what the instructions take in uniform registers)
-      constexpr uint32_t kIdQK = idesc_bf16_f32(128, kScanC, false, false);
+      constexpr uint32_t kIdQK = idesc_bf16_f32(128, 64, false, false);
+      const uint32_t id_qs = S == 2 ? idesc_bf16_f32(128, 128, false, false) : kIdQK;
       constexpr uint32_t kIdKV = idesc_bf16_f32(128, N, false, true);
       constexpr uint32_t kIdPV = idesc_bf16_f32(128, 64, false, true);
-      const uint32_t id_qs = S == 2 ? idesc_bf16_f32(128, 128, false, false)
-                                    : idesc_bf16_f32(128, 64, false, false);
       bool ok = true;
       const bool lead = elect_one();
       auto wait = [&](uint32_t bar, int turn) {
@@ -531,11 +560,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
               ++turn;
             }
           }
-          // (the other warp has issued the last chunk's PV, so it has waited for
-          // that chunk's phase)
-          if (!STATES && n >= 1) wait(pv_issued, n - 1);
           if (ok && lead) {
-            if (!STATES) mbar_arrive(kv_all);
+            // (PV of a chunk with rows behind the last token waits for their zeros)
+            if (!STATES && t1 - t0 < (n + 1) * kScanC) mbar_arrive(kv_all);
             umma_commit(u_done + 8 * ub);
             umma_commit(empty_of(tile_b(n)));
             umma_commit(empty_of(tile_x(n)));
@@ -543,69 +570,71 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           __syncwarp();
         }
       } else {  // QK, QS, PV
+        // By halves of the scores' columns: while the rows' warps form P of one,
+        // the other's PV and the next chunk's QK run.
         const uint64_t ds = sdesc_sw128(sb + L::kS, 16, 1024);
-        int pair = 0;
-        for (int n = 0; ok && n < nch; ++n) {
-          tile_full(tile_b(n));
-          tile_full(tile_c(n));
-          const uint64_t db = sdesc_sw128(place_of(tile_b(n)), 16, 1024);
+        auto issue_qk = [&](int n, int hh) {
+          if (hh == 0) {
+            tile_full(tile_b(n));
+            tile_full(tile_c(n));
+          }
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t db = sdesc_sw128(place_of(tile_b(n)) + hh * (kHalf / 2), 16, 1024);
           const uint64_t dc = sdesc_sw128(place_of(tile_c(n)), 16, 1024);
-          for (int s = 0; ok && s < S; ++s, ++pair) {
-            // P of the last pair is read
-            if (s > 0) wait(o_done, n);
-            else if (n > 0) wait(o_done + 8 * (S - 1), n - 1);
+          if (lead) {
+#pragma unroll 4
+            for (int ks = 0; ks < N / 16; ++ks) {
+              const uint32_t at = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+              umma_bf16(tmem + T::kSc + 64 * hh, dc + at, db + at, kIdQK, ks > 0);
+            }
+            umma_commit(sc_full + 8 * hh);
+            if (hh == 1) umma_commit(empty_of(tile_b(n)));
+          }
+          __syncwarp();
+        };
+        if (nch > 0) {
+          issue_qk(0, 0);
+          if (ok) issue_qk(0, 1);
+        }
+        for (int n = 0; ok && n < nch; ++n) {
+          wait(s_ready, n);
+          if (n > 0) wait(o_free, n - 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dc = sdesc_sw128(place_of(tile_c(n)), 16, 1024);
+          if (lead) {
+#pragma unroll 4
+            for (int ks = 0; ks < N / 16; ++ks) {
+              const uint32_t at = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+              umma_bf16(tmem + T::kOut, dc + at, ds + at, id_qs, ks > 0);
+            }
+            umma_commit(qs_done);
+            umma_commit(u_done);  // the state's terms have been read
+            umma_commit(empty_of(tile_c(n)));
+          }
+          __syncwarp();
+          tile_full(tile_x(n));
+          if (t1 - t0 < (n + 1) * kScanC) wait(kv_all, 0);
+          for (int hh = 0; ok && hh < 2; ++hh) {
+            wait(pv_ready + 8 * hh, n);
             if (!ok) break;
             tc_fence_after();
-            if (lead) {
-#pragma unroll 4
-              for (int ks = 0; ks < N / 16; ++ks) {
-                const uint32_t at = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
-                umma_bf16(tmem + T::kSc, dc + at, db + at, kIdQK, ks > 0);
-              }
-              umma_commit(sc_full);
-              if (s == S - 1) umma_commit(empty_of(tile_b(n)));
-            }
-            __syncwarp();
-            if (s == 0) {
-              wait(s_ready, n);
-              if (n > 0) wait(o_free, n - 1);
-              if (!ok) break;
-              tc_fence_after();
-              if (lead) {
-#pragma unroll 1
-                for (int t = 0; t < 2; ++t)
-#pragma unroll 4
-                  for (int ks = 0; ks < N / 16; ++ks) {
-                    const uint32_t at = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
-                    umma_bf16(tmem + T::kOut, dc + at, ds + (t * L::kSTerm >> 4) + at, id_qs,
-                              t > 0 || ks > 0);
-                  }
-                umma_commit(qs_done);
-                umma_commit(u_done);  // the state's terms have been read
-                umma_commit(empty_of(tile_c(n)));
-              }
-              __syncwarp();
-              tile_full(tile_x(n));
-              wait(kv_all, n);
-            }
-            wait(pv_ready, pair);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t v = sdesc_sw128(place_of(tile_x(n)) + s * kHalf, kHalf, 1024);
+            const uint64_t v = sdesc_sw128(place_of(tile_x(n)) + hh * (kHalf / 2), kHalf, 1024);
             if (lead) {
 #pragma unroll 1
-              for (int t = 0; t < 2; ++t)
-#pragma unroll 4
-                for (int ks = 0; ks < kScanC / 16; ++ks)
-                  umma_bf16_ts(tmem + T::kOut + 64 * s, tmem + T::kSc + 16 * ks + 8 * t,
-                               v + (ks * 2048 >> 4), kIdPV, 1u);
-              umma_commit(o_done + 8 * s);
-              if (s == S - 1) {
-                umma_commit(empty_of(tile_x(n)));
-                mbar_arrive(pv_issued);
-              }
+              for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int ks = 0; ks < kScanC / 32; ++ks)
+                  umma_bf16_ts(tmem + T::kOut + 64 * s,
+                               tmem + T::kSc + 64 * hh + 16 * ks + 8 * s,
+                               v + ((s * kHalf + ks * 2048) >> 4), kIdPV, 1u);
+              umma_commit(pv_done + 8 * hh);
+              if (hh == 1) umma_commit(empty_of(tile_x(n)));
             }
             __syncwarp();
+            wait(pv_done + 8 * hh, n);  // P is read
+            if (ok && n + 1 < nch) issue_qk(n + 1, hh);
           }
         }
       }
@@ -647,108 +676,147 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     regs_dec<kRegsRows>();
     const int qt = warp & 3, half = warp >> 2, i = 32 * qt + lane;  // row
     bool ok = true;
-    int pair = 0;
-    for (int n = 0; ok && n < nch; ++n) {
-      for (int s = 0; ok && s < S; ++s, ++pair) {
+    // What a slot takes from its table for a half of the columns: this row's L
+    // from the end of the column's block on (a block before every row) or from
+    // the block's start (on the diagonal); the column `lane`s factor, or L less
+    // log2 of the step; this row's L from the chunk's start on.  Read ahead.
+    struct Ahead {
+      float row, col, all;
+    } next[2] = {};
+    auto read_ahead = [&](int n, int hh) {
+      if (n >= nch) return;
+      const int kb = 2 * hh + half;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (s >= S) break;
         const float* tab = table(n, s);
-        const float loc = tab[kTabLoc + i], base = tab[kTabBase + qt];
-        const float skip = a.skip ? a.skip[head(s)] : 0.f;
-        ok = lin_wait_warp(sc_full, pair & 1, abort);
-        if (!ok) break;
-        tc_fence_after();
-        // P in place of the scores: 16 columns j of a step of the product
-        // become 8 of term 0 and 8 of term 1.  From the diagonal back, `between`
-        // the sum of the blocks between the step's and the row's 32 tokens.
-        float between = 0.f;
-        if (half == 0 && qt > 0) between = tab[kTabBlock + 2 * qt - 1];
-#pragma unroll 1
-        for (int st = 6 + half; st >= 0; st -= 2) {
-          uint32_t p[16];
-          if (st > 2 * qt + 1) {  // behind every row of the warp
+        const float4 blocks = *reinterpret_cast<const float4*>(tab + kTabBlock);
+        const float loc = tab[kTabLoc + i];
+        next[s].row = loc + ((kb == 0 && qt > 1 ? blocks.y : 0.f) +
+                             (kb <= 1 && qt > 2 ? blocks.z : 0.f));
+        if (hh == 0) next[s].all = loc + tab[kTabBase + qt];
+        if (kb <= qt) next[s].col = tab[(kb < qt ? kTabCol : kTabDiag) + 32 * kb + lane];
+      }
+    };
+    float* const cols = reinterpret_cast<float*>(smem + L::kCols + 256 * warp);
+    // P of a half of the columns in place of the scores: 32 columns a thread,
+    // block kb of 32 tokens; 16 columns of a step of the product become 8 of
+    // each slot
+    auto form_p = [&](int n, int hh) {
+      const int kb = 2 * hh + half;
+      const uint32_t at = my_lanes + T::kSc + 32 * kb;
+      __syncwarp();  // (the last half's columns have been read)
+      cols[lane] = next[0].col;
+      if (S == 2) cols[32 + lane] = next[1].col;
+      __syncwarp();
+      const float f0 = ex2(next[0].row), f1 = ex2(next[1].row);
+      ok = lin_wait_warp(sc_full + 8 * hh, n & 1, abort);
+      if (!ok) return;
+      tc_fence_after();
+      if (kb > qt) {  // behind every row
+        uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) p[e] = 0u;
-          } else {
-            uint32_t sc[16];
-            tmem_ld16(my_lanes + T::kSc + 16 * st, sc);
-            if (st < 2 * qt) {  // before every row
-              const float4* col = reinterpret_cast<const float4*>(tab + kTabCol + 16 * st);
-              const float rf = ex2(loc + between);
-              if (st > 1)
-                between += tab[kTabBlock + st] + tab[kTabBlock + st - 1];
-              tmem_ld_wait();
+        for (int e = 0; e < 16; ++e) p[e] = 0u;
+        tmem_st16(at, p);
+        tmem_st16(at + 16, p);
+        return;
+      }
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 c = col[e];
-                uint64_t x = f2_mul(f2_mul(f2(sc[4 * e], sc[4 * e + 1]), f2(rf, rf)), f2(c.x, c.y));
-                uint64_t y =
-                    f2_mul(f2_mul(f2(sc[4 * e + 2], sc[4 * e + 3]), f2(rf, rf)), f2(c.z, c.w));
-                p[2 * e] = take_term(x);
-                p[8 + 2 * e] = pack_term(x);
-                p[2 * e + 1] = take_term(y);
-                p[8 + 2 * e + 1] = pack_term(y);
-              }
-            } else {
-              const float4* locs = reinterpret_cast<const float4*>(tab + kTabLoc + 16 * st);
-              const float4* steps = reinterpret_cast<const float4*>(tab + kTabStep + 16 * st);
-              const int d = i - 16 * st;
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 c = locs[e], g = steps[e];
-                const float z[4] = {c.x, c.y, c.z, c.w}, w[4] = {g.x, g.y, g.z, g.w};
-                float y[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const int j = 4 * e + k;
-                  y[k] = d >= j ? __uint_as_float(sc[j]) * (ex2(loc - z[k]) * w[k]) : 0.f;
-                  if (d == j) y[k] += skip;
-                }
-                uint64_t x0 = f2(y[0], y[1]), x1 = f2(y[2], y[3]);
-                p[2 * e] = take_term(x0);
-                p[8 + 2 * e] = pack_term(x0);
-                p[2 * e + 1] = take_term(x1);
-                p[8 + 2 * e + 1] = pack_term(x1);
-              }
-            }
-          }
-          tmem_st16(my_lanes + T::kSc + 16 * st, p);
-        }
-        // the part before the chunk, scaled in place
-        if (s == 0) ok = lin_wait_warp(qs_done, n & 1, abort);
-        if (!ok) break;
-        tc_fence_after();
-        const float f = ex2(base + loc);
-        uint32_t o[32];
-        const uint32_t at = my_lanes + T::kOut + 64 * s + 32 * half;
-        tmem_ld32(at, o);
+      for (int k = 0; k < 2; ++k) {
+        uint32_t sc[16];
+        tmem_ld16(at + 16 * k, sc);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 x = f2_get(f2_mul(f2(o[e], o[e + 1]), f2(f, f)));
-          o[e] = __float_as_uint(x.x);
-          o[e + 1] = __float_as_uint(x.y);
+        for (int s = 0; s < 2; ++s) {
+          if (s >= S) break;
+          const float4* c4 = reinterpret_cast<const float4*>(cols + 32 * s + 16 * k);
+          uint32_t p[8];
+          if (kb < qt) {
+            const uint64_t f = s ? f2(f1, f1) : f2(f0, f0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 c = c4[e];
+              const uint32_t* x = sc + 4 * e;
+              p[2 * e] = pack_term(f2_mul(f2_mul(f2(x[0], x[1]), f), f2(c.x, c.y)));
+              p[2 * e + 1] = pack_term(f2_mul(f2_mul(f2(x[2], x[3]), f), f2(c.z, c.w)));
+            }
+          } else {
+            const float row = next[s].row, skip = a.skip ? a.skip[s ? head1 : head0] : 0.f;
+            const int d = lane - 16 * k;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 c = c4[e];
+              const float z[4] = {c.x, c.y, c.z, c.w};
+              float y[4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const int j = 4 * e + m;
+                y[m] = __uint_as_float(sc[j]) * ex2(row - z[m]);
+                y[m] = d >= j ? y[m] + (d == j ? skip : 0.f) : 0.f;
+              }
+              p[2 * e] = pack_bf16(y[0], y[1]);
+              p[2 * e + 1] = pack_bf16(y[2], y[3]);
+            }
+          }
+          tmem_st8(at + 16 * k + 8 * s, p);
         }
-        tmem_st32(at, o);
+      }
+    };
+    read_ahead(0, 0);
+#pragma unroll 1
+    for (int n = 0; ok && n < nch; ++n) {
+#pragma unroll 1
+      for (int hh = 0; hh < 2; ++hh) {
+        form_p(n, hh);
+        if (!ok) break;
+        const float all[2] = {next[0].all, next[1].all};
+        read_ahead(n + hh, hh ^ 1);
+        if (hh == 0) {  // the part before the chunk, scaled in place
+          ok = lin_wait_warp(qs_done, n & 1, abort);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (s >= S) break;
+            const float f = ex2(all[s]);
+            uint32_t o[32];
+            const uint32_t at = my_lanes + T::kOut + 64 * s + 32 * half;
+            tmem_ld32(at, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = f2_get(f2_mul(f2(o[e], o[e + 1]), f2(f, f)));
+              o[e] = __float_as_uint(x.x);
+              o[e + 1] = __float_as_uint(x.y);
+            }
+            tmem_st32(at, o);
+          }
+        }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(pv_ready);
+        mbar_arrive(pv_ready + 8 * hh);
       }
       // output rows: a whole chunk's go through shared memory (in place of C,
       // whose products are complete) and TMA; the rows behind a last token are
       // another request's
+      ok = ok && lin_wait_warp(o_done, n & 1, abort);
+      if (!ok) break;
+      tc_fence_after();
       const int t = t0 + n * kScanC + i;
       const bool whole = t0 + (n + 1) * kScanC <= t1;
       const uint32_t row = place_of(tile_c(n)) + i * 128;
       uint4* to_row = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
                                                static_cast<size_t>(t) * a.H * a.P + col0);
-#pragma unroll 1
-      for (int s = 0; ok && s < S; ++s) {
-        ok = lin_wait_warp(o_done + 8 * s, n & 1, abort);
-        if (!ok) break;
-        tc_fence_after();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (s >= S) break;
         uint32_t o[32], y[16];
         tmem_ld32(my_lanes + T::kOut + 64 * s + 32 * half, o);
         tmem_ld_wait();
+        if (s == S - 1) {
+          tc_fence_before();
+          mbar_arrive(o_free);
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           y[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
@@ -762,9 +830,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             to_row[8 * s + u] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
         }
       }
-      if (!ok) break;
-      tc_fence_before();
-      mbar_arrive(o_free);
       if (whole) fence_proxy_async_smem();
       mbar_arrive(y_full + 8 * (n & 1));
     }
@@ -803,7 +868,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       }
     }
     bool ok = true;
-    float log = 0.f;  // of the part's decay
+    float log = 0.f;                           // of the part's decay
+    float decay = mine && nch > 0 ? table(0, qt >> 1)[kTabDecay] : 0.f;  // a chunk ahead
     // R <- state after chunk n (n >= 0), and where `terms` its two terms to
     // shared memory for the next chunk's QS (the last one has read its own
     // by then: the chunk's sum was issued after it)
@@ -811,9 +877,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       const int ub = n >= 0 ? n % T::kUBufs : 0;
       uint64_t factor = 0ull, base = 0ull;
       if (n >= 0 && mine) {
-        const float x = table(n, qt >> 1)[kTabTotal];
-        const float d = decay_factor(x), one = is_small_decay(d) ? 1.f : 0.f;
-        log += x;
+        const float d = decay, one = is_small_decay(d) ? 1.f : 0.f;
+        if (n + 1 < nch) decay = table(n + 1, qt >> 1)[kTabDecay];
+        if (STATES) log += table(n, qt >> 1)[kTabTotal];
         factor = f2(d, d);
         base = f2(one, one);
       }
@@ -825,30 +891,23 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       if (mine) {
         const uint32_t my_row = sb + L::kS + r * 128;
 #pragma unroll
-        for (int c = 0; c < M / 32; ++c) {
+        for (int c = 0; c < M / 16; ++c) {
           if (n >= 0) {
-            uint32_t u[32];
-            tmem_ld32(my_lanes + T::kU + N * ub + half * M + 32 * c, u);
+            uint32_t u[16];
+            tmem_ld16(my_lanes + T::kU + N * ub + half * M + 16 * c, u);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              R[16 * c + e] = f2_add(f2_fma(R[16 * c + e], factor, f2_mul(R[16 * c + e], base)),
-                                     f2(u[2 * e], u[2 * e + 1]));
+            for (int e = 0; e < 8; ++e)
+              R[8 * c + e] = f2_add(f2_fma(R[8 * c + e], factor, f2_mul(R[8 * c + e], base)),
+                                    f2(u[2 * e], u[2 * e + 1]));
           }
           if (terms) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint64_t x = R[16 * c + 4 * k + e];
-                hi[e] = take_term(x);
-                lo[e] = pack_term(x);
-              }
-              const int u = half * (M / 8) + 4 * c + k;  // 16 bytes of the row
-              const uint32_t at = my_row + (u >> 3) * kHalf + (((u ^ r) & 7) << 4);
-              sts128(at, hi[0], hi[1], hi[2], hi[3]);
-              sts128(at + L::kSTerm, lo[0], lo[1], lo[2], lo[3]);
+            for (int k = 0; k < 2; ++k) {
+              const uint64_t* x = R + 8 * c + 4 * k;
+              const int u = half * (M / 8) + 2 * c + k;  // 16 bytes of the row
+              sts128(my_row + (u >> 3) * kHalf + (((u ^ r) & 7) << 4), pack_term(x[0]),
+                     pack_term(x[1]), pack_term(x[2]), pack_term(x[3]));
             }
           }
         }

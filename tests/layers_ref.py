@@ -120,16 +120,16 @@ def scan_bounds(ref, mag, smag, log, out_dtype, N, chunked):
     decay|) times that.  Chunks of 128 sum the log decays: a sum is off by 16
     roundings of 2^-24 of the chunk's absolute sum X, a difference of two by
     twice that, which is what its exponential is off by, and as many for each
-    chunk; steps are off by 2^-22.  Products of an output hold states and
-    weights to 16 bits (three such operands, with their sums 2^-13), a state's
-    to 24."""
+    chunk; steps are off by 2^-22.  Products of an output hold the weights of a
+    chunk's own tokens and the state before it to bf16 (half a step, 2^-8 of
+    each), a state's products hold 24 bits."""
     T = log.shape[0]
     big = float(log.abs().max()) if T else 0.0
     rel = (T + 8) * 2.0 ** -22 * (1 + big)
     if chunked and T:
         X = max(float(log[i:i + 128].abs().sum(0).max()) for i in range(0, T, 128))
         rel = rel + (T // 128 + 1) * 2.0 ** -19 * X
-    soft = 2.0 ** -13 if chunked else 0.0
+    soft = 2.0 ** -8 if chunked else 0.0
     return mag * (rel + N * 2.0 ** -23 + soft) + ref.abs() * half_step(out_dtype), smag * rel
 
 
