@@ -711,9 +711,11 @@ int phs_kv_read_paged(const phs_paged_pool *pool, const int32_t *block_table,
  * a (fp32 [H], <= 0) the rate, skip and dt_bias fp32 [H] or NULL (zero).  x
  * bf16 [tokens][H][P], b and c bf16 [tokens][G][N], dt bf16 or fp32
  * [tokens][H] (any stride of at least H); out dense [tokens][H][P].  P and N
- * 64 or 128.  softplus(x) = x above 20.  States are fp32 and stay so;
- * phs_selective_scan_prompt takes states and weights into its products to 16
- * bits (24 for what goes into the state).  In a prompt an infinite or NaN
+ * 64 or 128.  softplus(x) = x above 20.  States are fp32 and stay so: what goes
+ * into them has 24 bits.  phs_selective_scan_prompt forms its bf16 rows from
+ * chunks of 128 tokens: the weights of a chunk's own tokens (the skip on their
+ * diagonal) and the state before the chunk enter the products as bf16, sums are
+ * fp32.  A token's log decay is cut at -128.  In a prompt an infinite or NaN
  * value reaches the request's rows from the start of its chunk of 128 tokens
  * on, up to 127 tokens before its own; other requests are not reached.  A
  * request with a bad token range (outside the tokens, or beginning before an

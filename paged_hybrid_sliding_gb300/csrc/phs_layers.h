@@ -118,7 +118,7 @@ struct ScanArgs {
 };
 
 constexpr int kScanChunk = 128;  // tokens
-constexpr int kScanTable = 528;  // floats
+constexpr int kScanTable = 536;  // floats
 constexpr int kScanSort = 256;   // requests of a call that are put in order, at most
 
 int launch_scan_decode(int P, int N, const ScanArgs& a, cudaStream_t stream);

@@ -9,16 +9,18 @@
 // Four matrix products a chunk, on the tensor cores.  Heads of 64 go in pairs
 // (a head of 128 as two halves), so that x, the state and the output are 128
 // rows or columns ("slots" of 64, each with its head's decays):
-//   QK = C B^T     128 x 128 x N    once for each slot, its P in its place
+//   QK = C B^T     128 x 128 x N    once for both slots
 //   QS = C S^T     128 x 128 x N    A = C, B = S                (shared memory)
-//   PV = P X       128 x 64 x 128   A = P in tensor memory, B = X
+//   PV = P X       128 x 64 x 128   for each slot, A = P in tensor memory, B = X
 //   KV = X'^T B    128 x N x 128    A = X'^T in tensor memory, B = B
-// Decays make P and X' (x times exp(L_last - L_j) s_j) values of 24 bits, and
-// the state is an fp32 one.  They enter as sums of bf16 terms: P and S as two
-// (16 bits of each value), X' as three (24 bits: the state is kept in fp32 and
-// must stay one), and B, C and x are exact.  KV is accumulated chunk by chunk
-// from zero and added to the state in fp32 registers: the tensor cores' own
-// sums drop the bits below the running sum's last one.
+// B, C and x are exact.  Decays make P (exp(L_i - L_j) s_j C B^T) a value of 24
+// bits and the state is an fp32 one; both enter the rows' products as bf16: their
+// 2^-9 goes into sums that are rounded to bf16 in the end, an error 1.2 times that
+// rounding's own (two terms of each cost a third of the time: 577 us against 421
+// for 32,751 tokens of 64 heads).  What goes into the state keeps its 24 bits: X'
+// (x times exp(L_last - L_j) s_j) enters as a sum of three bf16 terms, and KV is
+// accumulated chunk by chunk from zero and added to the state in fp32 registers:
+// the tensor cores' own sums drop the bits below the running sum's last one.
 //
 // A first small launch turns the steps into tables for each chunk and head.
 // Sums of l that an exponential is taken of are formed over just their own
@@ -31,8 +33,8 @@
 //   warps 0-7   rows of the chunk, two threads a row: scores -> P, the
 //               inter-chunk part scaled, the output rows
 //   warps 8-15  rows of the state, two threads a row, in registers: state ->
-//               two terms in shared memory, X tile -> X'^T terms (by warps 0-7
-//               where only sums are formed, which have no rows)
+//               shared memory, X tile -> X'^T terms (by warps 0-7 where only sums
+//               are formed, which have no rows)
 //   warp 16     issues KV
 //   warp 17     TMA loads: a ring of B, C and X tiles
 //   warp 18     TMA stores of the output tiles, in C's place
@@ -44,10 +46,6 @@
 // that the segments start from, and the last one forms the rows.
 #include "phs_prompt.cuh"
 #include "phs_scan.cuh"
-
-#ifndef PHS_SCAN_BEFORE
-#define PHS_SCAN_BEFORE 1
-#endif
 
 namespace phs {
 
@@ -65,11 +63,17 @@ constexpr int kTabLoc = 0;      // sum of l from its 32 tokens' first one on
 constexpr int kTabDiag = 128;   // the same less log2 s_j
 constexpr int kTabCol = 256;    // exp(L_e - L_j) s_j, e the last of j's 32 tokens
 constexpr int kTabEnd = 384;    // exp(L_last - L_j) s_j
-constexpr int kTabBlock = 512;  // [4] sum of l of 32 tokens
-constexpr int kTabBase = 516;   // [4] sum of l before them
-constexpr int kTabTotal = 520;  // sum of l, natural
-constexpr int kTabDecay = 521;  // its decay_factor
-static_assert(kScanTable == 528, "a table");
+constexpr int kTabFrom = 512;   // [4][4] of rows in block q for columns in block k <= q, at 4 k + q:
+                                // what is added to kTabLoc for L_i - L_e, on the diagonal for
+                                // L_i - L_m, or kNoRoom
+constexpr int kTabBase = 528;   // [4] sum of l before each 32 tokens
+constexpr int kTabTotal = 532;  // sum of l, natural
+constexpr int kTabDecay = 533;  // its decay_factor
+// On the diagonal exp(L_i - L_j) is a product too, of exp(L_i - L_m) and exp(L_m -
+// L_j), m the 16th of the 32 tokens, unless one of the factors may be above 2^100 (half of the 32 tokens
+// decay by more): then each is taken by itself.
+constexpr float kNoRoom = 1e30f;
+static_assert(kScanTable == 536, "a table");
 
 // Tensor-memory columns: a chunk's sum U, scores (and P), the outputs of both
 // slots, and a ring of parts of X'^T (a step of 16 tokens: 3 terms of 8
@@ -83,6 +87,7 @@ struct ScanTmem {
   static constexpr int kSteps = STATES ? 4 : 1;  // of 16 tokens
   static constexpr uint32_t kPart = 24 * kSteps;
   static constexpr int kRing = (512 - kXp) / kPart;
+  static_assert(kXp + kRing * kPart <= 512, "tensor memory");
 };
 
 template <int N, bool STATES>
@@ -130,28 +135,35 @@ __device__ __forceinline__ int scan_by_length(const ScanArgs& a, int at, volatil
 }
 
 // ------------------------------------------------------------------ tables --
-// One CTA per (chunk, request, 32 heads), a warp four heads, a lane four
-// tokens.  A token's l is cut at -128: exp of that is zero in fp32, and sums
-// that hold more would lose the bits of their neighbours.
-__global__ void __launch_bounds__(256) phs_scan_table_kernel(const __grid_constant__ ScanArgs a) {
-  __shared__ float s_step[32][kScanC + 4];
-  const int b = blockIdx.y, n = blockIdx.x, h0 = blockIdx.z * 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// One CTA per (chunk, request, 16 heads), a warp a head, a lane four tokens.
+// A token's l is cut at -128: exp of that is zero in fp32, and sums that hold
+// more would lose the bits of their neighbours.
+constexpr int kTableHeads = 16;
+__global__ void __launch_bounds__(32 * kTableHeads)
+    phs_scan_table_kernel(const __grid_constant__ ScanArgs a) {
+  __shared__ float s_step[kTableHeads][kScanC + 4];
+  const int b = blockIdx.y, n = blockIdx.x, h0 = blockIdx.z * kTableHeads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = h0 + warp;
   pdl_launch_dependents();
   int t0, t1;
   if (!scan_tokens(a, b, t0, t1) || t0 + n * kScanC >= t1) return;
   const int64_t row = table_row(b, t0) + n;
   t0 += n * kScanC;
   const int v = min(kScanC, t1 - t0);
-  for (int t = warp; t < kScanC; t += 8)
-    s_step[lane][t] = t < v && h0 + lane < a.H ? scan_step(a, t0 + t, h0 + lane) : 0.f;
+  {  // two tokens of a warp at once
+    const int k = lane & (kTableHeads - 1);
+#pragma unroll
+    for (int m = 0; m < kScanC / (2 * kTableHeads); ++m) {
+      const int t = 2 * kTableHeads * m + 2 * warp + lane / kTableHeads;
+      s_step[k][t] = t < v && h0 + k < a.H ? scan_step(a, t0 + t, h0 + k) : 0.f;
+    }
+  }
   __syncthreads();
+  if (h >= a.H) return;
   constexpr float kLog2e = 1.4426950408889634f;
-  for (int k = 0; k < 4; ++k) {
-    const int h = h0 + 4 * warp + k;
-    if (h >= a.H) break;
+  {
     const float rate = a.rate[h];
-    const float4 s4 = *reinterpret_cast<const float4*>(&s_step[4 * warp + k][4 * lane]);
+    const float4 s4 = *reinterpret_cast<const float4*>(&s_step[warp][4 * lane]);
     const float s[4] = {s4.x, s4.y, s4.z, s4.w};
     float l[4], own = 0.f;
 #pragma unroll
@@ -183,13 +195,6 @@ __global__ void __launch_bounds__(256) phs_scan_table_kernel(const __grid_consta
     if ((lane & 7) == 7) after32 = 0.f;
     if (lane == 31) after = 0.f;
     if ((lane & 7) == 0) before = 0.f;
-    // before each 32 tokens
-    float sum = 0.f;
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      const float x = __shfl_sync(0xffffffffu, block, 8 * q);
-      if (lane / 8 > q) sum += x;
-    }
     float loc[4], diag[4], col[4], end[4], run = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -197,6 +202,7 @@ __global__ void __launch_bounds__(256) phs_scan_table_kernel(const __grid_consta
       loc[e] = (before + run) * kLog2e;
       diag[e] = loc[e] - log2f(s[e]);
     }
+    const float first16 = __shfl_sync(0xffffffffu, loc[3], (lane & 24) + 3);
     run = 0.f;
 #pragma unroll
     for (int e = 3; e >= 0; --e) {  // sums behind the token
@@ -210,10 +216,25 @@ __global__ void __launch_bounds__(256) phs_scan_table_kernel(const __grid_consta
         make_float4(diag[0], diag[1], diag[2], diag[3]);
     reinterpret_cast<float4*>(tab + kTabCol)[lane] = make_float4(col[0], col[1], col[2], col[3]);
     reinterpret_cast<float4*>(tab + kTabEnd)[lane] = make_float4(end[0], end[1], end[2], end[3]);
-    if ((lane & 7) == 0) {
-      tab[kTabBlock + lane / 8] = block * kLog2e;
-      tab[kTabBase + lane / 8] = sum * kLog2e;
+    // blocks' sums, by every lane: x[q]
+    float x[4], base = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = __shfl_sync(0xffffffffu, block, 8 * q) * kLog2e;
+    const float half16 = __shfl_sync(0xffffffffu, first16, 8 * (lane & 3));
+    if (lane < 16) {  // lane 4 k + q
+      const int k = lane >> 2, q = lane & 3;
+      float from = 0.f;
+      if (k == q)
+        from = half16 > -100.f && x[q] - half16 > -100.f ? -half16 : kNoRoom;
+#pragma unroll
+      for (int m = 1; m < 3; ++m)
+        if (k < m && m < q) from += x[m];
+      tab[kTabFrom + lane] = from;
     }
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      if (q < lane) base += x[q];
+    if (lane < 4) tab[kTabBase + lane] = base;
     if (lane == 0) {
       tab[kTabTotal] = total;
       tab[kTabDecay] = decay_factor(total);
@@ -351,7 +372,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   auto tile_c = [](int n) { return L::kPer * n + 1; };
   auto tile_x = [](int n) { return L::kPer * n + L::kPer - 1; };
 
-  constexpr int kBefore = STATES ? 0 : PHS_SCAN_BEFORE;  // parts of a warp before the state
+  constexpr int kBefore = STATES ? 0 : 1;  // parts of a warp before the state
   // parts of a chunk whose places in the ring are free when the state is there
   constexpr int kKnownFree = STATES ? 0 : T::kRing;
 
@@ -489,18 +510,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             tma_load_2d(place_of(tiles) + hf * kHalf, map, col + 64 * hf, t, full_of(tiles), pol);
           ++tiles;
         };
-        // The ring has no place for a whole chunk ahead: what comes next is
-        // brought as far as L2.
-        auto fetch = [&](const CUtensorMap* map, int col, int halves, int t) {
-          for (int hf = 0; hf < halves; ++hf) tma_prefetch_2d(map, col + 64 * hf, t);
-        };
         for (int n = 0; ok && n < nch; ++n) {
           const int t = t0 + n * kScanC;
-          for (int m = n ? n + 2 : 1; m <= n + 2 && m < nch; ++m) {
-            fetch(&tb, group * N, N / 64, t0 + m * kScanC);
-            if (!STATES) fetch(&tc, group * N, N / 64, t0 + m * kScanC);
-            fetch(&tx, col0, S, t0 + m * kScanC);
-          }
           load(&tb, group * N, N / 64, t);
           if (!STATES && ok) load(&tc, group * N, N / 64, t);
           if (ok) load(&tx, col0, S, t);
@@ -677,11 +688,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     const int qt = warp & 3, half = warp >> 2, i = 32 * qt + lane;  // row
     bool ok = true;
     // What a slot takes from its table for a half of the columns: this row's L
-    // from the end of the column's block on (a block before every row) or from
-    // the block's start (on the diagonal); the column `lane`s factor, or L less
-    // log2 of the step; this row's L from the chunk's start on.  Read ahead.
+    // from its 32 tokens' first one on, what to add to it, the column `lane`s
+    // factor, L before the 32 tokens.  Read ahead, and only read there: the
+    // warp would wait where it computes with them.
     struct Ahead {
-      float row, col, all;
+      float loc, from, col, base;
     } next[2] = {};
     auto read_ahead = [&](int n, int hh) {
       if (n >= nch) return;
@@ -690,14 +701,15 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       for (int s = 0; s < 2; ++s) {
         if (s >= S) break;
         const float* tab = table(n, s);
-        const float4 blocks = *reinterpret_cast<const float4*>(tab + kTabBlock);
-        const float loc = tab[kTabLoc + i];
-        next[s].row = loc + ((kb == 0 && qt > 1 ? blocks.y : 0.f) +
-                             (kb <= 1 && qt > 2 ? blocks.z : 0.f));
-        if (hh == 0) next[s].all = loc + tab[kTabBase + qt];
-        if (kb <= qt) next[s].col = tab[(kb < qt ? kTabCol : kTabDiag) + 32 * kb + lane];
+        next[s].loc = tab[kTabLoc + i];
+        next[s].base = tab[kTabBase + qt];
+        if (kb <= qt) {
+          next[s].from = tab[kTabFrom + 4 * kb + qt];
+          next[s].col = tab[(kb < qt ? kTabCol : kTabDiag) + 32 * kb + lane];
+        }
       }
     };
+    const float skip0 = a.skip ? a.skip[head0] : 0.f, skip1 = a.skip ? a.skip[head1] : 0.f;
     float* const cols = reinterpret_cast<float*>(smem + L::kCols + 256 * warp);
     // P of a half of the columns in place of the scores: 32 columns a thread,
     // block kb of 32 tokens; 16 columns of a step of the product become 8 of
@@ -705,11 +717,17 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     auto form_p = [&](int n, int hh) {
       const int kb = 2 * hh + half;
       const uint32_t at = my_lanes + T::kSc + 32 * kb;
+      const bool whole = kb < qt || (next[0].from < kNoRoom && next[1].from < kNoRoom);
+      float c0 = next[0].col, c1 = next[1].col;
+      if (kb == qt && whole) {
+        c0 = ex2(-next[0].from - c0);
+        c1 = ex2(-next[1].from - c1);
+      }
       __syncwarp();  // (the last half's columns have been read)
-      cols[lane] = next[0].col;
-      if (S == 2) cols[32 + lane] = next[1].col;
+      cols[lane] = c0;
+      cols[32 + lane] = c1;
       __syncwarp();
-      const float f0 = ex2(next[0].row), f1 = ex2(next[1].row);
+      const float f0 = ex2(next[0].loc + next[0].from), f1 = ex2(next[1].loc + next[1].from);
       ok = lin_wait_warp(sc_full + 8 * hh, n & 1, abort);
       if (!ok) return;
       tc_fence_after();
@@ -721,41 +739,35 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         tmem_st16(at + 16, p);
         return;
       }
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < 2; ++k) {
         uint32_t sc[16];
         tmem_ld16(at + 16 * k, sc);
         tmem_ld_wait();
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (s >= S) break;
+        const int d = lane - 16 * k;  // column of the diagonal
+#pragma unroll 1
+        for (int s = 0; s < S; ++s) {
           const float4* c4 = reinterpret_cast<const float4*>(cols + 32 * s + 16 * k);
+          const uint64_t f = s ? f2(f1, f1) : f2(f0, f0);
           uint32_t p[8];
           if (kb < qt) {
-            const uint64_t f = s ? f2(f1, f1) : f2(f0, f0);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float4 c = c4[e];
               const uint32_t* x = sc + 4 * e;
-              p[2 * e] = pack_term(f2_mul(f2_mul(f2(x[0], x[1]), f), f2(c.x, c.y)));
-              p[2 * e + 1] = pack_term(f2_mul(f2_mul(f2(x[2], x[3]), f), f2(c.z, c.w)));
+              p[2 * e] = pack_term(f2_mul(f2(x[0], x[1]), f2_mul(f, f2(c.x, c.y))));
+              p[2 * e + 1] = pack_term(f2_mul(f2(x[2], x[3]), f2_mul(f, f2(c.z, c.w))));
             }
           } else {
-            const float row = next[s].row, skip = a.skip ? a.skip[s ? head1 : head0] : 0.f;
-            const int d = lane - 16 * k;
+            const float skip = s ? skip1 : skip0, row = s ? next[1].loc : next[0].loc;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 c = c4[e];
-              const float z[4] = {c.x, c.y, c.z, c.w};
-              float y[4];
-#pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                const int j = 4 * e + m;
-                y[m] = __uint_as_float(sc[j]) * ex2(row - z[m]);
-                y[m] = d >= j ? y[m] + (d == j ? skip : 0.f) : 0.f;
-              }
-              p[2 * e] = pack_bf16(y[0], y[1]);
-              p[2 * e + 1] = pack_bf16(y[2], y[3]);
+            for (int e = 0; e < 8; ++e) {
+              const float2 c = reinterpret_cast<const float2*>(c4)[e];
+              const uint64_t own = f2(d == 2 * e ? skip : 0.f, d == 2 * e + 1 ? skip : 0.f);
+              uint64_t w = f2_mul(f, f2(c.x, c.y));
+              if (!whole) w = f2(ex2(row - c.x), ex2(row - c.y));
+              const float2 x = f2_get(f2_fma(f2(sc[2 * e], sc[2 * e + 1]), w, own));
+              p[e] = pack_bf16(d >= 2 * e ? x.x : 0.f, d >= 2 * e + 1 ? x.y : 0.f);
             }
           }
           tmem_st8(at + 16 * k + 8 * s, p);
@@ -769,28 +781,29 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       for (int hh = 0; hh < 2; ++hh) {
         form_p(n, hh);
         if (!ok) break;
-        const float all[2] = {next[0].all, next[1].all};
-        read_ahead(n + hh, hh ^ 1);
         if (hh == 0) {  // the part before the chunk, scaled in place
           ok = lin_wait_warp(qs_done, n & 1, abort);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (s >= S) break;
-            const float f = ex2(all[s]);
+          const float g0 = ex2(next[0].loc + next[0].base), g1 = ex2(next[1].loc + next[1].base);
+          read_ahead(n, 1);
+#pragma unroll 1
+          for (int s = 0; s < S; ++s) {
+            const uint64_t f = s ? f2(g1, g1) : f2(g0, g0);
             uint32_t o[32];
             const uint32_t at = my_lanes + T::kOut + 64 * s + 32 * half;
             tmem_ld32(at, o);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 x = f2_get(f2_mul(f2(o[e], o[e + 1]), f2(f, f)));
+              const float2 x = f2_get(f2_mul(f2(o[e], o[e + 1]), f));
               o[e] = __float_as_uint(x.x);
               o[e + 1] = __float_as_uint(x.y);
             }
             tmem_st32(at, o);
           }
+        } else {
+          read_ahead(n + 1, 0);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -807,29 +820,29 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       const uint32_t row = place_of(tile_c(n)) + i * 128;
       uint4* to_row = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
                                                static_cast<size_t>(t) * a.H * a.P + col0);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s >= S) break;
-        uint32_t o[32], y[16];
+#pragma unroll 1
+      for (int s = 0; s < S; ++s) {
+        uint32_t o[32];
         tmem_ld32(my_lanes + T::kOut + 64 * s + 32 * half, o);
         tmem_ld_wait();
-        if (s == S - 1) {
-          tc_fence_before();
-          mbar_arrive(o_free);
-        }
+        uint4 y[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          y[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+        for (int k = 0; k < 4; ++k) {
+          const float* x = reinterpret_cast<const float*>(o + 8 * k);
+          y[k] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                            pack_bf16(x[6], x[7]));
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int u = 4 * half + k;  // 16 bytes of the slot's row
           if (whole)
-            sts128(row + s * kHalf + (((u ^ i) & 7) << 4), y[4 * k], y[4 * k + 1], y[4 * k + 2],
-                   y[4 * k + 3]);
+            sts128(row + s * kHalf + (((u ^ i) & 7) << 4), y[k].x, y[k].y, y[k].z, y[k].w);
           else if (t < t1)
-            to_row[8 * s + u] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+            to_row[8 * s + u] = y[k];
         }
       }
+      tc_fence_before();
+      mbar_arrive(o_free);
       if (whole) fence_proxy_async_smem();
       mbar_arrive(y_full + 8 * (n & 1));
     }
@@ -870,6 +883,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     bool ok = true;
     float log = 0.f;                           // of the part's decay
     float decay = mine && nch > 0 ? table(0, qt >> 1)[kTabDecay] : 0.f;  // a chunk ahead
+    float total = STATES && mine && nch > 0 ? table(0, qt >> 1)[kTabTotal] : 0.f;
     // R <- state after chunk n (n >= 0), and where `terms` its two terms to
     // shared memory for the next chunk's QS (the last one has read its own
     // by then: the chunk's sum was issued after it)
@@ -878,8 +892,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       uint64_t factor = 0ull, base = 0ull;
       if (n >= 0 && mine) {
         const float d = decay, one = is_small_decay(d) ? 1.f : 0.f;
+        if (STATES) log += total;
         if (n + 1 < nch) decay = table(n + 1, qt >> 1)[kTabDecay];
-        if (STATES) log += table(n, qt >> 1)[kTabTotal];
+        if (STATES && n + 1 < nch) total = table(n + 1, qt >> 1)[kTabTotal];
         factor = f2(d, d);
         base = f2(one, one);
       }
@@ -1011,8 +1026,8 @@ int launch_scan_prompt_t(const CUtensorMap& tb, const CUtensorMap& tc, const CUt
   cfg.attrs = &early;
   cudaError_t err = cudaSuccess;
   if (a.max_chunks > 0) {
-    cfg.gridDim = dim3(a.max_chunks, a.B, (a.H + 31) / 32);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(a.max_chunks, a.B, (a.H + kTableHeads - 1) / kTableHeads);
+    cfg.blockDim = dim3(32 * kTableHeads);
     err = cudaLaunchKernelEx(&cfg, phs_scan_table_kernel, a);
     cfg.numAttrs = 1;
   }
