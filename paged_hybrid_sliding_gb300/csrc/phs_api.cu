@@ -2242,14 +2242,16 @@ int phs_causal_conv_prompt(const void* x, int64_t x_stride, const int32_t* cu_se
                            const int32_t* resume, int32_t batch, void* out, int32_t* dev_status,
                            void* stream) {
   ConvArgs a;
-  const int st =
+  int st =
       conv_args(a, x, x_stride, pool, weights, state_ids, batch, total_tokens, out, dev_status);
   if (st) return st;
   if (!cu_seqlens) return PHS_EINVAL;
   if (batch == 0) return PHS_OK;
   a.cu_seqlens = cu_seqlens;
   a.resume = resume;
-  return launch_conv_prompt(pool->width, a, reinterpret_cast<cudaStream_t>(stream));
+  DevInfo di;
+  if ((st = dev_info(di))) return st;
+  return launch_conv_prompt(pool->width, a, di.sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int phs_selective_scan_decode(const phs_scan_inputs* in, const phs_scan_pool* pool,

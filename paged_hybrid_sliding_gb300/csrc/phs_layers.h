@@ -84,7 +84,7 @@ struct ConvArgs {
 };
 
 int launch_conv_decode(int width, const ConvArgs& a, cudaStream_t stream);
-int launch_conv_prompt(int width, const ConvArgs& a, cudaStream_t stream);
+int launch_conv_prompt(int width, const ConvArgs& a, int num_sms, cudaStream_t stream);
 
 // ---------------------------------------------------------- selective scan --
 struct ScanArgs {

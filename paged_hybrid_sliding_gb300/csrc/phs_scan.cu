@@ -26,22 +26,25 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 // in three shuffles.  The step reads and writes each state once and computes 2
 // operations a byte, so it is bound by memory.
 template <int P, int N>
-__global__ void __launch_bounds__(256) phs_scan_decode_kernel(const ScanArgs a) {
+__global__ void __launch_bounds__(256, 4) phs_scan_decode_kernel(const ScanArgs a) {
   constexpr int R = P / 32, V = N / 32;  // rows of a thread, float4s of a row
   const int b = blockIdx.x, h = blockIdx.y;
-  const int64_t id = scan_state(a, b);
   const size_t orow = (static_cast<size_t>(b) * a.H + h) * P;
-  if (id < 0) {
+  const int r0 = threadIdx.x / 8, l = threadIdx.x % 8, g = h / (a.H / a.G);
+  // the state is on its way while the request's id is checked against others
+  const int64_t at = a.state_ids ? a.state_ids[b] : b;
+  float4* S = reinterpret_cast<float4*>(a.state + (at * a.H + h) * P * N) + r0 * (N / 4) + l;
+  float4 s[R][V];
+  if (at >= 0 && at < a.num_states) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int v = 0; v < V; ++v) s[r][v] = S[r * 8 * N + 8 * v];
+  }
+  if (scan_state(a, b) < 0) {
     if (threadIdx.x < P) store_out(a.out, orow + threadIdx.x, 0.f, a.out_f32);
     return;
   }
-  const int r0 = threadIdx.x / 8, l = threadIdx.x % 8, g = h / (a.H / a.G);
-  float4* S = reinterpret_cast<float4*>(a.state + (id * a.H + h) * P * N) + r0 * (N / 4) + l;
-  float4 s[R][V];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[r][v] = S[r * 8 * N + 8 * v];
   const __nv_bfloat16* bp = a.b + b * a.b_stride + g * N + 4 * l;
   const __nv_bfloat16* cp = a.c + b * a.c_stride + g * N + 4 * l;
   float4 bv[V], cv[V];

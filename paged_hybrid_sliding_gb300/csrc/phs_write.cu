@@ -252,7 +252,7 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 // all of them.  A head's absmax meets in shared memory; V's codes are
 // transposed there.
 template <int D>
-__global__ void __launch_bounds__(2 * D) phs_write_block_kernel(const __grid_constant__ WriteArgs a,
+__global__ void __launch_bounds__(2 * D, D == 128 ? 4 : 8) phs_write_block_kernel(const __grid_constant__ WriteArgs a,
                                                                 int heads_per_cta) {
   constexpr int U = D / 16, kWarps = D / 16;
   __shared__ uint32_t s_max[kWarps];
@@ -475,19 +475,32 @@ __global__ void __launch_bounds__(128) phs_read_back_kernel(const __grid_constan
   };
   const int half = p0 % kQBlock / kPage;
   const size_t block0 = static_cast<size_t>(page) * a.Hkv;
-  for (int e = tid; e < a.Hkv * count * (V / 2); e += 128) {  // K: 16 codes of a token
-    const int h = e / (count * (V / 2)), c = e % (count * (V / 2)), t = c / (V / 2), v = c % (V / 2);
-    const uint4 x = reinterpret_cast<const uint4*>(
-        a.k_codes + ((block0 + h) * kQBlock + 16 * half + first + t) * D)[v];
-    const float s = a.k_scale[block0 + h];
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
-    uint32_t y[8];
+  const int cells = count * (V / 2);  // K: 16 codes of a token, four at once
+  for (int e0 = tid; e0 < a.Hkv * cells; e0 += 4 * 128) {
+    uint4 x[4];
+    float s[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      y[i] = pack_bf16(value(w[i / 2], 2 * (i & 1), s), value(w[i / 2], 2 * (i & 1) + 1, s));
-    uint4* to = ko + t * per + h * V + 2 * v;
-    to[0] = make_uint4(y[0], y[1], y[2], y[3]);
-    to[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    for (int j = 0; j < 4; ++j) {
+      const int e = e0 + 128 * j, h = e / cells, c = e % cells;
+      if (e < a.Hkv * cells) {
+        x[j] = reinterpret_cast<const uint4*>(
+            a.k_codes + ((block0 + h) * kQBlock + 16 * half + first) * D)[c];
+        s[j] = a.k_scale[block0 + h];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = e0 + 128 * j, h = e / cells, c = e % cells, t = c / (V / 2), v = c % (V / 2);
+      if (e >= a.Hkv * cells) break;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[j]);
+      uint32_t y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        y[i] = pack_bf16(value(w[i / 2], 2 * (i & 1), s[j]), value(w[i / 2], 2 * (i & 1) + 1, s[j]));
+      uint4* to = ko + t * per + h * V + 2 * v;
+      to[0] = make_uint4(y[0], y[1], y[2], y[3]);
+      to[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
   }
   for (int e = tid; e < a.Hkv * V; e += 128) {  // V: 8 dims of the half's tokens
     const int h = e / V, v = e % V;
@@ -511,7 +524,7 @@ __global__ void __launch_bounds__(128) phs_read_back_kernel(const __grid_constan
 }
 
 template <int D>
-int launch_write_t(const WriteArgs& a, cudaStream_t stream) {
+int launch_write_t(const WriteArgs& a, int num_sms, cudaStream_t stream) {
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
@@ -525,7 +538,12 @@ int launch_write_t(const WriteArgs& a, cudaStream_t stream) {
     cfg.numAttrs = 1;  // the blocks start beside the tokens: they share no memory
   }
   if (a.k_codes && a.B > 0 && a.max_qblocks > 0) {
-    const int per = 4, groups = (a.Hkv + per - 1) / per;
+    // all heads of a block by one CTA, which forms their angles once, unless
+    // that leaves SMs without one
+    int per = a.Hkv;
+    while (per > 2 && int64_t{a.max_qblocks} * a.B * ((a.Hkv + per - 1) / per) < int64_t{8} * num_sms)
+      per = (per + 1) / 2;
+    const int groups = (a.Hkv + per - 1) / per;
     cfg.gridDim = dim3(a.max_qblocks * groups, a.B);
     cfg.blockDim = dim3(2 * D);
     if (cudaLaunchKernelEx(&cfg, phs_write_block_kernel<D>, a, per) != cudaSuccess)
@@ -539,7 +557,8 @@ int launch_write_t(const WriteArgs& a, cudaStream_t stream) {
 int launch_write(int D, WriteArgs a, int num_sms, cudaStream_t stream) {
   a.tile = kWriteMaxTile;
   while (a.tile > 1 && a.tokens < a.tile * 8 * num_sms) a.tile /= 2;
-  return D == 128 ? launch_write_t<128>(a, stream) : launch_write_t<64>(a, stream);
+  return D == 128 ? launch_write_t<128>(a, num_sms, stream)
+                  : launch_write_t<64>(a, num_sms, stream);
 }
 
 int launch_read_back(int D, const ReadArgs& a, cudaStream_t stream) {
