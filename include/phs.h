@@ -638,12 +638,13 @@ int phs_linear_attn_prompt(const void *q, int32_t num_q_heads, const void *k, co
  * Each block of 32 between the two is quantised as by
  * phs_kv_quant_int8_block32 (bit for bit what a bf16 write and that call
  * give), new tokens straight from k and v without touching their pages,
- * earlier ones from their pages.  At most max_qblocks blocks a request.
+ * earlier ones from their pages.  A block belongs to one request.  At most max_qblocks blocks a request.
  *   Device errors: a bad cu_seqlens refuses the whole call (PHS_ERANGE, no
  * cache is written); seq_lens below the new tokens, qlens_before or qlens bad
  * (negative, not a multiple of 32, qlens_before above qlens or above the
  * earlier tokens, qlens above seq_lens, more blocks than max_qblocks) refuse
- * the request (PHS_ERANGE); its q_out rows are zero.  A page or block outside
+ * the request (PHS_ERANGE); its q_out rows are zero.  (A request without new
+ * tokens is looked at where max_qblocks is above 0.)  A page or block outside
  * its pool or table (PHS_ERANGE) or a shared page (PHS_ESHARED) is not
  * written.  Without cu_seqlens a request of length 0 is inactive: nothing is
  * written, its q_out row is zero.  q_out rows of no request are left as they
@@ -702,7 +703,8 @@ int phs_kv_read_paged(const phs_paged_pool *pool, const int32_t *block_table,
  * phs_causal_conv_decode, else zero; the pool gets the last width - 1.  x and
  * out bf16 (out dense [tokens][channels]), sums fp32.  channels a multiple of
  * 8, width 2 to 4.  A cu_seqlens that decreases or leaves [0, total_tokens]
- * refuses the whole call (PHS_ERANGE, nothing is written).
+ * refuses the whole call (PHS_ERANGE, nothing is written).  In prompts out must
+ * not overlap x (PHS_EINVAL); a single token's out may be its x.
  *
  * Selective scan: state S [P][N] of head h, group g = h / (H / G),
  *     s   = softplus(dt[t][h] + dt_bias[h])
@@ -710,7 +712,8 @@ int phs_kv_read_paged(const phs_paged_pool *pool, const int32_t *block_table,
  *     y_t = S_t c[t][g] + skip[h] x[t][h]
  * a (fp32 [H], <= 0) the rate, skip and dt_bias fp32 [H] or NULL (zero).  x
  * bf16 [tokens][H][P], b and c bf16 [tokens][G][N], dt bf16 or fp32
- * [tokens][H] (any stride of at least H); out dense [tokens][H][P].  P and N
+ * [tokens][H] (any stride of at least H); out dense [tokens][H][P], apart from
+ * the inputs.  P and N
  * 64 or 128.  softplus(x) = x above 20.  States are fp32 and stay so: what goes
  * into them has 24 bits.  phs_selective_scan_prompt forms its bf16 rows from
  * chunks of 128 tokens: the weights of a chunk's own tokens (the skip on their

@@ -2246,6 +2246,13 @@ int phs_causal_conv_prompt(const void* x, int64_t x_stride, const int32_t* cu_se
       conv_args(a, x, x_stride, pool, weights, state_ids, batch, total_tokens, out, dev_status);
   if (st) return st;
   if (!cu_seqlens) return PHS_EINVAL;
+  // (a tile's rows are read again, as earlier inputs, by the next one)
+  if (total_tokens > 0) {
+    const uintptr_t xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t xe = xa + 2 * (uintptr_t(total_tokens - 1) * x_stride + pool->channels);
+    const uintptr_t oe = oa + 2 * uintptr_t(total_tokens) * pool->channels;
+    if (xa < oe && oa < xe) return PHS_EINVAL;
+  }
   if (batch == 0) return PHS_OK;
   a.cu_seqlens = cu_seqlens;
   a.resume = resume;

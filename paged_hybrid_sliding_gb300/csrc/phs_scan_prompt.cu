@@ -760,14 +760,28 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             }
           } else {
             const float skip = s ? skip1 : skip0, row = s ? next[1].loc : next[0].loc;
+            uint64_t w[8];
+            if (whole) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float4 c = c4[e];
+                w[2 * e] = f2_mul(f, f2(c.x, c.y));
+                w[2 * e + 1] = f2_mul(f, f2(c.z, c.w));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float4 c = c4[e];
+                w[2 * e] = f2(ex2(row - c.x), ex2(row - c.y));
+                w[2 * e + 1] = f2(ex2(row - c.z), ex2(row - c.w));
+              }
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float2 c = reinterpret_cast<const float2*>(c4)[e];
-              const uint64_t own = f2(d == 2 * e ? skip : 0.f, d == 2 * e + 1 ? skip : 0.f);
-              uint64_t w = f2_mul(f, f2(c.x, c.y));
-              if (!whole) w = f2(ex2(row - c.x), ex2(row - c.y));
-              const float2 x = f2_get(f2_fma(f2(sc[2 * e], sc[2 * e + 1]), w, own));
-              p[e] = pack_bf16(d >= 2 * e ? x.x : 0.f, d >= 2 * e + 1 ? x.y : 0.f);
+              const bool in0 = d >= 2 * e, in1 = d >= 2 * e + 1, in2 = d >= 2 * e + 2;
+              const float2 x = f2_get(f2_fma(f2(sc[2 * e], sc[2 * e + 1]), w[e],
+                                             f2(in1 ? 0.f : skip, in2 ? 0.f : skip)));
+              p[e] = pack_bf16(in0 ? x.x : 0.f, in1 ? x.y : 0.f);
             }
           }
           tmem_st8(at + 16 * k + 8 * s, p);

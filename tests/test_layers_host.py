@@ -13,6 +13,7 @@ from paged_hybrid_sliding_gb300 import _lib
 
 P = ctypes.c_void_p(1 << 20)   # an aligned address that no refused call reads
 ODD = ctypes.c_void_p((1 << 20) + 8)
+FAR = ctypes.c_void_p(1 << 24)
 
 
 def ref(x):
@@ -85,7 +86,7 @@ def test_kv_read(change, code):
     (dict(weight=ODD.value), -9), (dict(bias=ODD.value), -9), (dict(batch=-1), -1),
     (dict(batch=9), -2), (dict(out=None), -1), (dict(batch=0), 0)])
 def test_conv(change, code):
-    a = dict(x=P, xs=64, weight=P.value, bias=0, batch=2, out=P, pool={}) | change
+    a = dict(x=P, xs=64, weight=P.value, bias=0, batch=2, out=FAR, pool={}) | change
     pool = _lib.ConvPoolC(*(dict(c=P.value, n=4, ch=64, w=4) | a["pool"]).values())
     w = _lib.ConvWeightsC(a["weight"], a["bias"], 1)
     lib = phs.lib()
@@ -95,8 +96,17 @@ def test_conv(change, code):
         assert lib.phs_causal_conv_decode(a["x"], a["xs"], ref(pool), ref(w), None, a["batch"],
                                           a["out"], None, None) == code
     assert lib.phs_causal_conv_prompt(P, 64, None, 9, ref(_lib.ConvPoolC(P.value, 4, 64, 4)),
-                                      ref(_lib.ConvWeightsC(P.value, 0, 1)), None, None, 2, P, None,
+                                      ref(_lib.ConvWeightsC(P.value, 0, 1)), None, None, 2, FAR, None,
                                       None) == -1
+
+
+def test_conv_prompt_refuses_an_output_over_its_input():
+    pool, w = _lib.ConvPoolC(P.value, 4, 64, 4), _lib.ConvWeightsC(P.value, 0, 1)
+    for out in (1 << 20, (1 << 20) + 9 * 128 - 16, (1 << 20) - 9 * 128 + 16):
+        assert phs.lib().phs_causal_conv_prompt(P, 64, P, 9, ref(pool), ref(w), None, None, 2,
+                                                ctypes.c_void_p(out), None, None) == -1
+    assert phs.lib().phs_causal_conv_prompt(P, 64, P, 9, ref(pool), ref(w), None, None, 0,
+                                            ctypes.c_void_p((1 << 20) + 9 * 128), None, None) == 0
 
 
 @pytest.mark.parametrize("change,code", [
