@@ -716,9 +716,8 @@ int phs_kv_read_paged(const phs_paged_pool *pool, const int32_t *block_table,
  * the inputs.  P and N
  * 64 or 128.  softplus(x) = x above 20.  States are fp32 and stay so: what goes
  * into them has 24 bits.  phs_selective_scan_prompt forms its bf16 rows from
- * chunks of 128 tokens: the weights of a chunk's own tokens (the skip on their
- * diagonal) and the state before the chunk enter the products as bf16, sums are
- * fp32.  A token's log decay is cut at -128.  In a prompt an infinite or NaN
+ * chunks of 128 tokens: the weights of a chunk's own tokens and the state before
+ * the chunk enter the products as bf16, sums and the skip are fp32.  A token's log decay is cut at -128.  In a prompt an infinite or NaN
  * value reaches the request's rows from the start of its chunk of 128 tokens
  * on, up to 127 tokens before its own; other requests are not reached.  A
  * request with a bad token range (outside the tokens, or beginning before an

@@ -3,8 +3,7 @@
 // Prompts go in chunks of C = 128 tokens.  With l_t = s_t a a head's log decay
 // in token t (s_t its step), L_i = sum_{t <= i} l_t within the chunk and S
 // [P][N] the state before it, rows i, j of the chunk:
-//   Y = diag(exp L_i) C S^T + (exp(L_i - L_j) s_j C B^T, j <= i; + skip on the
-//       diagonal) X
+//   Y = diag(exp L_i) C S^T + (exp(L_i - L_j) s_j C B^T, j <= i) X + skip X
 //   S <- exp(L_last) S + sum_j exp(L_last - L_j) s_j x_j b_j^T
 // Four matrix products a chunk, on the tensor cores.  Heads of 64 go in pairs
 // (a head of 128 as two halves), so that x, the state and the output are 128
@@ -14,10 +13,11 @@
 //   PV = P X       128 x 64 x 128   for each slot, A = P in tensor memory, B = X
 //   KV = X'^T B    128 x N x 128    A = X'^T in tensor memory, B = B
 // B, C and x are exact.  Decays make P (exp(L_i - L_j) s_j C B^T) a value of 24
-// bits and the state is an fp32 one; both enter the rows' products as bf16: their
-// 2^-9 goes into sums that are rounded to bf16 in the end, an error 1.2 times that
-// rounding's own (two terms of each cost a third of the time: 577 us against 421
-// for 32,751 tokens of 64 heads).  What goes into the state keeps its 24 bits: X'
+// bits and the state is an fp32 one; both enter the rows' products as bf16, as
+// their sums are rounded to bf16 in the end: all in all an error 1.1 times that of
+// the last rounding alone.  (Two terms of each, for 16 bits of them, cost a third of
+// the time: 577 us against 421 for 32,751 tokens of 64 heads.)  The skip is added in
+// fp32.  What goes into the state keeps its 24 bits: X'
 // (x times exp(L_last - L_j) s_j) enters as a sum of three bf16 terms, and KV is
 // accumulated chunk by chunk from zero and added to the state in fp32 registers:
 // the tensor cores' own sums drop the bits below the running sum's last one.
@@ -44,6 +44,24 @@
 // a launch sums up their own states (B and X alone; a segment in `nsub` parts,
 // as this launch has fewer CTAs), a small one joins these sums into the states
 // that the segments start from, and the last one forms the rows.
+//
+// What bounds it: a chunk of a pair of heads (N = 128) takes some 9,500 cycles of a
+// CTA, of which the tensor cores' products need 3,300 (their rates here: 32 cycles
+// for a 128 x 64 x 16 product with A in tensor memory, 48 with both in shared
+// memory, 62 for 128 wide ones) and the arithmetic of P, X' and the state about
+// 2,800 of a scheduler.  The rest is the chain of steps through the roles, scores
+// to P to PV to the rows and back to QS, with two or three warps a scheduler to
+// hide each one's latency.  One prompt of 32,751 tokens, 64 heads of 64 and N =
+// 128: 421 us (tables 14, sums of segments 90, join 8) against 83 for its bytes.
+// What helped: P of both slots from one QK, in halves, so that PV and the next QK
+// run beside the other half's P (577 -> 509); bf16 operands (-> 468); table values
+// read a half ahead and only read there, since a warp waits where it computes
+// with a load's result; loops instead of unrolled copies of P (-> 445); no copies
+// to L2 ahead of the ring's (-> 421).  What did not: halves per slot with a QK
+// each (548 -> 690, the tensor cores' time), a longer suspension in the waits (452
+// -> 467), direct stores of the rows (467 -> 525), X ahead of C in the ring (425 ->
+// 446), terms formed by all 16 warps of the sums' launch (421 -> 437), parts of X'
+// ahead of the state: 0, 1, 2 of a warp 426, 421, 432.
 #include "phs_prompt.cuh"
 #include "phs_scan.cuh"
 
@@ -63,15 +81,15 @@ constexpr int kTabLoc = 0;      // sum of l from its 32 tokens' first one on
 constexpr int kTabDiag = 128;   // the same less log2 s_j
 constexpr int kTabCol = 256;    // exp(L_e - L_j) s_j, e the last of j's 32 tokens
 constexpr int kTabEnd = 384;    // exp(L_last - L_j) s_j
-constexpr int kTabFrom = 512;   // [4][4] of rows in block q for columns in block k <= q, at 4 k + q:
-                                // what is added to kTabLoc for L_i - L_e, on the diagonal for
-                                // L_i - L_m, or kNoRoom
+constexpr int kTabFrom = 512;   // [4][4] of rows in block q for columns in block k <= q, at
+                                // 4 k + q: what is added to kTabLoc for L_i - L_e, on the
+                                // diagonal for L_i - L_m, or kNoRoom
 constexpr int kTabBase = 528;   // [4] sum of l before each 32 tokens
 constexpr int kTabTotal = 532;  // sum of l, natural
 constexpr int kTabDecay = 533;  // its decay_factor
 // On the diagonal exp(L_i - L_j) is a product too, of exp(L_i - L_m) and exp(L_m -
-// L_j), m the 16th of the 32 tokens, unless one of the factors may be above 2^100 (half of the 32 tokens
-// decay by more): then each is taken by itself.
+// L_j), m the 16th of the 32 tokens, unless one of the factors may be above
+// 2^100 (half of the 32 tokens decay by more): then each is taken by itself.
 constexpr float kNoRoom = 1e30f;
 static_assert(kScanTable == 536, "a table");
 
@@ -102,6 +120,22 @@ struct ScanLayout {
   static constexpr int kAlloc = kCols + (STATES ? 0 : 8 * 256);
   static_assert(kAlloc <= 227 * 1024, "shared memory of the prompt kernel");
 };
+
+// The n lowest bits (n >= 0).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  uint32_t r;
+  asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(r) : "r"(n));
+  return r;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 
 // First chunk of part p of a request's `chunks`; a segment is nsub parts, and
 // part nseg * nsub is the end.
@@ -161,84 +195,82 @@ __global__ void __launch_bounds__(32 * kTableHeads)
   __syncthreads();
   if (h >= a.H) return;
   constexpr float kLog2e = 1.4426950408889634f;
-  {
-    const float rate = a.rate[h];
-    const float4 s4 = *reinterpret_cast<const float4*>(&s_step[warp][4 * lane]);
-    const float s[4] = {s4.x, s4.y, s4.z, s4.w};
-    float l[4], own = 0.f;
+  const float rate = a.rate[h];
+  const float4 s4 = *reinterpret_cast<const float4*>(&s_step[warp][4 * lane]);
+  const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+  float l[4], own = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      l[e] = 4 * lane + e < v ? fmaxf(s[e] * rate, -128.f) : 0.f;
-      own += l[e];
-    }
-    // sums of whole lanes: up to this one within its 8 (32 tokens), from it on
-    // within its 8 and within all
-    float pre = own, back32 = own, back = own;
+  for (int e = 0; e < 4; ++e) {
+    l[e] = 4 * lane + e < v ? fmaxf(s[e] * rate, -128.f) : 0.f;
+    own += l[e];
+  }
+  // sums of whole lanes: up to this one within its 8 (32 tokens), from it on
+  // within its 8 and within all
+  float pre = own, back32 = own, back = own;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      const float x = __shfl_up_sync(0xffffffffu, pre, o, 8);
-      if ((lane & 7) >= o) pre += x;
-      const float y = __shfl_down_sync(0xffffffffu, back32, o, 8);
-      if ((lane & 7) + o < 8) back32 += y;
-    }
+  for (int o = 1; o < 8; o <<= 1) {
+    const float x = __shfl_up_sync(0xffffffffu, pre, o, 8);
+    if ((lane & 7) >= o) pre += x;
+    const float y = __shfl_down_sync(0xffffffffu, back32, o, 8);
+    if ((lane & 7) + o < 8) back32 += y;
+  }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float x = __shfl_down_sync(0xffffffffu, back, o);
-      if (lane + o < 32) back += x;
-    }
-    const float total = __shfl_sync(0xffffffffu, back, 0);
-    const float block = __shfl_sync(0xffffffffu, pre, lane | 7);  // of these 32 tokens
-    // the same without this lane's own tokens
-    float after32 = __shfl_down_sync(0xffffffffu, back32, 1, 8);
-    float after = __shfl_down_sync(0xffffffffu, back, 1);
-    float before = __shfl_up_sync(0xffffffffu, pre, 1, 8);
-    if ((lane & 7) == 7) after32 = 0.f;
-    if (lane == 31) after = 0.f;
-    if ((lane & 7) == 0) before = 0.f;
-    float loc[4], diag[4], col[4], end[4], run = 0.f;
+  for (int o = 1; o < 32; o <<= 1) {
+    const float x = __shfl_down_sync(0xffffffffu, back, o);
+    if (lane + o < 32) back += x;
+  }
+  const float total = __shfl_sync(0xffffffffu, back, 0);
+  const float block = __shfl_sync(0xffffffffu, pre, lane | 7);  // of these 32 tokens
+  // the same without this lane's own tokens
+  float after32 = __shfl_down_sync(0xffffffffu, back32, 1, 8);
+  float after = __shfl_down_sync(0xffffffffu, back, 1);
+  float before = __shfl_up_sync(0xffffffffu, pre, 1, 8);
+  if ((lane & 7) == 7) after32 = 0.f;
+  if (lane == 31) after = 0.f;
+  if ((lane & 7) == 0) before = 0.f;
+  float loc[4], diag[4], col[4], end[4], run = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      run += l[e];
-      loc[e] = (before + run) * kLog2e;
-      diag[e] = loc[e] - log2f(s[e]);
-    }
-    const float first16 = __shfl_sync(0xffffffffu, loc[3], (lane & 24) + 3);
-    run = 0.f;
+  for (int e = 0; e < 4; ++e) {
+    run += l[e];
+    loc[e] = (before + run) * kLog2e;
+    diag[e] = loc[e] - log2f(s[e]);
+  }
+  const float first16 = __shfl_sync(0xffffffffu, loc[3], (lane & 24) + 3);
+  run = 0.f;
 #pragma unroll
-    for (int e = 3; e >= 0; --e) {  // sums behind the token
-      col[e] = expf(after32 + run) * s[e];
-      end[e] = expf(after + run) * s[e];
-      run += l[e];
-    }
-    float* tab = a.tables + (row * a.H + h) * kScanTable;
-    reinterpret_cast<float4*>(tab + kTabLoc)[lane] = make_float4(loc[0], loc[1], loc[2], loc[3]);
-    reinterpret_cast<float4*>(tab + kTabDiag)[lane] =
-        make_float4(diag[0], diag[1], diag[2], diag[3]);
-    reinterpret_cast<float4*>(tab + kTabCol)[lane] = make_float4(col[0], col[1], col[2], col[3]);
-    reinterpret_cast<float4*>(tab + kTabEnd)[lane] = make_float4(end[0], end[1], end[2], end[3]);
-    // blocks' sums, by every lane: x[q]
-    float x[4], base = 0.f;
+  for (int e = 3; e >= 0; --e) {  // sums behind the token
+    col[e] = ex2((after32 + run) * kLog2e) * s[e];
+    end[e] = expf(after + run) * s[e];
+    run += l[e];
+  }
+  float* tab = a.tables + (row * a.H + h) * kScanTable;
+  reinterpret_cast<float4*>(tab + kTabLoc)[lane] = make_float4(loc[0], loc[1], loc[2], loc[3]);
+  reinterpret_cast<float4*>(tab + kTabDiag)[lane] =
+      make_float4(diag[0], diag[1], diag[2], diag[3]);
+  reinterpret_cast<float4*>(tab + kTabCol)[lane] = make_float4(col[0], col[1], col[2], col[3]);
+  reinterpret_cast<float4*>(tab + kTabEnd)[lane] = make_float4(end[0], end[1], end[2], end[3]);
+  // blocks' sums, by every lane: x[q]
+  float x[4], base = 0.f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) x[q] = __shfl_sync(0xffffffffu, block, 8 * q) * kLog2e;
-    const float half16 = __shfl_sync(0xffffffffu, first16, 8 * (lane & 3));
-    if (lane < 16) {  // lane 4 k + q
-      const int k = lane >> 2, q = lane & 3;
-      float from = 0.f;
-      if (k == q)
-        from = half16 > -100.f && x[q] - half16 > -100.f ? -half16 : kNoRoom;
+  for (int q = 0; q < 4; ++q) x[q] = __shfl_sync(0xffffffffu, block, 8 * q) * kLog2e;
+  const float half16 = __shfl_sync(0xffffffffu, first16, 8 * (lane & 3));
+  if (lane < 16) {  // lane 4 k + q
+    const int k = lane >> 2, q = lane & 3;
+    float from = 0.f;
+    if (k == q)
+      from = half16 > -100.f && x[q] - half16 > -100.f ? -half16 : kNoRoom;
 #pragma unroll
-      for (int m = 1; m < 3; ++m)
-        if (k < m && m < q) from += x[m];
-      tab[kTabFrom + lane] = from;
-    }
+    for (int m = 1; m < 3; ++m)
+      if (k < m && m < q) from += x[m];
+    tab[kTabFrom + lane] = from;
+  }
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
-      if (q < lane) base += x[q];
-    if (lane < 4) tab[kTabBase + lane] = base;
-    if (lane == 0) {
-      tab[kTabTotal] = total;
-      tab[kTabDecay] = decay_factor(total);
-    }
+  for (int q = 0; q < 3; ++q)
+    if (q < lane) base += x[q];
+  if (lane < 4) tab[kTabBase + lane] = base;
+  if (lane == 0) {
+    tab[kTabTotal] = total;
+    tab[kTabDecay] = decay_factor(total);
   }
 }
 
@@ -447,7 +479,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           for (int st = 0; st < T::kSteps; ++st) {
             const int t = 16 * (T::kSteps * p + st);  // first token
             const float2 now[2] = {ahead[0], ahead[1]};
-            const int t_next = st + 1 < T::kSteps ? t + 16 : t + 16 + 16 * T::kSteps * (kTermWarps - 1);
+            const int t_next =
+                st + 1 < T::kSteps ? t + 16 : t + 16 + 16 * T::kSteps * (kTermWarps - 1);
             if (t_next < kScanC) weights_of(t_next);
             uint32_t w[3][2][4];
 #pragma unroll
@@ -759,7 +792,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
               p[2 * e + 1] = pack_term(f2_mul(f2(x[2], x[3]), f2_mul(f, f2(c.z, c.w))));
             }
           } else {
-            const float skip = s ? skip1 : skip0, row = s ? next[1].loc : next[0].loc;
+            const float row = s ? next[1].loc : next[0].loc;
             uint64_t w[8];
             if (whole) {
 #pragma unroll
@@ -778,9 +811,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const bool in0 = d >= 2 * e, in1 = d >= 2 * e + 1, in2 = d >= 2 * e + 2;
-              const float2 x = f2_get(f2_fma(f2(sc[2 * e], sc[2 * e + 1]), w[e],
-                                             f2(in1 ? 0.f : skip, in2 ? 0.f : skip)));
+              const bool in0 = d >= 2 * e, in1 = d >= 2 * e + 1;
+              const float2 x = f2_get(f2_mul(f2(sc[2 * e], sc[2 * e + 1]), w[e]));
               p[e] = pack_bf16(in0 ? x.x : 0.f, in1 ? x.y : 0.f);
             }
           }
@@ -795,24 +827,36 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       for (int hh = 0; hh < 2; ++hh) {
         form_p(n, hh);
         if (!ok) break;
-        if (hh == 0) {  // the part before the chunk, scaled in place
+        if (hh == 0) {  // the part before the chunk scaled in place, and the skip
           ok = lin_wait_warp(qs_done, n & 1, abort);
           if (!ok) break;
           tc_fence_after();
           const float g0 = ex2(next[0].loc + next[0].base), g1 = ex2(next[1].loc + next[1].base);
           read_ahead(n, 1);
+          ok = lin_wait_warp(full_of(tile_x(n)), turn_of(tile_x(n)) & 1, abort);
+          if (!ok) break;
+          const uint32_t xrow = place_of(tile_x(n)) + i * 128;
 #pragma unroll 1
           for (int s = 0; s < S; ++s) {
             const uint64_t f = s ? f2(g1, g1) : f2(g0, g0);
+            const float skip = s ? skip1 : skip0;
             uint32_t o[32];
             const uint32_t at = my_lanes + T::kOut + 64 * s + 32 * half;
             tmem_ld32(at, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 x = f2_get(f2_mul(f2(o[e], o[e + 1]), f));
-              o[e] = __float_as_uint(x.x);
-              o[e + 1] = __float_as_uint(x.y);
+            for (int k = 0; k < 4; ++k) {
+              const uint4 x = lds128(xrow + s * kHalf + ((((4 * half + k) ^ i) & 7) << 4));
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const int e = 8 * k + 2 * m;
+                const float2 y = f2_get(
+                    f2_fma(f2(o[e], o[e + 1]), f,
+                           f2_mul(f2(w[m] << 16, w[m] & 0xFFFF0000u), f2(skip, skip))));
+                o[e] = __float_as_uint(y.x);
+                o[e + 1] = __float_as_uint(y.y);
+              }
             }
             tmem_st32(at, o);
           }

@@ -99,7 +99,9 @@ __device__ __forceinline__ Request request(const WriteArgs& a, int b) {
 // A CTA takes `tile` tokens: their requests, positions and pages once, the
 // angles of their pairs once for all heads, then a thread one unit of a token
 // over heads, four at a time with their loads in flight.  Each row is read
-// and written once, so memory bounds it.
+// and written once, so memory bounds it: 32,751 tokens of 32 query and 8 KV
+// heads of 128 take 127 us, 120 for their bytes at the rate of a plain copy; a
+// token of each of 256 requests 5 us of the GPU's time.
 template <int D>
 __global__ void __launch_bounds__(kThreads) phs_write_kernel(const __grid_constant__ WriteArgs a) {
   constexpr int U = D / 16;
@@ -250,10 +252,15 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 // One CTA per (block of 32 tokens, some heads) of a request: a thread holds
 // one unit of a token, K and V, head after head, and its pairs' angles for
 // all of them.  A head's absmax meets in shared memory; V's codes are
-// transposed there.
+// transposed there.  About 400 instructions a thread and head bound it (52 % of
+// the issue slots, with the two barriers of a head): 65,521 tokens of 8 heads of
+// 128 take 125 us, 60 for their bytes.  Four CTAs an SM instead of three for
+// some spilled registers: 380 us against 397 for the call with its queries and
+// its reading back; all heads by one CTA: 358.  A warp for K or V of a head, with
+// its 32 rows in registers and no barrier, has too few warps: 420.
 template <int D>
-__global__ void __launch_bounds__(2 * D, D == 128 ? 4 : 8) phs_write_block_kernel(const __grid_constant__ WriteArgs a,
-                                                                int heads_per_cta) {
+__global__ void __launch_bounds__(2 * D, D == 128 ? 4 : 8)
+    phs_write_block_kernel(const __grid_constant__ WriteArgs a, int heads_per_cta) {
   constexpr int U = D / 16, kWarps = D / 16;
   __shared__ uint32_t s_max[kWarps];
   __shared__ __align__(16) uint8_t s_v[kQBlock * D];  // V codes, token-major
@@ -349,8 +356,9 @@ __global__ void __launch_bounds__(2 * D, D == 128 ? 4 : 8) phs_write_block_kerne
     uint2* ko = reinterpret_cast<uint2*>(a.k_codes + (block * kQBlock + t) * D);
     ko[va] = quant_codes8(reinterpret_cast<const uint32_t*>(&ka), sk, rk2, !(rk < INFINITY));
     ko[vb] = quant_codes8(reinterpret_cast<const uint32_t*>(&kb), sk, rk2, !(rk < INFINITY));
-    const uint2 c0 = quant_codes8(reinterpret_cast<const uint32_t*>(&xa), sv, rv2, !(rv < INFINITY));
-    const uint2 c1 = quant_codes8(reinterpret_cast<const uint32_t*>(&xb), sv, rv2, !(rv < INFINITY));
+    const bool divide = !(rv < INFINITY);
+    const uint2 c0 = quant_codes8(reinterpret_cast<const uint32_t*>(&xa), sv, rv2, divide);
+    const uint2 c1 = quant_codes8(reinterpret_cast<const uint32_t*>(&xb), sv, rv2, divide);
     reinterpret_cast<uint4*>(s_v)[tid] = make_uint4(c0.x, c0.y, c1.x, c1.y);
     if (tid == 0) {
       a.k_scale[block] = sk;
@@ -402,7 +410,9 @@ __global__ void __launch_bounds__(2 * D, D == 128 ? 4 : 8) phs_write_block_kerne
 }
 
 // --------------------------------------------------------------- read back --
-// One CTA per (page of 16 tokens, request).
+// One CTA per (page of 16 tokens, request).  65,521 tokens of 8 heads of 128, all but
+// the last in 8 bits: 71 us, 60 for their bytes (91 with one load of K's codes in
+// flight instead of four).
 template <int D>
 __global__ void __launch_bounds__(128) phs_read_back_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int V = D / 8;
@@ -496,7 +506,8 @@ __global__ void __launch_bounds__(128) phs_read_back_kernel(const __grid_constan
       uint32_t y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        y[i] = pack_bf16(value(w[i / 2], 2 * (i & 1), s[j]), value(w[i / 2], 2 * (i & 1) + 1, s[j]));
+        y[i] = pack_bf16(value(w[i / 2], 2 * (i & 1), s[j]),
+                         value(w[i / 2], 2 * (i & 1) + 1, s[j]));
       uint4* to = ko + t * per + h * V + 2 * v;
       to[0] = make_uint4(y[0], y[1], y[2], y[3]);
       to[1] = make_uint4(y[4], y[5], y[6], y[7]);
@@ -541,7 +552,8 @@ int launch_write_t(const WriteArgs& a, int num_sms, cudaStream_t stream) {
     // all heads of a block by one CTA, which forms their angles once, unless
     // that leaves SMs without one
     int per = a.Hkv;
-    while (per > 2 && int64_t{a.max_qblocks} * a.B * ((a.Hkv + per - 1) / per) < int64_t{8} * num_sms)
+    const int64_t blocks = int64_t{a.max_qblocks} * a.B;
+    while (per > 2 && blocks * ((a.Hkv + per - 1) / per) < int64_t{8} * num_sms)
       per = (per + 1) / 2;
     const int groups = (a.Hkv + per - 1) / per;
     cfg.gridDim = dim3(a.max_qblocks * groups, a.B);
