@@ -623,7 +623,8 @@ int phs_linear_attn_prompt(const void *q, int32_t num_q_heads, const void *k, co
  *
  * phs_rope_rotate: q_out[t] = q[t] rotated by positions[t] (device int32
  * [tokens]), k likewise (k NULL: q alone).  An output may be its own input
- * (same pointer and stride); else they must not overlap.
+ * (same pointer and stride); else no output may overlap an input or the
+ * other output (PHS_EINVAL; parts of the same wider rows do not).
  *
  * phs_kv_write_paged: request b brings tokens [cu_seqlens[b],
  * cu_seqlens[b + 1]) (device int32 [batch + 1], not decreasing, within
@@ -631,14 +632,16 @@ int phs_linear_attn_prompt(const void *q, int32_t num_q_heads, const void *k, co
  * batch).  seq_lens[b] counts the request's tokens AFTER the call, so its
  * new ones are the last; a token's position is its place in the request.
  * With rope k is rotated, and q (NULL: none) into q_out, dense bf16
- * [tokens][num_q_heads][D].  Tokens go to their pages as in
+ * [tokens][num_q_heads][D] (a dense q itself, or apart from q, k and v:
+ * PHS_EINVAL).  Tokens go to their pages as in
  * phs_kv_append_paged, page_refcount included.
  *   With int8: the request's first qlens[b] tokens (a multiple of 32) are
  * held in 8 bits after the call, its first qlens_before[b] were before it.
  * Each block of 32 between the two is quantised as by
  * phs_kv_quant_int8_block32 (bit for bit what a bf16 write and that call
  * give), new tokens straight from k and v without touching their pages,
- * earlier ones from their pages.  A block belongs to one request.  At most max_qblocks blocks a request.
+ * earlier ones from their pages.  A block belongs to one request.  At most
+ * max_qblocks blocks a request.
  *   Device errors: a bad cu_seqlens refuses the whole call (PHS_ERANGE, no
  * cache is written); seq_lens below the new tokens, qlens_before or qlens bad
  * (negative, not a multiple of 32, qlens_before above qlens or above the
@@ -704,7 +707,7 @@ int phs_kv_read_paged(const phs_paged_pool *pool, const int32_t *block_table,
  * out bf16 (out dense [tokens][channels]), sums fp32.  channels a multiple of
  * 8, width 2 to 4.  A cu_seqlens that decreases or leaves [0, total_tokens]
  * refuses the whole call (PHS_ERANGE, nothing is written).  In prompts out must
- * not overlap x (PHS_EINVAL); a single token's out may be its x.
+ * not overlap x (PHS_EINVAL); a single token's out may be its dense x.
  *
  * Selective scan: state S [P][N] of head h, group g = h / (H / G),
  *     s   = softplus(dt[t][h] + dt_bias[h])
@@ -713,13 +716,14 @@ int phs_kv_read_paged(const phs_paged_pool *pool, const int32_t *block_table,
  * a (fp32 [H], <= 0) the rate, skip and dt_bias fp32 [H] or NULL (zero).  x
  * bf16 [tokens][H][P], b and c bf16 [tokens][G][N], dt bf16 or fp32
  * [tokens][H] (any stride of at least H); out dense [tokens][H][P], apart from
- * the inputs.  P and N
- * 64 or 128.  softplus(x) = x above 20.  States are fp32 and stay so: what goes
- * into them has 24 bits.  phs_selective_scan_prompt forms its bf16 rows from
- * chunks of 128 tokens: the weights of a chunk's own tokens and the state before
- * the chunk enter the products as bf16, sums and the skip are fp32.  A token's log decay is cut at -128.  In a prompt an infinite or NaN
- * value reaches the request's rows from the start of its chunk of 128 tokens
- * on, up to 127 tokens before its own; other requests are not reached.  A
+ * the inputs (PHS_EINVAL).  P and N 64 or 128.  softplus(x) = x above 20.  States are fp32
+ * and stay so: what goes into them has 24 bits.  phs_selective_scan_prompt
+ * forms its bf16 rows from chunks of 128 tokens: the weights of a chunk's own
+ * tokens and the state before the chunk enter the products as bf16, sums and
+ * the skip are fp32; a token's log decay is cut at -128.  In a prompt an
+ * infinite or NaN value reaches the request's rows from the start of its chunk
+ * of 128 tokens on, up to 127 tokens before its own; other requests are not
+ * reached.  A
  * request with a bad token range (outside the tokens, or beginning before an
  * earlier one's end) or a length above max_seq_len records PHS_ERANGE and is
  * left out whole.  workspace: phs_scan_prompt_workspace_bytes of the same

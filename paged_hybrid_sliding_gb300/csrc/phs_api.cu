@@ -1903,6 +1903,28 @@ namespace {
 // Rows of `cols` elements at a stride: 16-byte pieces.
 bool bad_rows(int64_t stride, int64_t cols) { return stride < cols || stride % 8 != 0; }
 
+// Whether rows of `cols` elements at a stride and others share memory: parts of
+// the same wider rows do not; else rows whose ranges meet are taken to.
+struct Rows {
+  const void* at;
+  int64_t stride, cols, size;  // in elements of `size` bytes
+};
+bool overlap(const Rows& a, const Rows& b, int64_t tokens) {
+  if (tokens <= 0 || !a.at || !b.at) return false;
+  const uint64_t as = a.stride * a.size, bs = b.stride * b.size;  // bytes
+  const uint64_t ac = a.cols * a.size, bc = b.cols * b.size;
+  const uint64_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  if (x + (tokens - 1) * as + ac <= y || y + (tokens - 1) * bs + bc <= x) return false;
+  if (as != bs) return true;
+  const uint64_t d = y >= x ? (y - x) % as : (as - (x - y) % as) % as;  // b's first column in a's row
+  return d < ac || d + bc > as;
+}
+// The same, where an output may also be its own input.
+bool overlap_in_part(const Rows& in, const Rows& out, int64_t tokens) {
+  return !(in.at == out.at && (in.stride == out.stride || tokens <= 1)) &&
+         overlap(in, out, tokens);
+}
+
 int check_rope(const phs_rope* rope, int D) {
   if (!rope->turns || rope->rotary_dim <= 0 || !std::isfinite(rope->factor)) return PHS_EINVAL;
   if (rope->rotary_dim > D) return PHS_ESHAPE;
@@ -1942,6 +1964,11 @@ int phs_rope_rotate(const void* q, int64_t q_stride, int32_t num_q_heads, const 
   if (k && (bad_rows(k_stride, kc) || bad_rows(k_out_stride, kc))) return PHS_ESHAPE;
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out)) return PHS_EALIGN;
   if (tokens == 0) return PHS_OK;
+  const Rows qi{q, q_stride, qc, 2}, ki{k, k_stride, kc, 2};
+  const Rows qo{q_out, q_out_stride, qc, 2}, ko{k_out, k_out_stride, kc, 2};
+  if (overlap_in_part(qi, qo, tokens) || overlap_in_part(ki, ko, tokens) ||
+      overlap(qi, ko, tokens) || overlap(ki, qo, tokens) || overlap(qo, ko, tokens))
+    return PHS_EINVAL;
   WriteArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
@@ -2005,6 +2032,13 @@ int phs_kv_write_paged(const phs_paged_pool* pool, const void* k, int64_t k_stri
     a.max_qblocks = max_qblocks;
   }
   if (batch == 0) return PHS_OK;
+  if (q) {
+    const int64_t qc = int64_t{num_q_heads} * D;
+    const Rows qo{q_out, qc, qc, 2};
+    if (overlap_in_part({q, q_stride, qc, 2}, qo, tokens) ||
+        overlap({k, k_stride, kc, 2}, qo, tokens) || overlap({v, v_stride, kc, 2}, qo, tokens))
+      return PHS_EINVAL;
+  }
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
   a.k = reinterpret_cast<const __nv_bfloat16*>(k);
   a.v = reinterpret_cast<const __nv_bfloat16*>(v);
@@ -2090,6 +2124,7 @@ int conv_args(ConvArgs& a, const void* x, int64_t x_stride, const phs_conv_pool*
   if (!weights || !weights->weight || batch < 0 || tokens < 0) return PHS_EINVAL;
   if (tokens > 0 && (!x || !out)) return PHS_EINVAL;
   if (pool->width < 2 || pool->width > 4 || pool->channels % 8 != 0) return PHS_EUNSUPPORTED;
+  if (tokens > INT32_MAX - 65536) return PHS_EUNSUPPORTED;  // a tile's last row and more
   if (tokens > 0 && bad_rows(x_stride, pool->channels)) return PHS_ESHAPE;
   if (!state_ids && batch > pool->num_states) return PHS_ESHAPE;
   if (!aligned16(x) || !aligned16(out) || !aligned16(pool->c) || !aligned16(weights->weight) ||
@@ -2155,6 +2190,15 @@ int scan_args(ScanArgs& a, const phs_scan_inputs* in, const phs_scan_pool* pool,
   a.B = batch;
   a.out_f32 = out_dtype == PHS_OUT_F32;
   return PHS_OK;
+}
+
+bool scan_overlap(const ScanArgs& a, int P, int N, int64_t tokens) {
+  const int64_t hp = int64_t{a.H} * P, gn = int64_t{a.G} * N;
+  const Rows out{a.out, hp, hp, a.out_f32 ? 4 : 2};
+  return overlap({a.x, a.x_stride, hp, 2}, out, tokens) ||
+         overlap({a.b, a.b_stride, gn, 2}, out, tokens) ||
+         overlap({a.c, a.c_stride, gn, 2}, out, tokens) ||
+         overlap({a.dt, a.dt_stride, a.H, a.dt_f32 ? 4 : 2}, out, tokens);
 }
 
 // How a prompt call is spread over the SMs: 64-wide heads in pairs where a
@@ -2233,6 +2277,9 @@ int phs_causal_conv_decode(const void* x, int64_t x_stride, const phs_conv_pool*
   if (st) return st;
   if (batch > 65535) return PHS_EUNSUPPORTED;  // grid y
   if (batch == 0) return PHS_OK;
+  const int64_t channels = pool->channels;
+  if (overlap_in_part({x, x_stride, channels, 2}, {out, channels, channels, 2}, batch))
+    return PHS_EINVAL;
   return launch_conv_decode(pool->width, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -2247,12 +2294,9 @@ int phs_causal_conv_prompt(const void* x, int64_t x_stride, const int32_t* cu_se
   if (st) return st;
   if (!cu_seqlens) return PHS_EINVAL;
   // (a tile's rows are read again, as earlier inputs, by the next one)
-  if (total_tokens > 0) {
-    const uintptr_t xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
-    const uintptr_t xe = xa + 2 * (uintptr_t(total_tokens - 1) * x_stride + pool->channels);
-    const uintptr_t oe = oa + 2 * uintptr_t(total_tokens) * pool->channels;
-    if (xa < oe && oa < xe) return PHS_EINVAL;
-  }
+  const int64_t channels = pool->channels;
+  if (overlap({x, x_stride, channels, 2}, {out, channels, channels, 2}, total_tokens))
+    return PHS_EINVAL;
   if (batch == 0) return PHS_OK;
   a.cu_seqlens = cu_seqlens;
   a.resume = resume;
@@ -2269,6 +2313,7 @@ int phs_selective_scan_decode(const phs_scan_inputs* in, const phs_scan_pool* po
   const int st = scan_args(a, in, pool, weights, state_ids, batch, batch, out, out_dtype,
                            dev_status);
   if (st || batch == 0) return st;
+  if (scan_overlap(a, pool->head_dim, pool->state_dim, batch)) return PHS_EINVAL;
   return launch_scan_decode(pool->head_dim, pool->state_dim, a,
                             reinterpret_cast<cudaStream_t>(stream));
 }
@@ -2304,6 +2349,7 @@ int phs_selective_scan_prompt(const phs_scan_inputs* in, const int32_t* cu_seqle
                                 batch, a.H, a.G, pool->head_dim, pool->state_dim, total_tokens,
                                 max_seq_len))))
     return st;
+  if (scan_overlap(a, pool->head_dim, pool->state_dim, total_tokens)) return PHS_EINVAL;
   a.cu_seqlens = cu_seqlens;
   a.resume = resume;
   a.total_tokens = total_tokens;

@@ -52,7 +52,7 @@
 // 2,800 of a scheduler.  The rest is the chain of steps through the roles, scores
 // to P to PV to the rows and back to QS, with two or three warps a scheduler to
 // hide each one's latency.  One prompt of 32,751 tokens, 64 heads of 64 and N =
-// 128: 421 us (tables 14, sums of segments 90, join 8) against 83 for its bytes.
+// 128: 421 us (tables 14, sums of segments 90, join 8) against 101 for its bytes.
 // What helped: P of both slots from one QK, in halves, so that PV and the next QK
 // run beside the other half's P (577 -> 509); bf16 operands (-> 468); table values
 // read a half ahead and only read there, since a warp waits where it computes
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   // barriers: tile loaded / used, X' terms written / used; of a half of the
   // scores' columns: scores complete, P (and with the first half the
   // inter-chunk part) ready, P read; output tile written; state (the last
-  // chunk's sum is read, the state's terms written, rows behind the last token
+  // chunk's sum is read, the state written, rows behind the last token
   // zero), chunk sum complete; drain; inter-chunk part complete, outputs
   // complete, outputs read, all of the last chunk's KV issued
   auto bar = [sb](int i) { return sb + L::kBar + 8 * i; };
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     }
     for (int i = 0; i < T::kUBufs; ++i) {
       mbar_init(s_ready + 8 * i, 256);
-      mbar_init(u_done + 8 * i, STATES ? 1 : 2);  // KV, and QS done with the state's terms
+      mbar_init(u_done + 8 * i, STATES ? 1 : 2);  // KV, and QS done with the state
     }
     mbar_init(qs_done, 1);
     mbar_init(o_free, 256);
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
               umma_bf16(tmem + T::kOut, dc + at, ds + at, id_qs, ks > 0);
             }
             umma_commit(qs_done);
-            umma_commit(u_done);  // the state's terms have been read
+            umma_commit(u_done);  // the state has been read
             umma_commit(empty_of(tile_c(n)));
           }
           __syncwarp();
@@ -942,10 +942,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     float log = 0.f;                           // of the part's decay
     float decay = mine && nch > 0 ? table(0, qt >> 1)[kTabDecay] : 0.f;  // a chunk ahead
     float total = STATES && mine && nch > 0 ? table(0, qt >> 1)[kTabTotal] : 0.f;
-    // R <- state after chunk n (n >= 0), and where `terms` its two terms to
-    // shared memory for the next chunk's QS (the last one has read its own
-    // by then: the chunk's sum was issued after it)
-    auto next_state = [&](int n, bool terms) {
+    // R <- state after chunk n (n >= 0), and where `store` as bf16 to shared
+    // memory for the next chunk's QS (u_done counts the last one's reads too)
+    auto next_state = [&](int n, bool store) {
       const int ub = n >= 0 ? n % T::kUBufs : 0;
       uint64_t factor = 0ull, base = 0ull;
       if (n >= 0 && mine) {
@@ -974,7 +973,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
               R[8 * c + e] = f2_add(f2_fma(R[8 * c + e], factor, f2_mul(R[8 * c + e], base)),
                                     f2(u[2 * e], u[2 * e + 1]));
           }
-          if (terms) {
+          if (store) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const uint64_t* x = R + 8 * c + 4 * k;
@@ -984,7 +983,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
             }
           }
         }
-        if (terms) fence_proxy_async_smem();
+        if (store) fence_proxy_async_smem();
       }
       tc_fence_before();
       mbar_arrive(s_ready + 8 * ub);

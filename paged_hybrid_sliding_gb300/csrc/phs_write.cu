@@ -567,6 +567,8 @@ int launch_write_t(const WriteArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 int launch_write(int D, WriteArgs a, int num_sms, cudaStream_t stream) {
+  // (a limit of 1, 2, 4 or 8 CTAs an SM: 45 to 49 us for 1,514 ragged tokens
+  // written and read back, all within that call's own spread)
   a.tile = kWriteMaxTile;
   while (a.tile > 1 && a.tokens < a.tile * 8 * num_sms) a.tile /= 2;
   return D == 128 ? launch_write_t<128>(a, num_sms, stream)

@@ -180,3 +180,12 @@ def test_refusals_of_the_binding():
     with pytest.raises(ValueError):
         phs.causal_conv_prompt(x, dev([]), pool, w)
     assert torch.equal(pool.c, start)
+
+
+def test_a_token_over_its_own_input():
+    C, W, B = 264, 4, 5
+    w, pool, start = setup(C, W, B, 3, True, True)
+    x = rows(B, C, 0, 9).contiguous()
+    want = phs.causal_conv_decode(x, phs.ConvPool(start.clone()), w)
+    phs.causal_conv_decode(x, pool, w, out=x)
+    assert torch.equal(x, want)

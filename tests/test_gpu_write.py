@@ -50,6 +50,28 @@ def test_rotate(D, rotary, inter, T, Hq, Hk):
     assert q2 is q and torch.equal(q, qo) and torch.equal(k, ko)
 
 
+@pytest.mark.parametrize("T", [1, 3, 50])
+def test_rotate_parts_of_one_projection(T):
+    """q, k and v side by side in one row: q and k in place, or into parts of
+    other rows; nothing else changes."""
+    Hq, Hk, D = 4, 2, 64
+    rope, pos = phs.Rope.make(D), torch.arange(5, 5 + T, dtype=torch.int32, device="cuda")
+    rows = bf16((T, Hq + 2 * Hk, D), 4)
+    want = phs.rope_rotate(rows[:, :Hq].contiguous(), rows[:, Hq:Hq + Hk].contiguous(), pos, rope)
+    want = torch.cat([*want, rows[:, Hq + Hk:]], 1)
+    into = rows.clone()
+    parts = lambda r: (r[:, :Hq], r[:, Hq:Hq + Hk])
+    phs.rope_rotate(*parts(rows), pos, rope, *parts(into))
+    assert torch.equal(into, want)
+    phs.rope_rotate(*parts(rows), pos, rope, *parts(rows))
+    assert torch.equal(rows, want)
+    # an output over a part of an input is refused
+    before = rows.clone()
+    with pytest.raises(RuntimeError):
+        phs.rope_rotate(*parts(rows), pos, rope, rows[:, 1:1 + Hq], into[:, :Hk])
+    assert torch.equal(rows, before)
+
+
 def test_rotate_many_tokens():
     """Every tile size, and heads above one pass of a CTA."""
     rope = phs.Rope.make(64)
@@ -153,6 +175,18 @@ def test_write_tokens_as_append():
     phs.kv_append_paged(c.start, kr, v, dev(c.table), dev(lens))
     qr[4] = 0   # inactive
     assert int(st.item()) == 0 and same(c.pool, c.start) and torch.equal(out, qr)
+
+
+def test_queries_rotated_in_place():
+    lens = np.array([3, 40, 16], np.int32)
+    H, D, T = 2, 128, 20
+    cu, c = dev(np.array([0, 3, 9, 20])), Cache(lens, H, D, 6)
+    k, v, q = bf16((T, H, D), 1), bf16((T, H, D), 2), bf16((T, 6, D), 3)
+    a = (c.pool, k, v, dev(c.table), dev(lens))
+    rope = phs.Rope.make(64)
+    want = phs.kv_write_paged(*a, cu_seqlens=cu, rope=rope, q=q)
+    assert phs.kv_write_paged(*a, cu_seqlens=cu, rope=rope, q=q, q_out=q) is q
+    assert torch.equal(q, want)
 
 
 @pytest.mark.parametrize("H,D,inter,rotary", [(8, 128, False, 128), (3, 64, True, 64),

@@ -109,6 +109,65 @@ def test_conv_prompt_refuses_an_output_over_its_input():
                                             ctypes.c_void_p((1 << 20) + 9 * 128), None, None) == 0
 
 
+def at(address):
+    return ctypes.c_void_p(address)
+
+
+BASE = 1 << 20
+
+
+def test_more_rows_than_a_tile_counts():
+    pool, w = _lib.ConvPoolC(P.value, 4, 64, 4), _lib.ConvWeightsC(P.value, 0, 1)
+    assert phs.lib().phs_causal_conv_prompt(P, 64, P, 2**31 - 9, ref(pool), ref(w), None, None, 2,
+                                            at(1 << 50), None, None) == -7
+
+
+@pytest.mark.parametrize("q,qs,k,ks,qo,qos,ko,kos", [
+    # (9 tokens of 4 and 2 heads of 64: 512 and 256 bytes a row)
+    (0, 256, 1 << 20, 128, 16, 256, 2 << 20, 128),            # q_out over q, 16 bytes on
+    (0, 384, 1 << 20, 128, 0, 256, 2 << 20, 128),             # another stride
+    (0, 256, 1 << 20, 128, 2 << 20, 256, (1 << 20) + 9 * 256 - 16, 128),  # k_out over k's last
+    (0, 256, 1 << 20, 128, 1 << 20, 256, 2 << 20, 128),       # q_out over k
+    (0, 256, 1 << 20, 128, 2 << 20, 256, 8 * 512, 128),       # k_out over q
+    (0, 384, 512, 384, 2 << 20, 384, (2 << 20) + 496, 384),   # k_out over q_out in one row
+    (0, 384, 512, 384, 2 << 20, 384, (2 << 20) + 528, 384)])  # ... and in the next row
+def test_rotate_refuses_outputs_over_others(q, qs, k, ks, qo, qos, ko, kos):
+    a = [at(BASE + q), qs, 4, at(BASE + k), ks, 2, 64, 9, P, ref(rope()), at(BASE + qo), qos,
+         at(BASE + ko), kos, None]
+    assert phs.lib().phs_rope_rotate(*a) == -1
+
+
+@pytest.mark.parametrize("q,qs,k,v,qo", [
+    (0, 512, 1 << 20, 2 << 20, 16), (0, 768, 1 << 20, 2 << 20, 0),
+    (0, 512, 1 << 20, 2 << 20, (1 << 20) + 9 * 512 - 16),
+    (0, 512, 1 << 20, 2 << 20, (2 << 20) - 9 * 1024 + 16)])
+def test_write_refuses_an_output_over_its_inputs(q, qs, k, v, qo):
+    a = [ref(paged()), at(BASE + k), 256, at(BASE + v), 256, 9, P, P, 4, P, 2, ref(rope()),
+         at(BASE + q), qs, 8, at(BASE + qo)]
+    assert phs.lib().phs_kv_write_paged(*a, None, None, 0, None, None, 0, None, None, None) == -1
+
+
+@pytest.mark.parametrize("out,stride", [(16, 64), (-16, 64), (0, 72), (2 * 72 * 2 - 16, 72)])
+def test_conv_of_a_token_refuses_an_output_over_a_part_of_its_input(out, stride):
+    pool, w = _lib.ConvPoolC(P.value, 4, 64, 4), _lib.ConvWeightsC(P.value, 0, 1)
+    assert phs.lib().phs_causal_conv_decode(P, stride, ref(pool), ref(w), None, 3, at(BASE + out),
+                                            None, None) == -1
+
+
+@pytest.mark.parametrize("over", ["x", "b", "c", "dt"])
+def test_scan_refuses_an_output_over_its_inputs(over):
+    where = dict(x=0, b=1 << 20, c=2 << 20, dt=3 << 20)
+    v = {n: BASE + d for n, d in where.items()}
+    inputs = _lib.ScanInputsC(v["x"], v["b"], v["c"], v["dt"], 256, 128, 128, 4, 2, 0)
+    pool, w = _lib.ScanPoolC(P.value, 4, 4, 64, 64), _lib.ScanWeightsC(P.value, 0, 0)
+    lib = phs.lib()
+    assert lib.phs_selective_scan_decode(ref(inputs), ref(pool), ref(w), None, 2, at(v[over]), 1,
+                                         None, None) == -1
+    # its last bytes over the first ones
+    assert lib.phs_selective_scan_decode(ref(inputs), ref(pool), ref(w), None, 2,
+                                         at(v[over] - 2 * 1024 + 16), 1, None, None) == -1
+
+
 @pytest.mark.parametrize("change,code", [
     (dict(x=0), -1), (dict(x=ODD.value), -9), (dict(b=0), -1), (dict(c=ODD.value), -9),
     (dict(dt=0), -1), (dict(xs=128), -2), (dict(xs=260), -2), (dict(bs=64), -2), (dict(cs=64), -2),
