@@ -40,7 +40,8 @@ struct WriteArgs {
   const int32_t* qlens;
   int64_t num_qpages;
   int max_qpages, max_qblocks;
-  int tile;  // tokens of a CTA
+  int tile;           // tokens of a CTA
+  int q_with_blocks;  // 1: queries of tokens in new blocks are the blocks' launch's
 };
 
 struct ReadArgs {
@@ -62,7 +63,7 @@ struct ReadArgs {
   int Hkv, B, tokens, max_tokens, max_pages, max_qpages;
 };
 
-constexpr int kWriteMaxTile = 8;  // tokens
+constexpr int kWriteMaxTile = 16;  // tokens
 
 int launch_write(int D, WriteArgs a, int num_sms, cudaStream_t stream);
 int launch_read_back(int D, const ReadArgs& a, cudaStream_t stream);

@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(kThreads) phs_write_kernel(const __grid_consta
   __shared__ int s_owner[kWriteMaxTile], s_pos[kWriteMaxTile], s_q[kWriteMaxTile];
   __shared__ int64_t s_row[kWriteMaxTile];  // row (head 0, token's slot) of its page, or -1
   __shared__ float2 s_cs[kWriteMaxTile][D / 2];
-  if (a.k_codes) pdl_launch_dependents();
   const int tile = a.tile, r0 = blockIdx.x * tile, r1 = min(r0 + tile, a.tokens);
   const int tid = threadIdx.x;
   bool refused = false;
@@ -136,7 +135,9 @@ __global__ void __launch_bounds__(kThreads) phs_write_kernel(const __grid_consta
           if (!r.idle) set_status(a.status, PHS_ERANGE);
         } else {
           pos = r.len - r.n + (a.cu_seqlens ? r0 + tid - a.cu_seqlens[b] : 0);
-          if (pos >= r.qa) {
+          if (pos < r.qa) {
+            if (a.q_with_blocks) q = -1;
+          } else {
             const int lp = pos / kPage;
             const int page =
                 lp < a.max_pages ? a.block_table[static_cast<size_t>(b) * a.max_pages + lp] : -1;
@@ -154,7 +155,10 @@ __global__ void __launch_bounds__(kThreads) phs_write_kernel(const __grid_consta
     s_q[tid] = q;
     s_row[tid] = row;
   }
-  __syncthreads();
+  if (!__syncthreads_or(tid < r1 - r0 && ((a.q && s_q[tid] >= 0) || a.k_out || s_row[tid] >= 0))) {
+    pdl_wait_prior_grid();
+    return;
+  }
   const int half = a.rotary / 2;
   for (int e = tid; e < (r1 - r0) * half; e += kThreads)
     s_cs[e / half][e % half] = turn_cs(a.turns[e % half], s_pos[e / half], a.factor);
@@ -229,6 +233,7 @@ __global__ void __launch_bounds__(kThreads) phs_write_kernel(const __grid_consta
     for (int j = 0; j < 4; ++j)
       if (to[j]) *to[j] = x[j];
   }
+  pdl_wait_prior_grid();  // (this grid's end must not come before that of the blocks' one)
 }
 
 // ---------------------------------------------------------- 8-bit blocks --
@@ -254,20 +259,27 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 // all of them.  A head's absmax meets in shared memory; V's codes are
 // transposed there.  About 400 instructions a thread and head bound it (52 % of
 // the issue slots, with the two barriers of a head): 65,521 tokens of 8 heads of
-// 128 take 125 us, 60 for their bytes.  Four CTAs an SM instead of three for
-// some spilled registers: 380 us against 397 for the call with its queries and
-// its reading back; all heads by one CTA: 358.  A warp for K or V of a head, with
-// its 32 rows in registers and no barrier, has too few warps: 420.
+// 128 alone take 125 us, 60 for their bytes.  With `q_with_blocks` one more CTA
+// a block turns the new tokens' queries, four heads in flight, which memory
+// bounds: side by side both take 250 us for 32 query heads, 220 for their bytes
+// (288 one after the other).  Three CTAs an SM; with four, and some spilled
+// registers, 342 us against 329 for the call with its reading back (without
+// queries four were better, 380 against 397); eight query heads in flight 381, two
+// 349.  A warp for K or V of a head, with its 32 rows in registers and no
+// barrier, has too few warps: 420.
 template <int D>
-__global__ void __launch_bounds__(2 * D, D == 128 ? 4 : 8)
+__global__ void __launch_bounds__(2 * D, D == 128 ? 3 : 6)
     phs_write_block_kernel(const __grid_constant__ WriteArgs a, int heads_per_cta) {
   constexpr int U = D / 16, kWarps = D / 16;
   __shared__ uint32_t s_max[kWarps];
   __shared__ __align__(16) uint8_t s_v[kQBlock * D];  // V codes, token-major
   const int tid = threadIdx.x, b = blockIdx.y;
   const int groups = (a.Hkv + heads_per_cta - 1) / heads_per_cta;
-  const int jr = blockIdx.x / groups, h0 = blockIdx.x % groups * heads_per_cta;
+  const int ctas = groups + a.q_with_blocks;  // of a block
+  const int jr = blockIdx.x / ctas, h0 = blockIdx.x % ctas * heads_per_cta;
   const int h1 = min(h0 + heads_per_cta, a.Hkv);
+  const bool queries = static_cast<int>(blockIdx.x % ctas) == groups;
+  pdl_launch_dependents();
   bool refused = a.cu_seqlens &&
                  bad_ranges(a.cu_seqlens, a.B, a.tokens, [](int, int, int) {});
   Request r{};
@@ -277,7 +289,7 @@ __global__ void __launch_bounds__(2 * D, D == 128 ? 4 : 8)
   const int j = r.qb / kQBlock + jr;
   bool work = !refused && r.ok && j < r.qa / kQBlock;
   int qp = -1;
-  if (work) {
+  if (work && !queries) {
     if (j < a.max_qpages) qp = a.qtable[static_cast<size_t>(b) * a.max_qpages + j];
     if (qp < 0 || qp >= a.num_qpages) {
       if (tid == 0) set_status(a.status, PHS_ERANGE);
@@ -292,6 +304,35 @@ __global__ void __launch_bounds__(2 * D, D == 128 ? 4 : 8)
   const uint4 *kp = nullptr, *vp = nullptr;
   int64_t step = D / 8;  // vectors from a head to the next
   float2 cs[8];
+  if (queries) {
+    if (!work || !fresh) return;
+    if (turned) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) cs[e] = turn_cs(a.turns[8 * u + e], pos, a.factor);
+    }
+    const int64_t row = (a.cu_seqlens ? a.cu_seqlens[b] : b) + (pos - (r.len - r.n));
+    const uint4* from = reinterpret_cast<const uint4*>(a.q + row * a.q_stride);
+    uint4* to = reinterpret_cast<uint4*>(a.q_out + row * a.q_out_stride);
+    constexpr int kAhead = 4;
+#pragma unroll 1
+    for (int h = 0; h < a.Hq; h += kAhead, from += kAhead * D / 8, to += kAhead * D / 8) {
+      uint4 x[kAhead], y[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (h + i < a.Hq) {
+          x[i] = from[i * D / 8 + va];
+          y[i] = from[i * D / 8 + vb];
+        }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (h + i < a.Hq) {
+          if (turned) rotate_unit(x[i], y[i], cs, a.interleaved);
+          to[i * D / 8 + va] = x[i];
+          to[i * D / 8 + vb] = y[i];
+        }
+    }
+    return;
+  }
   int bad = 0;
   if (work) {
     if (fresh) {
@@ -315,10 +356,7 @@ __global__ void __launch_bounds__(2 * D, D == 128 ? 4 : 8)
     if (tid == 0) set_status(a.status, PHS_ERANGE);
     work = false;
   }
-  if (!work) {
-    pdl_wait_prior_grid();
-    return;
-  }
+  if (!work) return;
   kp += h0 * step;
   vp += h0 * step;
   uint4 ka = kp[va], kb = kp[vb], xa = vp[2 * u], xb = vp[2 * u + 1];
@@ -406,7 +444,6 @@ __global__ void __launch_bounds__(2 * D, D == 128 ? 4 : 8)
     xa = xa1;
     xb = xb1;
   }
-  pdl_wait_prior_grid();  // (this grid's end must not come before the other one's)
 }
 
 // --------------------------------------------------------------- read back --
@@ -535,31 +572,37 @@ __global__ void __launch_bounds__(128) phs_read_back_kernel(const __grid_constan
 }
 
 template <int D>
-int launch_write_t(const WriteArgs& a, int num_sms, cudaStream_t stream) {
+int launch_write_t(WriteArgs a, int num_sms, cudaStream_t stream) {
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.stream = stream;
   cfg.attrs = &early;
+  const int64_t blocks = a.k_codes ? int64_t{a.max_qblocks} * a.B : 0;
+  if (blocks > 0) {
+    // The blocks' queries go with them where there are blocks enough to fill
+    // the SMs: their copying then runs beside the blocks' arithmetic (325 us for
+    // 65,521 tokens written and read back, 358 apart).  With fewer a CTA a block
+    // would turn its queries' heads one after another.
+    a.q_with_blocks = a.q && blocks >= int64_t{4} * num_sms;
+    // All heads of a block by one CTA, which forms their angles once, unless
+    // that leaves SMs without one; beside queries in halves, which end
+    // together with those (322 us against 327).
+    int per = a.q_with_blocks ? (a.Hkv + 1) / 2 : a.Hkv;
+    while (per > 2 && blocks * ((a.Hkv + per - 1) / per) < int64_t{8} * num_sms)
+      per = (per + 1) / 2;
+    const int ctas = (a.Hkv + per - 1) / per + a.q_with_blocks;
+    cfg.gridDim = dim3(a.max_qblocks * ctas, a.B);
+    cfg.blockDim = dim3(2 * D);
+    if (cudaLaunchKernelEx(&cfg, phs_write_block_kernel<D>, a, per) != cudaSuccess)
+      return PHS_ECUDA;
+    cfg.numAttrs = 1;  // the tokens start beside the blocks: they share no memory
+  }
   if (a.tokens > 0) {
     cfg.gridDim = dim3((a.tokens + a.tile - 1) / a.tile);
     cfg.blockDim = dim3(kThreads);
     if (cudaLaunchKernelEx(&cfg, phs_write_kernel<D>, a) != cudaSuccess) return PHS_ECUDA;
-    cfg.numAttrs = 1;  // the blocks start beside the tokens: they share no memory
-  }
-  if (a.k_codes && a.B > 0 && a.max_qblocks > 0) {
-    // all heads of a block by one CTA, which forms their angles once, unless
-    // that leaves SMs without one
-    int per = a.Hkv;
-    const int64_t blocks = int64_t{a.max_qblocks} * a.B;
-    while (per > 2 && blocks * ((a.Hkv + per - 1) / per) < int64_t{8} * num_sms)
-      per = (per + 1) / 2;
-    const int groups = (a.Hkv + per - 1) / per;
-    cfg.gridDim = dim3(a.max_qblocks * groups, a.B);
-    cfg.blockDim = dim3(2 * D);
-    if (cudaLaunchKernelEx(&cfg, phs_write_block_kernel<D>, a, per) != cudaSuccess)
-      return PHS_ECUDA;
   }
   return cudaGetLastError() == cudaSuccess ? PHS_OK : PHS_ECUDA;
 }
@@ -567,8 +610,10 @@ int launch_write_t(const WriteArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 int launch_write(int D, WriteArgs a, int num_sms, cudaStream_t stream) {
-  // (a limit of 1, 2, 4 or 8 CTAs an SM: 45 to 49 us for 1,514 ragged tokens
-  // written and read back, all within that call's own spread)
+  // Tiles as long as that leaves eight CTAs an SM (a limit of 1, 2 or 4: 45 to 49
+  // us for 1,514 ragged tokens written and read back, within that call's own spread;
+  // tiles of up to 8, 16 and 32 tokens: 342, 338 and 350 us for 65,521 tokens with
+  // their queries by the blocks' launch, since more CTAs then have nothing to do).
   a.tile = kWriteMaxTile;
   while (a.tile > 1 && a.tokens < a.tile * 8 * num_sms) a.tile /= 2;
   return D == 128 ? launch_write_t<128>(a, num_sms, stream)

@@ -243,6 +243,61 @@ def test_write_8bit(H, D, inter, rotary, hot):
             assert torch.equal(c.rows(x, b, 0, cold), c.rows(z, b, 0, cold))
 
 
+@pytest.mark.parametrize("Hq,H,D,inter,rotary", [(32, 8, 128, False, 128), (5, 5, 128, True, 48),
+                                                 (7, 1, 64, False, 64), (1, 1, 64, True, 16),
+                                                 (6, 3, 128, False, 64)])
+def test_queries_that_go_with_their_blocks(Hq, H, D, inter, rotary):
+    """With enough blocks in the grid (max_qblocks is only a limit) the blocks'
+    launch turns the queries of their new tokens: nothing that comes out differs,
+    of a request that is refused and of one with a block outside the pool neither."""
+    old = np.array([0, 5, 31, 32, 100, 333, 64, 7], np.int32)
+    new = np.array([1, 100, 1, 64, 0, 37, 31, 700], np.int32)
+    lens, hot = old + new, np.array([0, 1, 40, 0, 0, 0, 70, 13])
+    before, after = (np.maximum(n - hot, 0) // 32 * 32 for n in (old, lens))
+    T, cu = int(new.sum()), np.concatenate([[0], np.cumsum(new)])
+    k, v = strided(bf16((T, H, D), 1), 8), bf16((T, H, D), 2)
+    q = strided(bf16((T, Hq, D), 3), 16)
+    rope = phs.Rope.make(rotary, interleaved=inter)
+    pos = torch.cat([torch.arange(int(o), int(o + n)) for o, n in zip(old, new)]).int().cuda()
+    want = phs.rope_rotate(q, None, pos, rope)[0]
+
+    def call(most, lens, qtable_of):
+        c, st = Cache(old + new, H, D, 21, qlens=np.maximum(after, 32)), status()
+        for x in (c.int8.k, c.int8.v, c.int8.k_scale, c.int8.v_scale):
+            x.zero_()
+        out = torch.full((T + 2, Hq, D), 9.0, dtype=torch.bfloat16, device="cuda")
+        got = phs.kv_write_paged(c.pool, k, v, dev(c.table), dev(lens), cu_seqlens=dev(cu), q=q,
+                                 q_out=out[:T], rope=rope, int8=c.int8,
+                                 qtable=dev(qtable_of(c.qtable)), qlens_before=dev(before),
+                                 qlens=dev(after), max_qblocks=most, status=st)
+        assert bool((out[T:] == 9).all())
+        return c, got, int(st.item())
+
+    def check(lens, qtable_of, want, code):
+        few, many = (call(most, lens, qtable_of) for most in (int((after - before).max()) // 32, 200))
+        for c, got, st in (few, many):
+            assert st == code and torch.equal(got, want)
+        a, b = few[0], many[0]
+        assert same(a.pool, b.pool)
+        for x, y in ((a.int8.k, b.int8.k), (a.int8.v, b.int8.v), (a.int8.k_scale, b.int8.k_scale),
+                     (a.int8.v_scale, b.int8.v_scale)):
+            assert torch.equal(x, y)
+
+    check(lens, lambda t: t, want, 0)
+
+    def missing(t):
+        t = t.copy()
+        t[7, 3] = -1
+        return t
+
+    check(lens, missing, want, -3)
+    refused = lens.copy()
+    refused[7] = 699                     # below its new tokens
+    zero = want.clone()
+    zero[int(cu[7]):] = 0
+    check(refused, lambda t: t, zero, -3)
+
+
 def test_write_8bit_tokens():
     """One token at a time: a block is quantised when its last token is old
     enough, wholly from pages, or with the new token as its last."""
