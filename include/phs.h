@@ -720,10 +720,11 @@ int phs_kv_read_paged(const phs_paged_pool *pool, const int32_t *block_table,
  * and stay so: what goes into them has 24 bits.  phs_selective_scan_prompt
  * forms its bf16 rows from chunks of 128 tokens: the weights of a chunk's own
  * tokens and the state before the chunk enter the products as bf16, sums and
- * the skip are fp32; a token's log decay is cut at -128.  In a prompt an
- * infinite or NaN value reaches the request's rows from the start of its chunk
- * of 128 tokens on, up to 127 tokens before its own; other requests are not
- * reached.  A
+ * the skip are fp32; a token's log decay is cut at -128.  (Requests of up to 16
+ * tokens, unless one alone in a call for longer ones, go token by token as
+ * phs_selective_scan_decode does.)  In a prompt an infinite or NaN value may
+ * reach the request's rows from the start of its chunk of 128 tokens on, up to
+ * 127 tokens before its own; other requests are not reached.  A
  * request with a bad token range (outside the tokens, or beginning before an
  * earlier one's end) or a length above max_seq_len records PHS_ERANGE and is
  * left out whole.  workspace: phs_scan_prompt_workspace_bytes of the same

@@ -2357,6 +2357,10 @@ int phs_selective_scan_prompt(const phs_scan_inputs* in, const int32_t* cu_seqle
   DevInfo di;
   if ((st = dev_info(di))) return st;
   const int P = pool->head_dim, N = pool->state_dim;
+  if (std::min(total_tokens, max_seq_len) <= kScanShort) {
+    a.short_len = kScanShort;
+    return launch_scan_short(P, N, a, false, reinterpret_cast<cudaStream_t>(stream));
+  }
   const ScanPlan plan = scan_plan(batch, a.H, a.G, P, N, total_tokens, max_seq_len, di.sms);
   a.P = P;
   a.slots = plan.slots;
@@ -2368,6 +2372,7 @@ int phs_selective_scan_prompt(const phs_scan_inputs* in, const int32_t* cu_seqle
   // (grids: rows along x, tables and sums along y and z)
   if (ctas > INT32_MAX || batch > 65535 || a.units > 65535) return PHS_EUNSUPPORTED;
   a.longest_first = ctas > di.sms && batch > 1 && batch <= kScanSort;
+  a.short_len = batch > 1 ? kScanShort : -1;
   char* ws = reinterpret_cast<char*>(workspace);
   a.tables = reinterpret_cast<float*>(ws);
   a.ws = reinterpret_cast<float*>(ws + plan.tables);

@@ -112,6 +112,7 @@ struct ScanArgs {
   int slots, units;     // 64 columns of x each, that go together; such units of a request
   int nseg, nsub;       // segments of each prompt, parts of a segment
   int max_chunks;       // of a request
+  int short_len;        // requests of up to so many tokens are the short ones' launch's; or -1
   bool longest_first;   // CTAs in order of their requests' lengths (B <= kScanSort)
   float* tables;        // [tokens / 128 + B + 1][H][kScanTable]
   float* ws;            // [B][units][nseg * nsub][64 slots][N]: sums of parts, then first states
@@ -120,9 +121,11 @@ struct ScanArgs {
 
 constexpr int kScanChunk = 128;  // tokens
 constexpr int kScanTable = 536;  // floats
+constexpr int kScanShort = 16;   // tokens, at most, that go one by one
 constexpr int kScanSort = 256;   // requests of a call that are put in order, at most
 
 int launch_scan_decode(int P, int N, const ScanArgs& a, cudaStream_t stream);
+int launch_scan_short(int P, int N, const ScanArgs& a, bool early, cudaStream_t stream);
 int launch_scan_prompt(int N, const CUtensorMap& tb, const CUtensorMap& tc, const CUtensorMap& tx,
                        const CUtensorMap& to, const ScanArgs& a, cudaStream_t stream);
 

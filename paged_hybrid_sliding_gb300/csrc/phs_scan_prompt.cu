@@ -40,6 +40,8 @@
 //   warp 18     TMA stores of the output tiles, in C's place
 //   warp 19     issues QK, QS and PV
 //
+// Requests of a few tokens are left to a launch of their own (phs_scan.cu).
+//
 // Where there are fewer (request, pair) than SMs, prompts are cut into segments:
 // a launch sums up their own states (B and X alone; a segment in `nsub` parts,
 // as this launch has fewer CTAs), a small one joins these sums into the states
@@ -147,14 +149,18 @@ __device__ __forceinline__ int part_chunk(const ScanArgs& a, int chunks, int p) 
 // do not overlap, so neither do these.
 __device__ __forceinline__ int64_t table_row(int b, int t0) { return t0 / kScanC + b; }
 
-// The request that comes `at`-th when the longest come first.  Where there are
-// more CTAs than SMs, the last ones to start then end soon.  All threads of
-// the CTA call it.
+// The request that comes `at`-th when the longest come first (any short one where
+// that one is short and another launch's).  Where there are more CTAs than SMs,
+// the last ones to start then end soon.  All threads of the CTA call it.
 __device__ __forceinline__ int scan_by_length(const ScanArgs& a, int at, volatile int* found) {
   static_assert(kScanSort <= kScanThreads, "a thread for each request");
   const int j = threadIdx.x;
-  if (j < a.B) {
-    const int64_t len = int64_t{a.cu_seqlens[j + 1]} - a.cu_seqlens[j];
+  int64_t len = 0;
+  if (j < a.B) len = int64_t{a.cu_seqlens[j + 1]} - a.cu_seqlens[j];
+  const bool more = j < a.B && len > a.short_len;
+  if (at >= __syncthreads_count(more)) {
+    if (j < a.B && !more) *found = j;
+  } else if (more) {
     int before = 0;
     int64_t from = a.cu_seqlens[0];
     for (int i = 0; i < a.B; ++i) {
@@ -180,7 +186,7 @@ __global__ void __launch_bounds__(32 * kTableHeads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = h0 + warp;
   pdl_launch_dependents();
   int t0, t1;
-  if (!scan_tokens(a, b, t0, t1) || t0 + n * kScanC >= t1) return;
+  if (!scan_tokens(a, b, t0, t1) || t0 + n * kScanC >= t1 || t1 - t0 <= a.short_len) return;
   const int64_t row = table_row(b, t0) + n;
   t0 += n * kScanC;
   const int v = min(kScanC, t1 - t0);
@@ -306,12 +312,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   auto head = [&](int slot) { return (col0 + 64 * slot) / a.P; };
   const int group = head(0) / (a.H / a.G);
 
-  if (STATES) pdl_launch_dependents();  // the join waits for this grid's end
+  // the join, or the short requests' launch, waits for this grid's end
+  if (STATES || a.short_len >= 0) pdl_launch_dependents();
 
   // ---- this CTA's chunks
   const int64_t id = scan_state(a, b);
   int t0, t1;
-  if (!scan_tokens(a, b, t0, t1)) {
+  if (!scan_tokens(a, b, t0, t1) || t1 - t0 <= a.short_len) {
     pdl_wait_prior_grid();
     return;
   }
@@ -1029,7 +1036,7 @@ __global__ void __launch_bounds__(128) phs_scan_join_kernel(const __grid_constan
   pdl_launch_dependents();
   const int64_t id = scan_state(a, b);
   int t0, t1;
-  const bool good = scan_tokens(a, b, t0, t1) && id >= 0;
+  const bool good = scan_tokens(a, b, t0, t1) && id >= 0 && t1 - t0 > a.short_len;
   pdl_wait_prior_grid();
   if (!good) return;
   const int chunks = (t1 - t0 + kScanC - 1) / kScanC, parts = a.nseg * a.nsub;
@@ -1107,6 +1114,7 @@ int launch_scan_prompt_t(const CUtensorMap& tb, const CUtensorMap& tc, const CUt
     cfg.dynamicSmemBytes = kRows;
     err = cudaLaunchKernelEx(&cfg, rows, tb, tc, tx, to, a);
   }
+  if (err == cudaSuccess && a.short_len >= 0) return launch_scan_short(a.P, N, a, true, stream);
   if (err != cudaSuccess) return PHS_ECUDA;
   return cudaGetLastError() == cudaSuccess ? PHS_OK : PHS_ECUDA;
 }

@@ -156,6 +156,71 @@ def test_prompt_in_parts_then_tokens():
     L.check(ins, torch.cat(got), [(0, 400)], [0], [1], True)
 
 
+@pytest.mark.parametrize("H,G,P,N", SHAPES)
+@pytest.mark.parametrize("lens", [[16], [1, 2, 15, 16, 0, 7], [17, 16, 1, 0, 200, 8, 5],
+                                  [16, 16, 300, 16]])
+def test_short_requests_are_their_tokens(lens, H, G, P, N):
+    """Requests of up to 16 tokens give bit for bit what their tokens give one
+    by one, beside longer ones too."""
+    B = len(lens)
+    L, M = (Layer(H, G, P, N, B + 2, B, plain=H == 4) for _ in range(2))
+    rng = np.random.default_rng(H + B)
+    ids, resume = rng.permutation(B + 2)[:B], rng.integers(0, 2, B)
+    ids[B - 1] = -1 if B > 4 else ids[B - 1]
+    cu = np.concatenate([[2], 2 + np.cumsum(lens)])
+    T = int(cu[-1]) + 1
+    ins = L.inputs(T, 11, torch.float32 if H == 6 else torch.bfloat16)
+    out, st = torch.full((T, H, P), 2.0, dtype=torch.bfloat16, device="cuda"), status()
+    phs.selective_scan_prompt(*ins, dev(cu), max(lens), L.pool, L.w, state_ids=dev(ids),
+                              resume=dev(resume), out=out, status=st)
+    assert int(st.item()) == 0
+    L.check(ins, out, list(zip(cu[:-1], cu[1:])), ids, resume, True)
+    assert bool((out[:2] == 2).all()) and bool((out[-1:] == 2).all())
+    for b, n in enumerate(lens):
+        if n > 16 or ids[b] < 0:
+            continue
+        if not resume[b]:
+            M.pool.s[ids[b]] = 0
+        for t in range(int(cu[b]), int(cu[b + 1])):
+            one = phs.selective_scan_decode(*(x[t:t + 1] for x in ins), M.pool, M.w,
+                                            state_ids=dev([ids[b]]))
+            assert torch.equal(out[t], one[0]), (b, t)
+        assert torch.equal(L.pool.s[ids[b]], M.pool.s[ids[b]]), b
+
+
+@pytest.mark.parametrize("rate,bias", [(-1e-4, 0.0), (0.0, 1.0), (-1e3, 3.0), (-0.01, -8.0),
+                                       (-1e30, 5.0)])
+def test_decay_extremes_of_short_requests(rate, bias):
+    L = Layer(2, 1, 64, 64, 3, 3)
+    L.w.rate[:], L.w.dt_bias[:] = rate, bias
+    ins = L.inputs(30, 5)
+    out = phs.selective_scan_prompt(*ins, dev([0, 16, 25, 30]), 16, L.pool, L.w,
+                                    resume=dev([1, 0, 1]))
+    L.check(ins, out, [(0, 16), (16, 25), (25, 30)], [0, 1, 2], [1, 0, 1], True)
+
+
+def test_bad_short_requests():
+    """A bad range, a state that an earlier request has, one outside the pool:
+    refused in the short requests' launch as in the others'."""
+    H, G, P, N = 2, 1, 64, 64
+    L = Layer(H, G, P, N, 4, 1)
+    ins = L.inputs(40, 3)
+    for extra, most in ((0, 16), (24, 300)):     # alone, and beside a longer request
+        L.pool.s.copy_(L.start)
+        out, st = torch.full((40, H, P), 2.0, dtype=torch.bfloat16, device="cuda"), status()
+        phs.selective_scan_prompt(*ins, dev([0, 5, 9, 16, 16 + extra]), most, L.pool, L.w,
+                                  state_ids=dev([1, 1, 7, 0]), out=out, status=st)
+        assert int(st.item()) in (-1, -3) and not out[5:16].any()
+        assert torch.equal(L.pool.s[[2, 3]], L.start[[2, 3]])
+        assert bool((out[16 + extra:] == 2).all()) and bool((out[:5] != 2).any())
+        L.pool.s.copy_(L.start)
+        out.fill_(2)
+        phs.selective_scan_prompt(*ins, dev([0, 12, 6, 16, 16 + extra]), most, L.pool, L.w,
+                                  state_ids=dev([1, 2, 3, 0]), out=out, status=st)
+        assert torch.equal(L.pool.s[[2, 3]], L.start[[2, 3]])
+        assert bool((out[12:16] == 2).all())
+
+
 def test_values_that_are_not_finite_stay_in_their_request():
     H, G, P, N = 2, 1, 64, 64
     L, M = Layer(H, G, P, N, 3, 1), Layer(H, G, P, N, 3, 1)
