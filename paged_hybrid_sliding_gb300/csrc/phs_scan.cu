@@ -30,7 +30,8 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 // registers do not hold a thread's loads; states of 128 x 128, 32 heads: 167 with
 // two, 248 with four).
 template <int P, int N>
-__global__ void __launch_bounds__(256, P * N > 8192 ? 2 : 4) phs_scan_decode_kernel(const ScanArgs a) {
+__global__ void __launch_bounds__(256, P * N > 8192 ? 2 : 4)
+    phs_scan_decode_kernel(const ScanArgs a) {
   constexpr int R = P / 32, V = N / 32;  // rows of a thread, float4s of a row
   const int b = blockIdx.x, h = blockIdx.y;
   const size_t orow = (static_cast<size_t>(b) * a.H + h) * P;
