@@ -2241,7 +2241,8 @@ ScanPlan scan_plan(int B, int H, int G, int P, int N, int total, int max_seq, in
     p.nseg = static_cast<int>(s);
     p.nsub = static_cast<int>(sub);
   }
-  p.tables = align256((total / C + B + 1) * H * kScanTable * sizeof(float));
+  // (in 64 bits: 65,535 requests of 128 heads have 4.5e9 floats of tables)
+  p.tables = align256(static_cast<size_t>(total / C + B + 1) * H * kScanTable * sizeof(float));
   if (p.nseg > 1)
     p.sums = align256(static_cast<size_t>(pairs) * p.nseg * p.nsub * 64 * p.slots * N * sizeof(float));
   p.need = p.tables + p.sums;
