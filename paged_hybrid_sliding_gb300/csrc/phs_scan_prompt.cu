@@ -89,9 +89,10 @@ constexpr int kTabFrom = 512;   // [4][4] of rows in block q for columns in bloc
 constexpr int kTabBase = 528;   // [4] sum of l before each 32 tokens
 constexpr int kTabTotal = 532;  // sum of l, natural
 constexpr int kTabDecay = 533;  // its decay_factor
-// On the diagonal exp(L_i - L_j) is a product too, of exp(L_i - L_m) and exp(L_m -
-// L_j), m the 16th of the 32 tokens, unless one of the factors may be above
-// 2^100 (half of the 32 tokens decay by more): then each is taken by itself.
+// On the diagonal exp(L_i - L_j) s_j is a product too, of exp(L_i - L_m) and exp(L_m -
+// L_j) s_j, m the 16th of the 32 tokens, unless the first may be above 2^100 or the
+// second leave 2^-124 to 2^124 (half of the 32 tokens decay by more, or steps are
+// tiny or huge beside it): then each is taken by itself.
 constexpr float kNoRoom = 1e30f;
 static_assert(kScanTable == 536, "a table");
 
@@ -235,11 +236,20 @@ __global__ void __launch_bounds__(32 * kTableHeads)
   if (lane == 31) after = 0.f;
   if ((lane & 7) == 0) before = 0.f;
   float loc[4], diag[4], col[4], end[4], run = 0.f;
+  float least = INFINITY, most = -INFINITY;  // log2 of the steps of these 32 tokens
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     run += l[e];
     loc[e] = (before + run) * kLog2e;
-    diag[e] = loc[e] - log2f(s[e]);
+    const float log_s = log2f(s[e]);
+    diag[e] = loc[e] - log_s;
+    if (s[e] > 0.f) least = fminf(least, log_s);  // (a step of zero weighs nothing)
+    most = fmaxf(most, log_s);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   }
   const float first16 = __shfl_sync(0xffffffffu, loc[3], (lane & 24) + 3);
   run = 0.f;
@@ -260,11 +270,17 @@ __global__ void __launch_bounds__(32 * kTableHeads)
 #pragma unroll
   for (int q = 0; q < 4; ++q) x[q] = __shfl_sync(0xffffffffu, block, 8 * q) * kLog2e;
   const float half16 = __shfl_sync(0xffffffffu, first16, 8 * (lane & 3));
+  least = __shfl_sync(0xffffffffu, least, 8 * (lane & 3));
+  most = __shfl_sync(0xffffffffu, most, 8 * (lane & 3));
   if (lane < 16) {  // lane 4 k + q
     const int k = lane >> 2, q = lane & 3;
     float from = 0.f;
-    if (k == q)
-      from = half16 > -100.f && x[q] - half16 > -100.f ? -half16 : kNoRoom;
+    if (k == q) {
+      const float rest = x[q] - half16;  // of the other 16
+      const bool room = half16 > -100.f && rest > -100.f && half16 + least > -124.f &&
+                        most - rest < 124.f;
+      from = room ? -half16 : kNoRoom;
+    }
 #pragma unroll
     for (int m = 1; m < 3; ++m)
       if (k < m && m < q) from += x[m];

@@ -29,3 +29,44 @@ def test_workspace_holds_a_table_for_each_chunk_and_head(B, H, P, N, total, most
     want = (total // CHUNK + B + 1) * H * TABLE * 4
     got = phs.scan_prompt_workspace_bytes(B, H, 1, P, N, total, most)
     assert want <= got <= want + 256
+
+
+# --------------------------------------------------------------------- steps --
+class Case:
+    """One request, alone in its call (chunks, from 17 tokens on)."""
+
+    def __init__(self, T, H, P, N, rate, step, seed, scale=1.0):
+        x, b, c = (synth.normal_bf16((T, h, n), seed + i, device="cuda")
+                   for i, (h, n) in enumerate(((H, P), (1, N), (1, N))))
+        self.ins = [x, step, b * scale, c]
+        self.w = phs.ScanWeights(torch.full((H,), rate, device="cuda"))
+        self.pool = phs.ScanPool.zeros(1, H, P, N)
+
+    def check(self, chunked=True):
+        T = self.ins[0].shape[0]
+        out = phs.selective_scan_prompt(*self.ins, dev([0, T]), T, self.pool, self.w)
+        y, S, m, A, log = ref.scan(*self.ins, torch.zeros_like(self.pool.s[0]), self.w.rate, None, None)
+        bo, bs = ref.scan_bounds(y, m, A, log, out.dtype, self.ins[2].shape[2], chunked)
+        # (fp32's lowest normal number is 2^-126: what is below may go out as zero, and
+        # comes in again times up to N values of c below 2^3)
+        ref.close(out, y, bo + 2.0 ** -115, "out")
+        ref.close(self.pool.s[0], S, bs + 2.0 ** -120, "state")
+
+
+@pytest.mark.parametrize("at,first", [(0, 1), (32, 33), (96, 104)])
+@pytest.mark.parametrize("dt", [-35.0, -41.0, -60.0])
+def test_a_tiny_step_before_a_strong_decay(at, first, dt):
+    """A step of 2^-50 to 2^-87 whose 32 tokens decay by up to 2^-99 behind it:
+    its own row is that step times c b x, and nothing else is in it."""
+    step = torch.full((128, 2), -100.0, device="cuda")
+    step[at] = dt
+    step[first:at + 16] = 4.5    # softplus: 4.511
+    Case(128, 2, 64, 64, -0.98, step, 5).check()
+
+
+@pytest.mark.parametrize("big", [2.0 ** 30, 2.0 ** 40, 2.0 ** 60])
+def test_huge_steps_that_decay_strongly(big):
+    """Steps far above softplus's bend, each decaying by 2^-6 (32 tokens by
+    2^-186): a weight is a step at most, whatever the factors it is formed of."""
+    step = torch.full((300, 2), big, device="cuda")
+    Case(300, 2, 64, 64, -4.15 / big, step, 7, 2.0 ** -20).check()
