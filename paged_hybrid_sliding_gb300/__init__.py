@@ -1208,7 +1208,8 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, scale=1.0, trained_
         # index of the pair that makes so many rotations in trained_len
         at = [half * math.log(trained_len / (2 * math.pi * r)) / math.log(base)
               for r in (high, low)]
-        first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), half - 1)
+        # (`last` may lie behind the slowest pair, which then keeps a part of its speed)
+        first, last = max(math.floor(at[0]), 0), math.ceil(at[1])
         slow = np.clip((i - first) / max(last - first, 0.001), 0, 1)
         return freq * (1 - slow) + freq / scale * slow, 0.1 * math.log(scale) + 1
     keep = np.clip((trained_len * freq / (2 * math.pi) - low) / (high - low), 0, 1)
