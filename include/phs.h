@@ -619,7 +619,8 @@ int phs_linear_attn_prompt(const void *q, int32_t num_q_heads, const void *k, co
  * Rows: x_stride is the number of elements from one token's row to the next
  * one's, at least heads * D, a multiple of 8; heads and their elements lie
  * side by side, pointers 16-byte aligned (a part of a wider projection's rows
- * will do).
+ * will do).  Here and below at most 2^31 - 65,537 rows of 2^31 - 1 elements
+ * (PHS_EUNSUPPORTED).
  *
  * phs_rope_rotate: q_out[t] = q[t] rotated by positions[t] (device int32
  * [tokens]), k likewise (k NULL: q alone).  An output may be its own input

@@ -1903,6 +1903,10 @@ namespace {
 // Rows of `cols` elements at a stride: 16-byte pieces.
 bool bad_rows(int64_t stride, int64_t cols) { return stride < cols || stride % 8 != 0; }
 
+// A kernel's last tile ends behind the last row, and a row's elements are
+// counted in 32 bits.
+bool too_many(int64_t rows, int64_t cols) { return rows > INT32_MAX - 65536 || cols > INT32_MAX; }
+
 // Whether rows of `cols` elements at a stride and others share memory: parts of
 // the same wider rows do not; else rows whose ranges meet are taken to.
 struct Rows {
@@ -1963,6 +1967,7 @@ int phs_rope_rotate(const void* q, int64_t q_stride, int32_t num_q_heads, const 
   if (bad_rows(q_stride, qc) || bad_rows(q_out_stride, qc)) return PHS_ESHAPE;
   if (k && (bad_rows(k_stride, kc) || bad_rows(k_out_stride, kc))) return PHS_ESHAPE;
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out)) return PHS_EALIGN;
+  if (too_many(tokens, qc) || (k && too_many(tokens, kc))) return PHS_EUNSUPPORTED;
   if (tokens == 0) return PHS_OK;
   const Rows qi{q, q_stride, qc, 2}, ki{k, k_stride, kc, 2};
   const Rows qo{q_out, q_out_stride, qc, 2}, ko{k_out, k_out_stride, kc, 2};
@@ -2006,6 +2011,7 @@ int phs_kv_write_paged(const phs_paged_pool* pool, const void* k, int64_t k_stri
   const int64_t kc = int64_t{pool->num_kv_heads} * D;
   if (tokens > 0 && (bad_rows(k_stride, kc) || bad_rows(v_stride, kc))) return PHS_ESHAPE;
   if (!aligned16(k) || !aligned16(v)) return PHS_EALIGN;
+  if (too_many(tokens, q ? int64_t{num_q_heads} * D : 0)) return PHS_EUNSUPPORTED;
   if (rope && (st = check_rope(rope, D))) return st;
   if (q) {
     if (!rope || !q_out || num_q_heads <= 0) return PHS_EINVAL;
@@ -2076,7 +2082,7 @@ int phs_kv_read_paged(const phs_paged_pool* pool, const int32_t* block_table,
   if (batch > 0 && (!block_table || !starts || !cu_seqlens)) return PHS_EINVAL;
   if (tokens > 0 && (!k_out || !v_out)) return PHS_EINVAL;
   if (!aligned16(k_out) || !aligned16(v_out)) return PHS_EALIGN;
-  if (batch > 65535) return PHS_EUNSUPPORTED;  // grid y
+  if (batch > 65535 || too_many(tokens, 0)) return PHS_EUNSUPPORTED;  // (grid y)
   ReadArgs a;
   std::memset(&a, 0, sizeof(a));
   if (int8) {
@@ -2124,7 +2130,7 @@ int conv_args(ConvArgs& a, const void* x, int64_t x_stride, const phs_conv_pool*
   if (!weights || !weights->weight || batch < 0 || tokens < 0) return PHS_EINVAL;
   if (tokens > 0 && (!x || !out)) return PHS_EINVAL;
   if (pool->width < 2 || pool->width > 4 || pool->channels % 8 != 0) return PHS_EUNSUPPORTED;
-  if (tokens > INT32_MAX - 65536) return PHS_EUNSUPPORTED;  // a tile's last row and more
+  if (too_many(tokens, 0)) return PHS_EUNSUPPORTED;
   if (tokens > 0 && bad_rows(x_stride, pool->channels)) return PHS_ESHAPE;
   if (!state_ids && batch > pool->num_states) return PHS_ESHAPE;
   if (!aligned16(x) || !aligned16(out) || !aligned16(pool->c) || !aligned16(weights->weight) ||
@@ -2344,6 +2350,7 @@ int phs_selective_scan_prompt(const phs_scan_inputs* in, const int32_t* cu_seqle
                      dev_status);
   if (st) return st;
   if (!cu_seqlens || max_seq_len < 0) return PHS_EINVAL;
+  if (too_many(total_tokens, 0)) return PHS_EUNSUPPORTED;
   if (batch == 0) return PHS_OK;
   if ((st = check_workspace(workspace, workspace_bytes,
                             phs_scan_prompt_workspace_bytes(

@@ -28,3 +28,48 @@ def test_parts_where_every_pair_turns_more_than_once(dim, base, trained):
                    0, 1)
     assert np.allclose(f, plain * (1 - slow) + plain / 8 * slow, rtol=1e-13, atol=0)
     assert plain[-1] / 8 * 1.05 < f[-1] < plain[-1]
+
+
+# --------------------------------------------------------- 32-bit row counts --
+# (a kernel's last tile ends behind the last token: its rows must not pass 2^31)
+MANY = 2 ** 31 - 9
+
+
+def ref(x):
+    return ctypes.byref(x)
+
+
+def pool(**kw):
+    return phs._lib.PagedPoolC(P.value, P.value, 8, 16, kw.get("heads", 1), 64)
+
+
+ROPE = phs._lib.RopeC(P.value, 64, 0, 1.0)
+
+
+@pytest.mark.parametrize("tokens,q_heads,k_heads", [(MANY, 1, 1), (3, 2 ** 25, 1), (3, 1, 2 ** 25)])
+def test_rotate_refuses_rows_past_32_bits(tokens, q_heads, k_heads):
+    qs, ks = q_heads * 64, k_heads * 64
+    assert phs.lib().phs_rope_rotate(P, qs, q_heads, FAR, ks, k_heads, 64, tokens, P, ref(ROPE), P,
+                                     qs, FAR, ks, None) == -7
+
+
+@pytest.mark.parametrize("tokens,q_heads", [(MANY, 1), (3, 2 ** 25)])
+def test_write_refuses_rows_past_32_bits(tokens, q_heads):
+    far = [ctypes.c_void_p(i << 50) for i in (1, 2, 3)]
+    assert phs.lib().phs_kv_write_paged(ref(pool()), far[0], 64, far[1], 64, tokens, P, P, 4, P, 2,
+                                        ref(ROPE), P, q_heads * 64, q_heads, far[2], None, None, 0,
+                                        None, None, 0, None, None, None) == -7
+
+
+def test_read_refuses_rows_past_32_bits():
+    assert phs.lib().phs_kv_read_paged(ref(pool()), P, 4, P, P, 2, MANY, MANY, None, None, 0, None, P,
+                                       FAR, None, None) == -7
+
+
+def test_scan_refuses_rows_past_32_bits():
+    v = [i << 50 for i in (1, 2, 3, 4)]
+    inputs = phs._lib.ScanInputsC(*v, 64, 64, 64, 1, 1, 0)
+    assert phs.lib().phs_selective_scan_prompt(
+        ref(inputs), P, MANY, MANY, ref(phs._lib.ScanPoolC(P.value, 4, 1, 64, 64)),
+        ref(phs._lib.ScanWeightsC(P.value, 0, 0)), None, None, 2, ctypes.c_void_p(5 << 50), P, 2 ** 62,
+        None, None) == -7
