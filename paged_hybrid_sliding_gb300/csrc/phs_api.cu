@@ -2256,6 +2256,10 @@ ScanPlan scan_plan(int B, int H, int G, int P, int N, int total, int max_seq, in
   return p;
 }
 
+// Whether every request of a call goes token by token, by one launch that keeps
+// nothing in the workspace.
+bool scan_by_token(int32_t total, int32_t max_seq) { return std::min(total, max_seq) <= kScanShort; }
+
 // [tokens] rows of `cols` bf16 at a stride; boxes of 128 tokens x 64 columns
 int map_bf16_strided(CUtensorMap* m, const void* base, int64_t tokens, int64_t cols,
                      int64_t stride) {
@@ -2330,8 +2334,9 @@ size_t phs_scan_prompt_workspace_bytes(int32_t batch, int32_t num_heads, int32_t
                                        int32_t max_seq_len) {
   if (batch < 0 || total_tokens < 0 || max_seq_len < 0 || num_heads <= 0 || num_groups <= 0 ||
       num_heads % num_groups != 0 || (head_dim != 64 && head_dim != 128) ||
-      (state_dim != 64 && state_dim != 128))
+      (state_dim != 64 && state_dim != 128) || num_heads > 65535)
     return 0;
+  if (scan_by_token(total_tokens, max_seq_len)) return 256;
   DevInfo di;
   if (dev_info(di)) return 0;
   return scan_plan(batch, num_heads, num_groups, head_dim, state_dim, total_tokens, max_seq_len,
@@ -2362,13 +2367,13 @@ int phs_selective_scan_prompt(const phs_scan_inputs* in, const int32_t* cu_seqle
   a.resume = resume;
   a.total_tokens = total_tokens;
   a.max_seq = max_seq_len;
-  DevInfo di;
-  if ((st = dev_info(di))) return st;
   const int P = pool->head_dim, N = pool->state_dim;
-  if (std::min(total_tokens, max_seq_len) <= kScanShort) {
+  if (scan_by_token(total_tokens, max_seq_len)) {
     a.short_len = kScanShort;
     return launch_scan_short(P, N, a, false, reinterpret_cast<cudaStream_t>(stream));
   }
+  DevInfo di;
+  if ((st = dev_info(di))) return st;
   const ScanPlan plan = scan_plan(batch, a.H, a.G, P, N, total_tokens, max_seq_len, di.sms);
   a.P = P;
   a.slots = plan.slots;
@@ -2386,16 +2391,11 @@ int phs_selective_scan_prompt(const phs_scan_inputs* in, const int32_t* cu_seqle
   a.ws = reinterpret_cast<float*>(ws + plan.tables);
   a.ws_log = reinterpret_cast<float*>(ws + plan.tables + plan.sums);
   CUtensorMap tb, tc, tx, to;
-  std::memset(&tb, 0, sizeof(tb));
-  if (total_tokens > 0) {
-    const int64_t hp = int64_t{a.H} * P, gn = int64_t{a.G} * N;
-    if ((st = map_bf16_strided(&tb, a.b, total_tokens, gn, a.b_stride))) return st;
-    if ((st = map_bf16_strided(&tc, a.c, total_tokens, gn, a.c_stride))) return st;
-    if ((st = map_bf16_strided(&tx, a.x, total_tokens, hp, a.x_stride))) return st;
-    if ((st = map_bf16_strided(&to, out, total_tokens, hp, hp))) return st;
-  } else {
-    tc = tx = to = tb;  // no chunk, no copy
-  }
+  const int64_t hp = int64_t{a.H} * P, gn = int64_t{a.G} * N;
+  if ((st = map_bf16_strided(&tb, a.b, total_tokens, gn, a.b_stride))) return st;
+  if ((st = map_bf16_strided(&tc, a.c, total_tokens, gn, a.c_stride))) return st;
+  if ((st = map_bf16_strided(&tx, a.x, total_tokens, hp, a.x_stride))) return st;
+  if ((st = map_bf16_strided(&to, out, total_tokens, hp, hp))) return st;
   return launch_scan_prompt(N, tb, tc, tx, to, a, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -1104,19 +1104,15 @@ int launch_scan_prompt_t(const CUtensorMap& tb, const CUtensorMap& tc, const CUt
   cudaLaunchConfig_t cfg{};
   cfg.stream = stream;
   cfg.attrs = &early;
-  cudaError_t err = cudaSuccess;
-  if (a.max_chunks > 0) {
-    cfg.gridDim = dim3(a.max_chunks, a.B, (a.H + kTableHeads - 1) / kTableHeads);
-    cfg.blockDim = dim3(32 * kTableHeads);
-    err = cudaLaunchKernelEx(&cfg, phs_scan_table_kernel, a);
-    cfg.numAttrs = 1;
-  }
+  cfg.gridDim = dim3(a.max_chunks, a.B, (a.H + kTableHeads - 1) / kTableHeads);
+  cfg.blockDim = dim3(32 * kTableHeads);
+  cudaError_t err = cudaLaunchKernelEx(&cfg, phs_scan_table_kernel, a);
+  cfg.numAttrs = 1;
   if (err == cudaSuccess && a.nseg > 1) {
     cfg.gridDim = dim3(a.B, a.units, (a.nseg - 1) * a.nsub);
     cfg.blockDim = dim3(kScanThreads);
     cfg.dynamicSmemBytes = kStates;
     err = cudaLaunchKernelEx(&cfg, states, tb, tc, tx, to, a);
-    cfg.numAttrs = 1;
     if (err == cudaSuccess) {
       cfg.gridDim = dim3(a.B, a.units, 64 * a.slots * N / 512);
       cfg.blockDim = dim3(128);

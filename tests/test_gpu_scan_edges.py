@@ -70,3 +70,29 @@ def test_huge_steps_that_decay_strongly(big):
     2^-186): a weight is a step at most, whatever the factors it is formed of."""
     step = torch.full((300, 2), big, device="cuda")
     Case(300, 2, 64, 64, -4.15 / big, step, 7, 2.0 ** -20).check()
+
+
+@pytest.mark.parametrize("B,lens,H,P,N", [
+    (16, [4] * 16, 8, 64, 128),                     # token by token
+    (1, [3000], 4, 64, 128),                        # cut into segments
+    (2, [700, 40], 3, 128, 64), (40, [130] * 40, 16, 64, 64)])
+def test_nothing_is_written_behind_the_workspace(B, lens, H, P, N):
+    """A workspace of the very size, full of NaN as a call may find it."""
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    T = int(cu[-1])
+    x, b, c = (synth.normal_bf16((T, h, n), i, device="cuda")
+               for i, (h, n) in enumerate(((H, P), (1, N), (1, N))))
+    dt = synth.normal_bf16((T, H), 9, device="cuda")
+    w = phs.ScanWeights(torch.full((H,), -2.0, device="cuda"))
+    need = phs.scan_prompt_workspace_bytes(B, H, 1, P, N, T, max(lens))
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    outs = []
+    for memory in (None, ws[:need]):
+        pool = phs.ScanPool.zeros(B, H, P, N)
+        outs += [phs.selective_scan_prompt(x, dt, b, c, dev(cu), max(lens), pool, w, workspace=memory),
+                 pool.s]
+    assert bool((ws[need:] == 0xFF).all())
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+    if need > 256:
+        with pytest.raises(phs.PhsError):
+            phs.selective_scan_prompt(x, dt, b, c, dev(cu), max(lens), pool, w, workspace=ws[:need - 256])

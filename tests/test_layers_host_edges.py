@@ -73,3 +73,14 @@ def test_scan_refuses_rows_past_32_bits():
         ref(inputs), P, MANY, MANY, ref(phs._lib.ScanPoolC(P.value, 4, 1, 64, 64)),
         ref(phs._lib.ScanWeightsC(P.value, 0, 0)), None, None, 2, ctypes.c_void_p(5 << 50), P, 2 ** 62,
         None, None) == -7
+
+
+# --------------------------------------------------------------- workspaces --
+@pytest.mark.parametrize("B,total,most", [(256, 1024, 4), (65535, 65535 * 16, 16), (1, 0, 0),
+                                          (3, 16, 400), (0, 0, 0)])
+def test_scans_token_by_token_need_next_to_no_workspace(B, total, most):
+    """Calls whose requests all go token by token keep nothing in the workspace;
+    0 stays the answer for what is not supported."""
+    assert phs.scan_prompt_workspace_bytes(B, 64, 8, 64, 128, total, most) == 256
+    assert phs.scan_prompt_workspace_bytes(B, 64, 8, 96, 128, total, most) == 0
+    assert phs.scan_prompt_workspace_bytes(B, 65536, 8, 64, 128, total, most) == 0
