@@ -14,7 +14,7 @@ from gpu_util import dev
 
 pytestmark = pytest.mark.gpu
 
-CHUNK, TABLE, SHORT = 128, 536, 16
+CHUNK, TABLE = 128, 536
 
 
 # ---------------------------------------------------------------- workspaces --
@@ -96,3 +96,105 @@ def test_nothing_is_written_behind_the_workspace(B, lens, H, P, N):
     if need > 256:
         with pytest.raises(phs.PhsError):
             phs.selective_scan_prompt(x, dt, b, c, dev(cu), max(lens), pool, w, workspace=ws[:need - 256])
+
+
+# ---------------------------------------------------- order of the requests --
+# Calls with more (request, pair of heads) than SMs take the longest requests
+# first, up to 256 requests.  Lengths of up to three chunks are never cut into
+# segments, so that a request alone gives the same bits.
+def alone(ins, lo, hi, start, resume, w):
+    pool = phs.ScanPool(start.clone()[None])
+    out = phs.selective_scan_prompt(*(t[lo:hi] for t in ins), dev([0, hi - lo]), hi - lo, pool, w,
+                                    resume=dev([resume]))
+    return out, pool.s[0]
+
+
+def batch_of(lens, H, P, N, seed):
+    T, B = int(sum(lens)), len(lens)
+    x, b, c = (synth.normal_bf16((T, h, n), seed + i, device="cuda")
+               for i, (h, n) in enumerate(((H, P), (1, N), (1, N))))
+    dt = synth.normal_bf16((T, H), seed + 3, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = phs.ScanWeights(-1 - 15 * torch.rand(H, generator=g, device="cuda"),
+                        torch.randn(H, generator=g, device="cuda"),
+                        torch.randn(H, generator=g, device="cuda") - 3)
+    start = torch.randn((B, H, P, N), generator=g, device="cuda")
+    return [x, dt, b, c], w, start
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+MIXED = [0, 17, 300, 300, 16, 129, 128, 127, 1, 300, 256, 257, 40, 0, 384, 15]
+ORDERS = {
+    "mixed": MIXED * 4, "equal": [130] * 64, "one long": [3] * 40 + [384] + [16] * 23,
+    "falling": list(range(320, 0, -5)), "rising": list(range(5, 325, 5)),
+    "none long": [16, 0, 1, 8] * 16, "all long": [20 + 7 * (i * 29 % 50) for i in range(64)],
+    "256": [17 + i * 37 % 150 for i in range(256)], "257": [17 + i * 37 % 150 for i in range(257)],
+}
+
+
+@pytest.mark.parametrize("P,N", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("name", ORDERS)
+def test_every_request_of_a_full_call_is_taken_once(name, P, N):
+    lens, H = ORDERS[name], 16
+    B = len(lens)
+    assert B * H * (P // 64) // 2 > sms()
+    ins, w, start = batch_of(lens, H, P, N, B)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    rng = np.random.default_rng(B)
+    ids, resume = rng.permutation(B), rng.integers(0, 2, B)
+    ids[5] = -3
+    runs = []
+    for _ in range(2):   # (the same bits each time)
+        pool, st = phs.ScanPool(start.clone()), torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full(ins[0].shape, 2.0, dtype=torch.bfloat16, device="cuda")
+        phs.selective_scan_prompt(*ins, dev(cu), max(lens), pool, w, state_ids=dev(ids),
+                                  resume=dev(resume), out=out, status=st)
+        assert int(st.item()) == 0
+        runs.append((out, pool.s))
+    assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])
+    out, S = runs[0]
+    for r in range(B):
+        lo, hi = int(cu[r]), int(cu[r + 1])
+        if ids[r] < 0:
+            assert not out[lo:hi].any()
+            continue
+        y, s = alone(ins, lo, hi, start[ids[r]], int(resume[r]), w)
+        assert torch.equal(out[lo:hi], y) and torch.equal(S[ids[r]], s), (r, lens[r])
+    kept = [i for i in range(B) if i not in set(ids.tolist())]
+    assert torch.equal(S[kept], start[kept])
+
+
+@pytest.mark.parametrize("P,N", [(64, 128), (128, 64)])
+def test_bad_requests_of_a_full_call(P, N):
+    """Ranges that fall, begin before an earlier end or are too long, ids that
+    others have or that lie outside the pool, among 64 requests by length."""
+    H, B = 16, 64
+    lens = [20 + 13 * (i * 29 % 20) for i in range(B)]
+    ins, w, start = batch_of(lens, H, P, N, 3)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    T = int(cu[-1])
+    cu[20] = cu[19] - 30         # 19 falls, 20 begins inside 18
+    cu[41] = cu[40] + max(lens) + 9   # 40 is too long, the next ones begin inside it
+    cu[50] = T + 5               # 49 ends behind the tokens, 50 begins there and falls
+    most = max(lens)
+    ids = np.arange(B)
+    ids[7], ids[30], ids[33] = ids[3], B + 4, -1
+    bad = {19, 20, 49, 50, 7, 30, 33}
+    bad |= {b for b in range(B) if not 0 <= cu[b + 1] - cu[b] <= most}   # (41 falls too)
+    bad |= {b for b in range(B) if any(cu[j] > cu[b] for j in range(b))}
+    assert len(bad) < B - 5 and any(cu[b + 1] - cu[b] > most for b in bad)
+    pool, st = phs.ScanPool(start.clone()), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full(ins[0].shape, 2.0, dtype=torch.bfloat16, device="cuda")
+    phs.selective_scan_prompt(*ins, dev(cu), most, pool, w, state_ids=dev(ids), out=out, status=st)
+    assert int(st.item()) in (-1, -3)
+    for r in range(B):
+        if r in bad:
+            if r != 7:
+                assert ids[r] < 0 or ids[r] >= B or torch.equal(pool.s[r], start[r]), r
+            continue
+        y, s = alone(ins, int(cu[r]), int(cu[r + 1]), start[r], 0, w)
+        assert torch.equal(out[cu[r]:cu[r + 1]], y) and torch.equal(pool.s[ids[r]], s), r
+    assert torch.equal(pool.s[[7, 30, 33]], start[[7, 30, 33]])

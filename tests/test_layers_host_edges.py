@@ -84,3 +84,41 @@ def test_scans_token_by_token_need_next_to_no_workspace(B, total, most):
     assert phs.scan_prompt_workspace_bytes(B, 64, 8, 64, 128, total, most) == 256
     assert phs.scan_prompt_workspace_bytes(B, 64, 8, 96, 128, total, most) == 0
     assert phs.scan_prompt_workspace_bytes(B, 65536, 8, 64, 128, total, most) == 0
+
+
+# ------------------------------------------------------ longest requests first --
+def by_length(cu, at, short_len):
+    """The scan's choice of the request that comes `at`-th, its threads one
+    after another: every request that may be written as the answer."""
+    B = len(cu) - 1
+    lens = [cu[j + 1] - cu[j] for j in range(B)]
+    more = [n > short_len for n in lens]
+    if at >= sum(more):
+        return [j for j in range(B) if not more[j]]
+    return [j for j in range(B) if more[j] and
+            sum(lens[i] > lens[j] or (lens[i] == lens[j] and i < j) for i in range(B)) == at]
+
+
+def test_longest_first_is_a_permutation():
+    """Whatever the offsets (falling ones among them), each place of a call gets
+    a request: the longer ones one place each, longest first, the others' places
+    any short one."""
+    rng = np.random.default_rng(1)
+    for trial in range(300):
+        B = int(rng.integers(2, 40))
+        kind = trial % 3
+        if kind == 0:
+            cu = np.concatenate([[0], np.cumsum(rng.integers(0, 40, B))])
+        elif kind == 1:
+            cu = np.concatenate([[0], np.cumsum(rng.choice([0, 5, 16, 17, 300], B))])
+        else:
+            cu = rng.integers(-50, 500, B + 1)
+        cu = cu.tolist()
+        lens = [cu[j + 1] - cu[j] for j in range(B)]
+        longer = [j for j in range(B) if lens[j] > 16]
+        got = [by_length(cu, at, 16) for at in range(B)]
+        assert all(len(g) == 1 for g in got[:len(longer)])
+        order = [g[0] for g in got[:len(longer)]]
+        assert sorted(order) == longer
+        assert order == sorted(longer, key=lambda j: (-lens[j], j))
+        assert all(g and all(lens[j] <= 16 for j in g) for g in got[len(longer):])
