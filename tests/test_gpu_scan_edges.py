@@ -198,3 +198,121 @@ def test_bad_requests_of_a_full_call(P, N):
         y, s = alone(ins, int(cu[r]), int(cu[r + 1]), start[r], 0, w)
         assert torch.equal(out[cu[r]:cu[r + 1]], y) and torch.equal(pool.s[ids[r]], s), r
     assert torch.equal(pool.s[[7, 30, 33]], start[[7, 30, 33]])
+
+
+# ------------------------------------------------------- what each token weighs --
+# Bounds of single terms.  A relative rounding error is 2^-24 in fp32, 2^-8 in bf16.
+def one_hot_rows(values, width, first=0):
+    """[len(values), width]: values[i] in column (first + i) % width."""
+    m = torch.zeros((len(values), width), dtype=values.dtype, device="cuda")
+    i = torch.arange(len(values), device="cuda")
+    m[i, (first + i) % width] = values
+    return m
+
+
+def bf16_of(x):
+    return x.bfloat16().double()
+
+
+@pytest.mark.parametrize("rate", [0.0, -1e-3])
+@pytest.mark.parametrize("T,H,P,N", [(128, 2, 64, 128), (100, 1, 64, 128), (17, 2, 128, 64),
+                                     (64, 3, 64, 64), (128, 1, 128, 128)])
+def test_a_state_keeps_24_bits_of_each_token(T, H, P, N, rate):
+    """Token t alone has a value in column t of b, so that each element of the
+    state is one token's weight x b.  Its weight and its product with x round
+    by 2^-24 each, three bf16 terms hold that to 2^-24, each of their three
+    products loses up to 2^-23 of the running sum: 2^-21 in all and 2^-24 for
+    the weight.  A decay's logarithm is off by 17 roundings of 2^-24 of the sum
+    behind the token, its exponential by 2 ulp (2^-22).  Two bf16 terms leave
+    up to 2^-16, which this must see."""
+    assert T <= N
+    x = synth.normal_bf16((T, H, P), 3, device="cuda")
+    b = one_hot_rows(synth.normal_bf16((T,), 4, device="cuda"), N)[:, None]
+    dt = torch.rand((T, H), generator=torch.Generator(device="cuda").manual_seed(T), device="cuda") * 19 + 21
+    pool, w = phs.ScanPool.zeros(1, H, P, N), phs.ScanWeights(torch.full((H,), rate, device="cuda"))
+    phs.selective_scan_prompt(x, dt, b, torch.zeros_like(b), dev([0, T]), T, pool, w)
+    log = (dt.double() * w.rate.double()).abs()        # (softplus above 20 is its argument)
+    behind = log.sum(0) - torch.cumsum(log, 0)
+    weight = torch.exp(-behind) * dt.double()
+    xw = weight[..., None] * x.double()                # [T, H, P]
+    want = torch.einsum("thp,tn->hpn", xw, b[:, 0].double())
+    rel = 2.0 ** -21 + 2.0 ** -24 + 17 * 2.0 ** -24 * behind + (2.0 ** -22 if rate else 0.0)
+    bound = torch.einsum("thp,tn->hpn", xw.abs() * rel[..., None], b[:, 0].double().abs())
+    ref.close(pool.s[0], want, bound, "state")
+    hi = bf16_of(xw)
+    two = torch.einsum("thp,tn->hpn", hi + bf16_of(xw - hi), b[:, 0].double())
+    assert bool(((two - want).abs() > bound).any())
+
+
+@pytest.mark.parametrize("H,P,N", [(2, 64, 128), (1, 128, 64)])
+def test_a_long_prompt_keeps_24_bits_of_each_token(H, P, N):
+    """The same for tokens spread over a prompt that goes in segments."""
+    T = 23 * 128 + 40
+    at = torch.arange(N, device="cuda") * (T // N) + 5
+    x, dt = synth.normal_bf16((T, H, P), 3, device="cuda"), torch.full((T, H), 25.3, device="cuda")
+    b = torch.zeros((T, 1, N), dtype=torch.bfloat16, device="cuda")
+    b[at, 0] = one_hot_rows(synth.normal_bf16((N,), 4, device="cuda"), N)
+    pool, w = phs.ScanPool.zeros(1, H, P, N), phs.ScanWeights(torch.zeros(H, device="cuda"))
+    phs.selective_scan_prompt(x, dt, b, torch.zeros_like(b), dev([0, T]), T, pool, w)
+    want = torch.einsum("thp,tn->hpn", x.double() * dt.double()[..., None], b[:, 0].double())
+    ref.close(pool.s[0], want, want.abs() * 2.0 ** -21, "state")
+
+
+@pytest.mark.parametrize("rate,lo,hi", [(-1.0, 1e-3, 0.1), (-8.0, 1e-3, 1.0), (0.0, 0.5, 0.5),
+                                        (-0.5, 0.01, 20.0)])
+@pytest.mark.parametrize("T,H,P,N", [(128, 1, 128, 64), (300, 1, 128, 128), (300, 2, 64, 128),
+                                     (100, 1, 64, 64), (17, 2, 64, 64), (257, 3, 64, 128)])
+@pytest.mark.parametrize("half", [0, 1])
+def test_each_weight_of_a_prompts_rows(T, H, P, N, rate, lo, hi, half):
+    """Token j alone has a value (1) in column j of x, so that column j of a row
+    is what that token weighs in it: of a chunk's own tokens one bf16 rounding
+    (2^-8), of earlier ones' state another for the row's own; 0 of later ones.
+    The decay's logarithm is off by 2^-19 of the chunk's sum for each chunk
+    (see scan_bounds), exponentials, steps and products by 2^-19."""
+    first = half * P if P < T else 0   # the tokens with values
+    g = torch.Generator(device="cuda").manual_seed(T)
+    s = torch.rand((T, H), generator=g, device="cuda") * (hi - lo) + lo
+    dt = torch.where(s > 20, s, torch.log(torch.expm1(s)))
+    beta, gamma = (synth.normal_bf16((T,), i, device="cuda") for i in (4, 5))
+    b, c = (torch.zeros((T, 1, N), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    b[:, 0, 7], c[:, 0, 7] = beta, gamma
+    n = min(P, T - first)
+    x = torch.zeros((T, H, P), dtype=torch.bfloat16, device="cuda")
+    x[first:first + n] = one_hot_rows(torch.ones(n, dtype=torch.bfloat16, device="cuda"), P)[:, None]
+    pool, w = phs.ScanPool.zeros(1, H, P, N), phs.ScanWeights(torch.full((H,), rate, device="cuda"))
+    out = phs.selective_scan_prompt(x, dt, b, c, dev([0, T]), T, pool, w)
+    y, S, m, A, log = ref.scan(x, dt, b, c, torch.zeros_like(pool.s[0]), w.rate, None, None)
+    X = max(float(log[i:i + 128].abs().sum(0).max()) for i in range(0, T, 128))
+    rel = torch.full((T, 1, 1), 2.0 ** -8, dtype=torch.float64, device="cuda")
+    rel[128:] = 2 * 2.0 ** -8 + 2.0 ** -16
+    # (a token of the same chunk as the row's: one rounding, in any chunk)
+    rel = rel + 2.0 ** -19 * (1 + (T // 128 + 1) * X)
+    ref.close(out, y, y.abs() * rel + 2.0 ** -115, "weights")
+
+
+@pytest.mark.parametrize("silu,skip", [(False, 0.0), (False, 1.0), (True, 0.0), (True, 1.0)])
+@pytest.mark.parametrize("H,P,N", [(2, 64, 128), (1, 128, 64)])
+def test_the_rows_mean_error(H, P, N, silu, skip):
+    """Root mean square error of a prompt's rows against that of rounding the
+    exact rows to bf16.  Each weight and each element of the state before a
+    chunk rounds as the row does, by up to 2^-8 of itself, independently: for
+    terms without a common sign the squares of their errors add up to what the
+    row's own rounding adds, terms with one cancel less.  A rounding's mean
+    square is 2^-16 / 3 E[1 / m^2] of the square, m the value's mantissa: E is
+    0.54 for one spread evenly over its logarithm, 0.45 to 0.6 for sums.  So at
+    most sqrt(1 + 0.6 / 0.45) = 1.53."""
+    T = 1500
+    g = torch.Generator(device="cuda").manual_seed(P)
+    x, b, c = (torch.randn((T, h, n), generator=g, device="cuda").bfloat16()
+               for h, n in ((H, P), (1, N), (1, N)))
+    if silu:
+        x, b, c = (torch.nn.functional.silu(t) for t in (x, b, c))
+    dt = torch.randn((T, H), generator=g, device="cuda") * 0.7
+    w = phs.ScanWeights(torch.full((H,), -4.0, device="cuda"), torch.full((H,), skip, device="cuda"),
+                        torch.full((H,), -4.0, device="cuda"))
+    pool = phs.ScanPool.zeros(1, H, P, N)
+    out = phs.selective_scan_prompt(x, dt, b, c, dev([0, T]), T, pool, w)
+    y, *_ = ref.scan(x, dt, b, c, torch.zeros_like(pool.s[0]), w.rate, w.skip, w.dt_bias)
+    rms = [float(((t.double() - y) ** 2).mean().sqrt()) for t in (out, y.bfloat16())]
+    print(f"rows' error {rms[0]:.3e}, of their rounding {rms[1]:.3e}: {rms[0] / rms[1]:.3f}")
+    assert rms[0] <= 1.53 * rms[1]

@@ -122,3 +122,31 @@ def test_longest_first_is_a_permutation():
         assert sorted(order) == longer
         assert order == sorted(longer, key=lambda j: (-lens[j], j))
         assert all(g and all(lens[j] <= 16 for j in g) for g in got[len(longer):])
+
+
+# ------------------------------------------------------------------- angles --
+def test_turns_against_angles_of_60_digits():
+    """The angle that position * turns (modulo 2^64) stands for, against base^(-2 i /
+    rotary_dim) * position / 2 pi in 60 decimal digits.  Frequencies are fp64:
+    a power, a product and a quotient, 2^-50 of themselves; turns round by
+    2^-65 of a turn; each a position's times."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+
+    def arctan_inverse(n):                       # of 1 / n
+        total, term, k = Decimal(0), Decimal(1) / n, 0
+        while abs(term) > Decimal(10) ** -58:
+            total += term / (2 * k + 1) * (-1) ** k
+            term, k = term / (n * n), k + 1
+        return total
+
+    pi = 4 * (4 * arctan_inverse(5) - arctan_inverse(239))
+    for dim, base in ((16, 10000.0), (64, 500.0), (128, 1e6)):
+        turns = phs.Rope.make(dim, base=base, device="cpu").turns.numpy().view(np.uint64).tolist()
+        for i, t in enumerate(turns):
+            turn = Decimal(base) ** (Decimal(-2 * i) / dim) / (2 * pi)
+            for pos in (1, 4095, 250_001, 2 ** 31 - 1):
+                got = Decimal((t * pos) % 2 ** 64) / 2 ** 64
+                off = (got - turn * pos) % 1     # of a turn, either way round
+                off = min(abs(off), 1 - abs(off))
+                assert off <= pos * (Decimal(2) ** -65 + turn * Decimal(2) ** -50), (dim, i, pos)
