@@ -1,8 +1,9 @@
 // phs_prompt.cuh -- device primitives of the chunked prompt kernels (linear
 // attention, the selective scan): waits of limited length shared by a CTA's
-// roles, register splits, packed fp32, values as sums of bf16 terms.
+// roles, register splits, values as sums of bf16 terms.
 #pragma once
 
+#include "phs_pairs.cuh"
 #include "phs_tc.cuh"
 
 namespace phs {
@@ -58,17 +59,6 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// Pairs of fp32 values, two to an instruction.
-__device__ __forceinline__ uint64_t f2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
 // (by fma with bf16 factors, here and below: shifts and masks would run on the
 // units that the conversions keep busy)
 __device__ __forceinline__ uint64_t f2_bf16(uint32_t w) {
@@ -82,27 +72,6 @@ __device__ __forceinline__ uint64_t f2_bf16(uint32_t w) {
       : "r"(w), "f"(0.f));
   return f2(lo, hi);
 }
-__device__ __forceinline__ float2 f2_get(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // bf16 pair of two values, and with take_term the values keep what it leaves
 __device__ __forceinline__ uint32_t pack_term(uint64_t x) {
   const float2 v = f2_get(x);

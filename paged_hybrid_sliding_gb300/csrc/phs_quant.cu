@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(128, PHS_QUANT_MIN_CTAS) phs_quant_kernel(cons
   const float s = __fdiv_rn(amax, 127.0f);
   const float rs = s != 0.f ? __fdiv_rn(1.0f, s) : 0.f;
   const bool always_divide = !(rs < INFINITY);
-  const uint64_t rs2 = f2_pack(rs, rs);
+  const uint64_t rs2 = f2(rs, rs);
   const size_t block = static_cast<size_t>(qp) * a.Hkv + h;  // (block, head) of 32 x D codes
   // K: straight to the pool; V: into the shared token-major tile
   uint2* out = which ? reinterpret_cast<uint2*>(s_v + kPage * half * D)

@@ -2,7 +2,7 @@
 // by the block quantiser and the quantising cache writes.
 #pragma once
 
-#include "phs_common.cuh"
+#include "phs_pairs.cuh"
 
 namespace phs {
 
@@ -13,34 +13,7 @@ namespace phs {
 // x + 128.
 constexpr float kRoundMagicOffset = 12582912.0f + 128.0f;
 
-// Packed fp32 pairs (two lanes of work per instruction on the FMA pipe,
-// each rounded to nearest as the scalar instruction would) and the
-// three-input min / max.
-__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f2_unpack(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
+// The three-input maximum and minimum.
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -65,17 +38,17 @@ __device__ __forceinline__ float fmin3(float a, float b, float c) {
 // instruction, each rounded as the scalar operation would be).
 __device__ __forceinline__ uint2 quant_codes8(const uint32_t* v, float s, uint64_t rs2,
                                               bool always_divide) {
-  const uint64_t magic2 = f2_pack(kRoundMagicOffset, kRoundMagicOffset);
+  const uint64_t magic2 = f2(kRoundMagicOffset, kRoundMagicOffset);
   uint32_t t[8];  // fl(rint(code) + 1.5 * 2^23): the code in the low byte
   float dmax = 0.f, dmin = 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     // bf16 pair -> fp32 pair: the bf16 bits are the high half of the fp32
-    const uint64_t f = f2_pack(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xFFFF0000u));
+    const uint64_t f = f2(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xFFFF0000u));
     const uint64_t y = f2_mul(f, rs2);
     const uint64_t tt = f2_add(y, magic2);
     const uint64_t d = f2_sub(y, f2_sub(tt, magic2));  // y - rint(y), in [-1/2, 1/2]
-    const float2 dd = f2_unpack(d), tf = f2_unpack(tt);
+    const float2 dd = f2_get(d), tf = f2_get(tt);
     dmax = fmax3(dmax, dd.x, dd.y);
     dmin = fmin3(dmin, dd.x, dd.y);
     t[2 * k] = __float_as_uint(tf.x);

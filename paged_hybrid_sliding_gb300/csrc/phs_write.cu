@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(2 * D, D == 128 ? 3 : 6)
     const float sv = __fdiv_rn(__uint_as_float(m & 0xFFFF0000u), 127.0f);
     const float rk = sk != 0.f ? __fdiv_rn(1.0f, sk) : 0.f;
     const float rv = sv != 0.f ? __fdiv_rn(1.0f, sv) : 0.f;
-    const uint64_t rk2 = f2_pack(rk, rk), rv2 = f2_pack(rv, rv);
+    const uint64_t rk2 = f2(rk, rk), rv2 = f2(rv, rv);
     const size_t block = static_cast<size_t>(qp) * a.Hkv + h;
     uint2* ko = reinterpret_cast<uint2*>(a.k_codes + (block * kQBlock + t) * D);
     ko[va] = quant_codes8(reinterpret_cast<const uint32_t*>(&ka), sk, rk2, !(rk < INFINITY));
