@@ -5,6 +5,7 @@
 // each channel kept between calls.
 #include "phs_layers.h"
 #include "phs_prompt.cuh"
+#include "phs_request.cuh"
 
 namespace phs {
 
@@ -31,23 +32,6 @@ __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// The channel's state, or -1 where the request has none: a negative id (an
-// inactive request), one outside the pool, or one that an earlier request
-// has.  All threads of the CTA call it.
-__device__ __forceinline__ int64_t conv_state(const ConvArgs& a, int b) {
-  if (!a.state_ids) return b;  // the launcher checked that B <= num_states
-  const int id = a.state_ids[b];
-  int again = 0;
-  for (int j = threadIdx.x; j < b; j += blockDim.x) again |= a.state_ids[j] == id;
-  again = __syncthreads_or(again);
-  if (id < 0) return -1;
-  if (id >= a.num_states || again) {
-    if (threadIdx.x == 0) set_status(a.status, again ? PHS_EINVAL : PHS_ERANGE);
-    return -1;
-  }
-  return id;
 }
 
 // A thread's filters.
@@ -97,7 +81,7 @@ struct Taps {
 template <int W>
 __global__ void phs_conv_decode_kernel(const ConvArgs a) {
   const int b = blockIdx.y, vec = blockIdx.x * blockDim.x + threadIdx.x, vecs = a.channels / kChan;
-  const int64_t id = conv_state(a, b);
+  const int64_t id = request_state(a, b);
   if (vec >= vecs) return;
   uint2* out = reinterpret_cast<uint2*>(a.out) + static_cast<size_t>(b) * vecs + vec;
   if (id < 0) {
@@ -165,7 +149,7 @@ __global__ void __launch_bounds__(256, 2) phs_conv_prompt_kernel(const ConvArgs 
   uint2* out = reinterpret_cast<uint2*>(a.out) + vec;
   for (int b = s_b0; b < s_b1; ++b) {
     const int lo = a.cu_seqlens[b], hi = a.cu_seqlens[b + 1];
-    const int64_t id = conv_state(a, b);
+    const int64_t id = request_state(a, b);
     if (!mine) continue;
     const bool begins = lo >= r0;
     // this tile's rows of the request

@@ -9,39 +9,9 @@
 #include "phs_merge.cuh"
 #include "phs_ops.h"
 #include "phs_prompt.cuh"
+#include "phs_request.cuh"
 
 namespace phs {
-
-// The state of request b, or -1 where it has none: a negative id (an
-// inactive request), one outside the pool, or one that an earlier request
-// of the call has (two requests must not update one state).  All threads of
-// the CTA call it.
-__device__ __forceinline__ int64_t request_state(const LinearArgs& a, int b) {
-  if (!a.state_ids) return b;  // the launcher checked that B <= num_states
-  const int id = a.state_ids[b];
-  int again = 0;
-  for (int j = threadIdx.x; j < b; j += blockDim.x) again |= a.state_ids[j] == id;
-  again = __syncthreads_or(again);
-  if (id < 0) return -1;
-  if (id >= a.num_states || again) {
-    if (threadIdx.x == 0) set_status(a.status, again ? PHS_EINVAL : PHS_ERANGE);
-    return -1;
-  }
-  return id;
-}
-
-// The token range of request b of a prompt call; false where it is bad: outside
-// the tokens, longer than stated, or beginning before the end of an earlier
-// one (two requests must not write one row).  All threads of the CTA call it.
-__device__ __forceinline__ bool request_tokens(const LinearArgs& a, int b, int& t0, int& t1) {
-  t0 = a.cu_seqlens[b];
-  t1 = a.cu_seqlens[b + 1];
-  int bad = t0 < 0 || t1 < t0 || t1 > a.total_tokens || t1 - t0 > a.max_seq;
-  for (int j = threadIdx.x; j < b; j += blockDim.x) bad |= a.cu_seqlens[j] > t0;
-  bad = __syncthreads_or(bad);
-  if (bad && threadIdx.x == 0) set_status(a.status, PHS_ERANGE);
-  return !bad;
-}
 
 // One CTA per (request, KV head).  A row of the state (one k index) is D/4
 // threads of one float4 each, read, updated and written back in registers; the

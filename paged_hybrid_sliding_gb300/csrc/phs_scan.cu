@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(256, P * N > 8192 ? 2 : 4)
 #pragma unroll
       for (int v = 0; v < V; ++v) s[r][v] = S[r * 8 * N + 8 * v];
   }
-  if (scan_state(a, b) < 0) {
+  if (request_state(a, b) < 0) {
     if (threadIdx.x < P) store_out(a.out, orow + threadIdx.x, 0.f, a.out_f32);
     return;
   }
@@ -96,9 +96,9 @@ __global__ void __launch_bounds__(256, P * N > 8192 ? 2 : 3)
   __shared__ float s_step[kScanShort], s_decay[kScanShort];
   __shared__ float s_y[kScanShort][P];
   const int b = blockIdx.x, h = blockIdx.y;
-  const int64_t id = scan_state(a, b);
+  const int64_t id = request_state(a, b);
   int t0, t1;
-  const bool good = scan_tokens(a, b, t0, t1);
+  const bool good = request_tokens(a, b, t0, t1);
   const int n = t1 - t0;
   if (!good || n > a.short_len) {
     pdl_wait_prior_grid();

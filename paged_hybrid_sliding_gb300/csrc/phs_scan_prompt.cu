@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(32 * kTableHeads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = h0 + warp;
   pdl_launch_dependents();
   int t0, t1;
-  if (!scan_tokens(a, b, t0, t1) || t0 + n * kScanC >= t1 || t1 - t0 <= a.short_len) return;
+  if (!request_tokens(a, b, t0, t1) || t0 + n * kScanC >= t1 || t1 - t0 <= a.short_len) return;
   const int64_t row = table_row(b, t0) + n;
   t0 += n * kScanC;
   const int v = min(kScanC, t1 - t0);
@@ -332,9 +332,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   if (STATES || a.short_len >= 0) pdl_launch_dependents();
 
   // ---- this CTA's chunks
-  const int64_t id = scan_state(a, b);
+  const int64_t id = request_state(a, b);
   int t0, t1;
-  if (!scan_tokens(a, b, t0, t1) || t1 - t0 <= a.short_len) {
+  if (!request_tokens(a, b, t0, t1) || t1 - t0 <= a.short_len) {
     pdl_wait_prior_grid();
     return;
   }
@@ -1050,9 +1050,9 @@ __global__ void __launch_bounds__(128) phs_scan_join_kernel(const __grid_constan
   const int b = blockIdx.x, unit = blockIdx.y, rows = 64 * a.slots;
   const int vecs = rows * N / 4, i = blockIdx.z * 128 + threadIdx.x;
   pdl_launch_dependents();
-  const int64_t id = scan_state(a, b);
+  const int64_t id = request_state(a, b);
   int t0, t1;
-  const bool good = scan_tokens(a, b, t0, t1) && id >= 0 && t1 - t0 > a.short_len;
+  const bool good = request_tokens(a, b, t0, t1) && id >= 0 && t1 - t0 > a.short_len;
   pdl_wait_prior_grid();
   if (!good) return;
   const int chunks = (t1 - t0 + kScanC - 1) / kScanC, parts = a.nseg * a.nsub;
