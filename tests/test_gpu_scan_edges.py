@@ -316,3 +316,39 @@ def test_the_rows_mean_error(H, P, N, silu, skip):
     rms = [float(((t.double() - y) ** 2).mean().sqrt()) for t in (out, y.bfloat16())]
     print(f"rows' error {rms[0]:.3e}, of their rounding {rms[1]:.3e}: {rms[0] / rms[1]:.3f}")
     assert rms[0] <= 1.53 * rms[1]
+
+
+# -------------------------------------------------------------------- limits --
+def test_as_many_requests_as_a_call_takes():
+    """65,535 requests of 17 tokens (the first to go in chunks): each its own."""
+    B, n, H, P, N = 65535, 17, 1, 64, 64
+    ins, w, start = batch_of([n], H, P, N, 2)
+    T = B * n
+    ins = [torch.cat([t.expand(512, *t.shape).flatten(0, 1) * (0.5 + i / 256) for i in range(128)])
+           [:T].contiguous() for t in (ins[0],)] + [t.repeat(B, *([1] * (t.dim() - 1))) for t in ins[1:]]
+    cu = torch.arange(0, T + 1, n, dtype=torch.int32, device="cuda")
+    pool, st = phs.ScanPool.zeros(B, H, P, N), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = phs.selective_scan_prompt(*ins, cu, n, pool, w, status=st)
+    assert int(st.item()) == 0
+    for b in [*range(0, B, 509), 512 * 3 - 1, 512 * 3, B - 1]:
+        y, s = alone(ins, b * n, b * n + n, torch.zeros_like(start[0]), 0, w)
+        assert torch.equal(out[b * n:b * n + n], y) and torch.equal(pool.s[b], s), b
+
+
+@pytest.mark.parametrize("H,G", [(65535, 1), (65534, 2)])
+def test_as_many_heads_as_a_call_takes(H, G):
+    T, P, N = 40, 64, 64
+    x = synth.normal_bf16((T, 64, P), 1, device="cuda")
+    x = torch.cat([x * (0.5 + i / 1024) for i in range(1024)], 1)[:, :H].contiguous()
+    b, c = (synth.normal_bf16((T, G, N), i, device="cuda") for i in (2, 3))
+    dt = synth.normal_bf16((T, 64), 4, device="cuda").repeat(1, 1024)[:, :H].contiguous()
+    w = phs.ScanWeights(-1 - torch.arange(H, device="cuda") % 7 * 1.0)
+    pool, st = phs.ScanPool.zeros(1, H, P, N), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = phs.selective_scan_prompt(x, dt, b, c, dev([0, T]), T, pool, w, status=st)
+    assert int(st.item()) == 0
+    for h in (0, 1, 2, 4095, 32766, 32767, 32768, 65000, H - 2, H - 1):
+        g, one = h // (H // G), phs.ScanPool.zeros(1, 1, P, N)
+        y = phs.selective_scan_prompt(x[:, h:h + 1].contiguous(), dt[:, h:h + 1], b[:, g:g + 1],
+                                      c[:, g:g + 1], dev([0, T]), T, one,
+                                      phs.ScanWeights(w.rate[h:h + 1].contiguous()))
+        assert torch.equal(out[:, h], y[:, 0]) and torch.equal(pool.s[0, h], one.s[0, 0]), h
