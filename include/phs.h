@@ -613,8 +613,9 @@ int phs_linear_attn_prompt(const void *q, int32_t num_q_heads, const void *k, co
  * 2^-64 of a turn whatever the position.  The first rotary_dim elements of a
  * head are rotated (a multiple of 16, at most D), the others copied: pair i
  * is elements i and i + rotary_dim / 2, with `interleaved` 2 i and 2 i + 1.
- * Scalings for long contexts change turns and factor.  Angles are taken to 32
- * bits of a turn, products in fp32, rounded once to bf16.
+ * Scalings for long contexts change turns and factor.  An angle is held to 24
+ * bits of half a turn (off by about pi 2^-25 at most), products are fp32,
+ * rounded once to bf16.
  *
  * Rows: x_stride is the number of elements from one token's row to the next
  * one's, at least heads * D, a multiple of 8; heads and their elements lie
@@ -702,7 +703,8 @@ int phs_kv_read_paged(const phs_paged_pool *pool, const int32_t *block_table,
  *
  * Causal convolution, one filter for each channel:
  *     y[t][c] = act(bias[c] + sum_k weight[c][k] x[t - width + 1 + k][c])
- * act(y) = y / (1 + exp(-y)) with `silu`, else y.  Inputs before a request's
+ * act(y) = y / (1 + exp(-y)) with `silu` (values between -2e-36 and 0, of sums
+ * below -87, may go out as zero), else y.  Inputs before a request's
  * first token are the pool's (oldest first) where resume[b] != 0 and in
  * phs_causal_conv_decode, else zero; the pool gets the last width - 1.  x and
  * out bf16 (out dense [tokens][channels]), sums fp32.  channels a multiple of
@@ -718,10 +720,13 @@ int phs_kv_read_paged(const phs_paged_pool *pool, const int32_t *block_table,
  * bf16 [tokens][H][P], b and c bf16 [tokens][G][N], dt bf16 or fp32
  * [tokens][H] (any stride of at least H); out dense [tokens][H][P], apart from
  * the inputs (PHS_EINVAL).  P and N 64 or 128.  softplus(x) = x above 20.  States are fp32
- * and stay so: what goes into them has 24 bits.  phs_selective_scan_prompt
- * forms its bf16 rows from chunks of 128 tokens: the weights of a chunk's own
- * tokens and the state before the chunk enter the products as bf16, sums and
- * the skip are fp32; a token's log decay is cut at -128.  (Requests of up to 16
+ * and stay so: what goes into them has 24 bits; an infinite one may become NaN.
+ * phs_selective_scan_prompt forms its bf16 rows from chunks of 128 tokens: the
+ * weights of a chunk's own tokens and the state before the chunk enter the
+ * products as bf16 (each off by up to 2^-8 of itself, so a row by up to 2^-8 of
+ * its terms' absolute sum beside its own rounding: it may differ from
+ * phs_selective_scan_decode's by more than one rounding), sums and the skip are
+ * fp32; a token's log decay is cut at -128.  (Requests of up to 16
  * tokens, unless one alone in a call for longer ones, go token by token as
  * phs_selective_scan_decode does.)  In a prompt an infinite or NaN value may
  * reach the request's rows from the start of its chunk of 128 tokens on, up to

@@ -63,8 +63,8 @@ struct Taps {
       for (int k = 0; k < W - 1; ++k) y = f2_fma(w[k][e], h[k].v[e], y);
       y = f2_fma(w[W - 1][e], x.v[e], y);
       if (silu) {
-        // y / (1 + exp(-y)): exp overflows to infinity below -88, where the
-        // quotient is the 0 that is wanted, of -infinity (its limit) too: that
+        // y / (1 + exp(-y)): below -87.3 the reciprocal is flushed to zero (the
+        // quotient is above -1.1e-36 there), of -infinity too, whose limit is 0: that
         // factor is cut at the lowest number, a NaN comes in by the other one
         const float2 z = f2_get(f2_mul(y, f2(-1.4426950408889634f, -1.4426950408889634f)));
         const float2 d = f2_get(f2_add(f2(ex2(z.x), ex2(z.y)), f2(1.f, 1.f))), v = f2_get(y);

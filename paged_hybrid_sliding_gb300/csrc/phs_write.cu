@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) phs_write_kernel(const __grid_consta
   __shared__ int64_t s_row[kWriteMaxTile];  // row (head 0, token's slot) of its page, or -1
   __shared__ float2 s_cs[kWriteMaxTile][D / 2];
   // (from the last tokens on: beside 8-bit blocks these have the work, and the others'
-  // CTAs end at once; 307 us against 320 for 65,521 tokens written and read back)
+  // CTAs end at once; 304 us against 317 for 65,521 tokens written and read back)
   const int tile = a.tile, r0 = (gridDim.x - 1 - blockIdx.x) * tile, r1 = min(r0 + tile, a.tokens);
   const int tid = threadIdx.x;
   bool refused = false;
@@ -263,12 +263,11 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 // the issue slots, with the two barriers of a head): 65,521 tokens of 8 heads of
 // 128 alone take 125 us, 60 for their bytes.  With `q_with_blocks` one more CTA
 // a block turns the new tokens' queries, four heads in flight, which memory
-// bounds: side by side both take 236 us for 32 query heads, 220 for their bytes
-// (288 one after the other).  Three CTAs an SM; with four, and some spilled
-// registers, 342 us against 329 for the call with its reading back (without
-// queries four were better, 380 against 397); three query heads in flight 315 against
-// 307, eight 381.  A warp for K or V of a head, with its 32 rows in registers and no
-// barrier, has too few warps: 420.
+// bounds: side by side both take 229 us for 32 query heads, 220 for their bytes.
+// All 65,521 tokens written and read back, in a replayed graph: 304 us; with four
+// CTAs an SM, and some spilled registers, 319; with three query heads in flight 311,
+// with eight 370.  A warp for K or V of a head, with its 32 rows in registers and no
+// barrier, has too few warps (a third slower).
 template <int D>
 __global__ void __launch_bounds__(2 * D, D == 128 ? 3 : 6)
     phs_write_block_kernel(const __grid_constant__ WriteArgs a, int heads_per_cta) {
@@ -450,7 +449,7 @@ __global__ void __launch_bounds__(2 * D, D == 128 ? 3 : 6)
 
 // --------------------------------------------------------------- read back --
 // One CTA per (page of 16 tokens, request).  65,521 tokens of 8 heads of 128, all but
-// the last in 8 bits: 71 us, 60 for their bytes (91 with one load of K's codes in
+// the last in 8 bits: 73 us, 60 for their bytes (91 with one load of K's codes in
 // flight instead of four).
 template <int D>
 __global__ void __launch_bounds__(128) phs_read_back_kernel(const __grid_constant__ ReadArgs a) {
@@ -584,13 +583,15 @@ int launch_write_t(WriteArgs a, int num_sms, cudaStream_t stream) {
   const int64_t blocks = a.k_codes ? int64_t{a.max_qblocks} * a.B : 0;
   if (blocks > 0) {
     // The blocks' queries go with them where there are blocks enough to fill
-    // the SMs: their copying then runs beside the blocks' arithmetic (307 us for
-    // 65,521 tokens written and read back, 358 apart).  With fewer a CTA a block
-    // would turn its queries' heads one after another.
+    // the SMs: their copying then runs beside the blocks' arithmetic (304 us for
+    // 65,521 tokens written and read back, 335 with the tokens' launch turning
+    // them).  With fewer a CTA a block would turn its queries' heads one after
+    // another, as it does where max_qblocks, a limit for every request, is
+    // far above the blocks that there are (the host does not know their number).
     a.q_with_blocks = a.q && blocks >= int64_t{4} * num_sms;
     // All heads of a block by one CTA, which forms their angles once, unless
     // that leaves SMs without one; beside queries in halves, which end
-    // together with those (307 us against 312; quarters 323).
+    // together with those (304 us against 308; quarters 319).
     int per = a.q_with_blocks ? (a.Hkv + 1) / 2 : a.Hkv;
     while (per > 2 && blocks * ((a.Hkv + per - 1) / per) < int64_t{8} * num_sms)
       per = (per + 1) / 2;
@@ -614,7 +615,7 @@ int launch_write_t(WriteArgs a, int num_sms, cudaStream_t stream) {
 int launch_write(int D, WriteArgs a, int num_sms, cudaStream_t stream) {
   // Tiles as long as that leaves eight CTAs an SM (a limit of 1, 2 or 4: 45 to 49
   // us for 1,514 ragged tokens written and read back, within that call's own spread;
-  // tiles of up to 8, 16 and 32 tokens: 316, 307 and 320 us for 65,521 tokens with
+  // tiles of up to 8, 16 and 32 tokens: 312, 304 and 317 us for 65,521 tokens with
   // their queries by the blocks' launch, since more CTAs then have nothing to do).
   a.tile = kWriteMaxTile;
   while (a.tile > 1 && a.tokens < a.tile * 8 * num_sms) a.tile /= 2;
