@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(256, P * N > 8192 ? 2 : 4)
 // 128, take 253 us here (161 for their states' bytes), of 16 tokens 597, of 17,
 // in chunks, 1,150.  Behind the chunks of longer requests, at whose end it fills
 // the SMs: 16 of 1 to 517 tokens 67 us (70 with chunks alone; limits of 8, 16, 24
-// and 32 tokens 67, 67, 66 and 72).
+// and 32 tokens 67, 67, 66 and 72).  The limit of 16 is that call's; in a call of
+// 256 requests chunks would first pay at about 35 tokens (29 us a token one by one).
 template <int P, int N>
 __global__ void __launch_bounds__(256, P * N > 8192 ? 2 : 3)
     phs_scan_short_kernel(const __grid_constant__ ScanArgs a) {

@@ -20,8 +20,9 @@
 // out of a SiLU (1.03 to 1.08 with a skip of about 1), 1.1 to 1.5 where they are
 // centred.  (Two terms of each, for 16 bits of them, leave the rounding alone; with
 // them the kernel took 577 us for 32,751 tokens of 64 heads, 468 without, other
-// changes of the same step among that; 421 now.)  The skip is added in fp32.  What goes into the state keeps its 24 bits: X'
-// (x times exp(L_last - L_j) s_j) enters as a sum of three bf16 terms, and KV is
+// changes of the same step among that; 421 now.)  The skip is added in fp32.
+// What goes into the state keeps its 24 bits: X' (x times exp(L_last - L_j)
+// s_j) enters as a sum of three bf16 terms, and KV is
 // accumulated chunk by chunk from zero and added to the state in fp32 registers:
 // the tensor cores' own sums drop the bits below the running sum's last one.
 //
