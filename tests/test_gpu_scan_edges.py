@@ -11,6 +11,7 @@ import layers_ref as ref
 import paged_hybrid_sliding_gb300 as phs
 import synth
 from gpu_util import dev
+from test_gpu_scan import Layer
 
 pytestmark = pytest.mark.gpu
 
@@ -352,3 +353,49 @@ def test_as_many_heads_as_a_call_takes(H, G):
                                       c[:, g:g + 1], dev([0, T]), T, one,
                                       phs.ScanWeights(w.rate[h:h + 1].contiguous()))
         assert torch.equal(out[:, h], y[:, 0]) and torch.equal(pool.s[0, h], one.s[0, 0]), h
+
+
+@pytest.mark.parametrize("H,P,N", [(2, 64, 128), (3, 128, 64)])
+@pytest.mark.parametrize("n", [0, 1, 16, 17, 129, 1000, 5990])
+@pytest.mark.parametrize("resume", [0, 1])
+def test_a_prompt_far_below_the_stated_length(H, P, N, n, resume):
+    """The plan is made for 6,000 tokens, cut into segments; most of them then
+    have no chunk."""
+    L = Layer(H, 1, P, N, 2, H)
+    ins = L.inputs(6000, 3)
+    out, st = torch.full((6000, H, P), 2.0, dtype=torch.bfloat16, device="cuda"), \
+        torch.zeros(1, dtype=torch.int32, device="cuda")
+    phs.selective_scan_prompt(*ins, dev([3, 3 + n]), 6000, L.pool, L.w, state_ids=dev([1]),
+                              resume=dev([resume]), out=out, status=st)
+    assert int(st.item()) == 0
+    L.check(ins, out, [(3, 3 + n)], [1], [resume], True)
+    assert bool((out[:3] == 2).all()) and bool((out[3 + n:] == 2).all())
+
+
+def test_a_captured_call_with_other_lengths_each_time():
+    """Offsets, ids and resume are read on the device: a graph made for the
+    longest call is replayed for others."""
+    L = Layer(4, 2, 64, 128, 5, 7)
+    ins = L.inputs(2000, 3)
+    out = torch.zeros((2000, 4, 64), dtype=torch.bfloat16, device="cuda")
+    cu, ids, resume = dev([0, 1000, 2000, 2000]), dev([0, 1, 2]), dev([0, 0, 0])
+    need = phs.scan_prompt_workspace_bytes(3, 4, 2, 64, 128, 2000, 2000)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    call = lambda: phs.selective_scan_prompt(*ins, cu, 2000, L.pool, L.w, state_ids=ids, resume=resume,
+                                             out=out, workspace=ws)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for offsets, i, r in (([0, 5, 1700, 1716], [4, 2, 0], [1, 0, 1]), ([0, 0, 2000, 2000], [3, 1, 2], [1, 1, 0]),
+                          ([100, 117, 134, 151], [2, -1, 3], [0, 1, 1]), ([0, 700, 1400, 2000], [1, 0, 4], [1, 1, 1])):
+        L.pool.s.copy_(L.start)
+        out.fill_(2)
+        cu.copy_(dev(offsets)), ids.copy_(dev(i)), resume.copy_(dev(r))
+        ws.fill_(0xFF)
+        graph.replay()
+        L.check(ins, out, list(zip(offsets[:-1], offsets[1:])), i, r, True)
+        assert bool((out[:offsets[0]] == 2).all()) and bool((out[offsets[-1]:] == 2).all())
