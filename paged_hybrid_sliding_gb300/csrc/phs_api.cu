@@ -1767,6 +1767,44 @@ int phs_linear_attn_decode(const void* q, int32_t num_q_heads, const phs_state_p
 
 namespace {
 
+// The cheaper of no segments of each prompt and as many as leave each CTA an SM to
+// itself, with the parts that a first launch sums a segment up in (shared by the
+// chunked prompt calls).  A call has `pairs` (request, unit of heads), `groups` CTAs
+// for each; the longest request has `chunks`, all units of all requests
+// `all_chunks`.  Costs in half microseconds: 16 for a CTA (of either launch); for a
+// chunk `chunk`, of which 4 for its state (in either launch); 4 for joining the sums.
+struct Segments {
+  long long time = -1;
+  int nseg = 1, nsub = 1;
+};
+Segments best_segments(long long pairs, int groups, long long chunks, long long all_chunks,
+                       long long chunk, int sms) {
+  Segments best;
+  const long long most = std::max(1LL, std::min(sms / (pairs * groups), chunks / 2));
+  for (const long long s : {1LL, most}) {
+    const long long per = (chunks + s - 1) / s;
+    long long time = 16 + per * chunk, sub = 1;
+    if (s == 1) {  // (a request's last chunk is half full on average)
+      time = std::max(time, groups * (pairs * 16 + chunk * all_chunks) / sms);
+    } else {
+      long long sums = -1;
+      for (long long n = 1; n <= 8 && n <= per; ++n) {
+        const long long waves = ((s - 1) * pairs * n + sms - 1) / sms;
+        const long long t = waves * (16 + 4 * ((per + n - 1) / n));
+        if (sums >= 0 && t >= sums) continue;
+        sums = t;
+        sub = n;
+      }
+      time += sums + 4;
+    }
+    if (best.time >= 0 && time >= best.time) continue;
+    best.time = time;
+    best.nseg = static_cast<int>(s);
+    best.nsub = static_cast<int>(sub);
+  }
+  return best;
+}
+
 // How a prompt call is spread over the SMs: segments of each prompt, parts
 // that a first launch sums a segment up in, and CTAs that share a KV head's
 // query heads.  Of the plans the one with the least time is taken, by these
@@ -1788,29 +1826,13 @@ LinearPlan linear_plan(int B, int G, int Hkv, int D, int total, int max_seq, int
   long long best = -1;
   for (int g = 1; g <= G; ++g) {
     if (G % g != 0) continue;
-    const long long most = std::max(1LL, std::min(sms / (pairs * g), chunks / 2));
-    for (const long long s : {1LL, most}) {
-      const long long per = (chunks + s - 1) / s, chunk = 4 + 3 * (G / g);
-      long long time = 16 + per * chunk, sub = 1;
-      if (s == 1) {  // (a request's last chunk is half full on average)
-        time = std::max(time, g * (pairs * 16 + Hkv * chunk * (total / C + B / 2)) / sms);
-      } else {
-        long long sums = -1;
-        for (long long n = 1; n <= 8 && n <= per; ++n) {
-          const long long waves = ((s - 1) * pairs * n + sms - 1) / sms;
-          const long long t = waves * (16 + 4 * ((per + n - 1) / n));
-          if (sums >= 0 && t >= sums) continue;
-          sums = t;
-          sub = n;
-        }
-        time += sums + 4;
-      }
-      if (best >= 0 && time >= best) continue;
-      best = time;
-      p.nseg = static_cast<int>(s);
-      p.nsub = static_cast<int>(sub);
-      p.ngrp = g;
-    }
+    const Segments s =
+        best_segments(pairs, g, chunks, Hkv * (total / C + B / 2), 4 + 3 * (G / g), sms);
+    if (best >= 0 && s.time >= best) continue;
+    best = s.time;
+    p.nseg = s.nseg;
+    p.nsub = s.nsub;
+    p.ngrp = g;
   }
   if (p.nseg > 1 || p.ngrp > 1)
     p.need = static_cast<size_t>(pairs) * p.nseg * p.nsub * D * D * sizeof(float);
@@ -2208,12 +2230,8 @@ bool scan_overlap(const ScanArgs& a, int P, int N, int64_t tokens) {
 }
 
 // How a prompt call is spread over the SMs: 64-wide heads in pairs where a
-// group has an even number of them, segments of each prompt, and parts that a
-// first launch sums a segment up in.  Of no segments and as many as leave each
-// CTA an SM to itself the plan with the least time is taken, by these costs in
-// half microseconds: 16 for a CTA (of either launch); for each chunk 4 for
-// its state (in either launch) and 4 for the rows of each slot; 4 for joining
-// the sums.
+// group has an even number of them, and segments by best_segments with 4 half
+// microseconds of a chunk for the rows of each slot.
 struct ScanPlan {
   int slots = 1, units = 1, nseg = 1, nsub = 1;
   size_t tables = 0, sums = 0, need = 0;  // bytes
@@ -2223,30 +2241,10 @@ ScanPlan scan_plan(int B, int H, int G, int P, int N, int total, int max_seq, in
   p.slots = P == 128 || H / G % 2 == 0 ? 2 : 1;
   p.units = H * (P / 64) / p.slots;
   const long long pairs = std::max(1LL, 1LL * B * p.units), C = kScanChunk;
-  const long long chunks = (std::min(total, max_seq) + C - 1) / C, chunk = 4 + 4 * p.slots;
-  const long long most = std::max(1LL, std::min(sms / pairs, chunks / 2));
-  long long best = -1;
-  for (const long long s : {1LL, most}) {
-    const long long per = (chunks + s - 1) / s;
-    long long time = 16 + per * chunk, sub = 1;
-    if (s == 1) {  // (a request's last chunk is half full on average)
-      time = std::max(time, (pairs * 16 + p.units * chunk * (total / C + B / 2)) / sms);
-    } else {
-      long long sums = -1;
-      for (long long n = 1; n <= 8 && n <= per; ++n) {
-        const long long waves = ((s - 1) * pairs * n + sms - 1) / sms;
-        const long long t = waves * (16 + 4 * ((per + n - 1) / n));
-        if (sums >= 0 && t >= sums) continue;
-        sums = t;
-        sub = n;
-      }
-      time += sums + 4;
-    }
-    if (best >= 0 && time >= best) continue;
-    best = time;
-    p.nseg = static_cast<int>(s);
-    p.nsub = static_cast<int>(sub);
-  }
+  const Segments s = best_segments(pairs, 1, (std::min(total, max_seq) + C - 1) / C,
+                                   p.units * (total / C + B / 2), 4 + 4 * p.slots, sms);
+  p.nseg = s.nseg;
+  p.nsub = s.nsub;
   // (in 64 bits: 65,535 requests of 128 heads have 4.5e9 floats of tables)
   p.tables = align256(static_cast<size_t>(total / C + B + 1) * H * kScanTable * sizeof(float));
   if (p.nseg > 1)

@@ -193,12 +193,6 @@ struct LinLayout {
   static_assert(kAlloc + kTables <= 227 * 1024, "shared memory of the prompt kernel");
 };
 
-// First chunk of part p of a request's `chunks`; a segment is nsub parts, and
-// part nseg * nsub is the end.
-__device__ __forceinline__ int part_chunk(const LinearArgs& a, int chunks, int p) {
-  return static_cast<int>(static_cast<int64_t>(chunks) * p / (a.nseg * a.nsub));
-}
-
 // The request that comes `at`-th when the longest come first.  Where there are
 // more CTAs than SMs, the last ones to start then end soon: 48.5 us against 61
 // for 16 prompts of 1 to 517 tokens, 32 heads on 8.  All threads of the CTA

@@ -39,4 +39,11 @@ __device__ __forceinline__ bool request_tokens(const Args& a, int b, int& t0, in
   return !bad;
 }
 
+// First chunk of part p of a request's `chunks`; a segment is nsub parts, and
+// part nseg * nsub is the end.
+template <class Args>
+__device__ __forceinline__ int part_chunk(const Args& a, int chunks, int p) {
+  return static_cast<int>(static_cast<int64_t>(chunks) * p / (a.nseg * a.nsub));
+}
+
 }  // namespace phs

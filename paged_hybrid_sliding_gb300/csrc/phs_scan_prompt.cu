@@ -18,9 +18,9 @@
 // row by up to 2^-8 of its terms' absolute sum beside its own rounding; root mean
 // square, and in units of that rounding's: 1.0 to 1.4 in all where b, c and x come
 // out of a SiLU (1.03 to 1.08 with a skip of about 1), 1.1 to 1.5 where they are
-// centred.  (Two terms of each, for 16 bits of them, leave the rounding alone; with
-// them the kernel took 577 us for 32,751 tokens of 64 heads, 468 without, other
-// changes of the same step among that; 421 now.)  The skip is added in fp32.
+// centred.  (Two terms of each, for 16 bits of them, leave that rounding alone; at
+// the step that left them out 32,751 tokens of 64 heads took 509 us with them, 468
+// without.)  The skip is added in fp32.
 // What goes into the state keeps its 24 bits: X' (x times exp(L_last - L_j)
 // s_j) enters as a sum of three bf16 terms, and KV is
 // accumulated chunk by chunk from zero and added to the state in fp32 registers:
@@ -142,12 +142,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
-}
-
-// First chunk of part p of a request's `chunks`; a segment is nsub parts, and
-// part nseg * nsub is the end.
-__device__ __forceinline__ int part_chunk(const ScanArgs& a, int chunks, int p) {
-  return static_cast<int>(static_cast<int64_t>(chunks) * p / (a.nseg * a.nsub));
 }
 
 // Row of the tables of request b's first chunk (t0 its first token): requests
