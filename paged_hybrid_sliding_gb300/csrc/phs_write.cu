@@ -466,9 +466,11 @@ __global__ void __launch_bounds__(128) phs_read_back_kernel(const __grid_constan
     if (tid == 0 && blockIdx.x == 0) set_status(a.status, PHS_ERANGE);
     return;
   }
+  // (pages behind the request's last one end here: of a start near 2^31 their tokens
+  // would pass it)
+  if (n == 0 || static_cast<int>(blockIdx.x) > (start % kPage + n - 1) / kPage) return;
   const int lp = start / kPage + blockIdx.x, p0 = lp * kPage;
   const int lo = max(start, p0), hi = min(start + n, p0 + kPage);
-  if (lo >= hi) return;
   const bool codes = p0 < qlen;
   int page = -1;
   int64_t pages = codes ? a.num_qpages : a.num_pages;

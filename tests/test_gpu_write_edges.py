@@ -109,3 +109,21 @@ def test_a_long_prompt_beside_many_tokens(H, D, Hq):
     assert int(st.item()) == 0 and same(c.pool, w.pool)
     for a, b in zip(int8_tensors(c.int8), int8_tensors(w.int8)):
         assert torch.equal(a, b)
+
+
+def test_reads_near_the_last_position():
+    """A start near 2^31 beside a longer request: its pages are outside the
+    table, its rows zero, the other's rows what they are."""
+    H, D = 2, 64
+    c, st = Cache(np.array([400, 400], np.int32), H, D, 3), status()
+    for start, n in ((2**31 - 100, 60), (2**31 - 17 - 33, 33), (2**31 - 18, 1)):
+        k, v = phs.kv_read_paged(c.pool, dev(c.table), torch.tensor([5, start], dtype=torch.int32).cuda(),
+                                 dev([0, 390, 390 + n]), 390 + n, 390, status=st)
+        assert int(st.item()) == -3 and not k[390:].any() and not v[390:].any()
+        assert torch.equal(k[:390], c.rows(c.pool.k, 0, 5, 395))
+        assert torch.equal(v[:390], c.rows(c.pool.v, 0, 5, 395))
+    st.zero_()   # one further on the range itself is refused
+    k = torch.full((391, H, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    phs.kv_read_paged(c.pool, dev(c.table), torch.tensor([5, 2**31 - 17], dtype=torch.int32).cuda(),
+                      dev([0, 390, 391]), 391, 390, k_out=k, v_out=k.clone(), status=st)
+    assert int(st.item()) == -3 and bool((k[390:] == 3).all())
